@@ -6,11 +6,12 @@ Three operators, as a serving step of a hybrid model uses them next to the recur
   append  cache4_append / cache4_read: key and value rows quantised into the pages, and the values that they stand for
   attn    cache4_attention: attention of packed ragged queries over the 4-bit pages
 
-Cache format.  cache is uint8 [pages][Hkv][page_bytes]; per page and head the bytes are, one after the other, the key
-codes [page_size][d/2], key scales [page_size][d/16], value codes [page_size][d/2] and value scales [page_size][d/16].
-A code is an e2m1 nibble (the even channel in the low nibble), a scale one e4m3 byte per 16 channels.  Of 16 channels x:
-scale = e4m3(max|x| / 6), code = e2m1(x / scale), both rounded to nearest, ties to even, held at the format's largest
-value; a scale of zero has codes of zero.
+Cache format.  cache is uint8 [pages][Hkv][page_bytes]; per page and head it holds page_size / 16 blocks of 16 tokens, and
+a block's bytes are, one after the other, the key codes [16 tokens][d/2], key scales [16 tokens][d/16], value codes
+[d/16 groups][16 tokens][8] and value scales [d/16 groups][16 tokens].  A code is an e2m1 nibble (the even channel in the
+low nibble), a scale one e4m3 byte per group of 16 channels.  Of 16 channels x: scale = e4m3(max|x| / 6), code =
+e2m1(x / scale), both rounded to nearest, ties to even, held at the format's largest value; a scale of zero has codes of
+zero.
 """
 import math
 import random
@@ -126,9 +127,11 @@ def _quantise(x):
 
 def _page_bytes(k, v):
     """One record per leading index from k, v [..., page, d]."""
-    kc, ks = _quantise(k)
-    vc, vs = _quantise(v)
-    return torch.cat([t.flatten(-2) for t in (kc, ks, vc, vs)], dim=-1)
+    kc, ks = [t.unflatten(-2, (-1, 16)).flatten(-2) for t in _quantise(k)]
+    vc, vs = [t.unflatten(-2, (-1, 16)) for t in _quantise(v)]
+    vc = vc.unflatten(-1, (-1, 8)).transpose(-3, -2).flatten(-3)
+    vs = vs.transpose(-2, -1).flatten(-2)
+    return torch.cat((kc, ks, vc, vs), dim=-1).flatten(-2)
 
 
 def _rows(gen, shape, dtype=torch.float32, chan=None):
@@ -225,9 +228,12 @@ def _append_plain(s):
 
 def _parts(rec, page, d):
     """Keys' and values' codes and scales of records [..., page_bytes], each [..., page, *]."""
-    a, b = page * d // 2, page * d // 16
-    cut = torch.split(rec, (a, b, a, b), dim=-1)
-    return [x.unflatten(-1, (page, -1)) for x in cut]
+    a, b = 16 * d // 2, 16 * d // 16
+    kc, ks, vc, vs = torch.split(rec.unflatten(-1, (page // 16, -1)), (a, b, a, b), dim=-1)
+    kc, ks = kc.unflatten(-1, (16, -1)), ks.unflatten(-1, (16, -1))
+    vc = vc.unflatten(-1, (d // 16, 16, 8)).transpose(-3, -2).flatten(-2)
+    vs = vs.unflatten(-1, (d // 16, 16)).transpose(-2, -1)
+    return [x.flatten(-3, -2) for x in (kc, ks, vc, vs)]
 
 
 def _attn_plain(s):
