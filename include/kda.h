@@ -64,6 +64,9 @@ extern "C" {
 #define KDA_STATUS_SEGMENT_OVERFLOW 0x4u /* segment table larger than planned      */
 #define KDA_STATUS_TIMEOUT 0x8u          /* a bounded on-chip wait gave up; unit left unfinished */
 #define KDA_STATUS_BAD_DRAFT_LEN 0x10u   /* draft_len[r] outside [0, Wd]                         */
+#define KDA_STATUS_NO_PAGES 0x20u        /* free list too short (or free_count out of range)     */
+#define KDA_STATUS_BAD_PAGE 0x40u        /* a page or slot outside the cache                     */
+#define KDA_STATUS_NOT_FINITE 0x80u      /* a key or value row is not finite                     */
 
 /* Kernel families, for kda_kernel_timing_stop. */
 #define KDA_KERNEL_CHUNK_LIST 0      /* chunk slot list of the two-kernel prefill */
@@ -78,7 +81,12 @@ extern "C" {
 #define KDA_KERNEL_BWD_WALK 9        /* kda_chunk_bwd, tensor cores: reverse state walk */
 #define KDA_KERNEL_BWD_CHUNK 10      /* kda_chunk_bwd, tensor cores: chunk gradients */
 #define KDA_KERNEL_BWD_COMPOSE 11    /* kda_chunk_bwd_cp: state gradient over the segments */
-#define KDA_KERNEL_KINDS 12
+#define KDA_KERNEL_PAGE_PLAN 12      /* kda_page_plan */
+#define KDA_KERNEL_CACHE4_APPEND 13  /* kda_cache4_append */
+#define KDA_KERNEL_CACHE4_READ 14    /* kda_cache4_read */
+#define KDA_KERNEL_CACHE4_ATTN 15    /* kda_cache4_attention */
+#define KDA_KERNEL_CACHE4_MERGE 16   /* kda_cache4_attention: shares of a long key axis joined */
+#define KDA_KERNEL_KINDS 17
 
 /* Human-readable name of a return status. Never NULL. */
 const char *kda_status_string(int status);
@@ -478,6 +486,120 @@ int kda_decode_verify_replay_ragged(void *state, void *conv_tail, const float *c
                                     int dv, int W, int Wd, float scale, float g_min,
                                     float eps_in, float eps_out, int conv_act,
                                     uint32_t *status, void *stream);
+
+/*
+ * The paged 4-bit key/value cache of a hybrid model's attention layers
+ * ("Inference : cache KV, decodage, quantification": attention layers with a
+ * growing cache stand next to the KDA layers, and each head's cache is a
+ * self-contained byte stream).  The pages fix neither a format nor an
+ * interface; these are this library's.
+ *
+ * cache       device uint8 [num_pages][Hkv][page_size * 9 * d / 8], page_size a
+ *             power of two from 16 to 256, d = 64 or 128.  A page and head
+ *             hold page_size / 16 blocks of 16 tokens; a block's bytes are
+ *             key codes    [16 tokens][d / 2],       key scales   [16 tokens][d / 16],
+ *             value codes  [d / 16 groups][16][8],   value scales [d / 16 groups][16].
+ *             A code is an e2m1 nibble (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *             negatives; the even channel in the low nibble), a scale one
+ *             e4m3 byte per group of 16 channels.  Of a group x, divided by
+ *             its head's scale where one is given:
+ *                 s = e4m3(max|x| / 6),  code = e2m1(x / s),  x' = code * s * head scale,
+ *             both rounded to nearest with ties to even and saturating; a
+ *             scale of zero has codes of zero.
+ * slot        token address: page * page_size + offset in the page; num_pages
+ *             * page_size < 2^31.  Negative slots are skipped.
+ * k_scale, v_scale  device f32 [Hkv] or NULL (1): the cache's units, the same
+ *             in every call on it.  A power of two keeps the division exact.
+ * A token whose key or value holds a NaN or an infinity in some head is
+ * marked in that head: queries that see it come out NaN, others are not
+ * touched, and KDA_STATUS_NOT_FINITE is set.
+ */
+
+/*
+ * Block tables, slot map and positions of a serving step, from the requests'
+ * lengths.  Request r has context_len[r] tokens in the cache, gets new_len[r]
+ * and holds page_count[r] pages (the first entries of its row of the block
+ * table; it may hold more than its tokens fill).  Pages that it lacks are
+ * taken from the end of the free list, in request order.
+ *  context_len, new_len, page_count  device int32 [R].
+ *  block_table   device int32 [R][max_pages]; only entries of newly taken
+ *                pages are written.  max_pages * page_size < 2^31.
+ *  free_pages    device int32 [num_free], the first free_count[0] are free.
+ *  T             rows of slot_map and positions; at least the sum of new_len.
+ *  cu_seqlens    device int32 [R + 1], prefix sums of new_len (the calls' cu_seqlens).
+ *  seq_len       device int32 [R], context_len + new_len.
+ *  slot_map, positions  device int32 [T]: slot and position of every new
+ *                token, packed by cu_seqlens; -1 past the last one.
+ *  page_count_out [R], free_count_out [1]: the counts after the call (other
+ *                buffers than page_count and free_count: many blocks read
+ *                those).
+ * A request whose lengths are negative, that does not fit max_pages, or whose
+ * rows end past T sets KDA_STATUS_BAD_SEQLENS; one whose pages are not there
+ * sets KDA_STATUS_NO_PAGES, and so do all later ones that need a page.  Such
+ * a request keeps its rows in cu_seqlens, with slots and positions of -1, its
+ * length and its pages.  A table entry below 0, or a slot past 2^31, sets
+ * KDA_STATUS_BAD_PAGE and gives slots of -1.
+ */
+int kda_page_plan(const int32_t *context_len, const int32_t *new_len, const int32_t *page_count,
+                  int32_t *block_table, const int32_t *free_pages, const int32_t *free_count,
+                  int R, int max_pages, int num_free, int page_size, int T, int32_t *cu_seqlens,
+                  int32_t *seq_len, int32_t *slot_map, int32_t *positions,
+                  int32_t *page_count_out, int32_t *free_count_out, uint32_t *status,
+                  void *stream);
+
+/*
+ * Key and value rows into the cache, at the slots of a slot map.
+ *  k, v       device, dtype in_dtype (bf16 | f32), rows of [Hkv][d], k_stride
+ *             and v_stride elements apart (at least Hkv * d, a multiple of 16
+ *             bytes: rows may lie inside a fused projection).
+ *  slot_map   device int32 [T], distinct where not negative.  A slot past the
+ *             cache sets KDA_STATUS_BAD_PAGE and is skipped.
+ */
+int kda_cache4_append(const void *k, const void *v, const int32_t *slot_map, void *cache, int T,
+                      int Hkv, int d, int num_pages, int page_size, long long k_stride,
+                      long long v_stride, const float *k_scale, const float *v_scale,
+                      int in_dtype, uint32_t *status, void *stream);
+
+/* The keys and values that slots [n] stand for: k, v device [n][Hkv][d], dtype
+ * out_dtype; zero for a negative slot or one past the cache, NaN for a marked
+ * token. */
+int kda_cache4_read(const void *cache, const int32_t *slots, int n, int Hkv, int d, int num_pages,
+                    int page_size, const float *k_scale, const float *v_scale, int out_dtype,
+                    void *k, void *v, uint32_t *status, void *stream);
+
+/*
+ * Attention of packed, ragged queries over the cache: single tokens, verify
+ * windows and prompt chunks in one call.
+ *     o_i = sum_j softmax_j(scale q_i . k_j) v_j over the visible keys j
+ *  q          device, in_dtype, rows of [Hq][d], q_stride elements apart
+ *             (as k_stride); query head x reads key head x / (Hq / Hkv).
+ *  block_table, seq_len  as kda_page_plan leaves them: request r's keys are
+ *             positions 0 .. seq_len[r] - 1, its new tokens among them.
+ *  cu_seqlens device int32 [R + 1]: request r's queries are rows
+ *             [cu[r], cu[r + 1]), the last of its seq_len[r] positions.  Query
+ *             i of n sees positions up to seq_len[r] - n + i, and with window
+ *             > 0 only the last `window` of those.  A query that sees nothing
+ *             gets o = 0 and lse = -inf.
+ *  max_new    an upper bound of the requests' new tokens (0: T).  It picks the
+ *             kernel's tile; a request with more is still computed.
+ *  o          device [T][Hq][d], in_dtype.  lse: device f32 [T][Hq] or NULL,
+ *             the natural log of the sum of e^{scale q.k}.
+ *  workspace  at least kda_cache4_attention_workspace_size(...) bytes.
+ * Products take f16 operands with fp32 accumulation: keys and values exactly
+ * as the cache holds them, queries scaled by a power of two per row, weights
+ * rounded to 11 bits; 32-bit queries and their weights in two f16 parts each.
+ * Running maximum and sum are fp32.  The same inputs give the same bits.
+ * A request with a length past max_pages * page_size or queries past T sets
+ * KDA_STATUS_BAD_SEQLENS and is skipped; a page outside the cache sets
+ * KDA_STATUS_BAD_PAGE, and that request's rows are unspecified.
+ */
+int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_table,
+                         const int32_t *seq_len, const int32_t *cu_seqlens, int R, int T, int Hq,
+                         int Hkv, int d, int num_pages, int page_size, int max_pages, int max_new,
+                         int window, float scale, long long q_stride, const float *k_scale,
+                         const float *v_scale, void *o, float *lse, int in_dtype, void *workspace,
+                         size_t workspace_bytes, uint32_t *status, void *stream);
+size_t kda_cache4_attention_workspace_size(int R, int T, int Hq, int Hkv, int d, int in_dtype);
 
 /*
  * Context-parallel prefill that allocates nothing.  (The pages have no

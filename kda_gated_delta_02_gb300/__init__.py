@@ -21,7 +21,8 @@ __all__ = ["chunk_fwd", "chunk_fwd_workspace_size", "chunk_fwd_prep_workspace_si
            "CP_OFF", "CP_ON", "CP_AUTO", "CONV_NONE", "CONV_SILU", "STATUS_BAD_SEQLENS",
            "STATUS_BAD_ACCEPTED_LEN", "STATUS_SEGMENT_OVERFLOW", "STATUS_TIMEOUT", "STATUS_BAD_DRAFT_LEN",
            "KERNEL_FAMILIES", "chunk_bwd", "chunk_fwd_host", "kernel_timing_start",
-           "kernel_timing_stop"]
+           "kernel_timing_stop", "page_plan", "cache4_alloc", "cache4_append", "cache4_read", "cache4_attention",
+           "cache4_attention_workspace_size", "STATUS_NO_PAGES", "STATUS_BAD_PAGE", "STATUS_NOT_FINITE"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -33,6 +34,7 @@ CONV_NONE, CONV_SILU = 0, 1
 DTYPE_BF16, DTYPE_F32 = 0, 1
 STATUS_BAD_SEQLENS, STATUS_BAD_ACCEPTED_LEN, STATUS_SEGMENT_OVERFLOW = 1, 2, 4
 STATUS_TIMEOUT, STATUS_BAD_DRAFT_LEN = 8, 16
+STATUS_NO_PAGES, STATUS_BAD_PAGE, STATUS_NOT_FINITE = 32, 64, 128
 
 
 class KDAError(RuntimeError):
@@ -105,6 +107,17 @@ def load_library():
         lib.kda_decode_verify_replay.restype = I
         lib.kda_decode_verify_replay.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I,
                                                  F, F, F, F, I, P, P]
+        L = ctypes.c_longlong
+        lib.kda_page_plan.restype = I
+        lib.kda_page_plan.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P, P]
+        lib.kda_cache4_append.restype = I
+        lib.kda_cache4_append.argtypes = [P, P, P, P, I, I, I, I, I, L, L, P, P, I, P, P]
+        lib.kda_cache4_read.restype = I
+        lib.kda_cache4_read.argtypes = [P, P, I, I, I, I, I, P, P, I, P, P, P, P]
+        lib.kda_cache4_attention.restype = I
+        lib.kda_cache4_attention.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, L, P, P, P, P, I, P, S, P, P]
+        lib.kda_cache4_attention_workspace_size.restype = S
+        lib.kda_cache4_attention_workspace_size.argtypes = [I, I, I, I, I, I]
         _lib = lib
         return lib
 
@@ -292,7 +305,8 @@ def segment_compose(M, Nm, S0=None, want_segment_states=True, stream=None):
 KERNEL_FAMILIES = ("kda_chunk_list_kernel", "kda_chunk_prep_kernel", "kda_chunk_walk_kernel",
                    "kda_chunk_tc_kernel", "kda_chunk_kernel", "kda_compose_kernel", "kda_segment_table_kernel",
                    "kda_decode_verify_replay", "kda_chunk_bwd_kernel", "kda_bwd_walk_kernel",
-                   "kda_bwd_chunk_kernel", "kda_bwd_compose_kernel")
+                   "kda_bwd_chunk_kernel", "kda_bwd_compose_kernel", "kda_page_plan", "kda_cache4_append",
+                   "kda_cache4_read", "kda_cache4_attention", "kda_cache4_merge")
 
 
 def chunk_fwd_host(q, k, v, g, beta, cu_seqlens, initial_state=None, output_final_state=True, scale=1.0,
@@ -510,3 +524,163 @@ def decode_verify_replay(state, conv_tail, conv_w, cached_qkv, cached_g, cached_
                                           int(conv_act), _ptr(status), _stream(stream))
         _check(rc, "kda_decode_verify_replay")
         return out
+
+
+# ------------------------------------------------------------------ paged 4-bit key/value cache
+def cache4_alloc(num_pages, Hkv, page_size, d, device="cuda"):
+    """An empty cache: zeroed uint8 [num_pages, Hkv, page_size * 9 * d / 8]
+    (include/kda.h describes the bytes; d = 64 or 128, page_size a power of
+    two from 16 to 256)."""
+    return torch.zeros((num_pages, Hkv, page_size * 9 * d // 8), dtype=torch.uint8, device=device)
+
+
+def _check_cache4(cache, page_size, d):
+    """(num_pages, Hkv) of a cache tensor that fits page_size and d."""
+    if cache.dtype != torch.uint8 or cache.dim() != 3:
+        raise KDAError("cache must be uint8 [num_pages, Hkv, page_size * 9 * d / 8]")
+    if cache.shape[2] != page_size * 9 * d // 8:
+        raise KDAError(f"cache must have shape [num_pages, Hkv, {page_size * 9 * d // 8}] at page_size {page_size} and "
+                       f"d {d}, got {tuple(cache.shape)}")
+    return cache.shape[0], cache.shape[1]
+
+
+def _rows(t, name):
+    """(pointer, stride in elements) of token rows [T, H, d]: a row is
+    contiguous, rows may be further apart (views of a fused projection)."""
+    if not t.is_cuda:
+        raise KDAError("KDA calls take CUDA tensors")
+    T, H, d = t.shape
+    s = t.stride()
+    if s[2] != 1 or (s[1] != d and H > 1):
+        raise KDAError(f"{name}'s heads and channels must be contiguous")
+    return t.data_ptr(), s[0] if T > 1 else H * d
+
+
+def _check_scales(k_scale, v_scale, Hkv):
+    _expect(k_scale, "k_scale", torch.float32, (Hkv,))
+    _expect(v_scale, "v_scale", torch.float32, (Hkv,))
+
+
+def page_plan(context_len, new_len, page_count, block_table, free_pages, free_count, page_size, tokens, status=None,
+              stream=None):
+    """Block tables, slot map and positions of a step, from device int32
+    lengths [R].  Pages that a request lacks come from the end of free_pages
+    (free_count [1] of them are free) into its row of block_table [R,
+    max_pages], in place.  Returns int32 (cu_seqlens [R + 1], seq_len [R],
+    slot_map [tokens], positions [tokens], page_count [R], free_count [1]);
+    the last two replace the arguments of those names in the next step.
+    `tokens` is at least the sum of new_len; rows past it get -1."""
+    i32 = torch.int32
+    if context_len.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise KDAError("context_len [R], block_table [R, max_pages] and free_pages [F] expected")
+    R, B = block_table.shape
+    _expect(context_len, "context_len", i32, (R,))
+    _expect(new_len, "new_len", i32, (R,))
+    _expect(page_count, "page_count", i32, (R,))
+    _expect(block_table, "block_table", i32, (R, B))
+    _expect(free_pages, "free_pages", i32, free_pages.shape)
+    _expect(free_count, "free_count", i32, (1,))
+    T = int(tokens)
+    if T < 0:
+        raise KDAError("tokens must not be negative")
+    with _on(stream):
+        lib = load_library()
+        # one allocation, each part on its own 16-byte boundary
+        up = lambda n: (n + 3) & ~3
+        sizes = (R + 1, R, T, T, R, 1)
+        buf = torch.empty(sum(up(n) for n in sizes), dtype=i32, device=block_table.device)
+        out, at = [], 0
+        for n in sizes:
+            out.append(buf[at:at + n])
+            at += up(n)
+        rc = lib.kda_page_plan(_ptr(context_len), _ptr(new_len), _ptr(page_count), _ptr(block_table), _ptr(free_pages),
+                               _ptr(free_count), R, B, free_pages.shape[0], int(page_size), T,
+                               *[t.data_ptr() for t in out], _ptr(status), _stream(stream))
+        _check(rc, "kda_page_plan")
+        return tuple(out)
+
+
+def cache4_append(k, v, slot_map, cache, page_size, k_scale=None, v_scale=None, status=None, stream=None):
+    """Quantise key and value rows [T, Hkv, d] (bf16 or f32) into the cache at
+    slot_map int32 [T] (negative: skipped), in place; returns the cache.  The
+    rows of k and v may lie further apart than Hkv * d (views of a fused
+    projection)."""
+    if k.dim() != 3:
+        raise KDAError("k and v must be [T, Hkv, d]")
+    T, H, d = k.shape
+    P, Hkv = _check_cache4(cache, page_size, d)
+    dt = _in_dtype(k)
+    _expect(k, "k", k.dtype, (T, Hkv, d))
+    _expect(v, "v", k.dtype, (T, Hkv, d))
+    _expect(slot_map, "slot_map", torch.int32, (T,))
+    _check_scales(k_scale, v_scale, Hkv)
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    rc = load_library().kda_cache4_append(kp, vp, _ptr(slot_map), _ptr(cache), T, Hkv, d, P, int(page_size), ks, vs,
+                                          _ptr(k_scale), _ptr(v_scale), dt, _ptr(status), _stream(stream))
+    _check(rc, "kda_cache4_append")
+    return cache
+
+
+def cache4_read(cache, slots, page_size, d, dtype=torch.bfloat16, k_scale=None, v_scale=None, status=None, stream=None):
+    """The keys and values [n, Hkv, d] that slots int32 [n] stand for (zero
+    for a negative slot)."""
+    P, Hkv = _check_cache4(cache, page_size, d)
+    n = slots.shape[0] if slots.dim() == 1 else -1
+    _expect(slots, "slots", torch.int32, (n,))
+    _check_scales(k_scale, v_scale, Hkv)
+    with _on(stream):
+        k, v = torch.empty((2, n, Hkv, d), dtype=dtype, device=cache.device).unbind(0)
+        rc = load_library().kda_cache4_read(_ptr(cache), _ptr(slots), n, Hkv, d, P, int(page_size), _ptr(k_scale),
+                                            _ptr(v_scale), _in_dtype(k), k.data_ptr(), v.data_ptr(), _ptr(status),
+                                            _stream(stream))
+        _check(rc, "kda_cache4_read")
+        return k, v
+
+
+def cache4_attention_workspace_size(R, T, Hq, Hkv, d, dtype=torch.bfloat16) -> int:
+    dt = DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16
+    return int(load_library().kda_cache4_attention_workspace_size(R, T, Hq, Hkv, d, dt))
+
+
+def cache4_attention(q, cache, block_table, seq_len, cu_seqlens, page_size, scale=None, max_new=0, window=0,
+                     k_scale=None, v_scale=None, out=None, return_lse=False, lse=None, workspace=None, status=None,
+                     stream=None):
+    """Attention of packed queries q [T, Hq, d] over the 4-bit cache: request
+    r's queries are rows [cu_seqlens[r], cu_seqlens[r + 1]), the last of its
+    seq_len[r] positions; each sees the positions up to its own (the last
+    `window` of them when that is not 0).  scale defaults to d ** -0.5.
+    max_new is an upper bound of the requests' query counts (0: T).  q's rows
+    may lie further apart than Hq * d.  Returns o [T, Hq, d] in q's dtype, and
+    lse f32 [T, Hq] with return_lse."""
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise KDAError("q must be [T, Hq, d] and block_table [R, max_pages]")
+    T, Hq, d = q.shape
+    R, B = block_table.shape
+    P, Hkv = _check_cache4(cache, page_size, d)
+    if Hkv < 1 or Hq % Hkv:
+        raise KDAError(f"the {Hq} query heads must be a multiple of the cache's {Hkv}")
+    dt = _in_dtype(q)
+    _expect(block_table, "block_table", torch.int32, (R, B))
+    _expect(seq_len, "seq_len", torch.int32, (R,))
+    _expect(cu_seqlens, "cu_seqlens", torch.int32, (R + 1,))
+    _expect(out, "out", q.dtype, (T, Hq, d))
+    _expect(lse, "lse", torch.float32, (T, Hq))
+    _check_scales(k_scale, v_scale, Hkv)
+    qp, qs = _rows(q, "q")
+    with _on(stream):
+        lib = load_library()
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        need = lib.kda_cache4_attention_workspace_size(R, T, Hq, Hkv, d, dt)
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        rc = lib.kda_cache4_attention(qp, _ptr(cache), _ptr(block_table), _ptr(seq_len), _ptr(cu_seqlens), R, T, Hq, Hkv,
+                                      d, P, int(page_size), B, int(max_new), int(window),
+                                      float(d ** -0.5 if scale is None else scale), qs, _ptr(k_scale), _ptr(v_scale),
+                                      _ptr(out), _ptr(lse), dt, _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+        _check(rc, "kda_cache4_attention")
+        return (out, lse) if return_lse else out

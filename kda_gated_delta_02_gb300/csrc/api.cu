@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/kda.h"
+#include "cache4.cuh"
 #include "kda_internal.h"
 
 namespace {
@@ -1191,6 +1192,115 @@ int kda_chunk_fwd_host(const void *q, const void *k, const void *v, const float 
     if (e == cudaSuccess) e = cudaEventRecord(ev_done, cs.out);
     if (e == cudaSuccess) e = cudaStreamWaitEvent(st, ev_done, 0);
     for (auto &x : ev) cudaEventDestroy(x);  // released once the work they mark completes
+    return cuda_status(e);
+}
+
+int kda_page_plan(const int32_t *context_len, const int32_t *new_len, const int32_t *page_count, int32_t *block_table,
+                  const int32_t *free_pages, const int32_t *free_count, int R, int max_pages, int num_free, int page_size,
+                  int T, int32_t *cu_seqlens, int32_t *seq_len, int32_t *slot_map, int32_t *positions,
+                  int32_t *page_count_out, int32_t *free_count_out, uint32_t *status, void *stream) {
+    if (R < 1 || T < 0 || max_pages < 1 || num_free < 0) return KDA_ERR_INVALID_ARG;
+    const int shift = kda::cache4::page_shift(page_size);
+    if (shift < 0 || ((long long)max_pages << shift) > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (!context_len || !new_len || !page_count || !block_table || !free_count || !cu_seqlens || !seq_len ||
+        !page_count_out || !free_count_out || (num_free > 0 && !free_pages) || (T > 0 && (!slot_map || !positions)))
+        return KDA_ERR_INVALID_ARG;
+    if (page_count_out == page_count || free_count_out == free_count) return KDA_ERR_INVALID_ARG;
+    kda::PagePlanArgs a{context_len, new_len, page_count, free_pages, free_count, block_table, R, max_pages, num_free,
+                        shift, T, cu_seqlens, seq_len, slot_map, positions, page_count_out, free_count_out, status};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed_launch(KDA_KERNEL_PAGE_PLAN, st, [&] { return kda::launch_page_plan(a, sm_count(), st); }));
+}
+
+// shape checks shared by the 4-bit cache calls; *shift gets log2(page_size)
+static int cache4_shape(int Hkv, int d, int num_pages, int page_size, int dtype, int *shift) {
+    if (Hkv < 1 || num_pages < 1 || (dtype != KDA_DTYPE_BF16 && dtype != KDA_DTYPE_F32)) return KDA_ERR_INVALID_ARG;
+    *shift = kda::cache4::page_shift(page_size);
+    if (!dim_ok(d) || *shift < 0 || ((long long)num_pages << *shift) > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED_SHAPE;
+    return KDA_OK;
+}
+
+// rows of `width` elements, `stride` apart, each on a 16-byte boundary
+static int row_stride(long long stride, long long width, int dtype) {
+    if (stride < width) return KDA_ERR_INVALID_ARG;
+    return stride % (dtype == KDA_DTYPE_BF16 ? 8 : 4) ? KDA_ERR_ALIGNMENT : KDA_OK;
+}
+
+int kda_cache4_append(const void *k, const void *v, const int32_t *slot_map, void *cache, int T, int Hkv, int d,
+                      int num_pages, int page_size, long long k_stride, long long v_stride, const float *k_scale,
+                      const float *v_scale, int in_dtype, uint32_t *status, void *stream) {
+    int shift = 0;
+    if (T < 0) return KDA_ERR_INVALID_ARG;
+    if (int rc = cache4_shape(Hkv, d, num_pages, page_size, in_dtype, &shift)) return rc;
+    if (!cache || (T > 0 && (!k || !v || !slot_map))) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return KDA_ERR_ALIGNMENT;
+    if (int rc = row_stride(k_stride, (long long)Hkv * d, in_dtype)) return rc;
+    if (int rc = row_stride(v_stride, (long long)Hkv * d, in_dtype)) return rc;
+    if (T == 0) return KDA_OK;
+    kda::Cache4RowsArgs a{k, v, k_stride, v_stride, nullptr, nullptr, slot_map, static_cast<uint8_t *>(cache), k_scale,
+                          v_scale, T, Hkv, num_pages << shift, shift, status};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed_launch(KDA_KERNEL_CACHE4_APPEND, st, [&] {
+        return kda::launch_cache4_append(a, d, in_dtype == KDA_DTYPE_BF16, st);
+    }));
+}
+
+int kda_cache4_read(const void *cache, const int32_t *slots, int n, int Hkv, int d, int num_pages, int page_size,
+                    const float *k_scale, const float *v_scale, int out_dtype, void *k, void *v, uint32_t *status,
+                    void *stream) {
+    int shift = 0;
+    if (n < 0) return KDA_ERR_INVALID_ARG;
+    if (int rc = cache4_shape(Hkv, d, num_pages, page_size, out_dtype, &shift)) return rc;
+    if (!cache || (n > 0 && (!k || !v || !slots))) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return KDA_ERR_ALIGNMENT;
+    if (n == 0) return KDA_OK;
+    kda::Cache4RowsArgs a{nullptr, nullptr, 0, 0, k, v, slots,
+                          const_cast<uint8_t *>(static_cast<const uint8_t *>(cache)), k_scale, v_scale, n, Hkv,
+                          num_pages << shift, shift, status};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed_launch(KDA_KERNEL_CACHE4_READ, st, [&] {
+        return kda::launch_cache4_read(a, d, out_dtype == KDA_DTYPE_BF16, st);
+    }));
+}
+
+size_t kda_cache4_attention_workspace_size(int R, int T, int Hq, int Hkv, int d, int in_dtype) {
+    if (R < 1 || T < 0 || Hq < 1 || Hkv < 1 || !dim_ok(d) || (in_dtype != KDA_DTYPE_BF16 && in_dtype != KDA_DTYPE_F32))
+        return 0;
+    return align256(kda::cache4_attn_workspace(sm_count(), d));
+}
+
+int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_table, const int32_t *seq_len,
+                         const int32_t *cu_seqlens, int R, int T, int Hq, int Hkv, int d, int num_pages, int page_size,
+                         int max_pages, int max_new, int window, float scale, long long q_stride, const float *k_scale,
+                         const float *v_scale, void *o, float *lse, int in_dtype, void *workspace,
+                         size_t workspace_bytes, uint32_t *status, void *stream) {
+    int shift = 0;
+    if (R < 1 || T < 0 || max_pages < 1 || max_new < 0 || window < 0) return KDA_ERR_INVALID_ARG;
+    if (int rc = cache4_shape(Hkv, d, num_pages, page_size, in_dtype, &shift)) return rc;
+    if (Hq < 1 || Hq % Hkv || ((long long)max_pages << shift) > 0x7fffffffLL ||
+        (long long)T * (Hq / Hkv) > 0x7fffffffLL)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (!cache || !block_table || !seq_len || !cu_seqlens || (T > 0 && (!q || !o))) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(workspace)) return KDA_ERR_ALIGNMENT;
+    if (int rc = row_stride(q_stride, (long long)Hq * d, in_dtype)) return rc;
+    if (!workspace || workspace_bytes < kda_cache4_attention_workspace_size(R, T, Hq, Hkv, d, in_dtype))
+        return KDA_ERR_WORKSPACE;
+    if (T == 0) return KDA_OK;
+    if (window >= (max_pages << shift)) window = 0;  // wider than any request
+    const int sms = sm_count();
+    char *ws = static_cast<char *>(workspace);
+    kda::Cache4AttnArgs a{q, q_stride, static_cast<const uint8_t *>(cache), block_table, seq_len, cu_seqlens, k_scale,
+                          v_scale, o, lse, R, T, Hq, Hkv, max_pages, num_pages, shift, window, scale, status,
+                          reinterpret_cast<int4 *>(ws),
+                          reinterpret_cast<float *>(ws + (size_t)kda::cache4_attn_workers(sms) * sizeof(int4))};
+    const bool bf16 = in_dtype == KDA_DTYPE_BF16;
+    const long long rows = (long long)(max_new > 0 && max_new < T ? max_new : T) * (Hq / Hkv);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st,
+                                 [&] { return kda::launch_cache4_attn(a, d, bf16, rows, sms, st); });
+    if (e == cudaSuccess)
+        e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st,
+                         [&] { return kda::launch_cache4_merge(a, d, bf16, rows, sms, st); });
     return cuda_status(e);
 }
 

@@ -1,0 +1,680 @@
+// cache4_attn.cu -- attention of packed, ragged queries over the 4-bit pages.
+//
+//   s_ij = scale q_i . k_j,   p_ij = e^{s_ij - max_j s_ij} over the visible j,
+//   o_i = sum_j p_ij v_j / sum_j p_ij,   lse_i = log sum_j e^{s_ij}
+//
+// Query i of a request with n new tokens and L cached ones (the new among
+// them) sits at position L - n + i and sees positions j <= its own (and
+// j > its own - window).  The query heads of a group share a key head, so a
+// row is a (token, head of the group) pair and rows of a request and key head
+// are cut into row tiles.
+//
+// Memory bounds the few-row case (9 d / 8 bytes per key and head against
+// 4 d flops per row).  Every warp is a worker of its own: it takes an equal,
+// contiguous share of all (request, key head, row tile, key tile) units in
+// that order, keeps its own ring of key tiles filled by bulk copies and meets
+// no barrier.  A key tile goes from shared memory to registers once, the
+// codes become f16 pairs (exact) in the lanes that hold them as operand
+// fragments, and the products run with keys on M and rows on N, so eight rows
+// cost as much as one and no operand is padded.  The weights turn from the
+// accumulator to an operand by an 8 x 8 transpose per register.  Running
+// maximum, sum and the accumulator are fp32; the weights are rounded to f16
+// (11 bits, scaled by 2^kLift so that small ones keep their bits), with a
+// second f16 part for 32-bit queries, and so are the queries (scaled by a
+// power of two per row), so that only that rounding separates the result from
+// fp32.  A worker whose share cuts a row tile's keys leaves (max, sum, sum of
+// weighted values), and cache4_merge_kernel joins the shares in key order.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cache4.cuh"
+#include "kda_internal.h"
+#include "kda_umma.cuh"
+
+namespace kda {
+namespace {
+
+using namespace cache4;
+
+constexpr int kTile = 32;    // keys per tile: two blocks
+constexpr int kWarps = 16;   // workers per CTA
+constexpr int kStages = 3;   // tiles in flight per worker
+constexpr float kLift = 8.f; // weights are 2^(s - max + kLift)
+constexpr uint32_t kWaitLimit = 1u << 24;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// transpose of an 8 x 8 matrix of 16-bit elements held one pair per lane
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    unsigned short r;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(r) : "r"(a));
+    return r;
+}
+
+// A request as the schedule sees it.
+struct Req {
+    int q0, n, len;      // first query row, new tokens, keys
+    int rows, row_tiles;
+    int units;           // key tiles of every row tile (the widest one's)
+    bool ok;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Req request(const Cache4AttnArgs &a, int r, int G) {
+    Req q;
+    const int c0 = a.cu_seqlens[r], c1 = a.cu_seqlens[r + 1], len = a.seq_len[r];
+    q.ok = c0 >= 0 && c1 >= c0 && c1 <= a.T && len >= 0 && len <= ((long long)a.max_pages << a.page_shift);
+    q.q0 = c0;
+    q.n = q.ok ? c1 - c0 : 0;
+    q.len = q.ok ? len : 0;
+    q.rows = q.n * G;
+    q.row_tiles = (q.rows + ROWS - 1) / ROWS;
+    int t = (q.len + kTile - 1) / kTile;
+    if (a.window > 0) {
+        // a row tile spans up to (ROWS - 1) / G + 2 tokens
+        const long long span = ((long long)a.window + (ROWS - 1) / G + 1) / kTile + 2;
+        if (span < t) t = (int)span;
+    }
+    q.units = t > 0 ? t : 1;  // a row tile that sees nothing is still written
+    return q;
+}
+
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+cache4_attn_kernel(const Cache4AttnArgs a) {
+    constexpr int ROWS = 8 * NT, KS = D / 16, BB = block_bytes(D), STAGE = 2 * BB;
+    constexpr int PARTS = F32 ? 2 : 1;  // f16 parts of a query or weight
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ long long s_prefix[kWarps * 32 + 1];
+    __shared__ long long s_sum[kWarps];
+    __shared__ __align__(8) uint64_t s_bar[kWarps * kStages];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+    const int G = a.Hq / a.Hkv;
+
+    // ---- units of all requests: prefix sums by slices of requests
+    const int per = (a.R + kWarps * 32 - 1) / (kWarps * 32);
+    const int r_lo = min(a.R, tid * per), r_hi = min(a.R, r_lo + per);
+    long long mine = 0;
+    bool bad = false;
+    for (int r = r_lo; r < r_hi; ++r) {
+        const Req q = request<ROWS>(a, r, G);
+        bad |= !q.ok;
+        mine += (long long)q.row_tiles * a.Hkv * q.units;
+    }
+    if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, KDA_STATUS_BAD_SEQLENS);
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    if (lane < kStages) umma::mbar_init(smem_addr(&s_bar[warp * kStages + lane]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    s_prefix[tid + 1] = before + x;
+    if (tid == 0) s_prefix[0] = 0;
+    __syncthreads();
+
+    const long long total = s_prefix[kWarps * 32];
+    const int workers = gridDim.x * kWarps;
+    // neighbouring workers sit on different SMs, so that few units spread over all of them
+    const int me = warp * gridDim.x + blockIdx.x;
+    const long long share = (total + workers - 1) / workers;
+    long long u = share * me;
+    const long long u_end = min(total, u + share);
+    int4 job = make_int4(-1, 0, 0, 0);
+    if (u >= u_end) {
+        if (lane == 0) a.jobs[me] = job;
+        return;
+    }
+    int r, slice = 0;
+    {
+        int hi = kWarps * 32;
+        while (hi - slice > 1) {
+            const int mid = (slice + hi) >> 1;
+            if (s_prefix[mid] <= u) slice = mid;
+            else hi = mid;
+        }
+        r = slice * per;
+    }
+    long long at = s_prefix[slice];  // first unit of request r
+    const uint32_t ring = smem_addr(smem) + warp * (kStages * STAGE);
+    const uint32_t bars = smem_addr(&s_bar[warp * kStages]);
+    uint32_t stage = 0, phase = 0;   // next stage to read and its parity
+    bool dead = false;
+
+    while (u < u_end && !dead) {
+        const Req q = request<ROWS>(a, r, G);
+        const long long req_units = (long long)q.row_tiles * a.Hkv * q.units;
+        if (u >= at + req_units) {
+            at += req_units;
+            ++r;
+            continue;
+        }
+        const int item = (int)((u - at) / q.units), unit0 = (int)((u - at) % q.units);
+        const int unit1 = (int)min((long long)q.units, unit0 + (u_end - u));
+        u += unit1 - unit0;
+        const int h = item / q.row_tiles, rt = item % q.row_tiles;
+        // positions of the tile's first and last token, and the keys they see
+        const int row0 = rt * ROWS, row1 = min(q.rows, row0 + ROWS) - 1;
+        const int pos0 = q.len - q.n + row0 / G, pos1 = q.len - q.n + row1 / G;
+        const int key_lo = a.window > 0 ? max(0, pos0 - a.window + 1) : 0;
+        const int tile_lo = key_lo / kTile;
+        const int tiles = max(0, (pos1 + kTile) / kTile - tile_lo);  // pos1 >= -n; empty rows give 0
+        const int first = tile_lo + min(unit0, tiles), last = tile_lo + min(unit1, tiles);
+
+        // ---- query fragments: row g of every 8, channels (D / 4) t4 ...
+        uint32_t qf[NT][PARTS][KS][2];
+        float fac[NT][2];
+        const float base = a.scale * kLog2e * (a.k_scale ? a.k_scale[h] : 1.f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int rr = row0 + nt * 8 + g;
+            float v[D / 4];
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) v[i] = 0.f;
+            if (rr < q.rows) {
+                const size_t e = (size_t)(q.q0 + rr / G) * a.q_stride + (size_t)(h * G + rr % G) * D + t4 * (D / 4);
+                if constexpr (F32) {
+                    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + e);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const float4 w = __ldg(p + i);
+                        v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
+                    }
+                } else {
+                    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + e);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const uint4 w = __ldg(p + i);
+                        const uint32_t s[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            v[8 * i + 2 * j] = __uint_as_float(s[j] << 16);
+                            v[8 * i + 2 * j + 1] = __uint_as_float(s[j] & 0xffff0000u);
+                        }
+                    }
+                }
+            }
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(v[i]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // a power of two that brings the row's largest element to [2^8, 2^9)
+            const int ex = min(max((int)(__float_as_uint(top) >> 23), 9), 253);
+            const float up = __uint_as_float((uint32_t)(262 - ex) << 23);
+            const float down = __uint_as_float((uint32_t)(ex - 8) << 23);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float lo = v[4 * ks + 2 * b] * up, hi = v[4 * ks + 2 * b + 1] * up;
+                    qf[nt][0][ks][b] = pack_f16(lo, hi);
+                    if constexpr (F32) {
+                        const float2 w = unpack_f16(qf[nt][0][ks][b]);
+                        qf[nt][PARTS - 1][ks][b] = pack_f16(lo - w.x, hi - w.y);
+                    }
+                }
+            // this lane's accumulator columns are rows 2 t4 and 2 t4 + 1
+#pragma unroll
+            for (int j = 0; j < 2; ++j) fac[nt][j] = base * __shfl_sync(0xffffffffu, down, (2 * t4 + j) * 4);
+        }
+        // last visible key of the columns' rows (-1: padding or nothing to see)
+        int see[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int rr = row0 + nt * 8 + 2 * t4 + j;
+                see[nt][j] = rr < q.rows ? q.len - q.n + rr / G : -1;
+            }
+
+        float m[NT][2], l[NT][2], acc[NT][KS][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
+        }
+
+        // ---- ring: pages of 32 tables entries at a time in the lanes
+        const int32_t *table = a.block_table + (size_t)r * a.max_pages;
+        const int used_pages = (q.len + (1 << a.page_shift) - 1) >> a.page_shift;
+        int page_base = -64, page_here = 0;
+        auto page_of = [&](int p) {
+            if (p >= page_base + 32 || p < page_base) {
+                page_base = p;
+                const int i = p + lane;
+                page_here = 0;
+                if (i < used_pages) {
+                    page_here = table[i];
+                    if (page_here < 0 || page_here >= a.num_pages) {
+                        page_here = 0;  // refused below through the status; the read stays in the pool
+                        if (a.status) atomicOr(a.status, KDA_STATUS_BAD_PAGE);
+                    }
+                }
+                __syncwarp();
+            }
+            return __shfl_sync(0xffffffffu, page_here, p - page_base);
+        };
+        auto block_addr = [&](int page, int blk) {
+            return a.cache + (((size_t)page * a.Hkv + h) << (a.page_shift - 4)) * BB + (size_t)blk * BB;
+        };
+        auto fill = [&](int tile, uint32_t st) {
+            const int key = tile * kTile;
+            const uint32_t dst = ring + st * STAGE, bar = bars + st * 8;
+            const bool two = key + 16 < q.len;  // a second block with keys in it
+            const int pg = page_of(key >> a.page_shift);
+            const int blk = (key & ((1 << a.page_shift) - 1)) >> 4;
+            if (a.page_shift > 4) {
+                if (lane == 0) {
+                    const uint32_t bytes = two ? 2 * BB : BB;
+                    umma::mbar_expect_tx(bar, bytes);
+                    umma::bulk_load(dst, block_addr(pg, blk), bytes, bar);
+                }
+            } else {
+                const int pg2 = two ? page_of((key >> 4) + 1) : 0;
+                if (lane == 0) {
+                    umma::mbar_expect_tx(bar, two ? 2 * BB : BB);
+                    umma::bulk_load(dst, block_addr(pg, 0), BB, bar);
+                    if (two) umma::bulk_load(dst + BB, block_addr(pg2, 0), BB, bar);
+                }
+            }
+        };
+        uint32_t put = stage;
+        int filled = first;
+#pragma unroll 1
+        for (; filled < last && filled < first + kStages; ++filled) {
+            fill(filled, put);
+            put = put + 1 == kStages ? 0 : put + 1;
+        }
+
+#pragma unroll 1
+        for (int tile = first; tile < last; ++tile) {
+            if (!umma::mbar_wait(bars + stage * 8, phase, kWaitLimit)) {
+                dead = true;
+                if (lane == 0 && a.status) atomicOr(a.status, KDA_STATUS_TIMEOUT);
+                // the copies in flight end before the warp leaves
+                for (int i = tile; i < filled; ++i) {
+                    umma::mbar_wait(bars + stage * 8, phase, kWaitLimit);
+                    if (++stage == kStages) stage = 0, phase ^= 1;
+                }
+                break;
+            }
+            const uint32_t buf = ring + stage * STAGE;
+            const int key0 = tile * kTile;
+            const bool two = key0 + 16 < q.len;
+            // ---- S^T = K Q^T, 16 keys x 8 rows per product; row g of a
+            // product is key 4 (g / 2) + (g & 1), row g + 8 two further, so
+            // that lane t4 ends up with the weights of keys 4 t4 .. 4 t4 + 3
+            float s[2][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[mt][nt][j] = 0.f;
+                if (mt == 1 && !two) continue;
+                const uint32_t blk = buf + mt * BB;
+                const int tok = 4 * (g >> 1) + (g & 1);
+                uint32_t kw[2][D / 32], sc[2][KS / 4];
+                if constexpr (D == 128) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 w = lds128(blk + (tok + 2 * i) * 64 + t4 * 16);
+                        kw[i][0] = w.x, kw[i][1] = w.y, kw[i][2] = w.z, kw[i][3] = w.w;
+                        const uint32_t f = scales_to_f16(lds16(blk + off_ks(D) + (tok + 2 * i) * 8 + t4 * 2));
+                        sc[i][0] = __byte_perm(f, f, 0x1010);
+                        sc[i][1] = __byte_perm(f, f, 0x3232);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint2 w = lds64(blk + (tok + 2 * i) * 32 + t4 * 8);
+                        kw[i][0] = w.x, kw[i][1] = w.y;
+                        const uint32_t f = scales_to_f16(lds8(blk + off_ks(D) + (tok + 2 * i) * 4 + t4));
+                        sc[i][0] = __byte_perm(f, f, 0x1010);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    uint32_t x0[4], x1[4];
+                    codes_to_f16(kw[0][w], x0);
+                    codes_to_f16(kw[1][w], x1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x0[j] = mul_f16x2(x0[j], sc[0][w >> 1]);
+                        x1[j] = mul_f16x2(x1[j], sc[1][w >> 1]);
+                    }
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int p = PARTS - 1; p >= 0; --p)
+                                mma_f16(s[mt][nt], x0[2 * hh], x1[2 * hh], x0[2 * hh + 1], x1[2 * hh + 1],
+                                        qf[nt][p][2 * w + hh][0], qf[nt][p][2 * w + hh][1]);
+                }
+            }
+            // ---- masks: only tiles that some row of the tile does not see whole
+            const bool edge = key0 + kTile > pos0 + 1 || (a.window > 0 && key0 <= pos1 - a.window);
+            if (edge) {
+                const int tok = key0 + 4 * (g >> 1) + (g & 1);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = tok + mt * 16 + (j >> 1) * 2, sees = see[nt][j & 1];
+                            if (key > sees || (a.window > 0 && key <= sees - a.window)) s[mt][nt][j] = -INFINITY;
+                        }
+            }
+            // ---- running maximum and weights
+            uint32_t pf[NT][PARTS][2][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float top[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    top[j] = fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]), fmaxf(s[1][nt][j], s[1][nt][j + 2]));
+                    top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 4));
+                    top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
+                    top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+                    top[j] = fmaxf(m[nt][j], top[j] * fac[nt][j]);
+                }
+                if (__any_sync(0xffffffffu, top[0] > m[nt][0] || top[1] > m[nt][1])) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float shrink = top[j] == -INFINITY ? 1.f : exp2_fast(m[nt][j] - top[j]);
+                        l[nt][j] *= shrink;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            acc[nt][i][j] *= shrink;
+                            acc[nt][i][j + 2] *= shrink;
+                        }
+                        m[nt][j] = top[j];
+                    }
+                }
+                float off[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) off[j] = kLift - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    float w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        w[j] = exp2_fast(fmaf(s[mt][nt][j], fac[nt][j & 1], off[j & 1]));
+                        l[nt][j & 1] += w[j];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t hi = pack_f16(w[2 * i], w[2 * i + 1]);
+                        pf[nt][0][mt][i] = transpose8(hi);
+                        if constexpr (F32) {
+                            const float2 b = unpack_f16(hi);
+                            pf[nt][PARTS - 1][mt][i] = transpose8(pack_f16(w[2 * i] - b.x, w[2 * i + 1] - b.y));
+                        }
+                    }
+                }
+            }
+            // ---- O^T += V^T P^T: lane (g, t4) holds channels (D / 8) g ... of keys 4 t4 .. 4 t4 + 3
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                if (mt == 1 && !two) continue;
+                const uint32_t blk = buf + mt * BB;
+                constexpr int W = D / 64;  // code words per key and lane
+                uint32_t vw[4][W], sv;
+                if constexpr (D == 128) {
+                    const uint4 w0 = lds128(blk + off_vc(D) + g * 128 + t4 * 32);
+                    const uint4 w1 = lds128(blk + off_vc(D) + g * 128 + t4 * 32 + 16);
+                    vw[0][0] = w0.x, vw[0][W - 1] = w0.y, vw[1][0] = w0.z, vw[1][W - 1] = w0.w;
+                    vw[2][0] = w1.x, vw[2][W - 1] = w1.y, vw[3][0] = w1.z, vw[3][W - 1] = w1.w;
+                    sv = lds32(blk + off_vs(D) + g * 16 + t4 * 4);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        vw[i][0] = lds32(blk + off_vc(D) + (g >> 1) * 128 + (t4 * 4 + i) * 8 + (g & 1) * 4);
+                    sv = lds32(blk + off_vs(D) + (g >> 1) * 16 + t4 * 4);
+                }
+                if (key0 + kTile > q.len) {
+                    // keys past the end hold anything, NaN scales too: a zero weight does not undo that
+                    const int over = key0 + mt * 16 + t4 * 4 + 4 - q.len;
+                    if (over > 0) sv = over >= 4 ? 0u : sv & (0xffffffffu >> (8 * over));
+                }
+                const uint32_t s01 = scales_to_f16(sv & 0xffffu), s23 = scales_to_f16(sv >> 16);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd channels, keys (0, 1) and (2, 3)
+                    constexpr uint32_t M = 0x0f0f0f0fu;
+                    codes_to_f16((vw[0][w] & M) | ((vw[1][w] << 4) & ~M), e01);
+                    codes_to_f16(((vw[0][w] >> 4) & M) | (vw[1][w] & ~M), o01);
+                    codes_to_f16((vw[2][w] & M) | ((vw[3][w] << 4) & ~M), e23);
+                    codes_to_f16(((vw[2][w] >> 4) & M) | (vw[3][w] & ~M), o23);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = mul_f16x2(e01[i], s01), a1 = mul_f16x2(o01[i], s01);
+                        const uint32_t a2 = mul_f16x2(e23[i], s23), a3 = mul_f16x2(o23[i], s23);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int p = PARTS - 1; p >= 0; --p)
+                                mma_f16(acc[nt][w * 4 + i], a0, a1, a2, a3, pf[nt][p][mt][0], pf[nt][p][mt][1]);
+                    }
+                }
+            }
+            __syncwarp();  // every lane has read the stage
+            if (filled < last) {
+                fill(filled, stage);
+                ++filled;
+            }
+            if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+        if (dead) break;
+
+        // ---- the rows' sums over all lanes of a column
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+                l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+                l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+            }
+        const bool whole = unit0 == 0 && unit1 == q.units;
+        if (whole) {
+            const float vs = a.v_scale ? a.v_scale[h] : 1.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int rr = row0 + nt * 8 + 2 * t4 + j;
+                    if (rr >= q.rows) continue;
+                    const size_t head = (size_t)(q.q0 + rr / G) * a.Hq + h * G + rr % G;
+                    const bool none = m[nt][j] == -INFINITY && l[nt][j] == 0.f;
+                    const float inv = none ? 0.f : vs / l[nt][j];
+                    float y[D / 8];
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        y[2 * i] = none ? 0.f : acc[nt][i][j] * inv;
+                        y[2 * i + 1] = none ? 0.f : acc[nt][i][j + 2] * inv;
+                    }
+                    if constexpr (F32) {
+                        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.o) + head * D + g * (D / 8));
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i)
+                            p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    } else {
+                        uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + head * D + g * (D / 8));
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(y[8 * i + 2 * c], y[8 * i + 2 * c + 1]);
+                                w[c] = *reinterpret_cast<const uint32_t *>(&b);
+                            }
+                            p[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    if (a.lse && g == 0)
+                        a.lse[head] = none ? -INFINITY : (m[nt][j] + log2f(l[nt][j]) - kLift) * kLn2;
+                }
+        } else {
+            // part 1 starts a row tile that goes on, part 0 continues one
+            const int part = unit0 == 0 ? 1 : 0;
+            float *w = a.parts + ((size_t)me * 2 + part) * (ROWS * (D + 2));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = nt * 8 + 2 * t4 + j;
+                    if (g == 0) {
+                        w[row] = m[nt][j];
+                        w[ROWS + row] = l[nt][j];
+                    }
+                    float4 *p = reinterpret_cast<float4 *>(w + 2 * ROWS + row * D + g * (D / 8));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)
+                        p[i] = make_float4(acc[nt][2 * i][j], acc[nt][2 * i][j + 2], acc[nt][2 * i + 1][j],
+                                           acc[nt][2 * i + 1][j + 2]);
+                }
+            if (part == 1) {
+                const long long item_end = u - unit1 + q.units;  // one past the row tile's last unit
+                job = make_int4(r, h, rt, (int)((item_end - 1) / share));
+            }
+        }
+    }
+    if (lane == 0) a.jobs[me] = dead ? make_int4(-1, 0, 0, 0) : job;
+}
+
+// The shares of a row tile's keys, in key order: o = sum_p 2^{m_p - M} O_p / sum_p 2^{m_p - M} l_p.
+// One CTA per worker (it has work where a row tile starts in that worker's
+// share and ends in a later one), four channels of a row per thread.
+template <int D, int ROWS, bool F32>
+__global__ void __launch_bounds__(ROWS * D / 4)
+cache4_merge_kernel(const Cache4AttnArgs a) {
+    const int w0 = blockIdx.x, row = threadIdx.x / (D / 4), c = threadIdx.x % (D / 4) * 4;
+    const int4 job = a.jobs[w0];
+    if (job.x < 0) return;
+    const int G = a.Hq / a.Hkv;
+    const Req q = request<ROWS>(a, job.x, G);
+    const int rr = job.z * ROWS + row;
+    if (rr >= q.rows) return;
+    const size_t step = (size_t)ROWS * (D + 2);
+    const float *part = a.parts + ((size_t)w0 * 2 + 1) * step;  // the first share; later ones are their workers' part 0
+    float m = part[row];
+    for (int w = w0 + 1; w <= job.w; ++w) m = fmaxf(m, a.parts[(size_t)w * 2 * step + row]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int w = w0; w <= job.w; ++w) {
+        const float *p = a.parts + ((size_t)w * 2 + (w == w0)) * step;
+        const float f = exp2_fast(p[row] - ref);
+        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * ROWS + row * D + c);
+        l = fmaf(f, p[ROWS + row], l);
+        y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
+    }
+    const size_t head = (size_t)(q.q0 + rr / G) * a.Hq + job.y * G + rr % G;
+    const bool none = m == -INFINITY && l == 0.f;
+    const float inv = none ? 0.f : (a.v_scale ? a.v_scale[job.y] : 1.f) / l;
+    y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    if constexpr (F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + head * D + c) = y;
+    } else {
+        const __nv_bfloat162 b0 = __floats2bfloat162_rn(y.x, y.y), b1 = __floats2bfloat162_rn(y.z, y.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + head * D + c) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
+    }
+    if (a.lse && c == 0) a.lse[head] = none ? -INFINITY : (m + log2f(l) - kLift) * kLn2;
+}
+
+constexpr int smem_bytes(int d) { return kWarps * kStages * 2 * block_bytes(d); }
+
+template <int D, int NT, bool F32>
+cudaError_t launch_attn(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
+    auto kernel = cache4_attn_kernel<D, NT, F32>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(D));
+    if (e != cudaSuccess) return e;
+    kernel<<<sms, kWarps * 32, smem_bytes(D), st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch_merge(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
+    cache4_merge_kernel<D, 8 * NT, F32><<<cache4_attn_workers(sms), 2 * NT * D, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int cache4_attn_workers(int sms) { return sms * kWarps; }
+size_t cache4_attn_workspace(int sms, int d) {
+    return (size_t)cache4_attn_workers(sms) * (sizeof(int4) + 2 * 16 * (size_t)(d + 2) * sizeof(float));
+}
+
+// 16 rows a tile when a request may have more than 8 (the keys' conversion to
+// f16 is then shared by two products); 32-bit queries have two f16 parts and
+// keep 8.
+#define KDA_ATTN(F)                                                                       \
+    const bool wide = bf16 && rows > 8;                                                   \
+    if (d == 128)                                                                         \
+        return !bf16 ? F<128, 1, true>(a, sms, st) : wide ? F<128, 2, false>(a, sms, st) : F<128, 1, false>(a, sms, st); \
+    return !bf16 ? F<64, 1, true>(a, sms, st) : wide ? F<64, 2, false>(a, sms, st) : F<64, 1, false>(a, sms, st);
+
+cudaError_t launch_cache4_attn(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st) {
+    KDA_ATTN(launch_attn)
+}
+cudaError_t launch_cache4_merge(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st) {
+    KDA_ATTN(launch_merge)
+}
+
+}  // namespace kda

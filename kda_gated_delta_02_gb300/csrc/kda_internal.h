@@ -187,4 +187,52 @@ cudaError_t launch_verify_tc(const VerifyArgs &a, cudaStream_t st);
 // Single-token decode (Wd = 0) on the CUDA cores (dk = dv = 64 or 128).
 cudaError_t launch_decode_token(const VerifyArgs &a, cudaStream_t st);
 
+// Block tables, slot map and positions of a step (page_plan.cu).
+struct PagePlanArgs {
+    const int32_t *context_len, *new_len, *page_count, *free_pages, *free_count;
+    int32_t *block_table;  // [R][max_pages]
+    int R, max_pages, num_free, page_shift, T;
+    int32_t *cu_seqlens, *seq_len, *slot_map, *positions, *page_count_out, *free_count_out;
+    uint32_t *status;
+};
+cudaError_t launch_page_plan(const PagePlanArgs &a, int sms, cudaStream_t st);
+
+// Rows into the 4-bit pages and back (cache4_rows.cu).
+struct Cache4RowsArgs {
+    const void *k, *v;            // append: rows of Hkv x d channels, k_stride / v_stride elements apart
+    long long k_stride, v_stride;
+    void *k_out, *v_out;          // read: [T][Hkv][d]
+    const int32_t *slots;
+    uint8_t *cache;
+    const float *k_scale, *v_scale;  // [Hkv] or null
+    int T, Hkv, num_slots, page_shift;
+    uint32_t *status;
+};
+cudaError_t launch_cache4_append(const Cache4RowsArgs &a, int d, bool bf16, cudaStream_t st);
+cudaError_t launch_cache4_read(const Cache4RowsArgs &a, int d, bool bf16, cudaStream_t st);
+
+// Attention over the 4-bit pages (cache4_attn.cu).
+struct Cache4AttnArgs {
+    const void *q;                // rows of Hq x d channels, q_stride elements apart
+    long long q_stride;
+    const uint8_t *cache;
+    const int32_t *block_table, *seq_len, *cu_seqlens;
+    const float *k_scale, *v_scale;  // [Hkv] or null
+    void *o;                      // [T][Hq][d]
+    float *lse;                   // [T][Hq] or null
+    int R, T, Hq, Hkv, max_pages, num_pages, page_shift, window;
+    float scale;
+    uint32_t *status;
+    // work split over the key axis (cache4_attn_workspace): one job record per
+    // worker, and two partial results (rows x (d + 2) f32) per worker
+    int4 *jobs;
+    float *parts;
+};
+// warps that share the work of a call, and the workspace they need
+int cache4_attn_workers(int sms);
+size_t cache4_attn_workspace(int sms, int d);
+// rows: an upper bound of the query rows (tokens x heads of a group) of one request
+cudaError_t launch_cache4_attn(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st);
+cudaError_t launch_cache4_merge(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st);
+
 }  // namespace kda

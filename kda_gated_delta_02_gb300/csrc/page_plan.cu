@@ -1,0 +1,158 @@
+// page_plan.cu -- block tables, slot map and positions of a serving step from
+// the requests' lengths.
+//
+//   rows_r = max(new_r, 0),  cu = exclusive prefix sum of rows
+//   need_r = max(0, ceil((context_r + rows_r) / page) - held_r), 0 for a refused request
+//   base_r = sum_{s < r} need_s;  request r is served when base_r + need_r <= free_count or need_r = 0
+//   table[r][held_r + i] = free[free_count - 1 - (base_r + i)],  i < need_r
+//   slot[cu_r + i] = table[r][(context_r + i) / page] * page + (context_r + i) % page
+//
+// Integer work on a few kilobytes to a few megabytes: what bounds it is the
+// chain of dependent steps (load lengths, two prefix sums, a table entry,
+// store), not bandwidth.  So every CTA repeats the prefix sums over all
+// requests, 1,024 at a time, instead of waiting for another CTA or launch to
+// do them, and then writes its share of the tokens and of the fresh pages,
+// finding a token's request by bisection in the prefix held in shared memory.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cache4.cuh"
+#include "kda_internal.h"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 1024;
+
+// inclusive prefix sum over the CTA's threads; every thread gets the total too
+__device__ __forceinline__ long long scan(long long x, long long *warp_sums, long long &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // the previous scan's sums have been read
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    long long w = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    return x + (warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
+}
+
+// last index in [0, n) whose start is at most x (starts ascending, starts[0] <= x)
+__device__ __forceinline__ int find(const int *starts, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (starts[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kThreads)
+page_plan_kernel(PagePlanArgs a) {
+    __shared__ long long warp_sums[32];
+    __shared__ int s_row[kThreads + 1], s_base[kThreads + 1], s_ctx[kThreads], s_held[kThreads];
+    __shared__ int s_used;
+    const int tid = threadIdx.x, nthr = blockDim.x;
+    const int page_mask = (1 << a.page_shift) - 1;
+    const int width = gridDim.x * nthr, me = blockIdx.x * nthr + tid;
+    const bool writer = blockIdx.x == 0;
+    const int count = a.free_count[0];
+    const bool count_ok = count >= 0 && count <= a.num_free;
+    const int avail = count_ok ? count : 0;
+    uint32_t bad = count_ok ? 0u : KDA_STATUS_NO_PAGES;
+    if (tid == 0) s_used = 0;
+    long long rows_before = 0, pages_before = 0;
+    for (int r0 = 0; r0 < a.R; r0 += nthr) {
+        const int n = min(nthr, a.R - r0), r = r0 + tid;
+        int ctx = 0, rows = 0, held = 0;
+        bool ok = false;
+        if (tid < n) {
+            ctx = a.context_len[r];
+            held = a.page_count[r];
+            const int neu = a.new_len[r];
+            rows = max(neu, 0);
+            ok = neu >= 0 && ctx >= 0 && held >= 0 && held <= a.max_pages &&
+                 (long long)ctx + rows <= (long long)a.max_pages << a.page_shift;
+        }
+        long long total_rows, total_need;
+        const long long row_end = rows_before + scan(rows, warp_sums, total_rows);
+        ok = ok && row_end <= a.T;
+        if (tid < n && !ok) bad |= KDA_STATUS_BAD_SEQLENS;
+        const int need = ok ? max(0, (int)(((long long)ctx + rows + page_mask) >> a.page_shift) - held) : 0;
+        const long long base_end = pages_before + scan(need, warp_sums, total_need);
+        if (need && base_end > avail) {
+            ok = false;
+            bad |= KDA_STATUS_NO_PAGES;
+        }
+        s_row[tid] = (int)min(row_end - rows, (long long)a.T);
+        s_base[tid] = (int)min(base_end - need, (long long)avail);
+        s_ctx[tid] = ok ? ctx : -1;
+        s_held[tid] = held;
+        // bases ascend, so the served requests hold a prefix of the hand-out order
+        if (ok && need) atomicMax(&s_used, (int)base_end);
+        if (writer && tid < n) {
+            a.cu_seqlens[r] = (int)min(row_end - rows, 0x7fffffffLL);
+            if (r == a.R - 1) a.cu_seqlens[a.R] = (int)min(row_end, 0x7fffffffLL);
+            a.seq_len[r] = ok ? ctx + rows : ctx;
+            a.page_count_out[r] = ok ? held + need : held;
+        }
+        __syncthreads();
+        // fresh pages of this group of requests, f counting in hand-out order
+        const int f1 = (int)min(pages_before + total_need, (long long)avail);
+        for (long long f = min(pages_before, (long long)avail) + me; f < f1; f += width) {
+            const int i = find(s_base, n, (int)f);
+            if (s_ctx[i] >= 0)
+                a.block_table[(size_t)(r0 + i) * a.max_pages + s_held[i] + ((int)f - s_base[i])] =
+                    a.free_pages[avail - 1 - (int)f];
+        }
+        const int t1 = (int)min(rows_before + total_rows, (long long)a.T);
+        for (long long t = min(rows_before, (long long)a.T) + me; t < t1; t += width) {
+            const int i = find(s_row, n, (int)t);
+            int pos = -1, slot = -1;
+            if (s_ctx[i] >= 0) {
+                pos = s_ctx[i] + ((int)t - s_row[i]);
+                const int pi = pos >> a.page_shift;
+                const long long pg = pi < s_held[i] ? a.block_table[(size_t)(r0 + i) * a.max_pages + pi]
+                                                    : a.free_pages[avail - 1 - (s_base[i] + pi - s_held[i])];
+                const long long at = (pg << a.page_shift) + (pos & page_mask);
+                if (pg >= 0 && at <= 0x7fffffffLL) slot = (int)at;
+                else bad |= KDA_STATUS_BAD_PAGE;
+            }
+            a.slot_map[t] = slot;
+            a.positions[t] = pos;
+        }
+        __syncthreads();  // the group's shared arrays have been read
+        rows_before += total_rows;
+        pages_before += total_need;
+    }
+    for (long long t = min(rows_before, (long long)a.T) + me; t < a.T; t += width) {
+        a.slot_map[t] = -1;
+        a.positions[t] = -1;
+    }
+    if (writer && tid == 0) a.free_count_out[0] = count_ok ? count - s_used : count;
+    if (bad && a.status) atomicOr(a.status, bad);
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PagePlanArgs &a, int sms, cudaStream_t st) {
+    // few requests: 256 threads, whose barriers cost less; the grid covers the
+    // tokens once up to two CTAs per SM
+    const int threads = a.R <= 256 ? 256 : kThreads;
+    long grid = ((long)a.T + threads - 1) / threads;
+    const long most = 2L * sms * kThreads / threads;
+    grid = grid < 1 ? 1 : grid > most ? most : grid;
+    page_plan_kernel<<<(unsigned)grid, threads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace kda
