@@ -39,7 +39,7 @@ using namespace cache4;
 constexpr int kTile = 32;    // keys per tile: two blocks
 constexpr int kWarps = 16;   // workers per CTA
 constexpr int kStages = 3;   // tiles in flight per worker
-constexpr float kLift = 8.f; // weights are 2^(s - max + kLift)
+constexpr float kLift = 15.f; // weights are 2^(s - max + kLift), at most 2^15 of f16's 65504
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -209,7 +209,10 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
         // ---- query fragments: row g of every 8, channels (D / 4) t4 ...
         uint32_t qf[NT][PARTS][KS][2];
         float fac[NT][2];
+        // the sign (and a zero) of the scale goes into the queries: the factor stays positive, so that it may
+        // follow the maximum and a masked score stays -inf
         const float base = a.scale * kLog2e * (a.k_scale ? a.k_scale[h] : 1.f);
+        const float sign = base < 0.f ? -1.f : base == 0.f ? 0.f : 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int rr = row0 + nt * 8 + g;
@@ -246,7 +249,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // a power of two that brings the row's largest element to [2^8, 2^9)
             const int ex = min(max((int)(__float_as_uint(top) >> 23), 9), 253);
-            const float up = __uint_as_float((uint32_t)(262 - ex) << 23);
+            const float up = sign * __uint_as_float((uint32_t)(262 - ex) << 23);
             const float down = __uint_as_float((uint32_t)(ex - 8) << 23);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
@@ -261,7 +264,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                 }
             // this lane's accumulator columns are rows 2 t4 and 2 t4 + 1
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fac[nt][j] = base * __shfl_sync(0xffffffffu, down, (2 * t4 + j) * 4);
+            for (int j = 0; j < 2; ++j) fac[nt][j] = fmaxf(fabsf(base) * __shfl_sync(0xffffffffu, down, (2 * t4 + j) * 4), 1e-37f);
         }
         // last visible key of the columns' rows (-1: padding or nothing to see)
         int see[NT][2];

@@ -1,0 +1,375 @@
+"""The paged 4-bit cache on the GPU: rows in and out against the format's
+definition, and attention against a 64-bit reference on the cache's own bytes,
+with per-element bounds from the kernel's roundings (cache4_ref)."""
+import numpy as np
+import pytest
+import torch
+
+import cache4_ref as ref
+import kda_gated_delta_02_gb300 as kda
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def status_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def dev(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x), dtype=dtype, device="cuda")
+
+
+def to64(t):
+    return t.detach().cpu().double().numpy()
+
+
+# ------------------------------------------------------------------ rows
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,d,page", [(1, 1, 64, 16), (77, 3, 128, 16), (300, 2, 64, 64), (130, 5, 128, 256)])
+def test_rows_come_back_as_the_format_says(T, H, d, page, dtype):
+    g = torch.Generator().manual_seed(T * 7 + d)
+    P = -(-T // page) + 2
+    k = (torch.randn(T, H, d, generator=g) * torch.exp(torch.randn(T, H, 1, generator=g) * 3)).to(DT[dtype])
+    v = torch.randn(T, H, d, generator=g).to(DT[dtype])
+    k[0] = 0
+    v[T // 2, :, :16] = 1e-6  # scale underflows to zero
+    k[T - 1, 0, 3] = 1e5      # saturates
+    slots = torch.randperm(P * page, generator=g)[:T].to(torch.int32)
+    slots[T // 3] = -1
+    before = torch.randint(0, 255, (P, H, page * 9 * d // 8), generator=g, dtype=torch.uint8)
+    cache, st = before.cuda(), status_word()
+    kda.cache4_append(k.cuda(), v.cuda(), slots.cuda(), cache, page, status=st)
+    ko, vo = kda.cache4_read(cache, slots.cuda(), page, d, dtype=DT[dtype], status=st)
+    assert st.item() == 0
+    keep = (slots >= 0).numpy()
+    for got, x in ((ko, k), (vo, v)):
+        want = ref.held(x.float().numpy()) * keep[:, None, None]
+        # six significant bits and exponents from -10 to 11: exact in every type
+        assert np.array_equal(to64(got), want)
+    # the bytes, through the reference's own reading of the layout
+    dk, dv = ref.decode(cache.cpu().numpy(), d)
+    at = slots.numpy()[keep]
+    assert np.array_equal(dk[at // page, :, at % page], ref.held(k.float().numpy())[keep])
+    assert np.array_equal(dv[at // page, :, at % page], ref.held(v.float().numpy())[keep])
+    # no byte of another slot changed
+    other = np.setdiff1d(np.arange(P * page), at)
+    raw = lambda c: c.cpu().numpy().reshape(P, H, page // 16, ref.block_bytes(d))
+    a, b = raw(before), raw(cache)
+    ka, kb = 16 * d // 2, 16 * d // 16
+    for p, o in zip(other // page, other % page):
+        blk, tok = o // 16, o % 16
+        pieces = [slice(tok * d // 2, (tok + 1) * d // 2), slice(ka + tok * d // 16, ka + (tok + 1) * d // 16)]
+        pieces += [slice(ka + kb + grp * 128 + tok * 8, ka + kb + grp * 128 + tok * 8 + 8) for grp in range(d // 16)]
+        pieces += [slice(2 * ka + kb + grp * 16 + tok, 2 * ka + kb + grp * 16 + tok + 1) for grp in range(d // 16)]
+        for s in pieces:
+            assert np.array_equal(a[p, :, blk, s], b[p, :, blk, s])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rounding_at_every_tie(dtype):
+    """Rows whose largest element sets the scale to every mantissa of e4m3 (ties of max / 6 among them) and whose other
+    elements sit on and next to every midpoint of the codes."""
+    mids = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
+    rows = []
+    for e in (-9, -7, -6, 0, 3, 8):
+        for m in np.arange(16, 32) / 16:  # halves of a scale step: ties of the scale itself
+            s = m * 2.0 ** e
+            near = [x * s * f for x in mids for f in (1.0, 1 + 2.0 ** -7)]
+            rows.append([6 * s] + [x * (-1) ** i for i, x in enumerate(near)] + [0.0])
+    x = torch.tensor(rows, dtype=torch.float64).to(DT[dtype])
+    x = x.reshape(-1, 1, 16).repeat(1, 1, 4)  # d = 64
+    T, page = x.shape[0], 16
+    cache = kda.cache4_alloc(-(-T // page), 1, page, 64)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    kda.cache4_append(x.cuda(), (-x).cuda(), slots, cache, page)
+    k, v = kda.cache4_read(cache, slots, page, 64, dtype=DT[dtype])
+    want = ref.held(x.float().numpy())
+    assert np.array_equal(to64(k), want) and np.array_equal(to64(v), -want)
+
+
+def test_rows_of_a_fused_projection_and_head_scales():
+    T, Hq, H, d, page = 53, 4, 2, 128, 32
+    g = torch.Generator().manual_seed(3)
+    qkv = torch.randn(T, (Hq + 2 * H) * d, generator=g).bfloat16().cuda()
+    k = qkv[:, Hq * d:(Hq + H) * d].view(T, H, d)
+    v = qkv[:, (Hq + H) * d:].view(T, H, d)
+    ks, vs = torch.tensor([0.25, 8.0], device="cuda"), torch.tensor([2.0 ** -6, 1.0], device="cuda")
+    cache = kda.cache4_alloc(2, H, page, d)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    kda.cache4_append(k, v, slots, cache, page, k_scale=ks, v_scale=vs)
+    ko, vo = kda.cache4_read(cache, slots, page, d, dtype=torch.float32, k_scale=ks, v_scale=vs)
+    assert np.array_equal(to64(ko), ref.held(k.float().cpu().numpy(), ks.cpu().numpy()))
+    assert np.array_equal(to64(vo), ref.held(v.float().cpu().numpy(), vs.cpu().numpy()))
+
+
+@pytest.mark.parametrize("where,what", [("k", float("nan")), ("v", float("inf")), ("k", float("-inf")), ("v", float("nan"))])
+def test_rows_that_are_not_finite_are_marked(where, what):
+    T, H, d, page = 20, 2, 64, 16
+    x = {n: torch.randn(T, H, d).bfloat16() for n in "kv"}
+    x[where][7, 1, 50] = what
+    cache, st = kda.cache4_alloc(2, H, page, d), status_word()
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    kda.cache4_append(x["k"].cuda(), x["v"].cuda(), slots, cache, page, status=st)
+    assert st.item() == kda.STATUS_NOT_FINITE
+    k, v = kda.cache4_read(cache, slots, page, d, dtype=torch.float32)
+    marked = torch.zeros(T, H, dtype=torch.bool)
+    marked[7, 1] = True
+    for t in (k, v):
+        assert torch.equal(t.isnan().all(-1).cpu(), marked) and torch.equal(t.isnan().any(-1).cpu(), marked)
+
+
+def test_slots_past_the_cache_are_refused():
+    T, H, d, page = 6, 1, 64, 16
+    x = torch.ones(T, H, d, device="cuda").bfloat16()
+    cache, st = kda.cache4_alloc(1, H, page, d), status_word()
+    slots = dev([0, 16, 15, -1, 2 ** 31 - 1, -5])
+    kda.cache4_append(x, x, slots, cache, page, status=st)
+    assert st.item() == kda.STATUS_BAD_PAGE
+    st.zero_()
+    k, _ = kda.cache4_read(cache, slots, page, d, status=st)
+    assert st.item() == kda.STATUS_BAD_PAGE
+    one = ref.held(np.ones((1, 1, 64)))[0, 0, 0]  # 1 / 6 is not an e4m3 number
+    assert k[:, 0, 0].tolist() == [one, 0, one, 0, 0, 0]
+
+
+# ------------------------------------------------------------------ attention
+class Case:
+    """A cache with requests of the given lengths on shuffled pages; what no request holds has random bytes, NaN scales
+    among them."""
+
+    def __init__(self, lengths, new, Hq, H, d, page, dtype="bf16", seed=0, gain=1.0, ks=None, vs=None, extra_pages=3):
+        g = torch.Generator().manual_seed(seed)
+        self.page, self.d, self.lengths, self.new = page, d, lengths, new
+        pages = [-(-n // page) for n in lengths]
+        P, B = sum(pages) + extra_pages, max(max(pages), 1) + 1
+        perm = torch.randperm(P, generator=g).numpy()
+        self.table = np.full((len(lengths), B), -1, dtype=np.int64)
+        at, slots = 0, []
+        for r, n in enumerate(pages):
+            self.table[r, :n] = perm[at:at + n]
+            at += n
+            p = np.arange(lengths[r])
+            slots.append(self.table[r, p // page] * page + p % page if lengths[r] else np.zeros(0, dtype=np.int64))
+        slots = np.concatenate(slots)
+        total = len(slots)
+        self.k = torch.randn(total, H, d, generator=g) * torch.exp(0.5 * torch.randn(1, H, d, generator=g))
+        self.v = torch.randn(total, H, d, generator=g)
+        self.ks = None if ks is None else dev(ks, torch.float32)
+        self.vs = None if vs is None else dev(vs, torch.float32)
+        raw = torch.randint(0, 256, (P, H, page * 9 * d // 8), generator=g, dtype=torch.uint8)
+        raw[:, :, ::5] = 0x7F
+        self.cache = raw.cuda()
+        self.slots = dev(slots)
+        if total:
+            kda.cache4_append(self.k.bfloat16().cuda(), self.v.bfloat16().cuda(), self.slots, self.cache, page,
+                              k_scale=self.ks, v_scale=self.vs)
+        self.cu = np.concatenate(([0], np.cumsum(new)))
+        self.q = (gain * torch.randn(int(self.cu[-1]), Hq, d, generator=g)).to(DT[dtype])
+        self.args = (self.cache, dev(self.table), dev(lengths), dev(self.cu), page)
+
+    def run(self, q=None, **kw):
+        return kda.cache4_attention((self.q if q is None else q).cuda(), *self.args, k_scale=self.ks, v_scale=self.vs, **kw)
+
+    def want(self, scale=None, window=0):
+        k, v = ref.decode(self.cache.cpu().numpy(), self.d)
+        k = k * (1 if self.ks is None else self.ks.cpu().double().numpy()[:, None, None])
+        v = v * (1 if self.vs is None else self.vs.cpu().double().numpy()[:, None, None])
+        return ref.attention(to64(self.q), k, v, self.table, self.lengths, self.cu, self.page,
+                             self.d ** -0.5 if scale is None else scale, window)
+
+    def check(self, scale=None, window=0, **kw):
+        st = status_word()
+        o, lse = self.run(scale=scale, window=window, return_lse=True, status=st, **kw)
+        assert st.item() == 0
+        want = self.want(scale, window)
+        bo, bl = ref.attention_bounds(*want, bf16=self.q.dtype == torch.bfloat16)
+        assert np.all(np.isfinite(to64(o)))
+        assert np.all(np.abs(to64(o) - want[0]) <= bo), float(np.max(np.abs(to64(o) - want[0]) / bo))
+        none = np.isneginf(want[1])
+        got = to64(lse)
+        assert np.array_equal(np.isneginf(got), none) and np.all(to64(o)[none] == 0)
+        assert np.all(np.abs(got[~none] - want[1][~none]) <= bl[~none])
+        return o, lse
+
+
+EDGE = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129, 255, 300]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,H,d,page", [(8, 1, 128, 64), (6, 2, 64, 16), (3, 3, 128, 16), (24, 2, 128, 32),
+                                         (16, 1, 64, 256), (40, 2, 64, 128), (34, 1, 128, 64)])
+def test_single_tokens_at_every_edge_length(Hq, H, d, page, dtype):
+    lengths = [n for n in EDGE if n > 0]
+    Case(lengths, [1] * len(lengths), Hq, H, d, page, dtype, seed=Hq + d).check(max_new=1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [0, 1, 7, 40])
+@pytest.mark.parametrize("Hq,H,d,page", [(8, 1, 128, 64), (4, 2, 64, 16), (12, 1, 128, 16)])
+def test_ragged_windows_of_queries(Hq, H, d, page, window, dtype):
+    """Several queries per request: some more than the cache holds (those see nothing), requests without queries and
+    without keys among them."""
+    lengths = [0, 5, 1, 40, 97, 0, 130, 64]
+    new = [0, 8, 3, 8, 1, 4, 7, 0]
+    Case(lengths, new, Hq, H, d, page, dtype, seed=window).check(window=window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("Hq,H,d,page,n,L", [(8, 2, 128, 64, 70, 200), (3, 1, 64, 16, 129, 129), (5, 1, 128, 32, 61, 333),
+                                             (1, 1, 64, 128, 200, 260)])
+def test_prompt_chunks(Hq, H, d, page, n, L, window, dtype):
+    Case([L, 33, L + 7], [n, 33, 2], Hq, H, d, page, dtype, seed=n).check(window=window, max_new=n)
+
+
+def test_one_long_request_is_joined_from_its_shares():
+    Case([20011], [1], 8, 1, 64, 64, seed=5).check(max_new=1)
+    Case([9001, 17], [8, 8], 8, 2, 64, 16, seed=6).check(max_new=8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scales_and_sharp_and_flat_maps(dtype):
+    c = Case([150, 33], [3, 1], 8, 2, 128, 32, dtype, seed=9, ks=[0.5, 4.0], vs=[2.0 ** -8, 1.0])
+    c.check()
+    c.check(scale=0.0)
+    c.check(scale=-0.3)
+    Case([150], [2], 4, 1, 128, 16, dtype, seed=10, gain=30.0).check()      # one key takes almost all
+    Case([150], [2], 4, 1, 128, 16, dtype, seed=11, gain=2.0 ** -40).check()  # queries far below one
+
+
+def test_an_upper_bound_that_is_too_low_still_gives_every_query():
+    Case([90, 12], [40, 2], 4, 1, 128, 64, seed=12).check(max_new=1)
+
+
+def test_queries_of_a_fused_projection_and_given_buffers():
+    c = Case([70, 9], [5, 2], 4, 2, 64, 16, seed=13)
+    o, lse = c.check()
+    wide = torch.randn(7, 4 * 64 + 96).bfloat16().cuda()
+    wide[:, 32:32 + 256] = c.q.cuda().view(7, 256)
+    view = wide[:, 32:32 + 256].view(7, 4, 64)
+    out, l2 = torch.full((9, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((9, 4), 7.0, device="cuda")
+    kda.cache4_attention(view, *c.args, out=out[1:8], lse=l2[1:8], return_lse=True)
+    assert torch.equal(out[1:8], o) and torch.equal(l2[1:8], lse)
+    assert (out[[0, 8]] == 7).all() and (l2[[0, 8]] == 7).all()
+
+
+def test_rows_past_the_last_request_are_not_touched():
+    c = Case([40, 9], [2, 1], 8, 1, 128, 16, seed=14)
+    q = torch.cat((c.q, torch.full((4, 8, 128), float("nan"), dtype=torch.bfloat16)))
+    out = torch.full((7, 8, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    c.run(q=q, out=out, max_new=2)
+    assert torch.equal(out[:3], c.run(max_new=2)) and (out[3:] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [3, 60])
+def test_a_marked_token_reaches_only_queries_that_see_it(n, dtype):
+    """A key or value that is not finite sits at a position that the last queries see and the first do not, next to
+    keys of the same tile that all see."""
+    L, H, page, d = 80, 2, 16, 128
+    c = Case([L], [n], 4, H, d, page, dtype, seed=15)
+    clean = c.run()
+    pos = L - 2
+    x = torch.randn(1, H, d)
+    x[0, 1, 5] = float("inf")
+    kda.cache4_append(c.k[pos:pos + 1].bfloat16().cuda(), x.bfloat16().cuda(), c.slots[pos:pos + 1], c.cache, page)
+    o, lse = c.run(return_lse=True)
+    sees = torch.zeros(n, 4, dtype=torch.bool)
+    sees[n - 2:, 2:] = True  # the head with the mark, positions L - 2 and L - 1
+    assert torch.equal(o.isnan().all(-1).cpu(), sees) and torch.equal(o.isnan().any(-1).cpu(), sees)
+    assert torch.equal(lse.isnan().cpu(), sees)
+    assert torch.equal(o[:n - 2], clean[:n - 2])
+
+
+def test_queries_that_are_not_finite_stay_alone():
+    c = Case([50, 20], [4, 1], 4, 1, 64, 16, seed=16)
+    clean = c.run()
+    q = c.q.clone()
+    q[1, 2, 3] = float("nan")
+    o = c.run(q=q)
+    assert o[1, 2].isnan().all()
+    o[1, 2] = clean[1, 2]
+    assert torch.equal(o, clean)
+
+
+@pytest.mark.parametrize("new", [1, 8, 50])
+def test_the_same_call_gives_the_same_bits(new):
+    c = Case([3000, 70, 500], [new] * 3, 16, 2, 128, 32, seed=17)
+    a = c.run(return_lse=True)
+    for _ in range(3):
+        b = c.run(return_lse=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_another_stream_and_a_graph():
+    c = Case([700, 33], [2, 1], 8, 2, 128, 64, seed=18)
+    want = c.run()
+    q, args = c.q.cuda(), c.args
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = kda.cache4_attention(q, *args, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    out = torch.empty_like(got)
+    with torch.cuda.stream(s):
+        kda.cache4_attention(q, *args, out=out)
+        graph = torch.cuda.CUDAGraph()
+        s.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            kda.cache4_attention(q, *args, out=out)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_pages_past_4_gib(new):
+    """Byte offsets of the pages need 64 bits."""
+    H, d, page = 4, 128, 64
+    P = (5 << 30) // (H * page * 9 * d // 8)
+    cache = kda.cache4_alloc(P, H, page, d)
+    L = 150
+    table = dev([[P - 1, 1, P - 2]])
+    pos = torch.arange(L, device="cuda")
+    slots = (table[0, pos // page] * page + pos % page).int()
+    k, v = torch.randn(2, L, H, d, device="cuda").bfloat16().unbind(0)
+    kda.cache4_append(k, v, slots, cache, page)
+    ko, _ = kda.cache4_read(cache, slots, page, d, dtype=torch.float32)
+    assert np.array_equal(to64(ko), ref.held(k.float().cpu().numpy()))
+    q = torch.randn(new, 8, d, device="cuda").bfloat16()
+    o = kda.cache4_attention(q, cache, table, dev([L]), dev([0, new]), page)
+    small = cache[[P - 1, 1, P - 2]].contiguous()
+    assert torch.equal(o, kda.cache4_attention(q, small, dev([[0, 1, 2]]), dev([L]), dev([0, new]), page))
+
+
+def near(a, b):
+    """Two results whose shares of the keys were cut differently: each within half a bf16 step (2^-8) and the weights'
+    rounding (2^-11 of the weighted |v|, here below four times the largest output) of the exact one."""
+    return bool(((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -8 * b.abs().max()).all())
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_bad_lengths_and_pages_are_refused(new):
+    c = Case([60, 60, 60], [new] * 3, 8, 1, 64, 16, seed=19)
+    want = c.run()
+    cache, table, lengths, cu, page = c.args
+    st, out = status_word(), torch.full_like(want, 5.0)
+    bad = lengths.clone()
+    bad[1] = table.shape[1] * page + 1
+    kda.cache4_attention(c.q.cuda(), cache, table, bad, cu, page, out=out, status=st)
+    assert st.item() == kda.STATUS_BAD_SEQLENS
+    assert near(out[:new], want[:new]) and near(out[2 * new:], want[2 * new:]) and (out[new:2 * new] == 5).all()
+    for cut in ([0, new, 3 * new + 1, 3 * new], [0, new, -1, 3 * new]):  # queries past the end, and before the start
+        st.zero_()
+        out.fill_(5.0)
+        kda.cache4_attention(c.q.cuda(), cache, table, lengths, dev(cut), page, out=out, status=st)
+        assert st.item() == kda.STATUS_BAD_SEQLENS and near(out[:new], want[:new])
+    for entry in (-1, cache.shape[0], 2 ** 31 - 1):
+        st.zero_()
+        t2 = table.clone()
+        t2[1, 1] = entry
+        o = kda.cache4_attention(c.q.cuda(), cache, t2, lengths, cu, page, status=st)
+        assert st.item() == kda.STATUS_BAD_PAGE
+        assert torch.equal(o[:new], want[:new]) and torch.equal(o[2 * new:], want[2 * new:])
