@@ -1266,7 +1266,9 @@ int kda_cache4_read(const void *cache, const int32_t *slots, int n, int Hkv, int
 size_t kda_cache4_attention_workspace_size(int R, int T, int Hq, int Hkv, int d, int in_dtype) {
     if (R < 1 || T < 0 || Hq < 1 || Hkv < 1 || !dim_ok(d) || (in_dtype != KDA_DTYPE_BF16 && in_dtype != KDA_DTYPE_F32))
         return 0;
-    return align256(kda::cache4_attn_workspace(sm_count(), d));
+    const int sms = sm_count();
+    const size_t a = kda::cache4_attn_workspace(sms, d), b = kda::cache4_attn_tc_workspace(sms, d);
+    return align256(a > b ? a : b);
 }
 
 int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_table, const int32_t *seq_len,
@@ -1296,11 +1298,15 @@ int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_
     const bool bf16 = in_dtype == KDA_DTYPE_BF16;
     const long long rows = (long long)(max_new > 0 && max_new < T ? max_new : T) * (Hq / Hkv);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st,
-                                 [&] { return kda::launch_cache4_attn(a, d, bf16, rows, sms, st); });
+    const bool tc = bf16 && rows > 16;
+    cudaError_t e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st, [&] {
+        return tc ? kda::launch_cache4_attn_tc(a, d, rows, sms, st) : kda::launch_cache4_attn(a, d, bf16, rows, sms, st);
+    });
     if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st,
-                         [&] { return kda::launch_cache4_merge(a, d, bf16, rows, sms, st); });
+        e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st, [&] {
+            return tc ? kda::launch_cache4_merge_tc(a, d, rows, sms, st)
+                      : kda::launch_cache4_merge(a, d, bf16, rows, sms, st);
+        });
     return cuda_status(e);
 }
 

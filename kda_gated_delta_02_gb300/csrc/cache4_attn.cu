@@ -28,6 +28,7 @@
 #include <stdint.h>
 
 #include "cache4.cuh"
+#include "cache4_sched.cuh"
 #include "kda_internal.h"
 #include "kda_umma.cuh"
 
@@ -40,8 +41,6 @@ constexpr int kTile = 32;    // keys per tile: two blocks
 constexpr int kWarps = 16;   // workers per CTA
 constexpr int kStages = 3;   // tiles in flight per worker
 constexpr float kLift = 15.f; // weights are 2^(s - max + kLift), at most 2^15 of f16's 65504
-constexpr uint32_t kWaitLimit = 1u << 24;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -59,152 +58,33 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return r;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 r;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 r;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t r;
-    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(r) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    unsigned short r;
-    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(r) : "r"(a));
-    return r;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t r;
-    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(r) : "r"(a));
-    return r;
-}
-
-// A request as the schedule sees it.
-struct Req {
-    int q0, n, len;      // first query row, new tokens, keys
-    int rows, row_tiles;
-    int units;           // key tiles of every row tile (the widest one's)
-    bool ok;
-};
-
-template <int ROWS>
-__device__ __forceinline__ Req request(const Cache4AttnArgs &a, int r, int G) {
-    Req q;
-    const int c0 = a.cu_seqlens[r], c1 = a.cu_seqlens[r + 1], len = a.seq_len[r];
-    q.ok = c0 >= 0 && c1 >= c0 && c1 <= a.T && len >= 0 && len <= ((long long)a.max_pages << a.page_shift);
-    q.q0 = c0;
-    q.n = q.ok ? c1 - c0 : 0;
-    q.len = q.ok ? len : 0;
-    q.rows = q.n * G;
-    q.row_tiles = (q.rows + ROWS - 1) / ROWS;
-    int t = (q.len + kTile - 1) / kTile;
-    if (a.window > 0) {
-        // a row tile spans up to (ROWS - 1) / G + 2 tokens
-        const long long span = ((long long)a.window + (ROWS - 1) / G + 1) / kTile + 2;
-        if (span < t) t = (int)span;
-    }
-    q.units = t > 0 ? t : 1;  // a row tile that sees nothing is still written
-    return q;
-}
-
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 cache4_attn_kernel(const Cache4AttnArgs a) {
     constexpr int ROWS = 8 * NT, KS = D / 16, BB = block_bytes(D), STAGE = 2 * BB;
     constexpr int PARTS = F32 ? 2 : 1;  // f16 parts of a query or weight
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ long long s_prefix[kWarps * 32 + 1];
-    __shared__ long long s_sum[kWarps];
+    __shared__ long long s_prefix[kWarps * 32 + 33];
     __shared__ __align__(8) uint64_t s_bar[kWarps * kStages];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int G = a.Hq / a.Hkv;
 
-    // ---- units of all requests: prefix sums by slices of requests
-    const int per = (a.R + kWarps * 32 - 1) / (kWarps * 32);
-    const int r_lo = min(a.R, tid * per), r_hi = min(a.R, r_lo + per);
-    long long mine = 0;
-    bool bad = false;
-    for (int r = r_lo; r < r_hi; ++r) {
-        const Req q = request<ROWS>(a, r, G);
-        bad |= !q.ok;
-        mine += (long long)q.row_tiles * a.Hkv * q.units;
-    }
-    if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, KDA_STATUS_BAD_SEQLENS);
-    long long x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) s_sum[warp] = x;
     if (lane < kStages) umma::mbar_init(smem_addr(&s_bar[warp * kStages + lane]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    s_prefix[tid + 1] = before + x;
-    if (tid == 0) s_prefix[0] = 0;
-    __syncthreads();
-
-    const long long total = s_prefix[kWarps * 32];
-    const int workers = gridDim.x * kWarps;
     // neighbouring workers sit on different SMs, so that few units spread over all of them
     const int me = warp * gridDim.x + blockIdx.x;
-    const long long share = (total + workers - 1) / workers;
-    long long u = share * me;
-    const long long u_end = min(total, u + share);
+    Walk<ROWS, kTile> walk(a);
+    walk.begin(a, s_prefix, me, gridDim.x * kWarps);
     int4 job = make_int4(-1, 0, 0, 0);
-    if (u >= u_end) {
-        if (lane == 0) a.jobs[me] = job;
-        return;
-    }
-    int r, slice = 0;
-    {
-        int hi = kWarps * 32;
-        while (hi - slice > 1) {
-            const int mid = (slice + hi) >> 1;
-            if (s_prefix[mid] <= u) slice = mid;
-            else hi = mid;
-        }
-        r = slice * per;
-    }
-    long long at = s_prefix[slice];  // first unit of request r
     const uint32_t ring = smem_addr(smem) + warp * (kStages * STAGE);
     const uint32_t bars = smem_addr(&s_bar[warp * kStages]);
     uint32_t stage = 0, phase = 0;   // next stage to read and its parity
     bool dead = false;
 
-    while (u < u_end && !dead) {
-        const Req q = request<ROWS>(a, r, G);
-        const long long req_units = (long long)q.row_tiles * a.Hkv * q.units;
-        if (u >= at + req_units) {
-            at += req_units;
-            ++r;
-            continue;
-        }
-        const int item = (int)((u - at) / q.units), unit0 = (int)((u - at) % q.units);
-        const int unit1 = (int)min((long long)q.units, unit0 + (u_end - u));
-        u += unit1 - unit0;
-        const int h = item / q.row_tiles, rt = item % q.row_tiles;
-        // positions of the tile's first and last token, and the keys they see
-        const int row0 = rt * ROWS, row1 = min(q.rows, row0 + ROWS) - 1;
-        const int pos0 = q.len - q.n + row0 / G, pos1 = q.len - q.n + row1 / G;
-        const int key_lo = a.window > 0 ? max(0, pos0 - a.window + 1) : 0;
-        const int tile_lo = key_lo / kTile;
-        const int tiles = max(0, (pos1 + kTile) / kTile - tile_lo);  // pos1 >= -n; empty rows give 0
-        const int first = tile_lo + min(unit0, tiles), last = tile_lo + min(unit1, tiles);
+    Item it;
+    while (!dead && walk.next(a, it)) {
+        const Req &q = it.q;
+        const int h = it.h, row0 = it.row0, pos0 = it.pos0, pos1 = it.pos1, first = it.first, last = it.last;
 
         // ---- query fragments: row g of every 8, channels (D / 4) t4 ...
         uint32_t qf[NT][PARTS][KS][2];
@@ -288,7 +168,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
         }
 
         // ---- ring: pages of 32 tables entries at a time in the lanes
-        const int32_t *table = a.block_table + (size_t)r * a.max_pages;
+        const int32_t *table = a.block_table + (size_t)it.r * a.max_pages;
         const int used_pages = (q.len + (1 << a.page_shift) - 1) >> a.page_shift;
         int page_base = -64, page_here = 0;
         auto page_of = [&](int p) {
@@ -531,8 +411,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
                 l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
             }
-        const bool whole = unit0 == 0 && unit1 == q.units;
-        if (whole) {
+        if (it.whole()) {
             const float vs = a.v_scale ? a.v_scale[h] : 1.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -572,7 +451,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                 }
         } else {
             // part 1 starts a row tile that goes on, part 0 continues one
-            const int part = unit0 == 0 ? 1 : 0;
+            const int part = it.starts() ? 1 : 0;
             float *w = a.parts + ((size_t)me * 2 + part) * (ROWS * (D + 2));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -589,55 +468,10 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                         p[i] = make_float4(acc[nt][2 * i][j], acc[nt][2 * i][j + 2], acc[nt][2 * i + 1][j],
                                            acc[nt][2 * i + 1][j + 2]);
                 }
-            if (part == 1) {
-                const long long item_end = u - unit1 + q.units;  // one past the row tile's last unit
-                job = make_int4(r, h, rt, (int)((item_end - 1) / share));
-            }
+            if (part == 1) job = make_int4(it.r, h, it.rt, it.last_worker);
         }
     }
     if (lane == 0) a.jobs[me] = dead ? make_int4(-1, 0, 0, 0) : job;
-}
-
-// The shares of a row tile's keys, in key order: o = sum_p 2^{m_p - M} O_p / sum_p 2^{m_p - M} l_p.
-// One CTA per worker (it has work where a row tile starts in that worker's
-// share and ends in a later one), four channels of a row per thread.
-template <int D, int ROWS, bool F32>
-__global__ void __launch_bounds__(ROWS * D / 4)
-cache4_merge_kernel(const Cache4AttnArgs a) {
-    const int w0 = blockIdx.x, row = threadIdx.x / (D / 4), c = threadIdx.x % (D / 4) * 4;
-    const int4 job = a.jobs[w0];
-    if (job.x < 0) return;
-    const int G = a.Hq / a.Hkv;
-    const Req q = request<ROWS>(a, job.x, G);
-    const int rr = job.z * ROWS + row;
-    if (rr >= q.rows) return;
-    const size_t step = (size_t)ROWS * (D + 2);
-    const float *part = a.parts + ((size_t)w0 * 2 + 1) * step;  // the first share; later ones are their workers' part 0
-    float m = part[row];
-    for (int w = w0 + 1; w <= job.w; ++w) m = fmaxf(m, a.parts[(size_t)w * 2 * step + row]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int w = w0; w <= job.w; ++w) {
-        const float *p = a.parts + ((size_t)w * 2 + (w == w0)) * step;
-        const float f = exp2_fast(p[row] - ref);
-        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * ROWS + row * D + c);
-        l = fmaf(f, p[ROWS + row], l);
-        y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
-    }
-    const size_t head = (size_t)(q.q0 + rr / G) * a.Hq + job.y * G + rr % G;
-    const bool none = m == -INFINITY && l == 0.f;
-    const float inv = none ? 0.f : (a.v_scale ? a.v_scale[job.y] : 1.f) / l;
-    y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-    if constexpr (F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + head * D + c) = y;
-    } else {
-        const __nv_bfloat162 b0 = __floats2bfloat162_rn(y.x, y.y), b1 = __floats2bfloat162_rn(y.z, y.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + head * D + c) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
-    }
-    if (a.lse && c == 0) a.lse[head] = none ? -INFINITY : (m + log2f(l) - kLift) * kLn2;
 }
 
 constexpr int smem_bytes(int d) { return kWarps * kStages * 2 * block_bytes(d); }
@@ -653,8 +487,7 @@ cudaError_t launch_attn(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
 
 template <int D, int NT, bool F32>
 cudaError_t launch_merge(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
-    cache4_merge_kernel<D, 8 * NT, F32><<<cache4_attn_workers(sms), 2 * NT * D, 0, st>>>(a);
-    return cudaGetLastError();
+    return merge_shares<D, 8 * NT, kTile, F32>(a, cache4_attn_workers(sms), kLift, st);
 }
 
 }  // namespace

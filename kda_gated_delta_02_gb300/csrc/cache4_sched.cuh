@@ -1,0 +1,230 @@
+// cache4_sched.cuh -- what the attention kernels over the 4-bit pages share:
+// the division of the work among workers, the join of shares, small helpers.
+//
+// An item is a row tile (ROWS rows: pairs of a token and a head of the group)
+// of one request and key head; a unit is one key tile (TILE keys) of an item.
+// Units are numbered request by request, head by head, row tile by row tile,
+// and every worker takes an equal, contiguous range of them, so one long
+// request or many short ones load the SMs alike.  Row tiles of a request
+// count as many units as its widest one; they are taken from both ends in
+// turn (0, last, 1, last - 1, ...), so that under a causal mask neighbours
+// share the load.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cache4.cuh"
+#include "kda_internal.h"
+
+namespace kda {
+namespace cache4 {
+
+constexpr uint32_t kWaitLimit = 1u << 24;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    unsigned short r;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(r) : "r"(a));
+    return r;
+}
+
+// A request as the schedule sees it.
+struct Req {
+    int q0, n, len;  // first query row, new tokens, keys
+    int rows, row_tiles;
+    int units;       // key tiles of every row tile (the widest one's)
+    bool ok;
+};
+
+template <int ROWS, int TILE>
+__device__ __forceinline__ Req request(const Cache4AttnArgs &a, int r, int G) {
+    Req q;
+    const int c0 = a.cu_seqlens[r], c1 = a.cu_seqlens[r + 1], len = a.seq_len[r];
+    q.ok = c0 >= 0 && c1 >= c0 && c1 <= a.T && len >= 0 && len <= ((long long)a.max_pages << a.page_shift);
+    q.q0 = c0;
+    q.n = q.ok ? c1 - c0 : 0;
+    q.len = q.ok ? len : 0;
+    q.rows = q.n * G;
+    q.row_tiles = (q.rows + ROWS - 1) / ROWS;
+    int t = (q.len + TILE - 1) / TILE;
+    if (a.window > 0) {
+        // a row tile spans up to (ROWS - 1) / G + 2 tokens
+        const long long span = ((long long)a.window + (ROWS - 1) / G + 1) / TILE + 2;
+        if (span < t) t = (int)span;
+    }
+    q.units = t > 0 ? t : 1;  // a row tile that sees nothing is still written
+    return q;
+}
+
+struct Item {
+    Req q;
+    int r, h, rt, row0;     // request, key head, row tile and its first row
+    int pos0, pos1;         // positions of the tile's first and last token
+    int first, last;        // key tiles of this worker's share
+    int unit0, unit1;       // the same as units of the item
+    int last_worker;        // the worker that ends the item
+    __device__ __forceinline__ bool starts() const { return unit0 == 0; }
+    __device__ __forceinline__ bool whole() const { return unit0 == 0 && unit1 == q.units; }
+};
+
+template <int ROWS, int TILE>
+struct Walk {
+    int G, r;
+    long long u, u_end, at, share;  // next unit, end of the range, first unit of request r, units per worker
+
+    __device__ __forceinline__ explicit Walk(const Cache4AttnArgs &a) : G(a.Hq / a.Hkv), r(0), u(0), u_end(0), at(0), share(1) {}
+
+    // All threads of the CTA; prefix has blockDim.x + 33 entries of shared
+    // memory, free again after the CTA's next barrier.
+    __device__ __forceinline__ void begin(const Cache4AttnArgs &a, long long *prefix, int worker, int workers) {
+        const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
+        long long *sums = prefix + nthr + 1;
+        const int per = (a.R + nthr - 1) / nthr;
+        const int r_lo = min(a.R, tid * per), r_hi = min(a.R, r_lo + per);
+        long long x = 0;
+        bool bad = false;
+        for (int i = r_lo; i < r_hi; ++i) {
+            const Req q = request<ROWS, TILE>(a, i, G);
+            bad |= !q.ok;
+            x += (long long)q.row_tiles * a.Hkv * q.units;
+        }
+        if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, KDA_STATUS_BAD_SEQLENS);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sums[warp] = x;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) x += sums[w];
+        prefix[tid + 1] = x;
+        if (tid == 0) prefix[0] = 0;
+        __syncthreads();
+        const long long total = prefix[nthr];
+        share = total > workers ? (total + workers - 1) / workers : 1;
+        u = share * worker;
+        u_end = min(total, u + share);
+        if (u >= u_end) return;
+        int lo = 0, hi = nthr;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        r = lo * per;
+        at = prefix[lo];
+    }
+
+    __device__ __forceinline__ bool next(const Cache4AttnArgs &a, Item &it) {
+        while (u < u_end) {
+            it.q = request<ROWS, TILE>(a, r, G);
+            const long long units = (long long)it.q.row_tiles * a.Hkv * it.q.units;
+            if (u >= at + units) {
+                at += units;
+                ++r;
+                continue;
+            }
+            const long long item = (u - at) / it.q.units;
+            it.unit0 = (int)((u - at) % it.q.units);
+            it.unit1 = (int)min((long long)it.q.units, it.unit0 + (u_end - u));
+            it.last_worker = (int)((u - it.unit0 + it.q.units - 1) / share);
+            u += it.unit1 - it.unit0;
+            it.r = r;
+            it.h = (int)(item / it.q.row_tiles);
+            const int i = (int)(item % it.q.row_tiles);
+            it.rt = i & 1 ? it.q.row_tiles - 1 - (i >> 1) : i >> 1;
+            it.row0 = it.rt * ROWS;
+            const int row1 = min(it.q.rows, it.row0 + ROWS) - 1;
+            it.pos0 = it.q.len - it.q.n + it.row0 / G;
+            it.pos1 = it.q.len - it.q.n + row1 / G;
+            const int key_lo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
+            const int tile_lo = key_lo / TILE;
+            const int tiles = max(0, (it.pos1 + TILE) / TILE - tile_lo);  // none where pos1 < 0
+            it.first = tile_lo + min(it.unit0, tiles);
+            it.last = tile_lo + min(it.unit1, tiles);
+            return true;
+        }
+        return false;
+    }
+};
+
+// The shares of a row tile's keys, in key order: o = sum_p 2^{m_p - M} O_p / sum_p 2^{m_p - M} l_p.
+// A share is (m [ROWS], l [ROWS], O [ROWS][D]); worker w has two places, 1 for
+// a row tile that starts in its range and 0 for one that it goes on with.
+// One CTA per worker and RB rows (it has work where a row tile starts in that
+// worker's range and ends in a later one), four channels of a row per thread.
+template <int D, int ROWS, int TILE, int RB, bool F32>
+__global__ void __launch_bounds__(RB * D / 4)
+cache4_merge_kernel(const Cache4AttnArgs a, float lift) {
+    const int w0 = blockIdx.x, row = blockIdx.y * RB + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4) * 4;
+    const int4 job = a.jobs[w0];
+    if (job.x < 0) return;
+    const int G = a.Hq / a.Hkv;
+    const Req q = request<ROWS, TILE>(a, job.x, G);
+    const int rr = job.z * ROWS + row;
+    if (rr >= q.rows) return;
+    const size_t step = (size_t)ROWS * (D + 2);
+    float m = a.parts[((size_t)w0 * 2 + 1) * step + row];
+    for (int w = w0 + 1; w <= job.w; ++w) m = fmaxf(m, a.parts[(size_t)w * 2 * step + row]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int w = w0; w <= job.w; ++w) {
+        const float *p = a.parts + ((size_t)w * 2 + (w == w0)) * step;
+        const float f = exp2_fast(p[row] - ref);
+        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * ROWS + (size_t)row * D + c);
+        l = fmaf(f, p[ROWS + row], l);
+        y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
+    }
+    const size_t head = (size_t)(q.q0 + rr / G) * a.Hq + job.y * G + rr % G;
+    const bool none = m == -INFINITY && l == 0.f;
+    const float inv = none ? 0.f : (a.v_scale ? a.v_scale[job.y] : 1.f) / l;
+    y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    if constexpr (F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + head * D + c) = y;
+    } else {
+        const __nv_bfloat162 b0 = __floats2bfloat162_rn(y.x, y.y), b1 = __floats2bfloat162_rn(y.z, y.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + head * D + c) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
+    }
+    if (a.lse && c == 0) a.lse[head] = none ? -INFINITY : (m + log2f(l) - lift) * kLn2;
+}
+
+template <int D, int ROWS, int TILE, bool F32>
+cudaError_t merge_shares(const Cache4AttnArgs &a, int workers, float lift, cudaStream_t st) {
+    constexpr int RB = ROWS < 16 ? ROWS : 16;
+    cache4_merge_kernel<D, ROWS, TILE, RB, F32><<<dim3(workers, ROWS / RB), RB * D / 4, 0, st>>>(a, lift);
+    return cudaGetLastError();
+}
+
+}  // namespace cache4
+}  // namespace kda

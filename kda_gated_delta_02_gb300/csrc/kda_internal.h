@@ -234,5 +234,9 @@ size_t cache4_attn_workspace(int sms, int d);
 // rows: an upper bound of the query rows (tokens x heads of a group) of one request
 cudaError_t launch_cache4_attn(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st);
 cudaError_t launch_cache4_merge(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st);
+// The same on the tcgen05 tensor cores, for bf16 queries with many rows (cache4_attn_tc.cu).
+size_t cache4_attn_tc_workspace(int sms, int d);
+cudaError_t launch_cache4_attn_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, cudaStream_t st);
+cudaError_t launch_cache4_merge_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, cudaStream_t st);
 
 }  // namespace kda
