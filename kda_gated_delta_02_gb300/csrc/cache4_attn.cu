@@ -83,7 +83,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
 
     Item it;
     while (!dead && walk.next(a, it)) {
-        const Req &q = it.q;
+        const Req &q = walk.q;
         const int h = it.h, row0 = it.row0, pos0 = it.pos0, pos1 = it.pos1, first = it.first, last = it.last;
 
         // ---- query fragments: row g of every 8, channels (D / 4) t4 ...
@@ -451,7 +451,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                 }
         } else {
             // part 1 starts a row tile that goes on, part 0 continues one
-            const int part = it.starts() ? 1 : 0;
+            const int part = it.starts ? 1 : 0;
             float *w = a.parts + ((size_t)me * 2 + part) * (ROWS * (D + 2));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -468,7 +468,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                         p[i] = make_float4(acc[nt][2 * i][j], acc[nt][2 * i][j + 2], acc[nt][2 * i + 1][j],
                                            acc[nt][2 * i + 1][j + 2]);
                 }
-            if (part == 1) job = make_int4(it.r, h, it.rt, it.last_worker);
+            if (part == 1) job = make_int4(it.r, h, it.rt, walk.last_worker());
         }
     }
     if (lane == 0) a.jobs[me] = dead ? make_int4(-1, 0, 0, 0) : job;

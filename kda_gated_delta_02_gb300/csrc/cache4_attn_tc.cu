@@ -71,16 +71,59 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
+// Polls until the phase with this parity is over, at most `limit` times.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .u32 n;\nmov.u32 n, %3;\n"
+        "AGAIN:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n@p bra DONE;\n"
+        "sub.u32 n, n, 1;\nsetp.ne.u32 p, n, 0;\n@p bra AGAIN;\nsetp.ne.u32 p, n, n;\n"
+        "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(limit)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// 32 consecutive columns of this thread's tensor memory lane, without the wait:
+// several loads go out together, then umma::wait_ld() and hold() on each array
+__device__ __forceinline__ void ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void hold(uint32_t (&r)[32]) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
+}
+
+__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&s)[2][32]) {
+    ld32_async(taddr, s[0]);
+    ld32_async(taddr + 32, s[1]);
+    umma::wait_ld();
+    hold(s[0]);
+    hold(s[1]);
+}
+__device__ __forceinline__ void st32b(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -146,12 +189,8 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     // a bounded wait that gives up when any role has; `wait` for whole warps,
     // whose lanes then agree
     auto wait1 = [&](int i, uint32_t parity) {
-        for (uint32_t n = 0; n < 64; ++n) {
-            if (umma::mbar_wait(bar(i), parity & 1, kWaitLimit / 64)) return true;
-            if (misc[1]) return false;
-        }
+        if (poll(bar(i), parity & 1, kWaitLimit)) return true;
         misc[1] = 1;
-        if (a.status) atomicOr(a.status, KDA_STATUS_TIMEOUT);
         return false;
     };
     auto wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait1(i, parity)) != 0; };
@@ -166,7 +205,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         int4 job = make_int4(-1, 0, 0, 0);
         auto work = [&]() {
             while (walk.next(a, it)) {
-                const Req &q = it.q;
+                const Req &q = walk.q;
                 const int rr = it.row0 + my;
                 const bool valid = rr < q.rows;
                 const int tok = min(rr, q.rows - 1) / G, x = valid ? rr % G : 0;
@@ -217,22 +256,42 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     const uint32_t ts = tq + b * 128;
                     if (!wait(C::b_s_full + b, parity)) return;
                     umma::fence_after();
+                    if (it.row0 + t * 128 + lane_base >= q.rows) {
+                        // no row of this warp is there: its weights may be anything (rows do not mix)
+                        umma::fence_before();
+                        arrive(bar(C::b_p_full + b));
+                        continue;
+                    }
                     const int key0 = tile * kTile;
                     const bool edge = key0 + kTile > see_lo + 1 || (a.window > 0 && key0 <= see_hi - a.window);
                     const int hi = sees - key0;                                             // last visible column
                     const int lo = a.window > 0 ? sees - a.window - key0 : -1;              // last hidden one before
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        umma::ld32(ts + c * 32, s);
-                        if (edge) {
+                    if (edge) {
+                        // hidden columns become -inf where they are; few tiles have any
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t s[32];
+                            ld32_async(ts + c * 32, s);
+                            umma::wait_ld();
+                            hold(s);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (c * 32 + i > hi || c * 32 + i <= lo) s[i] = -INFINITY;
+                                if (i > hi - c * 32 || i <= lo - c * 32) s[i] = 0xff800000u;
+                            st32b(ts + c * 32, s);
                         }
+                        wait_st();
+                    }
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t s[2][32];
+                        load64(ts + c * 64, s);
+                        float tops[4] = {top, top, top, top};
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(s[i], s[i + 1]));
+                        for (int i = 0; i < 64; i += 2)
+                            tops[i / 2 % 4] = fmaxf(tops[i / 2 % 4], fmaxf(__uint_as_float(s[i / 32][i % 32]),
+                                                                           __uint_as_float(s[i / 32][i % 32 + 1])));
+                        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     }
                     top *= fac;
                     if (tile == it.first) {
@@ -259,25 +318,26 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         }
                     }
                     const float off = kLift - (m == -INFINITY ? 0.f : m);
+                    const float2 fac2 = make_float2(fac, fac), off2 = make_float2(off, off);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    // the weights take the place of columns of S that have been read
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t s[2][32], p[32];
+                        load64(ts + c * 64, s);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        umma::ld32(ts + c * 32, s);
-                        if (edge) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c * 32 + i > hi || c * 32 + i <= lo) s[i] = -INFINITY;
+                        for (int i = 0; i < 32; ++i) {
+                            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[i / 16][i % 16 * 2]),
+                                                                    __uint_as_float(s[i / 16][i % 16 * 2 + 1])),
+                                                        fac2, off2);
+                            const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                            sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+                            p[i] = pack_f16(e.x, e.y);
                         }
-                        uint32_t p[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float x0 = exp2_fast(fmaf(s[2 * i], fac, off)), x1 = exp2_fast(fmaf(s[2 * i + 1], fac, off));
-                            l += x0 + x1;
-                            p[i] = pack_f16(x0, x1);
-                        }
-                        // the weights take columns of S that this warp has read
-                        st16(ts + c * 16, p);
+                        st32b(ts + c * 32, p);
                     }
+                    sum[0] = __fadd2_rn(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
                     wait_st();
                     umma::fence_before();
                     arrive(bar(C::b_p_full + b));
@@ -287,49 +347,41 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     umma::fence_after();
                 }
                 const bool none = it.last == it.first || (m == -INFINITY && l == 0.f);
-                if (it.whole()) {
-                    const float inv = none ? 0.f : (a.v_scale ? a.v_scale[it.h] : 1.f) / l;
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        if (it.last > it.first) umma::ld32(to + c * 32, o);
-                        if (valid) {
-                            uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + head * D + c * 32);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t u[4];
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const __nv_bfloat162 y = __floats2bfloat162_rn(none ? 0.f : o[8 * i + 2 * j] * inv,
-                                                                                   none ? 0.f : o[8 * i + 2 * j + 1] * inv);
-                                    u[j] = *reinterpret_cast<const uint32_t *>(&y);
-                                }
-                                p[i] = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
-                        }
-                    }
-                    if (valid && a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(l) - kLift) * kLn2;
-                } else {
-                    const int part = it.starts() ? 1 : 0;
-                    float *w = a.parts + ((size_t)me * 2 + part) * ((size_t)C::ROWS * (D + 2));
-                    if (valid) {
-                        w[my] = none ? -INFINITY : m;
-                        w[C::ROWS + my] = l;
-                    }
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        if (it.last > it.first) umma::ld32(to + c * 32, o);
-                        if (valid) {
-                            float4 *p = reinterpret_cast<float4 *>(w + 2 * C::ROWS + (size_t)my * D + c * 32);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                p[i] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                            : make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                        }
-                    }
-                    if (part == 1) job = make_int4(it.r, it.h, it.rt, it.last_worker);
+                const bool whole = it.whole();
+                const float f = none ? 0.f : whole ? (a.v_scale ? a.v_scale[it.h] : 1.f) / l : 1.f;
+                float *part = a.parts + ((size_t)me * 2 + (it.starts ? 1 : 0)) * ((size_t)C::ROWS * (D + 2));
+                if (valid && whole && a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(l) - kLift) * kLn2;
+                if (valid && !whole) {
+                    part[my] = none ? -INFINITY : m;
+                    part[C::ROWS + my] = l;
                 }
+                char *dst = whole ? reinterpret_cast<char *>(static_cast<__nv_bfloat16 *>(a.o) + head * D)
+                                  : reinterpret_cast<char *>(part + 2 * C::ROWS + (size_t)my * D);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    if (it.last > it.first) umma::ld32(to + c * 32, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * f;
+                    if (valid && whole) {
+                        uint4 *p = reinterpret_cast<uint4 *>(dst) + c * 4;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * i + 2 * j], o[8 * i + 2 * j + 1]);
+                                u[j] = *reinterpret_cast<const uint32_t *>(&y);
+                            }
+                            p[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                    } else if (valid) {
+                        float4 *p = reinterpret_cast<float4 *>(dst) + c * 8;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) p[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+                if (it.starts && !whole) job = make_int4(it.r, it.h, it.rt, walk.last_worker());
                 // the reads of O come before the next row tile's products (released by its first weights)
                 umma::fence_before();
             }
@@ -338,47 +390,58 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         if (tid == 0) a.jobs[me] = misc[1] ? make_int4(-1, 0, 0, 0) : job;
     } else if (warp < C::SOFT + C::DEQ) {
         // ------------------------------------------------------------ dequant
-        const int d = tid - C::SOFT * 32;  // 0 .. 255
+        const int d = tid - C::SOFT * 32;
+        // Keys: four lanes per key; lane g takes the channel groups g and (d =
+        // 128) g + 4, so the eight lanes of a 128-byte store row write eight
+        // different chunks.  Values: sixteen lanes per block and group, a key
+        // each.  A thread's place in the swizzle is the same in every block.
+        constexpr int NK = D / 64, STEP = 8 / C::DEQ;      // channel halves; passes over 64 keys
+        const int key = d >> 2, g = d & 3;
+        const uint32_t k_codes = (key >> 4) * BB + (key & 15) * (D / 2) + g * 8;
+        const uint32_t k_scale = (key >> 4) * BB + off_ks(D) + (key & 15) * (D / 16) + g;
+        const uint32_t k_out0 = umma::kmaj(key, g * 16, 128), k_out1 = umma::kmaj(key, g * 16 + 8, 128);
+        const int tok = d & 15, grp = (d >> 4) % (D / 16), blk = (d >> 4) / (D / 16);
+        constexpr int VPASS = 64 * D / 16 / (C::DEQ * 32), VBLK = 4 / VPASS;  // passes; blocks per pass
+        const uint32_t v_codes = blk * BB + off_vc(D) + grp * 128 + tok * 8;
+        const uint32_t v_scale = blk * BB + off_vs(D) + grp * 16 + tok;
+        const uint32_t v_out0 = umma::mnmaj(grp * 16, blk * 16 + tok, NK), v_out1 = umma::mnmaj(grp * 16 + 8, blk * 16 + tok, NK);
         uint32_t n = 0, raws = 0;
         auto work = [&]() {
             while (walk.next(a, it)) {
+#pragma unroll 1
                 for (int tile = it.first; tile < it.last; ++tile, ++n) {
                     const uint32_t ks = sb + C::off_k + (n & 1) * C::OPERAND, vs = sb + C::off_v + (n & 1) * C::OPERAND;
                     if (!wait(C::b_k_empty + (n & 1), (n >> 1) + 1)) return;
-                    // keys: four lanes per key, lane g the channel groups g and (d = 128) g + 4
-#pragma unroll
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t ri = (raws + half) % C::RAWS;
                         if (!wait(C::b_raw_full + ri, (raws + half) / C::RAWS)) return;
-                        const uint32_t raw = sb + C::off_raw + ri * C::RAW;
+                        const uint32_t raw = sb + C::off_raw + ri * C::RAW, out = ks + half * 8192;
 #pragma unroll
-                        for (int i = 0; i < D / 64 * (8 / C::DEQ); ++i) {
-                            const int key = (d >> 2) + i / (D / 64) * (8 * C::DEQ), grp = (d & 3) + 4 * (i % (D / 64));
-                            const int blk = key >> 4, tok = key & 15, kk = half * 64 + key;
-                            const uint2 w = lds64(raw + blk * BB + tok * (D / 2) + grp * 8);
-                            const uint32_t f = scale_pair(lds8(raw + blk * BB + off_ks(D) + tok * (D / 16) + grp));
-                            convert(w, f, ks + umma::kmaj(kk, grp * 16, 128), ks + umma::kmaj(kk, grp * 16 + 8, 128));
-                        }
+                        for (int p = 0; p < STEP; ++p)
+#pragma unroll
+                            for (int j = 0; j < NK; ++j) {
+                                const uint32_t in = raw + p * (C::DEQ / 2) * BB, to = out + p * C::DEQ * 1024 + j * 16384;
+                                convert(lds64(in + k_codes + j * 32), scale_pair(lds8(in + k_scale + j * 4)), to + k_out0,
+                                        to + k_out1);
+                            }
                     }
                     umma::fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) arrive(bar(C::b_k_full + (n & 1)));
-                    // values: sixteen lanes per block and group, one key each
                     if (!wait(C::b_v_empty + (n & 1), (n >> 1) + 1)) return;
-#pragma unroll
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t ri = (raws + half) % C::RAWS;
-                        const uint32_t raw = sb + C::off_raw + ri * C::RAW;
+                        const uint32_t raw = sb + C::off_raw + ri * C::RAW, out = vs + half * (8 * NK * 1024);
+                        // past the end the bytes are anything, NaN scales too: a zero weight does not undo that
+                        const int left = walk.q.len - (tile * kTile + half * 64 + blk * 16 + tok);
 #pragma unroll
-                        for (int i = 0; i < D / 64 * (8 / C::DEQ); ++i) {
-                            const int pair = (d >> 4) + 2 * C::DEQ * i, tok = d & 15;
-                            const int blk = pair / (D / 16), grp = pair % (D / 16);
-                            const int kk = half * 64 + blk * 16 + tok;
-                            const uint2 w = lds64(raw + blk * BB + off_vc(D) + grp * 128 + tok * 8);
-                            uint32_t f = scale_pair(lds8(raw + blk * BB + off_vs(D) + grp * 16 + tok));
-                            // past the end the bytes are anything, NaN scales too: a zero weight does not undo that
-                            if (tile * kTile + kk >= it.q.len) f = 0;
-                            convert(w, f, vs + umma::mnmaj(grp * 16, kk, D / 64), vs + umma::mnmaj(grp * 16 + 8, kk, D / 64));
+                        for (int p = 0; p < VPASS; ++p) {
+                            uint32_t f = scale_pair(lds8(raw + p * VBLK * BB + v_scale));
+                            if (p * VBLK * 16 >= left) f = 0;
+                            const uint32_t to = out + p * VBLK * 2 * NK * 1024;
+                            convert(lds64(raw + p * VBLK * BB + v_codes), f, to + v_out0, to + v_out1);
                         }
                         __syncwarp();
                         if (lane == 0) arrive(bar(C::b_raw_empty + ri));
@@ -403,7 +466,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         const uint32_t ri = raws % C::RAWS;
                         const int key = tile * kTile + half * 64 + lane * chunk * 16;
                         // blocks of this lane's copy that hold keys
-                        const int left = (it.q.len - key + 15) >> 4;
+                        const int left = (walk.q.len - key + 15) >> 4;
                         const int mine = lane * chunk < 4 ? min(max(left, 0), chunk) : 0;
                         int page = 0;
                         if (mine > 0) {
@@ -461,8 +524,10 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                 if (!wait1(C::b_q_full, items++)) return;
                 if (!wait1(C::b_k_full + (n & 1), n >> 1)) return;
                 umma::fence_after();
+#pragma unroll 1
                 for (int t = 0; t < QT; ++t) scores(t, n, QT == 2 ? t : n & 1);
                 umma::commit(bar(C::b_k_empty + (n & 1)));
+#pragma unroll 1
                 for (int j = 0; j < tiles; ++j, ++n) {
                     if (QT == 1 && j + 1 < tiles) {
                         if (!wait1(C::b_k_full + ((n + 1) & 1), (n + 1) >> 1)) return;
@@ -470,6 +535,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         scores(0, n + 1, (n + 1) & 1);
                         umma::commit(bar(C::b_k_empty + ((n + 1) & 1)));
                     }
+#pragma unroll 1
                     for (int t = 0; t < QT; ++t) {
                         const int b = QT == 2 ? t : n & 1;
                         if (t == 0 && !wait1(C::b_v_full + (n & 1), n >> 1)) return;
@@ -495,6 +561,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
+    if (tid == 0 && misc[1] && a.status) atomicOr(a.status, KDA_STATUS_TIMEOUT);
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
 }
 

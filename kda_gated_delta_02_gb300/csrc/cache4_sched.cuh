@@ -85,22 +85,22 @@ __device__ __forceinline__ Req request(const Cache4AttnArgs &a, int r, int G) {
 }
 
 struct Item {
-    Req q;
     int r, h, rt, row0;     // request, key head, row tile and its first row
     int pos0, pos1;         // positions of the tile's first and last token
     int first, last;        // key tiles of this worker's share
-    int unit0, unit1;       // the same as units of the item
-    int last_worker;        // the worker that ends the item
-    __device__ __forceinline__ bool starts() const { return unit0 == 0; }
-    __device__ __forceinline__ bool whole() const { return unit0 == 0 && unit1 == q.units; }
+    bool starts, ends;      // whether the share holds the item's first and last unit
+    __device__ __forceinline__ bool whole() const { return starts && ends; }
 };
 
 template <int ROWS, int TILE>
 struct Walk {
-    int G, r;
-    long long u, u_end, at, share;  // next unit, end of the range, first unit of request r, units per worker
+    int G;
+    int r, h, i, unit;          // the next item and its unit
+    long long u, u_end, share;  // the next unit's number, the end of the range, units per worker
+    Req q;                      // request r
 
-    __device__ __forceinline__ explicit Walk(const Cache4AttnArgs &a) : G(a.Hq / a.Hkv), r(0), u(0), u_end(0), at(0), share(1) {}
+    __device__ __forceinline__ explicit Walk(const Cache4AttnArgs &a)
+        : G(a.Hq / a.Hkv), r(0), h(0), i(0), unit(0), u(0), u_end(0), share(1) {}
 
     // All threads of the CTA; prefix has blockDim.x + 33 entries of shared
     // memory, free again after the CTA's next barrier.
@@ -111,10 +111,11 @@ struct Walk {
         const int r_lo = min(a.R, tid * per), r_hi = min(a.R, r_lo + per);
         long long x = 0;
         bool bad = false;
-        for (int i = r_lo; i < r_hi; ++i) {
-            const Req q = request<ROWS, TILE>(a, i, G);
-            bad |= !q.ok;
-            x += (long long)q.row_tiles * a.Hkv * q.units;
+#pragma unroll 1
+        for (int k = r_lo; k < r_hi; ++k) {
+            const Req e = request<ROWS, TILE>(a, k, G);
+            bad |= !e.ok;
+            x += (long long)e.row_tiles * a.Hkv * e.units;
         }
         if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, KDA_STATUS_BAD_SEQLENS);
 #pragma unroll
@@ -124,6 +125,7 @@ struct Walk {
         }
         if (lane == 31) sums[warp] = x;
         __syncthreads();
+#pragma unroll 1
         for (int w = 0; w < warp; ++w) x += sums[w];
         prefix[tid + 1] = x;
         if (tid == 0) prefix[0] = 0;
@@ -140,40 +142,56 @@ struct Walk {
             else hi = mid;
         }
         r = lo * per;
-        at = prefix[lo];
+        long long off = u - prefix[lo];
+#pragma unroll 1
+        for (;; ++r) {
+            q = request<ROWS, TILE>(a, r, G);
+            const long long units = (long long)q.row_tiles * a.Hkv * q.units;
+            if (off < units) break;
+            off -= units;
+        }
+        const long long item = off / q.units;
+        unit = (int)(off - item * q.units);
+        h = (int)(item / q.row_tiles);
+        i = (int)(item - (long long)h * q.row_tiles);
     }
 
     __device__ __forceinline__ bool next(const Cache4AttnArgs &a, Item &it) {
-        while (u < u_end) {
-            it.q = request<ROWS, TILE>(a, r, G);
-            const long long units = (long long)it.q.row_tiles * a.Hkv * it.q.units;
-            if (u >= at + units) {
-                at += units;
-                ++r;
-                continue;
+        if (u >= u_end) return false;
+        if (unit == q.units) {
+            unit = 0;
+            if (++i == q.row_tiles) {
+                i = 0;
+                if (++h == a.Hkv) {
+                    h = 0;
+#pragma unroll 1
+                    do q = request<ROWS, TILE>(a, ++r, G);
+                    while (q.row_tiles == 0);
+                }
             }
-            const long long item = (u - at) / it.q.units;
-            it.unit0 = (int)((u - at) % it.q.units);
-            it.unit1 = (int)min((long long)it.q.units, it.unit0 + (u_end - u));
-            it.last_worker = (int)((u - it.unit0 + it.q.units - 1) / share);
-            u += it.unit1 - it.unit0;
-            it.r = r;
-            it.h = (int)(item / it.q.row_tiles);
-            const int i = (int)(item % it.q.row_tiles);
-            it.rt = i & 1 ? it.q.row_tiles - 1 - (i >> 1) : i >> 1;
-            it.row0 = it.rt * ROWS;
-            const int row1 = min(it.q.rows, it.row0 + ROWS) - 1;
-            it.pos0 = it.q.len - it.q.n + it.row0 / G;
-            it.pos1 = it.q.len - it.q.n + row1 / G;
-            const int key_lo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
-            const int tile_lo = key_lo / TILE;
-            const int tiles = max(0, (it.pos1 + TILE) / TILE - tile_lo);  // none where pos1 < 0
-            it.first = tile_lo + min(it.unit0, tiles);
-            it.last = tile_lo + min(it.unit1, tiles);
-            return true;
         }
-        return false;
+        const int unit1 = (int)min((long long)q.units, unit + (u_end - u));
+        it.r = r;
+        it.h = h;
+        it.rt = i & 1 ? q.row_tiles - 1 - (i >> 1) : i >> 1;
+        it.row0 = it.rt * ROWS;
+        const int row1 = min(q.rows, it.row0 + ROWS) - 1;
+        it.pos0 = q.len - q.n + it.row0 / G;
+        it.pos1 = q.len - q.n + row1 / G;
+        const int key_lo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
+        const int tile_lo = key_lo / TILE;
+        const int tiles = max(0, (it.pos1 + TILE) / TILE - tile_lo);  // none where pos1 < 0
+        it.first = tile_lo + min(unit, tiles);
+        it.last = tile_lo + min(unit1, tiles);
+        it.starts = unit == 0;
+        it.ends = unit1 == q.units;
+        u += unit1 - unit;
+        unit = unit1;
+        return true;
     }
+
+    // the worker whose range ends the current item
+    __device__ __forceinline__ int last_worker() const { return (int)((u - unit + q.units - 1) / share); }
 };
 
 // The shares of a row tile's keys, in key order: o = sum_p 2^{m_p - M} O_p / sum_p 2^{m_p - M} l_p.
