@@ -5,8 +5,9 @@
 // QT x 128 rows and key tiles of 128.  One persistent CTA per SM, warps by
 // role:
 //   producer   1 warp   bulk copies of 64 keys at a time into a raw ring
-//   dequant    12 - 4 QT warps  codes and scales -> f16 (exact), into the swizzled
-//                       shared-memory operands K (K-major) and V (N-major)
+//   dequant    12 - 4 QT warps, half for the keys and half for the values: codes
+//                       and scales -> f16 (exact), into the swizzled shared-
+//                       memory operands K (K-major) and V (N-major)
 //   products   1 thread S = Q K^T into tensor memory, O += P V with P read
 //                       from tensor memory (it takes the place of S)
 //   softmax    4 QT warps, a thread per row: maximum, weights (f16, lifted by
@@ -164,9 +165,9 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
             umma::mbar_init(bar(C::b_raw_empty + i), C::DEQ);
         }
         for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(bar(C::b_k_full + i), C::DEQ);
+            umma::mbar_init(bar(C::b_k_full + i), C::DEQ / 2);
             umma::mbar_init(bar(C::b_k_empty + i), 1);
-            umma::mbar_init(bar(C::b_v_full + i), C::DEQ);
+            umma::mbar_init(bar(C::b_v_full + i), C::DEQ / 2);
             umma::mbar_init(bar(C::b_v_empty + i), 1);
             umma::mbar_init(bar(C::b_s_full + i), 1);
             umma::mbar_init(bar(C::b_p_full + i), 128);
@@ -391,65 +392,91 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     } else if (warp < C::SOFT + C::DEQ) {
         // ------------------------------------------------------------ dequant
         const int d = tid - C::SOFT * 32;
+        constexpr int NK = D / 64, NG = D / 16, BATCH = 4;
+        constexpr int THR = C::DEQ * 16;                   // threads for the keys, and as many for the values
+        const bool for_keys = d < THR;
+        const int e = for_keys ? d : d - THR;
         // Keys: four lanes per key; lane g takes the channel groups g and (d =
         // 128) g + 4, so the eight lanes of a 128-byte store row write eight
-        // different chunks.  Values: sixteen lanes per block and group, a key
-        // each.  A thread's place in the swizzle is the same in every block.
-        constexpr int NK = D / 64, STEP = 8 / C::DEQ;      // channel halves; passes over 64 keys
-        const int key = d >> 2, g = d & 3;
-        const uint32_t k_codes = (key >> 4) * BB + (key & 15) * (D / 2) + g * 8;
-        const uint32_t k_scale = (key >> 4) * BB + off_ks(D) + (key & 15) * (D / 16) + g;
-        const uint32_t k_out0 = umma::kmaj(key, g * 16, 128), k_out1 = umma::kmaj(key, g * 16 + 8, 128);
-        const int tok = d & 15, grp = (d >> 4) % (D / 16), blk = (d >> 4) / (D / 16);
-        constexpr int VPASS = 64 * D / 16 / (C::DEQ * 32), VBLK = 4 / VPASS;  // passes; blocks per pass
-        const uint32_t v_codes = blk * BB + off_vc(D) + grp * 128 + tok * 8;
-        const uint32_t v_scale = blk * BB + off_vs(D) + grp * 16 + tok;
-        const uint32_t v_out0 = umma::mnmaj(grp * 16, blk * 16 + tok, NK), v_out1 = umma::mnmaj(grp * 16 + 8, blk * 16 + tok, NK);
+        // different chunks.
+        constexpr int K_ROWS = THR / 4, K_STEPS = 64 / K_ROWS * NK;       // keys per pass; conversions per 64 keys
+        // Values: sixteen lanes per block and group, a key each.
+        constexpr int PAIRS = THR / 16, V_STEPS = 4 * NG / PAIRS;         // (block, group) pairs per pass
+        constexpr int SPLIT = NG > PAIRS ? NG / PAIRS : 1;                // passes over the groups of a block
+        constexpr int V_BLKS = PAIRS > NG ? PAIRS / NG : 1;               // blocks per pass
+        uint32_t codes, scale, out0, out1;
+        int blk_key;  // key of the first conversion in its 64
+        if (for_keys) {
+            const int key = e >> 2, g = e & 3;
+            codes = (key >> 4) * BB + (key & 15) * (D / 2) + g * 8;
+            scale = (key >> 4) * BB + off_ks(D) + (key & 15) * NG + g;
+            out0 = umma::kmaj(key, g * 16, 128), out1 = umma::kmaj(key, g * 16 + 8, 128);
+            blk_key = key;
+        } else {
+            const int tok = e & 15, grp = (e >> 4) % NG, blk = (e >> 4) / NG;
+            codes = blk * BB + off_vc(D) + grp * 128 + tok * 8;
+            scale = blk * BB + off_vs(D) + grp * 16 + tok;
+            out0 = umma::mnmaj(grp * 16, blk * 16 + tok, NK), out1 = umma::mnmaj(grp * 16 + 8, blk * 16 + tok, NK);
+            blk_key = blk * 16 + tok;
+        }
+        const int b_empty = for_keys ? C::b_k_empty : C::b_v_empty, b_full = for_keys ? C::b_k_full : C::b_v_full;
         uint32_t n = 0, raws = 0;
         auto work = [&]() {
             while (walk.next(a, it)) {
 #pragma unroll 1
                 for (int tile = it.first; tile < it.last; ++tile, ++n) {
-                    const uint32_t ks = sb + C::off_k + (n & 1) * C::OPERAND, vs = sb + C::off_v + (n & 1) * C::OPERAND;
-                    if (!wait(C::b_k_empty + (n & 1), (n >> 1) + 1)) return;
+                    if (!wait(b_empty + (n & 1), (n >> 1) + 1)) return;
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t ri = (raws + half) % C::RAWS;
-                        if (!wait(C::b_raw_full + ri, (raws + half) / C::RAWS)) return;
-                        const uint32_t raw = sb + C::off_raw + ri * C::RAW, out = ks + half * 8192;
+                    for (int half = 0; half < 2; ++half, ++raws) {
+                        const uint32_t ri = raws % C::RAWS;
+                        if (!wait(C::b_raw_full + ri, raws / C::RAWS)) return;
+                        const uint32_t raw = sb + C::off_raw + ri * C::RAW;
+                        uint2 w[BATCH];
+                        uint32_t f[BATCH];
+                        if (for_keys) {
+                            const uint32_t out = sb + C::off_k + (n & 1) * C::OPERAND + half * 8192;
 #pragma unroll
-                        for (int p = 0; p < STEP; ++p)
+                            for (int p = 0; p < K_STEPS; p += BATCH) {
 #pragma unroll
-                            for (int j = 0; j < NK; ++j) {
-                                const uint32_t in = raw + p * (C::DEQ / 2) * BB, to = out + p * C::DEQ * 1024 + j * 16384;
-                                convert(lds64(in + k_codes + j * 32), scale_pair(lds8(in + k_scale + j * 4)), to + k_out0,
-                                        to + k_out1);
+                                for (int j = 0; j < BATCH && p + j < K_STEPS; ++j) {
+                                    const int row = (p + j) / NK * K_ROWS, c = (p + j) % NK;
+                                    w[j] = lds64(raw + codes + row / 16 * BB + c * 32);
+                                    f[j] = lds8(raw + scale + row / 16 * BB + c * 4);
+                                }
+#pragma unroll
+                                for (int j = 0; j < BATCH && p + j < K_STEPS; ++j) {
+                                    const uint32_t to = out + (p + j) / NK * K_ROWS * 128 + (p + j) % NK * 16384;
+                                    convert(w[j], scale_pair(f[j]), to + out0, to + out1);
+                                }
                             }
-                    }
-                    umma::fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) arrive(bar(C::b_k_full + (n & 1)));
-                    if (!wait(C::b_v_empty + (n & 1), (n >> 1) + 1)) return;
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t ri = (raws + half) % C::RAWS;
-                        const uint32_t raw = sb + C::off_raw + ri * C::RAW, out = vs + half * (8 * NK * 1024);
-                        // past the end the bytes are anything, NaN scales too: a zero weight does not undo that
-                        const int left = walk.q.len - (tile * kTile + half * 64 + blk * 16 + tok);
+                        } else {
+                            const uint32_t out = sb + C::off_v + (n & 1) * C::OPERAND + half * (8 * NK * 1024);
+                            // past the end the bytes are anything, NaN scales too: a zero weight does not undo that
+                            const int left = walk.q.len - (tile * kTile + half * 64 + blk_key);
 #pragma unroll
-                        for (int p = 0; p < VPASS; ++p) {
-                            uint32_t f = scale_pair(lds8(raw + p * VBLK * BB + v_scale));
-                            if (p * VBLK * 16 >= left) f = 0;
-                            const uint32_t to = out + p * VBLK * 2 * NK * 1024;
-                            convert(lds64(raw + p * VBLK * BB + v_codes), f, to + v_out0, to + v_out1);
+                            for (int p = 0; p < V_STEPS; p += BATCH) {
+#pragma unroll
+                                for (int j = 0; j < BATCH && p + j < V_STEPS; ++j) {
+                                    const int blk = (p + j) / SPLIT * V_BLKS, c = (p + j) % SPLIT * PAIRS;
+                                    w[j] = lds64(raw + codes + blk * BB + c * 128);
+                                    f[j] = lds8(raw + scale + blk * BB + c * 16);
+                                    if (blk * 16 >= left) f[j] = 0;
+                                }
+#pragma unroll
+                                for (int j = 0; j < BATCH && p + j < V_STEPS; ++j) {
+                                    const int blk = (p + j) / SPLIT * V_BLKS, c = (p + j) % SPLIT * PAIRS;
+                                    // c is a multiple of 64 channels where it is not 0
+                                    const uint32_t to = out + blk * 2 * NK * 1024 + c / 4 * 1024;
+                                    convert(w[j], scale_pair(f[j]), to + out0, to + out1);
+                                }
+                            }
                         }
                         __syncwarp();
                         if (lane == 0) arrive(bar(C::b_raw_empty + ri));
                     }
                     umma::fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) arrive(bar(C::b_v_full + (n & 1)));
-                    raws += 2;
+                    if (lane == 0) arrive(bar(b_full + (n & 1)));
                 }
             }
         };
