@@ -8,7 +8,7 @@
 //   dequant    12 - 4 QT warps, half for the keys and half for the values: codes
 //                       and scales -> f16 (exact), into the swizzled shared-
 //                       memory operands K (K-major) and V (N-major)
-//   products   1 thread S = Q K^T into tensor memory, O += P V with P read
+//   products   1 warp   S = Q K^T into tensor memory, O += P V with P read
 //                       from tensor memory (it takes the place of S)
 //   softmax    4 QT warps, a thread per row: maximum, weights (f16, lifted by
 //                       2^kLift), sum, and the accumulator's rescaling
@@ -64,12 +64,35 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D += A B with A in tensor memory (f16, two consecutive K per column, the lower one in the low half)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Products and commits are written for a whole warp that runs convergent, with
+// one lane (elect.sync) issuing: operands that the compiler knows to be
+// uniform sit in uniform registers, which the instruction takes, instead of
+// being moved there for every product (about 100 cycles each from a branch of
+// one thread).
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
     asm volatile(
-        "{\n.reg .pred pp;\nsetp.ne.b32 pp, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pp;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc));
+        "{\n.reg .pred pp, e;\nsetp.ne.b32 e, %5, 0;\nsetp.ne.b32 pp, %4, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pp;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead));
+}
+// A in tensor memory (f16, two consecutive K per column, the lower one in the low half)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+    asm volatile(
+        "{\n.reg .pred pp, e;\nsetp.ne.b32 e, %5, 0;\nsetp.ne.b32 pp, %4, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pp;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead));
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+    asm volatile(
+        "{\n.reg .pred e;\nsetp.ne.b32 e, %1, 0;\n"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(lead)
+        : "memory");
 }
 
 // Polls until the phase with this parity is over, at most `limit` times.
@@ -154,7 +177,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     constexpr int BB = block_bytes(D), KS = D / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sb = smem_addr(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int G = a.Hq / a.Hkv;
     auto bar = [&](int i) { return sb + C::off_bar + i * 8; };
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::off_misc);
@@ -522,68 +545,69 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
             for (uint32_t i = raws > C::RAWS ? raws - C::RAWS : 0; i < raws; ++i)
                 umma::mbar_wait(bar(C::b_raw_full + i % C::RAWS), (i / C::RAWS) & 1, kWaitLimit);
         }
-    } else if (lane == 0) {
+    } else {
         // ------------------------------------------------------------ products
         constexpr uint32_t id_s = idesc_f16(128, 128, 0), id_o = idesc_f16(128, D, 1);
-        const uint32_t sb4 = sb >> 4;
+        const uint32_t lead = elect();
+        const uint32_t sb4 = __shfl_sync(0xffffffffu, sb >> 4, 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
         uint32_t n = 0, items = 0;
         auto scores = [&](int t, uint32_t tile, int b) {
             const uint32_t q4 = sb4 + ((C::off_q + t * C::OPERAND) >> 4), k4 = sb4 + ((C::off_k + (tile & 1) * C::OPERAND) >> 4);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                umma::mma(tmem + b * 128, umma::sdesc4(q4 + o, 16, 1024), umma::sdesc4(k4 + o, 16, 1024), id_s, ks > 0);
+                mma_ss(tm + b * 128, umma::sdesc4(q4 + o, 16, 1024), umma::sdesc4(k4 + o, 16, 1024), id_s, ks > 0, lead);
             }
-            umma::commit(bar(C::b_s_full + b));
+            commit(bar(C::b_s_full + b), lead);
         };
         auto values = [&](int t, uint32_t tile, int b, bool acc) {
             const uint32_t v4 = sb4 + ((C::off_v + (tile & 1) * C::OPERAND) >> 4);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-                mma_ts(tmem + C::t_o + t * D, tmem + b * 128 + ks * 8,
-                       umma::sdesc4(v4 + ((ks * 16 * D * 2) >> 4), 1024, 16 * D), id_o, acc || ks > 0);
-            umma::commit(bar(C::b_o_done + t));
+                mma_ts(tm + C::t_o + t * D, tm + b * 128 + ks * 8, umma::sdesc4(v4 + ((ks * 16 * D * 2) >> 4), 1024, 16 * D),
+                       id_o, acc || ks > 0, lead);
+            commit(bar(C::b_o_done + t), lead);
         };
         auto work = [&]() {
             while (walk.next(a, it)) {
-                const int tiles = it.last - it.first;
+                const int tiles = __shfl_sync(0xffffffffu, it.last - it.first, 0);
                 if (tiles == 0) continue;
-                if (!wait1(C::b_q_full, items++)) return;
-                if (!wait1(C::b_k_full + (n & 1), n >> 1)) return;
+                if (!wait(C::b_q_full, items++)) return;
+                if (!wait(C::b_k_full + (n & 1), n >> 1)) return;
                 umma::fence_after();
-#pragma unroll 1
+#pragma unroll
                 for (int t = 0; t < QT; ++t) scores(t, n, QT == 2 ? t : n & 1);
-                umma::commit(bar(C::b_k_empty + (n & 1)));
+                commit(bar(C::b_k_empty + (n & 1)), lead);
 #pragma unroll 1
                 for (int j = 0; j < tiles; ++j, ++n) {
                     if (QT == 1 && j + 1 < tiles) {
-                        if (!wait1(C::b_k_full + ((n + 1) & 1), (n + 1) >> 1)) return;
+                        if (!wait(C::b_k_full + ((n + 1) & 1), (n + 1) >> 1)) return;
                         umma::fence_after();
                         scores(0, n + 1, (n + 1) & 1);
-                        umma::commit(bar(C::b_k_empty + ((n + 1) & 1)));
+                        commit(bar(C::b_k_empty + ((n + 1) & 1)), lead);
                     }
-#pragma unroll 1
+                    if (!wait(C::b_v_full + (n & 1), n >> 1)) return;
+#pragma unroll
                     for (int t = 0; t < QT; ++t) {
                         const int b = QT == 2 ? t : n & 1;
-                        if (t == 0 && !wait1(C::b_v_full + (n & 1), n >> 1)) return;
-                        if (!wait1(C::b_p_full + b, QT == 2 ? n : n >> 1)) return;
+                        if (!wait(C::b_p_full + b, QT == 2 ? n : n >> 1)) return;
                         umma::fence_after();
                         values(t, n, b, j > 0);
                         if (QT == 2 && j + 1 < tiles) {
-                            if (t == 0 && !wait1(C::b_k_full + ((n + 1) & 1), (n + 1) >> 1)) return;
+                            if (t == 0 && !wait(C::b_k_full + ((n + 1) & 1), (n + 1) >> 1)) return;
                             umma::fence_after();
                             scores(t, n + 1, t);
                         }
                     }
-                    umma::commit(bar(C::b_v_empty + (n & 1)));
-                    if (QT == 2 && j + 1 < tiles) umma::commit(bar(C::b_k_empty + ((n + 1) & 1)));
+                    commit(bar(C::b_v_empty + (n & 1)), lead);
+                    if (QT == 2 && j + 1 < tiles) commit(bar(C::b_k_empty + ((n + 1) & 1)), lead);
                 }
             }
         };
         work();
         // products in flight end before the CTA leaves
-        umma::commit(bar(C::b_drain));
-        umma::mbar_wait(bar(C::b_drain), 0, kWaitLimit);
+        commit(bar(C::b_drain), lead);
+        wait1(C::b_drain, 0);
     }
     umma::fence_before();
     __syncthreads();
