@@ -10,7 +10,8 @@
 //                       memory operands K (K-major) and V (N-major)
 //   products   1 warp   S = Q K^T into tensor memory, O += P V with P read
 //                       from tensor memory (it takes the place of S)
-//   softmax    4 QT warps, a thread per row: maximum, weights (f16, lifted by
+//   queries    2 warps  the next item's query rows, scaled, as f16
+//   softmax    8 warps  a thread per row and tile (or stream): maximum, weights (f16, lifted by
 //                       2^kLift), sum, and the accumulator's rescaling
 // The running maximum that the weights refer to moves only when it would rise
 // by more than 2^8, so the accumulator (in tensor memory) is rescaled a few
@@ -41,22 +42,33 @@ constexpr float kSlack = 8.f;
 
 template <int D, int QT>
 struct Cfg {
-    // 14 warps: 128 registers per thread
-    static constexpr int SOFT = 4 * QT, DEQ = 12 - SOFT, WARPS = SOFT + DEQ + 2, THREADS = WARPS * 32;
+    // Whole warpgroups by role, whose registers are shared out anew at the start:
+    // a CTA of 16 warps is launched with 128 a thread, one of 20 with 96.  With
+    // one row tile memory bounds the call and conversion gets two warpgroups.
+    static constexpr int SOFT = 8, DEQ = QT == 2 ? 4 : 8, WARPS = SOFT + DEQ + 4, THREADS = WARPS * 32;
+    static constexpr int R_LAUNCH = QT == 2 ? 128 : 96;
+    static constexpr int R_SOFT = QT == 2 ? 144 : 112, R_DEQ = QT == 2 ? 128 : 80, R_MISC = 96;
+    // the others give up what the softmax warpgroups take, and nobody waits for more than there is
+    static_assert(R_SOFT >= R_LAUNCH && R_DEQ <= R_LAUNCH && R_MISC <= R_LAUNCH, "who takes and who gives registers");
+    static_assert(2 * R_SOFT + DEQ / 4 * R_DEQ + R_MISC <= WARPS / 4 * R_LAUNCH, "registers of the CTA");
     static constexpr int ROWS = 128 * QT;
     static constexpr int OPERAND = 128 * D * 2;       // 128 rows of f16
     static constexpr int RAW = 4 * block_bytes(D);    // 64 keys
     static constexpr int RAWS = QT == 2 ? 3 : 6;      // raw stages
     static constexpr int off_q = 0, off_k = QT * OPERAND, off_v = off_k + 2 * OPERAND, off_raw = off_v + 2 * OPERAND;
     static constexpr int off_bar = off_raw + RAWS * RAW;
-    // barriers: raw full / empty, K and V full / empty, S full, P full, O done, Q full, drain
+    // barriers: raw full / empty, K and V full / empty, S full, P full (two halves), O done, Q full /
+    // empty, O free, the two streams' exchange, drain
     static constexpr int b_raw_full = 0, b_raw_empty = RAWS, b_k_full = 2 * RAWS, b_k_empty = b_k_full + 2,
                          b_v_full = b_k_full + 4, b_v_empty = b_k_full + 6, b_s_full = b_k_full + 8,
-                         b_p_full = b_k_full + 10, b_o_done = b_k_full + 12, b_q_full = b_k_full + 14,
-                         b_drain = b_k_full + 15, BARS = b_k_full + 16;
+                         b_p_full = b_k_full + 10, b_o_done = b_k_full + 14, b_q_full = b_k_full + 16,
+                         b_q_empty = b_k_full + 17, b_o_free = b_k_full + 18, b_pair = b_k_full + 19,
+                         b_drain = b_k_full + 20, BARS = b_k_full + 21;
     static constexpr int off_misc = off_bar + BARS * 8;  // TMEM address, dead flag
-    static constexpr int SMEM = off_misc + 16;
-    // tensor memory columns: S (and P over it) 2 x 128, O QT x D
+    static constexpr int off_ml = off_misc + 16;         // maxima and sums of the two streams
+    static constexpr int off_fac = off_ml + 2 * 128 * 8; // factors of the rows' scores, two items
+    static constexpr int SMEM = off_fac + 2 * ROWS * 4;
+    // tensor memory columns: S (and P over it) 2 x 128, O 2 x D
     static constexpr int t_o = 256;
 };
 
@@ -126,6 +138,21 @@ __device__ __forceinline__ void ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void ld16_async(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void hold16(float (&r)[16]) {
+    asm volatile(""
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
+                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void hold(uint32_t (&r)[32]) {
     asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
           "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
@@ -150,6 +177,14 @@ __device__ __forceinline__ void st32b(uint32_t taddr, const uint32_t (&r)[32]) {
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
+        "tcgen05.wait::st.sync.aligned;\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -168,6 +203,32 @@ __device__ __forceinline__ void convert(uint2 w, uint32_t scale, uint32_t a0, ui
 __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
     const uint32_t f = scales_to_f16(byte);
     return __byte_perm(f, f, 0x1010);
+}
+
+// A query row goes in scaled by a power of two that brings its largest element
+// to [2^8, 2^9), as f16; its scores get the inverse and the softmax scale as a
+// factor.  The sign (and a zero) of the scale goes into the row, so that the
+// factor is positive and may follow the maximum.
+__device__ __forceinline__ uint32_t magnitude(const uint4 &w) {  // of eight bf16, which orders as an integer
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, max((u[j] << 16) & 0x7fffffffu, u[j] & 0x7fff0000u));
+    return top;
+}
+__device__ __forceinline__ int exponent(uint32_t top) { return min(max((int)(top >> 23), 9), 253); }
+__device__ __forceinline__ float scale_up(float base, int ex) {
+    return (base < 0.f ? -1.f : base == 0.f ? 0.f : 1.f) * __uint_as_float((uint32_t)(262 - ex) << 23);
+}
+__device__ __forceinline__ float factor(float base, int ex) {
+    return fmaxf(fabsf(base) * __uint_as_float((uint32_t)(ex - 8) << 23), 1e-37f);
+}
+__device__ __forceinline__ void store_query(uint32_t addr, const uint4 &w, float up) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = pack_f16(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xffff0000u) * up);
+    sts128(addr, f[0], f[1], f[2], f[3]);
 }
 
 template <int D, int QT>
@@ -193,11 +254,15 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
             umma::mbar_init(bar(C::b_v_full + i), C::DEQ / 2);
             umma::mbar_init(bar(C::b_v_empty + i), 1);
             umma::mbar_init(bar(C::b_s_full + i), 1);
-            umma::mbar_init(bar(C::b_p_full + i), 128);
+            umma::mbar_init(bar(C::b_p_full + 2 * i), 128);
+            umma::mbar_init(bar(C::b_p_full + 2 * i + 1), 128);
             umma::mbar_init(bar(C::b_o_done + i), 1);
         }
-        umma::mbar_init(bar(C::b_q_full), C::ROWS);
+        umma::mbar_init(bar(C::b_q_full), QT == 2 ? 256 : 64);
+        umma::mbar_init(bar(C::b_q_empty), 1);
+        umma::mbar_init(bar(C::b_o_free), 256);
         umma::mbar_init(bar(C::b_drain), 1);
+        umma::mbar_init(bar(C::b_pair), 256);
         misc[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -221,77 +286,63 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
 
     Item it;
     if (warp < C::SOFT) {
-        // ------------------------------------------------------------ softmax: a thread per row
-        const int t = warp >> 2, lane_base = (warp & 3) * 32;
-        const int my = t * 128 + lane_base + lane;
-        const uint32_t tq = tmem + ((uint32_t)lane_base << 16);
-        uint32_t n = 0;  // key tiles so far
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::R_SOFT));
+        // ------------------------------------------------------------ softmax: a thread per row and stream
+        const int t = warp >> 2, lane_base = (warp & 3) * 32, r = lane_base + lane;
+        const int my = (QT == 2 ? t * 128 : 0) + r;
+        const uint32_t tq = tmem + ((uint32_t)lane_base << 16), ts = tq + t * 128, to = tq + C::t_o + t * D;
+        uint32_t n = 0, mine = 0, items = 0;  // key tiles so far, those of this stream, items with key tiles
         int4 job = make_int4(-1, 0, 0, 0);
         auto work = [&]() {
             while (walk.next(a, it)) {
                 const Req &q = walk.q;
                 const int rr = it.row0 + my;
-                const bool valid = rr < q.rows;
+                const bool valid = rr < q.rows, idle = it.row0 + my - lane >= q.rows;
                 const int tok = min(rr, q.rows - 1) / G, x = valid ? rr % G : 0;
                 const size_t head = (size_t)(q.q0 + tok) * a.Hq + it.h * G + x;
+                const bool some = it.last > it.first;
                 float m = -INFINITY, l = 0.f, fac = 1.f;
-                if (it.last > it.first) {
-                    // the query row, scaled by a power of two to [2^8, 2^9) at its largest, as f16
+                const float base = a.scale * kLog2e * (a.k_scale ? a.k_scale[it.h] : 1.f);
+                if (QT == 2 && some) {
+                    // this thread's query row (its warps' last products have read the row before)
                     const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                                                      (size_t)(q.q0 + tok) * a.q_stride +
                                                                      (size_t)(it.h * G + x) * D);
-                    uint32_t top = 0;  // magnitudes, which order as integers
-#pragma unroll 4
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 w = __ldg(p + i);
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint4 w[D / 8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) top = max(top, max((u[j] << 16) & 0x7fffffffu, u[j] & 0x7fff0000u));
-                    }
-                    if (!valid) top = 0;
-                    const int ex = min(max((int)(top >> 23), 9), 253);
-                    const float base = a.scale * kLog2e * (a.k_scale ? a.k_scale[it.h] : 1.f);
-                    // the sign (and a zero) of the scale goes into the query: the factor stays positive
-                    const float up = (base < 0.f ? -1.f : base == 0.f || !valid ? 0.f : 1.f) *
-                                     __uint_as_float((uint32_t)(262 - ex) << 23);
-                    fac = fmaxf(fabsf(base) * __uint_as_float((uint32_t)(ex - 8) << 23), 1e-37f);
-                    const uint32_t row = sb + C::off_q + t * C::OPERAND;
-                    const int r = lane_base + lane;
-#pragma unroll 4
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 w = __ldg(p + i);
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t f[4];
+                    for (int i = 0; i < D / 8; ++i) w[i] = __ldg(p + i);
+                    uint32_t top = 0;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            f[j] = pack_f16(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xffff0000u) * up);
-                        sts128(row + umma::kmaj(r, i * 8, 128), f[0], f[1], f[2], f[3]);
-                    }
+                    for (int i = 0; i < D / 8; ++i) top = max(top, magnitude(w[i]));
+                    const int ex = exponent(top);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i)
+                        store_query(sb + C::off_q + t * C::OPERAND + umma::kmaj(r, i * 8, 128), w[i],
+                                    valid ? scale_up(base, ex) : 0.f);
+                    fac = factor(base, ex);
                     umma::fence_proxy_async();
                     arrive(bar(C::b_q_full));
                 }
                 // positions this row sees (a padding row sees what the last row does), and what the whole warp sees
                 const int sees = q.len - q.n + tok;
                 const int see_lo = __reduce_min_sync(0xffffffffu, sees), see_hi = __reduce_max_sync(0xffffffffu, sees);
-                const uint32_t to = tq + C::t_o + t * D;
+                bool begun = false;
+#pragma unroll 1
                 for (int tile = it.first; tile < it.last; ++tile, ++n) {
-                    const int b = QT == 2 ? t : (int)(n & 1);
-                    const uint32_t parity = QT == 2 ? n : n >> 1;
-                    const uint32_t ts = tq + b * 128;
-                    if (!wait(C::b_s_full + b, parity)) return;
+                    if (QT == 1 && (int)(n & 1) != t) continue;
+                    if (!wait(C::b_s_full + t, mine++)) return;
                     umma::fence_after();
-                    if (it.row0 + t * 128 + lane_base >= q.rows) {
+                    if (idle) {
                         // no row of this warp is there: its weights may be anything (rows do not mix)
                         umma::fence_before();
-                        arrive(bar(C::b_p_full + b));
+                        arrive(bar(C::b_p_full + 2 * t));
+                        arrive(bar(C::b_p_full + 2 * t + 1));
                         continue;
                     }
                     const int key0 = tile * kTile;
-                    const bool edge = key0 + kTile > see_lo + 1 || (a.window > 0 && key0 <= see_hi - a.window);
-                    const int hi = sees - key0;                                             // last visible column
-                    const int lo = a.window > 0 ? sees - a.window - key0 : -1;              // last hidden one before
-                    if (edge) {
+                    if (key0 + kTile > see_lo + 1 || (a.window > 0 && key0 <= see_hi - a.window)) {
                         // hidden columns become -inf where they are; few tiles have any
+                        const int hi = sees - key0, lo = a.window > 0 ? hi - a.window : -1;
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t s[32];
@@ -305,10 +356,10 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         }
                         wait_st();
                     }
+                    uint32_t s[2][32];
                     float top = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
-                        uint32_t s[2][32];
                         load64(ts + c * 64, s);
                         float tops[4] = {top, top, top, top};
 #pragma unroll
@@ -317,60 +368,83 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                                                                            __uint_as_float(s[i / 32][i % 32 + 1])));
                         top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     }
+                    // (the scores that have arrived came after the queries and their factors)
+                    if (QT == 1 && !begun) fac = reinterpret_cast<volatile float *>(smem + C::off_fac)[(items & 1) * C::ROWS + my];
                     top *= fac;
-                    if (tile == it.first) {
+                    if (!begun) {
                         m = top;
+                        begun = true;
                     } else {
+                        // (this stream's last product onto O came before the scores that have arrived)
                         const bool rise = top > m + kSlack || (m == -INFINITY && top > m);
                         if (__any_sync(0xffffffffu, rise)) {
-                            // with one row tile the last product onto O may still run
-                            if (QT == 1) {
-                                if (!wait(C::b_o_done, n - 1)) return;
-                                umma::fence_after();
-                            }
                             const float f = rise ? exp2_fast(m - top) : 1.f;
                             l *= f;
                             if (rise) m = top;
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                float o[32];
-                                umma::ld32(to + c * 32, o);
+                            for (int c = 0; c < D / 16; ++c) {
+                                float o[16];
+                                umma::ld16(to + c * 16, o);
+                                uint32_t u[16];
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= f;
-                                umma::st32(to + c * 32, o);
+                                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * f);
+                                st16(to + c * 16, u);
                             }
                         }
                     }
                     const float off = kLift - (m == -INFINITY ? 0.f : m);
                     const float2 fac2 = make_float2(fac, fac), off2 = make_float2(off, off);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    // the weights take the place of columns of S that have been read
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t s[2][32], p[32];
-                        load64(ts + c * 64, s);
+                    // the weights take the place of columns of S that have been read; the products may start on
+                    // the first half
+                    auto half = [&](int c, const uint32_t(&s0)[32], const uint32_t(&s1)[32]) {
+                        uint32_t p[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[i / 16][i % 16 * 2]),
-                                                                    __uint_as_float(s[i / 16][i % 16 * 2 + 1])),
-                                                        fac2, off2);
-                            const float2 e = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                            const uint32_t(&v)[32] = i < 16 ? s0 : s1;
+                            const float2 y = __ffma2_rn(
+                                make_float2(__uint_as_float(v[i % 16 * 2]), __uint_as_float(v[i % 16 * 2 + 1])), fac2, off2);
+                            const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
                             sum[i & 1] = __fadd2_rn(sum[i & 1], e);
                             p[i] = pack_f16(e.x, e.y);
                         }
                         st32b(ts + c * 32, p);
+                        wait_st();
+                        umma::fence_before();
+                        arrive(bar(C::b_p_full + 2 * t + c));
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        load64(ts + c * 64, s);
+                        half(c, s[0], s[1]);
                     }
                     sum[0] = __fadd2_rn(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
-                    wait_st();
-                    umma::fence_before();
-                    arrive(bar(C::b_p_full + b));
                 }
-                if (it.last > it.first) {
-                    if (!wait(C::b_o_done + (QT == 2 ? t : 0), n - 1)) return;
+                if (some) {
+                    if (mine > 0 && !wait(C::b_o_done + t, mine - 1)) return;
                     umma::fence_after();
                 }
-                const bool none = it.last == it.first || (m == -INFINITY && l == 0.f);
+                // with one row tile the streams' results are joined: each takes half the channels
+                float fo[2] = {1.f, 1.f};
+                if (QT == 1 && some) {
+                    volatile float2 *ml = reinterpret_cast<volatile float2 *>(smem + C::off_ml);
+                    ml[t * 128 + r].x = begun ? m : -INFINITY;
+                    ml[t * 128 + r].y = l;
+                    umma::fence_before();
+                    arrive(bar(C::b_pair));
+                    if (!wait(C::b_pair, items)) return;
+                    umma::fence_after();
+                    const float m0 = ml[r].x, m1 = ml[128 + r].x, l0 = ml[r].y, l1 = ml[128 + r].y;
+                    // (both have read before either writes again: the next item's Q is complete only after both)
+                    m = fmaxf(m0, m1);
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    fo[0] = exp2_fast(m0 - ref), fo[1] = exp2_fast(m1 - ref);
+                    l = fo[0] * l0 + fo[1] * l1;
+                    // a stream without a tile has no sum in tensor memory
+                    if (it.last - it.first == 1) fo[((n - 1) & 1) ^ 1] = -1.f;
+                }
+                const bool none = !some || (m == -INFINITY && l == 0.f);
                 const bool whole = it.whole();
                 const float f = none ? 0.f : whole ? (a.v_scale ? a.v_scale[it.h] : 1.f) / l : 1.f;
                 float *part = a.parts + ((size_t)me * 2 + (it.starts ? 1 : 0)) * ((size_t)C::ROWS * (D + 2));
@@ -382,15 +456,31 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                 char *dst = whole ? reinterpret_cast<char *>(static_cast<__nv_bfloat16 *>(a.o) + head * D)
                                   : reinterpret_cast<char *>(part + 2 * C::ROWS + (size_t)my * D);
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
-                    if (it.last > it.first) umma::ld32(to + c * 32, o);
+                for (int c = QT == 2 ? 0 : t * (D / 32); c < (QT == 2 ? D / 16 : (t + 1) * (D / 32)); ++c) {
+                    float o[16];
+                    if (QT == 2) {
+                        if (some) umma::ld16(to + c * 16, o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * f;
+                        for (int i = 0; i < 16; ++i) o[i] = none ? 0.f : o[i] * f;
+                    } else {
+                        float y[16];
+                        if (some) {
+                            ld16_async(tq + C::t_o + c * 16, o);
+                            ld16_async(tq + C::t_o + D + c * 16, y);
+                            umma::wait_ld();
+                            hold16(o);
+                            hold16(y);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float y0 = fo[0] == -1.f ? 0.f : o[i] * fo[0], y1 = fo[1] == -1.f ? 0.f : y[i] * fo[1];
+                            o[i] = none ? 0.f : (y0 + y1) * f;
+                        }
+                    }
                     if (valid && whole) {
-                        uint4 *p = reinterpret_cast<uint4 *>(dst) + c * 4;
+                        uint4 *p = reinterpret_cast<uint4 *>(dst) + c * 2;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             uint32_t u[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -400,19 +490,25 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                             p[i] = make_uint4(u[0], u[1], u[2], u[3]);
                         }
                     } else if (valid) {
-                        float4 *p = reinterpret_cast<float4 *>(dst) + c * 8;
+                        float4 *p = reinterpret_cast<float4 *>(dst) + c * 4;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) p[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 4; ++i) p[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
                 if (it.starts && !whole) job = make_int4(it.r, it.h, it.rt, walk.last_worker());
-                // the reads of O come before the next row tile's products (released by its first weights)
+                // the reads of O come before the next item's products: those of a row tile of two follow the
+                // weights of its own warps, those of two streams wait until both streams have read
                 umma::fence_before();
+                if (some) {
+                    if (QT == 1) arrive(bar(C::b_o_free));
+                    ++items;
+                }
             }
         };
         work();
         if (tid == 0) a.jobs[me] = misc[1] ? make_int4(-1, 0, 0, 0) : job;
     } else if (warp < C::SOFT + C::DEQ) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::R_DEQ));
         // ------------------------------------------------------------ dequant
         const int d = tid - C::SOFT * 32;
         constexpr int NK = D / 64, NG = D / 16, BATCH = 4;
@@ -504,7 +600,9 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
             }
         };
         work();
-    } else if (warp == C::SOFT + C::DEQ) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::R_MISC));
+    if (warp == C::SOFT + C::DEQ) {
         // ------------------------------------------------------------ producer
         uint32_t raws = 0;
         const int chunk = a.page_shift < 6 ? 1 << (a.page_shift - 4) : 4;  // blocks per copy
@@ -545,7 +643,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
             for (uint32_t i = raws > C::RAWS ? raws - C::RAWS : 0; i < raws; ++i)
                 umma::mbar_wait(bar(C::b_raw_full + i % C::RAWS), (i / C::RAWS) & 1, kWaitLimit);
         }
-    } else {
+    } else if (warp == C::SOFT + C::DEQ + 1) {
         // ------------------------------------------------------------ products
         constexpr uint32_t id_s = idesc_f16(128, 128, 0), id_o = idesc_f16(128, D, 1);
         const uint32_t lead = elect();
@@ -560,13 +658,19 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
             }
             commit(bar(C::b_s_full + b), lead);
         };
-        auto values = [&](int t, uint32_t tile, int b, bool acc) {
+        auto values = [&](int t, uint32_t tile, bool acc, uint32_t parity) {
             const uint32_t v4 = sb4 + ((C::off_v + (tile & 1) * C::OPERAND) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_ts(tm + C::t_o + t * D, tm + b * 128 + ks * 8, umma::sdesc4(v4 + ((ks * 16 * D * 2) >> 4), 1024, 16 * D),
+            for (int ks = 0; ks < 8; ++ks) {
+                if (ks % 4 == 0) {
+                    if (!wait(C::b_p_full + 2 * t + ks / 4, parity)) return false;
+                    umma::fence_after();
+                }
+                mma_ts(tm + C::t_o + t * D, tm + t * 128 + ks * 8, umma::sdesc4(v4 + ((ks * 16 * D * 2) >> 4), 1024, 16 * D),
                        id_o, acc || ks > 0, lead);
+            }
             commit(bar(C::b_o_done + t), lead);
+            return true;
         };
         auto work = [&]() {
             while (walk.next(a, it)) {
@@ -578,6 +682,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
 #pragma unroll
                 for (int t = 0; t < QT; ++t) scores(t, n, QT == 2 ? t : n & 1);
                 commit(bar(C::b_k_empty + (n & 1)), lead);
+                if (tiles == 1) commit(bar(C::b_q_empty), lead);
 #pragma unroll 1
                 for (int j = 0; j < tiles; ++j, ++n) {
                     if (QT == 1 && j + 1 < tiles) {
@@ -585,22 +690,28 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         umma::fence_after();
                         scores(0, n + 1, (n + 1) & 1);
                         commit(bar(C::b_k_empty + ((n + 1) & 1)), lead);
+                        if (j + 2 == tiles) commit(bar(C::b_q_empty), lead);
                     }
+                    if (QT == 1 && j == 0 && !wait(C::b_o_free, items)) return;
                     if (!wait(C::b_v_full + (n & 1), n >> 1)) return;
+                    if (QT == 1) {
+                        if (!values(n & 1, n, j > 1, n >> 1)) return;
+                    } else {
 #pragma unroll
-                    for (int t = 0; t < QT; ++t) {
-                        const int b = QT == 2 ? t : n & 1;
-                        if (!wait(C::b_p_full + b, QT == 2 ? n : n >> 1)) return;
-                        umma::fence_after();
-                        values(t, n, b, j > 0);
-                        if (QT == 2 && j + 1 < tiles) {
-                            if (t == 0 && !wait(C::b_k_full + ((n + 1) & 1), (n + 1) >> 1)) return;
-                            umma::fence_after();
-                            scores(t, n + 1, t);
+                        for (int t = 0; t < QT; ++t) {
+                            if (!values(t, n, j > 0, n)) return;
+                            if (j + 1 < tiles) {
+                                if (t == 0 && !wait(C::b_k_full + ((n + 1) & 1), (n + 1) >> 1)) return;
+                                umma::fence_after();
+                                scores(t, n + 1, t);
+                            }
                         }
                     }
                     commit(bar(C::b_v_empty + (n & 1)), lead);
-                    if (QT == 2 && j + 1 < tiles) commit(bar(C::b_k_empty + ((n + 1) & 1)), lead);
+                    if (QT == 2 && j + 1 < tiles) {
+                        commit(bar(C::b_k_empty + ((n + 1) & 1)), lead);
+                        if (j + 2 == tiles) commit(bar(C::b_q_empty), lead);
+                    }
                 }
             }
         };
@@ -608,6 +719,49 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         // products in flight end before the CTA leaves
         commit(bar(C::b_drain), lead);
         wait1(C::b_drain, 0);
+    } else if (QT == 1) {
+        // ------------------------------------------------------------ queries: D / 8 lanes per row, ahead of the item
+        constexpr int LANES = D / 8, STEP = 64 / LANES, BATCH = 8;
+        const int e = tid - (C::SOFT + C::DEQ + 2) * 32, chunk = e % LANES, sub = e / LANES;
+        uint32_t items = 0;
+        auto work = [&]() {
+            while (walk.next(a, it)) {
+                if (it.last == it.first) continue;
+                const Req &q = walk.q;
+                const float base = a.scale * kLog2e * (a.k_scale ? a.k_scale[it.h] : 1.f);
+                volatile float *facs = reinterpret_cast<volatile float *>(smem + C::off_fac) + (items & 1) * C::ROWS;
+#pragma unroll 1
+                for (int r0 = 0; r0 < C::ROWS; r0 += BATCH * STEP) {
+                    uint4 w[BATCH];
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) {
+                        const int rr = it.row0 + r0 + j * STEP + sub;
+                        w[j] = make_uint4(0, 0, 0, 0);
+                        if (rr < q.rows)
+                            w[j] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                                         (size_t)(q.q0 + rr / G) * a.q_stride +
+                                                                         (size_t)(it.h * G + rr % G) * D) + chunk);
+                    }
+                    // the last item's products have read Q
+                    if (r0 == 0 && !wait(C::b_q_empty, items + 1)) return;
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) {
+                        const int row = r0 + j * STEP + sub;
+                        uint32_t top = magnitude(w[j]);
+#pragma unroll
+                        for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int ex = exponent(top);
+                        store_query(sb + C::off_q + umma::kmaj(row, chunk * 8, 128), w[j], scale_up(base, ex));
+                        if (chunk == 0) facs[row] = factor(base, ex);
+                    }
+                }
+                umma::fence_proxy_async();
+                arrive(bar(C::b_q_full));
+                ++items;
+            }
+        };
+        work();
+    }
     }
     umma::fence_before();
     __syncthreads();
