@@ -609,21 +609,31 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         auto work = [&]() {
             while (walk.next(a, it)) {
                 const int32_t *table = a.block_table + (size_t)it.r * a.max_pages;
+                const int pages = (walk.q.len + (1 << a.page_shift) - 1) >> a.page_shift;
+                int from = 0, entry = 0, held = 0;  // 32 table entries, one per lane, from page `from` on
+#pragma unroll 1
                 for (int tile = it.first; tile < it.last; ++tile)
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half, ++raws) {
                         const uint32_t ri = raws % C::RAWS;
-                        const int key = tile * kTile + half * 64 + lane * chunk * 16;
+                        const int key0 = tile * kTile + half * 64, key = key0 + lane * chunk * 16;
                         // blocks of this lane's copy that hold keys
                         const int left = (walk.q.len - key + 15) >> 4;
                         const int mine = lane * chunk < 4 ? min(max(left, 0), chunk) : 0;
-                        int page = 0;
-                        if (mine > 0) {
-                            page = __ldg(table + (key >> a.page_shift));
-                            if (page < 0 || page >= a.num_pages) {
-                                page = 0;
-                                if (a.status) atomicOr(a.status, KDA_STATUS_BAD_PAGE);
+                        const int page0 = key0 >> a.page_shift;
+                        if (page0 + 3 >= from + held) {
+                            from = page0, held = 32;
+                            entry = 0;
+                            if (from + lane < pages) {
+                                entry = __ldg(table + from + lane);
+                                if (entry < 0 || entry >= a.num_pages) {
+                                    entry = 0;  // the read stays in the pool
+                                    if (a.status) atomicOr(a.status, KDA_STATUS_BAD_PAGE);
+                                }
                             }
+                            __syncwarp();
                         }
+                        const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - from) & 31);
                         const int all = __reduce_add_sync(0xffffffffu, mine);
                         if (!wait(C::b_raw_empty + ri, raws / C::RAWS + 1)) return;
                         if (lane == 0) umma::mbar_expect_tx(bar(C::b_raw_full + ri), all * BB);
