@@ -48,6 +48,8 @@ def library_path() -> str:
 def load_library():
     """Load libkda.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -135,7 +137,7 @@ def _ptr(t):
         raise KDAError("KDA calls take CUDA tensors")
     if not t.is_contiguous():
         raise KDAError("KDA calls take contiguous tensors")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _hptr(t):
@@ -150,8 +152,9 @@ def _hptr(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _on(stream):
@@ -177,7 +180,7 @@ def _expect(t, name, dtype, shape):
         return
     if t.dtype != dtype:
         raise KDAError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise KDAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -578,26 +581,24 @@ def page_plan(context_len, new_len, page_count, block_table, free_pages, free_co
     _expect(new_len, "new_len", i32, (R,))
     _expect(page_count, "page_count", i32, (R,))
     _expect(block_table, "block_table", i32, (R, B))
-    _expect(free_pages, "free_pages", i32, free_pages.shape)
+    if free_pages.dtype != i32:
+        raise KDAError(f"free_pages must be {i32}, got {free_pages.dtype}")
     _expect(free_count, "free_count", i32, (1,))
     T = int(tokens)
     if T < 0:
         raise KDAError("tokens must not be negative")
     with _on(stream):
         lib = load_library()
-        # one allocation, each part on its own 16-byte boundary
-        up = lambda n: (n + 3) & ~3
-        sizes = (R + 1, R, T, T, R, 1)
-        buf = torch.empty(sum(up(n) for n in sizes), dtype=i32, device=block_table.device)
-        out, at = [], 0
-        for n in sizes:
-            out.append(buf[at:at + n])
-            at += up(n)
+        dev = block_table.device
+        cu, seq = torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev)
+        slots, pos = torch.empty(T, dtype=i32, device=dev), torch.empty(T, dtype=i32, device=dev)
+        count, free = torch.empty(R, dtype=i32, device=dev), torch.empty(1, dtype=i32, device=dev)
         rc = lib.kda_page_plan(_ptr(context_len), _ptr(new_len), _ptr(page_count), _ptr(block_table), _ptr(free_pages),
-                               _ptr(free_count), R, B, free_pages.shape[0], int(page_size), T,
-                               *[t.data_ptr() for t in out], _ptr(status), _stream(stream))
+                               _ptr(free_count), R, B, free_pages.shape[0], int(page_size), T, cu.data_ptr(),
+                               seq.data_ptr(), slots.data_ptr(), pos.data_ptr(), count.data_ptr(), free.data_ptr(),
+                               _ptr(status), _stream(stream))
         _check(rc, "kda_page_plan")
-        return tuple(out)
+        return cu, seq, slots, pos, count, free
 
 
 def cache4_append(k, v, slot_map, cache, page_size, k_scale=None, v_scale=None, status=None, stream=None):
@@ -630,7 +631,8 @@ def cache4_read(cache, slots, page_size, d, dtype=torch.bfloat16, k_scale=None, 
     _expect(slots, "slots", torch.int32, (n,))
     _check_scales(k_scale, v_scale, Hkv)
     with _on(stream):
-        k, v = torch.empty((2, n, Hkv, d), dtype=dtype, device=cache.device).unbind(0)
+        k = torch.empty((n, Hkv, d), dtype=dtype, device=cache.device)
+        v = torch.empty((n, Hkv, d), dtype=dtype, device=cache.device)
         rc = load_library().kda_cache4_read(_ptr(cache), _ptr(slots), n, Hkv, d, P, int(page_size), _ptr(k_scale),
                                             _ptr(v_scale), _in_dtype(k), k.data_ptr(), v.data_ptr(), _ptr(status),
                                             _stream(stream))
@@ -675,12 +677,12 @@ def cache4_attention(q, cache, block_table, seq_len, cu_seqlens, page_size, scal
         if lse is None and return_lse:
             lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
         need = lib.kda_cache4_attention_workspace_size(R, T, Hq, Hkv, d, dt)
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
+        if workspace is None or workspace.nbytes < need:
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
         rc = lib.kda_cache4_attention(qp, _ptr(cache), _ptr(block_table), _ptr(seq_len), _ptr(cu_seqlens), R, T, Hq, Hkv,
                                       d, P, int(page_size), B, int(max_new), int(window),
                                       float(d ** -0.5 if scale is None else scale), qs, _ptr(k_scale), _ptr(v_scale),
-                                      _ptr(out), _ptr(lse), dt, _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+                                      _ptr(out), _ptr(lse), dt, _ptr(workspace), workspace.nbytes, _ptr(status),
+                                      _stream(stream))
         _check(rc, "kda_cache4_attention")
         return (out, lse) if return_lse else out

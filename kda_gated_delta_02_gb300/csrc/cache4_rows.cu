@@ -21,103 +21,121 @@ namespace {
 
 using namespace cache4;
 
+// 16 channels as loaded: eight words of bf16 pairs, or sixteen floats
 template <bool BF16>
-__device__ __forceinline__ void load16(const void *base, size_t elem, float (&x)[16]) {
-    if constexpr (BF16) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + elem);
+struct Group {
+    uint32_t w[BF16 ? 8 : 16];
+    __device__ __forceinline__ void load(const void *base, size_t elem) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + elem * (BF16 ? 2 : 4));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint4 w = __ldg(p + h);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[h * 8 + 2 * j] = __uint_as_float(u[j] << 16);
-                x[h * 8 + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-            }
-        }
-    } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + elem);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const float4 w = __ldg(p + h);
-            x[4 * h] = w.x, x[4 * h + 1] = w.y, x[4 * h + 2] = w.z, x[4 * h + 3] = w.w;
+        for (int i = 0; i < (BF16 ? 2 : 4); ++i) {
+            const uint4 x = __ldg(p + i);
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
         }
     }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store16(void *base, size_t elem, const float (&x)[16]) {
-    if constexpr (BF16) {
-        uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + elem);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t u[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x[h * 8 + 2 * j], x[h * 8 + 2 * j + 1]);
-                u[j] = *reinterpret_cast<const uint32_t *>(&v);
-            }
-            p[h] = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-    } else {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + elem);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) p[h] = make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
+    // channels 2 i and 2 i + 1
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (BF16) return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        else return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     }
+};
+
+// eight codes of four pairs, the first pair in the low byte
+__device__ __forceinline__ uint32_t to_codes(const float2 (&y)[4]) {
+    uint32_t r;
+    asm("{\n.reg .b8 a, b, c, d;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\ncvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\ncvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        "mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(r)
+        : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x), "f"(y[3].y));
+    return r;
 }
 
-// codes and scale byte of a group; returns whether it is finite
-__device__ __forceinline__ bool quantise(float (&x)[16], float head_scale, uint2 &codes, uint32_t &scale) {
-    float top = 0.f;
-    bool finite = true;
+// Codes and scale byte of a group; returns whether it is finite.
+//
+// The quotients decide ties, so they have to be exact where the true quotient
+// is a midpoint of the codes.  bf16 channels without a head scale: x has 8
+// significant bits, s has 4 and a midpoint m has 3, so x / s is m itself or at
+// least 2^-8 m >= 2^-10 away from it.  x * (1 / s), off by 2^-22 of its value
+// at most, is therefore brought to the nearest multiple of 2^-12 (adding and
+// taking away 3 * 2^10, whose unit that is): midpoints become exact and no
+// quotient changes sides.  This took the 12 instructions of a division per
+// channel down to two for a pair.  Other inputs are divided.
+template <bool BF16, bool SCALED>
+__device__ __forceinline__ bool quantise(const Group<BF16> &g, float head_scale, uint2 &codes, uint32_t &scale) {
+    float top;
+    bool finite;
+    float2 x[8];
+    if constexpr (BF16 && !SCALED) {
+        uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if (head_scale != 1.f) x[i] = x[i] / head_scale;
-        finite = finite && fabsf(x[i]) <= 3.402823466e38f;
-        top = fmaxf(top, fabsf(x[i]));
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, g.w[i] & 0x7fff7fffu);
+        m = max(m & 0xffffu, m >> 16);
+        finite = m < 0x7f80u;
+        top = __uint_as_float(m << 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = g.pair(i);
+    } else {
+        top = 0.f;
+        finite = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = g.pair(i);
+            if constexpr (SCALED) x[i].x = x[i].x / head_scale, x[i].y = x[i].y / head_scale;
+            finite = finite && fabsf(x[i].x) <= 3.402823466e38f && fabsf(x[i].y) <= 3.402823466e38f;
+            top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        }
     }
     unsigned short b;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(b) : "f"(0.f), "f"(top / 6.f));
     scale = b & 0xffu;
     const float s = e4m3_to_float(scale);
-    uint32_t w[2] = {0, 0};
+    codes = make_uint2(0, 0);
     if (s > 0.f) {
+        float2 y[2][4];
+        if constexpr (BF16 && !SCALED) {
+            const float r = 1.f / s;
+            const float2 r2 = make_float2(r, r), unit = make_float2(3072.f, 3072.f), back = make_float2(-3072.f, -3072.f);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            unsigned short c;
-            asm("{\n.reg .b8 z;\ncvt.rn.satfinite.e2m1x2.f32 z, %1, %2;\ncvt.u16.u8 %0, z;\n}\n"
-                : "=h"(c)
-                : "f"(x[i + 1] / s), "f"(x[i] / s));
-            w[i >> 3] |= (uint32_t)c << ((i & 7) * 4);
+            for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = __fadd2_rn(__ffma2_rn(x[i], r2, unit), back);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = make_float2(x[i].x / s, x[i].y / s);
         }
+        codes = make_uint2(to_codes(y[0]), to_codes(y[1]));
     }
-    codes = make_uint2(w[0], w[1]);
     return finite;
 }
 
-template <int D, bool BF16>
+// the block of a slot and head
+template <int D>
+__device__ __forceinline__ uint8_t *block_of(const Cache4RowsArgs &a, int slot, int h) {
+    const int page = slot >> a.page_shift, blk = (slot & ((1 << a.page_shift) - 1)) >> 4;
+    return a.cache + ((((size_t)page * a.Hkv + h) << (a.page_shift - 4)) + blk) * block_bytes(D);
+}
+
+template <int D, bool BF16, bool SCALED>
 __global__ void __launch_bounds__(256)
 cache4_append_kernel(Cache4RowsArgs a) {
     constexpr int GROUPS = D / 16;  // lanes of a token and head: 8 or 4 neighbours in a warp
-    const long long items = (long long)a.T * a.Hkv * GROUPS;
-    const long long item = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const bool live = item < items;
-    const int grp = (int)(item % GROUPS);
-    const long long th = live ? item / GROUPS : 0;
-    const int h = (int)(th % a.Hkv), t = (int)(th / a.Hkv);
-    const int slot = live ? a.slots[t] : -1;
+    const uint32_t th = blockIdx.x * (256 / GROUPS) + threadIdx.x / GROUPS;  // below 2^32 (checked at the launch)
+    const int grp = threadIdx.x % GROUPS;
+    const uint32_t t = th / (uint32_t)a.Hkv, h = th - t * (uint32_t)a.Hkv;
+    const bool live = t < (uint32_t)a.T;
+    const int slot = live ? __ldg(a.slots + t) : -1;
     const bool in_range = slot < a.num_slots;
     if (live && !in_range && a.status) atomicOr(a.status, KDA_STATUS_BAD_PAGE);
-    const bool write = live && slot >= 0 && in_range;
+    const bool write = slot >= 0 && in_range;
     uint2 kc = make_uint2(0, 0), vc = make_uint2(0, 0);
     uint32_t ks = 0, vs = 0;
     bool finite = true;
     if (write) {
-        float x[16];
-        load16<BF16>(a.k, (size_t)t * a.k_stride + (size_t)h * D + grp * 16, x);
-        finite = quantise(x, a.k_scale ? a.k_scale[h] : 1.f, kc, ks);
-        load16<BF16>(a.v, (size_t)t * a.v_stride + (size_t)h * D + grp * 16, x);
-        finite = quantise(x, a.v_scale ? a.v_scale[h] : 1.f, vc, vs) && finite;
+        Group<BF16> k, v;
+        k.load(a.k, (size_t)t * a.k_stride + h * D + grp * 16);
+        v.load(a.v, (size_t)t * a.v_stride + h * D + grp * 16);
+        finite = quantise<BF16, SCALED>(k, SCALED && a.k_scale ? a.k_scale[h] : 1.f, kc, ks);
+        finite = quantise<BF16, SCALED>(v, SCALED && a.v_scale ? a.v_scale[h] : 1.f, vc, vs) && finite;
     }
 #pragma unroll
     for (int o = 1; o < GROUPS; o <<= 1) finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) && finite;
@@ -128,26 +146,43 @@ cache4_append_kernel(Cache4RowsArgs a) {
         vs = 0;
         if (grp == 0 && a.status) atomicOr(a.status, KDA_STATUS_NOT_FINITE);
     }
-    const int page = slot >> a.page_shift, in_page = slot & ((1 << a.page_shift) - 1);
-    const int blk = in_page >> 4, tok = in_page & 15;
-    uint8_t *b = a.cache + (((size_t)page * a.Hkv + h) * ((size_t)1 << (a.page_shift - 4)) + blk) * block_bytes(D);
+    const int tok = slot & 15;
+    uint8_t *b = block_of<D>(a, slot, h);
     *reinterpret_cast<uint2 *>(b + tok * (D / 2) + grp * 8) = kc;
     b[off_ks(D) + tok * GROUPS + grp] = (uint8_t)ks;
     *reinterpret_cast<uint2 *>(b + off_vc(D) + grp * 128 + tok * 8) = vc;
     b[off_vs(D) + grp * 16 + tok] = (uint8_t)vs;
 }
 
-__device__ __forceinline__ void values(uint2 codes, float s, float head_scale, float (&x)[16]) {
-    const uint32_t w[2] = {codes.x, codes.y};
+// 16 channels that codes and a scale byte stand for, stored as bf16 or f32
+template <bool BF16>
+__device__ __forceinline__ void store_values(void *base, size_t elem, uint2 codes, uint32_t scale, float head_scale) {
+    const uint32_t f = scales_to_f16(scale), s = __byte_perm(f, f, 0x1010);
+    uint32_t x[2][4];
+    codes_to_f16(codes.x, x[0]);
+    codes_to_f16(codes.y, x[1]);
+    uint4 *p = reinterpret_cast<uint4 *>(static_cast<char *>(base) + elem * (BF16 ? 2 : 4));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        uint32_t f[4];
-        codes_to_f16(w[h], f);
+        float2 y[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 v = unpack_f16(f[j]);
-            x[h * 8 + 2 * j] = v.x * s * head_scale;
-            x[h * 8 + 2 * j + 1] = v.y * s * head_scale;
+            y[j] = unpack_f16(mul_f16x2(x[h][j], s));
+            y[j].x *= head_scale, y[j].y *= head_scale;
+        }
+        if constexpr (BF16) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(y[j].x, y[j].y);
+                u[j] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+            p[h] = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                p[2 * h + j] = make_uint4(__float_as_uint(y[2 * j].x), __float_as_uint(y[2 * j].y),
+                                          __float_as_uint(y[2 * j + 1].x), __float_as_uint(y[2 * j + 1].y));
         }
     }
 }
@@ -156,48 +191,43 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(256)
 cache4_read_kernel(Cache4RowsArgs a) {
     constexpr int GROUPS = D / 16;
-    const long long item = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (item >= (long long)a.T * a.Hkv * GROUPS) return;
-    const int grp = (int)(item % GROUPS);
-    const long long th = item / GROUPS;
-    const int h = (int)(th % a.Hkv), t = (int)(th / a.Hkv);
-    const int slot = a.slots[t];
+    const uint32_t th = blockIdx.x * (256 / GROUPS) + threadIdx.x / GROUPS;
+    const int grp = threadIdx.x % GROUPS;
+    const uint32_t t = th / (uint32_t)a.Hkv, h = th - t * (uint32_t)a.Hkv;
+    if (t >= (uint32_t)a.T) return;
+    const int slot = __ldg(a.slots + t);
     if (slot >= a.num_slots && a.status) atomicOr(a.status, KDA_STATUS_BAD_PAGE);
     uint2 kc = make_uint2(0, 0), vc = make_uint2(0, 0);
-    float ks = 0.f, vs = 0.f;
+    uint32_t ks = 0, vs = 0;
     if (slot >= 0 && slot < a.num_slots) {
-        const int page = slot >> a.page_shift, in_page = slot & ((1 << a.page_shift) - 1);
-        const int blk = in_page >> 4, tok = in_page & 15;
-        const uint8_t *b =
-            a.cache + (((size_t)page * a.Hkv + h) * ((size_t)1 << (a.page_shift - 4)) + blk) * block_bytes(D);
+        const int tok = slot & 15;
+        const uint8_t *b = block_of<D>(a, slot, h);
         kc = *reinterpret_cast<const uint2 *>(b + tok * (D / 2) + grp * 8);
         vc = *reinterpret_cast<const uint2 *>(b + off_vc(D) + grp * 128 + tok * 8);
-        ks = e4m3_to_float(b[off_ks(D) + tok * GROUPS + grp]);
-        vs = e4m3_to_float(b[off_vs(D) + grp * 16 + tok]);
-        if (ks != ks) vs = ks;  // a marked token's value is not known either
+        ks = b[off_ks(D) + tok * GROUPS + grp];
+        vs = b[off_vs(D) + grp * 16 + tok];
+        if ((ks & 0x7fu) == kScaleNaN) vs = ks;  // a marked token's value is not known either
     }
-    float x[16];
-    values(kc, ks, a.k_scale ? a.k_scale[h] : 1.f, x);
-    store16<BF16>(a.k_out, ((size_t)t * a.Hkv + h) * D + grp * 16, x);
-    values(vc, vs, a.v_scale ? a.v_scale[h] : 1.f, x);
-    store16<BF16>(a.v_out, ((size_t)t * a.Hkv + h) * D + grp * 16, x);
+    const size_t e = ((size_t)t * a.Hkv + h) * D + grp * 16;
+    store_values<BF16>(a.k_out, e, kc, ks, a.k_scale ? a.k_scale[h] : 1.f);
+    store_values<BF16>(a.v_out, e, vc, vs, a.v_scale ? a.v_scale[h] : 1.f);
+}
+
+template <bool READ, int D, bool BF16>
+cudaError_t launch(const Cache4RowsArgs &a, cudaStream_t st) {
+    const long long th = (long long)a.T * a.Hkv, per = 256 / (D / 16);
+    if (th + per > 0xffffffffLL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)((th + per - 1) / per);
+    if constexpr (READ) cache4_read_kernel<D, BF16><<<grid, 256, 0, st>>>(a);
+    else if (a.k_scale || a.v_scale) cache4_append_kernel<D, BF16, true><<<grid, 256, 0, st>>>(a);
+    else cache4_append_kernel<D, BF16, false><<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 template <bool READ>
 cudaError_t launch(const Cache4RowsArgs &a, int d, bool bf16, cudaStream_t st) {
-    const long long items = (long long)a.T * a.Hkv * (d / 16);
-    const long long grid = (items + 255) / 256;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const unsigned g = (unsigned)grid;
-#define KDA_ROWS(D, B)                                                     \
-    if (READ) cache4_read_kernel<D, B><<<g, 256, 0, st>>>(a);              \
-    else cache4_append_kernel<D, B><<<g, 256, 0, st>>>(a);
-    if (d == 128 && bf16) { KDA_ROWS(128, true) }
-    else if (d == 128) { KDA_ROWS(128, false) }
-    else if (bf16) { KDA_ROWS(64, true) }
-    else { KDA_ROWS(64, false) }
-#undef KDA_ROWS
-    return cudaGetLastError();
+    if (d == 128) return bf16 ? launch<READ, 128, true>(a, st) : launch<READ, 128, false>(a, st);
+    return bf16 ? launch<READ, 64, true>(a, st) : launch<READ, 64, false>(a, st);
 }
 
 }  // namespace
