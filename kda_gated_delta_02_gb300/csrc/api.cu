@@ -1220,6 +1220,8 @@ static int cache4_shape(int Hkv, int d, int num_pages, int page_size, int dtype,
     return KDA_OK;
 }
 
+static bool on32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 // rows of `width` elements, `stride` apart, each on a 16-byte boundary
 static int row_stride(long long stride, long long width, int dtype) {
     if (stride < width) return KDA_ERR_INVALID_ARG;
@@ -1237,8 +1239,10 @@ int kda_cache4_append(const void *k, const void *v, const int32_t *slot_map, voi
     if (int rc = row_stride(k_stride, (long long)Hkv * d, in_dtype)) return rc;
     if (int rc = row_stride(v_stride, (long long)Hkv * d, in_dtype)) return rc;
     if (T == 0) return KDA_OK;
+    const long long size = in_dtype == KDA_DTYPE_BF16 ? 2 : 4;
     kda::Cache4RowsArgs a{k, v, k_stride, v_stride, nullptr, nullptr, slot_map, static_cast<uint8_t *>(cache), k_scale,
-                          v_scale, T, Hkv, num_pages << shift, shift, status};
+                          v_scale, T, Hkv, num_pages << shift, shift,
+                          on32(k) && on32(v) && (k_stride * size) % 32 == 0 && (v_stride * size) % 32 == 0, status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(timed_launch(KDA_KERNEL_CACHE4_APPEND, st, [&] {
         return kda::launch_cache4_append(a, d, in_dtype == KDA_DTYPE_BF16, st);
@@ -1256,7 +1260,7 @@ int kda_cache4_read(const void *cache, const int32_t *slots, int n, int Hkv, int
     if (n == 0) return KDA_OK;
     kda::Cache4RowsArgs a{nullptr, nullptr, 0, 0, k, v, slots,
                           const_cast<uint8_t *>(static_cast<const uint8_t *>(cache)), k_scale, v_scale, n, Hkv,
-                          num_pages << shift, shift, status};
+                          num_pages << shift, shift, on32(k) && on32(v), status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(timed_launch(KDA_KERNEL_CACHE4_READ, st, [&] {
         return kda::launch_cache4_read(a, d, out_dtype == KDA_DTYPE_BF16, st);

@@ -21,17 +21,37 @@ namespace {
 
 using namespace cache4;
 
+// 32 bytes in one access where rows lie on 32-byte boundaries (a lane's share
+// of a bf16 row is then one whole sector), in two otherwise
+__device__ __forceinline__ void load32(const char *p, bool wide, uint32_t *w) {
+    if (wide) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store32(char *p, bool wide, const uint32_t *w) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // 16 channels as loaded: eight words of bf16 pairs, or sixteen floats
 template <bool BF16>
 struct Group {
     uint32_t w[BF16 ? 8 : 16];
-    __device__ __forceinline__ void load(const void *base, size_t elem) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + elem * (BF16 ? 2 : 4));
-#pragma unroll
-        for (int i = 0; i < (BF16 ? 2 : 4); ++i) {
-            const uint4 x = __ldg(p + i);
-            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-        }
+    __device__ __forceinline__ void load(const void *base, size_t elem, bool wide) {
+        const char *p = static_cast<const char *>(base) + elem * (BF16 ? 2 : 4);
+        load32(p, wide, w);
+        if constexpr (!BF16) load32(p + 32, wide, w + 8);
     }
     // channels 2 i and 2 i + 1
     __device__ __forceinline__ float2 pair(int i) const {
@@ -132,8 +152,8 @@ cache4_append_kernel(Cache4RowsArgs a) {
     bool finite = true;
     if (write) {
         Group<BF16> k, v;
-        k.load(a.k, (size_t)t * a.k_stride + h * D + grp * 16);
-        v.load(a.v, (size_t)t * a.v_stride + h * D + grp * 16);
+        k.load(a.k, (size_t)t * a.k_stride + h * D + grp * 16, a.wide);
+        v.load(a.v, (size_t)t * a.v_stride + h * D + grp * 16, a.wide);
         finite = quantise<BF16, SCALED>(k, SCALED && a.k_scale ? a.k_scale[h] : 1.f, kc, ks);
         finite = quantise<BF16, SCALED>(v, SCALED && a.v_scale ? a.v_scale[h] : 1.f, vc, vs) && finite;
     }
@@ -156,35 +176,26 @@ cache4_append_kernel(Cache4RowsArgs a) {
 
 // 16 channels that codes and a scale byte stand for, stored as bf16 or f32
 template <bool BF16>
-__device__ __forceinline__ void store_values(void *base, size_t elem, uint2 codes, uint32_t scale, float head_scale) {
+__device__ __forceinline__ void store_values(void *base, size_t elem, uint2 codes, uint32_t scale, float head_scale,
+                                             bool wide) {
     const uint32_t f = scales_to_f16(scale), s = __byte_perm(f, f, 0x1010);
-    uint32_t x[2][4];
+    uint32_t x[2][4], u[BF16 ? 8 : 16];
     codes_to_f16(codes.x, x[0]);
     codes_to_f16(codes.y, x[1]);
-    uint4 *p = reinterpret_cast<uint4 *>(static_cast<char *>(base) + elem * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float2 y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y[j] = unpack_f16(mul_f16x2(x[h][j], s));
-            y[j].x *= head_scale, y[j].y *= head_scale;
-        }
+    for (int j = 0; j < 8; ++j) {
+        const float2 v = unpack_f16(mul_f16x2(x[j >> 2][j & 3], s)), y = make_float2(v.x * head_scale, v.y * head_scale);
         if constexpr (BF16) {
-            uint32_t u[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(y[j].x, y[j].y);
-                u[j] = *reinterpret_cast<const uint32_t *>(&v);
-            }
-            p[h] = make_uint4(u[0], u[1], u[2], u[3]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
+            u[j] = *reinterpret_cast<const uint32_t *>(&b);
         } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                p[2 * h + j] = make_uint4(__float_as_uint(y[2 * j].x), __float_as_uint(y[2 * j].y),
-                                          __float_as_uint(y[2 * j + 1].x), __float_as_uint(y[2 * j + 1].y));
+            u[2 * j] = __float_as_uint(y.x);
+            u[2 * j + 1] = __float_as_uint(y.y);
         }
     }
+    char *p = static_cast<char *>(base) + elem * (BF16 ? 2 : 4);
+    store32(p, wide, u);
+    if constexpr (!BF16) store32(p + 32, wide, u + 8);
 }
 
 template <int D, bool BF16>
@@ -209,8 +220,8 @@ cache4_read_kernel(Cache4RowsArgs a) {
         if ((ks & 0x7fu) == kScaleNaN) vs = ks;  // a marked token's value is not known either
     }
     const size_t e = ((size_t)t * a.Hkv + h) * D + grp * 16;
-    store_values<BF16>(a.k_out, e, kc, ks, a.k_scale ? a.k_scale[h] : 1.f);
-    store_values<BF16>(a.v_out, e, vc, vs, a.v_scale ? a.v_scale[h] : 1.f);
+    store_values<BF16>(a.k_out, e, kc, ks, a.k_scale ? a.k_scale[h] : 1.f, a.wide);
+    store_values<BF16>(a.v_out, e, vc, vs, a.v_scale ? a.v_scale[h] : 1.f, a.wide);
 }
 
 template <bool READ, int D, bool BF16>

@@ -206,6 +206,7 @@ struct Cache4RowsArgs {
     uint8_t *cache;
     const float *k_scale, *v_scale;  // [Hkv] or null
     int T, Hkv, num_slots, page_shift;
+    bool wide;                    // every row starts on a 32-byte boundary
     uint32_t *status;
 };
 cudaError_t launch_cache4_append(const Cache4RowsArgs &a, int d, bool bf16, cudaStream_t st);
