@@ -69,6 +69,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int G = a.Hq / a.Hkv;
 
+    allow_dependents();
     if (lane < kStages) umma::mbar_init(smem_addr(&s_bar[warp * kStages + lane]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     // neighbouring workers sit on different SMs, so that few units spread over all of them

@@ -243,6 +243,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     auto bar = [&](int i) { return sb + C::off_bar + i * 8; };
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + C::off_misc);
 
+    allow_dependents();
     if (tid == 0) {
         for (int i = 0; i < C::RAWS; ++i) {
             umma::mbar_init(bar(C::b_raw_full + i), 1);

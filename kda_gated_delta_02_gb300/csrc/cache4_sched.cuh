@@ -197,51 +197,116 @@ struct Walk {
 // The shares of a row tile's keys, in key order: o = sum_p 2^{m_p - M} O_p / sum_p 2^{m_p - M} l_p.
 // A share is (m [ROWS], l [ROWS], O [ROWS][D]); worker w has two places, 1 for
 // a row tile that starts in its range and 0 for one that it goes on with.
-// One CTA per worker and RB rows (it has work where a row tile starts in that
-// worker's range and ends in a later one), four channels of a row per thread.
-template <int D, int ROWS, int TILE, int RB, bool F32>
-__global__ void __launch_bounds__(RB * D / 4)
-cache4_merge_kernel(const Cache4AttnArgs a, float lift) {
-    const int w0 = blockIdx.x, row = blockIdx.y * RB + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4) * 4;
-    const int4 job = a.jobs[w0];
-    if (job.x < 0) return;
+//
+// A CTA joins one row of the row tiles that start in 16 workers' ranges (and
+// end in later ones).  Up to 16 shares are one warp's work, different warps
+// taking different row tiles; more are dealt out to the CTA's eight warps in
+// contiguous runs, whose sums are added in that order.  What it costs is the
+// chain of dependent loads (one thread walking 200 shares took 50 us) and the
+// number of CTAs (one per worker and row, most with nothing to do, 15 us).
+// The launch is a programmatic dependent of the attention kernel: its CTAs
+// take their places as that kernel's leave.
+constexpr int kMergeWorkers = 16;
+
+template <int D>
+struct Sum {
+    static constexpr int C = D / 32;  // channels per lane
+    float l, y[C];
+    __device__ __forceinline__ void clear() {
+        l = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) y[c] = 0.f;
+    }
+    __device__ __forceinline__ void add(float f, const float *share, int rows, int row, int lane) {
+        l = fmaf(f, share[rows + row], l);
+        const float *o = share + 2 * rows + (size_t)row * D + lane * C;
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(o + c);
+            y[c] = fmaf(f, v.x, y[c]);
+            y[c + 1] = fmaf(f, v.y, y[c + 1]);
+        }
+    }
+};
+
+template <int D, int ROWS, int TILE, bool F32>
+__global__ void __launch_bounds__(256)
+cache4_merge_kernel(const Cache4AttnArgs a, int workers, float lift) {
+    constexpr int C = D / 32, W = kMergeWorkers;
+    __shared__ float s_l[8], s_y[8][D];
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
     const int G = a.Hq / a.Hkv;
-    const Req q = request<ROWS, TILE>(a, job.x, G);
-    const int rr = job.z * ROWS + row;
-    if (rr >= q.rows) return;
     const size_t step = (size_t)ROWS * (D + 2);
-    float m = a.parts[((size_t)w0 * 2 + 1) * step + row];
-    for (int w = w0 + 1; w <= job.w; ++w) m = fmaxf(m, a.parts[(size_t)w * 2 * step + row]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int w = w0; w <= job.w; ++w) {
-        const float *p = a.parts + ((size_t)w * 2 + (w == w0)) * step;
-        const float f = exp2_fast(p[row] - ref);
-        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * ROWS + (size_t)row * D + c);
-        l = fmaf(f, p[ROWS + row], l);
-        y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
+    int4 mine = make_int4(-1, 0, 0, 0);
+    if (lane < W && blockIdx.x * W + lane < workers) mine = a.jobs[blockIdx.x * W + lane];
+    uint32_t left = __ballot_sync(0xffffffffu, mine.x >= 0);
+    for (int k = 0; left; ++k) {
+        const int i = __ffs(left) - 1, w0 = blockIdx.x * W + i;
+        left &= left - 1;
+        const int4 job = make_int4(__shfl_sync(0xffffffffu, mine.x, i), __shfl_sync(0xffffffffu, mine.y, i),
+                                   __shfl_sync(0xffffffffu, mine.z, i), __shfl_sync(0xffffffffu, mine.w, i));
+        const int n = job.w - w0 + 1;
+        const bool wide = n > 16;
+        if (!wide && k % 8 != warp) continue;
+        const Req q = request<ROWS, TILE>(a, job.x, G);
+        const int rr = job.z * ROWS + row;
+        if (rr >= q.rows) continue;  // the same in every warp
+        const float *first = a.parts + ((size_t)w0 * 2 + 1) * step, *later = a.parts + (size_t)w0 * 2 * step;
+        auto share = [&](int j) { return j == 0 ? first : later + (size_t)j * 2 * step; };
+        float m = -INFINITY;
+        for (int j = lane; j < n; j += 32) m = fmaxf(m, share(j)[row]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ref = m == -INFINITY ? 0.f : m;
+        const int per = wide ? (n + 7) / 8 : n, lo = wide ? min(n, warp * per) : 0, hi = min(n, lo + per);
+        Sum<D> sum;
+        sum.clear();
+#pragma unroll 8
+        for (int j = lo; j < hi; ++j) sum.add(exp2_fast(share(j)[row] - ref), share(j), ROWS, row, lane);
+        if (wide) {
+            __syncthreads();  // the last row tile's sums have been read
+            if (lane == 0) s_l[warp] = sum.l;
+#pragma unroll
+            for (int c = 0; c < C; ++c) s_y[warp][lane * C + c] = sum.y[c];
+            __syncthreads();
+            if (warp) continue;
+            for (int w = 1; w < 8; ++w) {
+                sum.l += s_l[w];
+#pragma unroll
+                for (int c = 0; c < C; ++c) sum.y[c] += s_y[w][lane * C + c];
+            }
+        }
+        const size_t head = (size_t)(q.q0 + rr / G) * a.Hq + job.y * G + rr % G;
+        const bool none = m == -INFINITY && sum.l == 0.f;
+        const float inv = none ? 0.f : (a.v_scale ? a.v_scale[job.y] : 1.f) / sum.l;
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+            const float2 v = none ? make_float2(0.f, 0.f) : make_float2(sum.y[c] * inv, sum.y[c + 1] * inv);
+            const size_t e = head * D + lane * C + c;
+            if constexpr (F32) *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + e) = v;
+            else
+                *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.o) + e) = __floats2bfloat162_rn(v.x, v.y);
+        }
+        if (a.lse && lane == 0) a.lse[head] = none ? -INFINITY : (m + log2f(sum.l) - lift) * kLn2;
     }
-    const size_t head = (size_t)(q.q0 + rr / G) * a.Hq + job.y * G + rr % G;
-    const bool none = m == -INFINITY && l == 0.f;
-    const float inv = none ? 0.f : (a.v_scale ? a.v_scale[job.y] : 1.f) / l;
-    y = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-    if constexpr (F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + head * D + c) = y;
-    } else {
-        const __nv_bfloat162 b0 = __floats2bfloat162_rn(y.x, y.y), b1 = __floats2bfloat162_rn(y.z, y.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + head * D + c) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
-    }
-    if (a.lse && c == 0) a.lse[head] = none ? -INFINITY : (m + log2f(l) - lift) * kLn2;
 }
+
+// lets the merge kernel's CTAs be placed as this kernel's leave
+__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 template <int D, int ROWS, int TILE, bool F32>
 cudaError_t merge_shares(const Cache4AttnArgs &a, int workers, float lift, cudaStream_t st) {
-    constexpr int RB = ROWS < 16 ? ROWS : 16;
-    cache4_merge_kernel<D, ROWS, TILE, RB, F32><<<dim3(workers, ROWS / RB), RB * D / 4, 0, st>>>(a, lift);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((workers + kMergeWorkers - 1) / kMergeWorkers), ROWS);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache4_merge_kernel<D, ROWS, TILE, F32>, a, workers, lift);
 }
 
 }  // namespace cache4
