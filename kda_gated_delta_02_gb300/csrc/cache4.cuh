@@ -59,6 +59,16 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// f16 pairs times the low / high half of another pair
+__device__ __forceinline__ uint32_t mul_low(uint32_t a, uint32_t s) {
+    const __half2 r = __hmul2_rn(*reinterpret_cast<__half2 *>(&a), __low2half2(*reinterpret_cast<__half2 *>(&s)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t mul_high(uint32_t a, uint32_t s) {
+    const __half2 r = __hmul2_rn(*reinterpret_cast<__half2 *>(&a), __high2half2(*reinterpret_cast<__half2 *>(&s)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
 // f16 pair, lo in the low half
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;

@@ -37,9 +37,14 @@ namespace {
 
 using namespace cache4;
 
-constexpr int kTile = 32;    // keys per tile: two blocks
-constexpr int kWarps = 16;   // workers per CTA
-constexpr int kStages = 3;   // tiles in flight per worker
+// Work on a tile that does not grow with it (the wait, the copies, the maximum
+// across lanes, the schedule) was a sixth of the instructions at 32 keys, and
+// instruction issue is what comes after the copies here: 64 keys, in 12 warps
+// of up to 168 registers.
+constexpr int kTile = 64;                // keys per tile
+constexpr int kBlocks = kTile / 16;      // blocks per tile
+constexpr int kWarps = 12;               // workers per CTA
+constexpr int stages(int d) { return d == 128 ? 2 : 4; }  // tiles in flight per worker: 221 KB
 constexpr float kLift = 15.f; // weights are 2^(s - max + kLift), at most 2^15 of f16's 65504
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -61,7 +66,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 cache4_attn_kernel(const Cache4AttnArgs a) {
-    constexpr int ROWS = 8 * NT, KS = D / 16, BB = block_bytes(D), STAGE = 2 * BB;
+    constexpr int ROWS = 8 * NT, KS = D / 16, BB = block_bytes(D), STAGE = kBlocks * BB, kStages = stages(D);
     constexpr int PARTS = F32 ? 2 : 1;  // f16 parts of a query or weight
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ long long s_prefix[kWarps * 32 + 33];
@@ -168,48 +173,36 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                 for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
         }
 
-        // ---- ring: pages of 32 tables entries at a time in the lanes
+        // ---- ring: block table entries, 32 at a time, one per lane; a copy is
+        // what a page holds of the tile, issued by a lane of its own
         const int32_t *table = a.block_table + (size_t)it.r * a.max_pages;
-        const int used_pages = (q.len + (1 << a.page_shift) - 1) >> a.page_shift;
-        int page_base = -64, page_here = 0;
-        auto page_of = [&](int p) {
-            if (p >= page_base + 32 || p < page_base) {
-                page_base = p;
-                const int i = p + lane;
-                page_here = 0;
-                if (i < used_pages) {
-                    page_here = table[i];
-                    if (page_here < 0 || page_here >= a.num_pages) {
-                        page_here = 0;  // refused below through the status; the read stays in the pool
+        const int pages = (q.len + (1 << a.page_shift) - 1) >> a.page_shift;
+        const int chunk = a.page_shift < 6 ? 1 << (a.page_shift - 4) : kBlocks;  // blocks per copy
+        const uint8_t *base_h = a.cache + (((size_t)h << (a.page_shift - 4)) * BB);
+        const size_t page_bytes = (((size_t)a.Hkv << (a.page_shift - 4)) * BB);
+        int from = 0, held = 0, entry = 0;
+        auto fill = [&](int tile, uint32_t st) {
+            const int key0 = tile * kTile, key = key0 + lane * chunk * 16, page0 = key0 >> a.page_shift;
+            if (page0 + kBlocks > from + held) {
+                from = page0, held = 32, entry = 0;
+                if (from + lane < pages) {
+                    entry = table[from + lane];
+                    if (entry < 0 || entry >= a.num_pages) {
+                        entry = 0;  // the read stays in the pool
                         if (a.status) atomicOr(a.status, KDA_STATUS_BAD_PAGE);
                     }
                 }
                 __syncwarp();
             }
-            return __shfl_sync(0xffffffffu, page_here, p - page_base);
-        };
-        auto block_addr = [&](int page, int blk) {
-            return a.cache + (((size_t)page * a.Hkv + h) << (a.page_shift - 4)) * BB + (size_t)blk * BB;
-        };
-        auto fill = [&](int tile, uint32_t st) {
-            const int key = tile * kTile;
-            const uint32_t dst = ring + st * STAGE, bar = bars + st * 8;
-            const bool two = key + 16 < q.len;  // a second block with keys in it
-            const int pg = page_of(key >> a.page_shift);
-            const int blk = (key & ((1 << a.page_shift) - 1)) >> 4;
-            if (a.page_shift > 4) {
-                if (lane == 0) {
-                    const uint32_t bytes = two ? 2 * BB : BB;
-                    umma::mbar_expect_tx(bar, bytes);
-                    umma::bulk_load(dst, block_addr(pg, blk), bytes, bar);
-                }
-            } else {
-                const int pg2 = two ? page_of((key >> 4) + 1) : 0;
-                if (lane == 0) {
-                    umma::mbar_expect_tx(bar, two ? 2 * BB : BB);
-                    umma::bulk_load(dst, block_addr(pg, 0), BB, bar);
-                    if (two) umma::bulk_load(dst + BB, block_addr(pg2, 0), BB, bar);
-                }
+            const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - from) & 31);
+            const int all = min(kBlocks, (q.len - key0 + 15) >> 4);  // blocks with keys
+            const uint32_t bar = bars + st * 8;
+            if (lane == 0) umma::mbar_expect_tx(bar, all * BB);
+            __syncwarp();
+            const int mine = min(chunk, all - lane * chunk);
+            if (mine > 0) {
+                const int blk = (key & ((1 << a.page_shift) - 1)) >> 4;
+                umma::bulk_load(ring + st * STAGE + lane * chunk * BB, base_h + page * page_bytes + blk * BB, mine * BB, bar);
             }
         };
         uint32_t put = stage;
@@ -222,49 +215,46 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
 
 #pragma unroll 1
         for (int tile = first; tile < last; ++tile) {
-            if (!umma::mbar_wait(bars + stage * 8, phase, kWaitLimit)) {
+            if (!__all_sync(0xffffffffu, poll(bars + stage * 8, phase, kWaitLimit))) {
                 dead = true;
                 if (lane == 0 && a.status) atomicOr(a.status, KDA_STATUS_TIMEOUT);
                 // the copies in flight end before the warp leaves
                 for (int i = tile; i < filled; ++i) {
-                    umma::mbar_wait(bars + stage * 8, phase, kWaitLimit);
+                    poll(bars + stage * 8, phase, kWaitLimit);
                     if (++stage == kStages) stage = 0, phase ^= 1;
                 }
                 break;
             }
             const uint32_t buf = ring + stage * STAGE;
             const int key0 = tile * kTile;
-            const bool two = key0 + 16 < q.len;
+            const int blocks = (q.len - key0 + 15) >> 4;  // with keys in them, of this tile's
             // ---- S^T = K Q^T, 16 keys x 8 rows per product; row g of a
             // product is key 4 (g / 2) + (g & 1), row g + 8 two further, so
             // that lane t4 ends up with the weights of keys 4 t4 .. 4 t4 + 3
-            float s[2][NT][4];
+            float s[kBlocks][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
+            for (int mt = 0; mt < kBlocks; ++mt) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[mt][nt][j] = 0.f;
-                if (mt == 1 && !two) continue;
+                if (mt >= blocks) continue;
                 const uint32_t blk = buf + mt * BB;
                 const int tok = 4 * (g >> 1) + (g & 1);
-                uint32_t kw[2][D / 32], sc[2][KS / 4];
+                uint32_t kw[2][D / 32], sc[2];
                 if constexpr (D == 128) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint4 w = lds128(blk + (tok + 2 * i) * 64 + t4 * 16);
                         kw[i][0] = w.x, kw[i][1] = w.y, kw[i][2] = w.z, kw[i][3] = w.w;
-                        const uint32_t f = scales_to_f16(lds16(blk + off_ks(D) + (tok + 2 * i) * 8 + t4 * 2));
-                        sc[i][0] = __byte_perm(f, f, 0x1010);
-                        sc[i][1] = __byte_perm(f, f, 0x3232);
+                        sc[i] = scales_to_f16(lds16(blk + off_ks(D) + (tok + 2 * i) * 8 + t4 * 2));
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint2 w = lds64(blk + (tok + 2 * i) * 32 + t4 * 8);
                         kw[i][0] = w.x, kw[i][1] = w.y;
-                        const uint32_t f = scales_to_f16(lds8(blk + off_ks(D) + (tok + 2 * i) * 4 + t4));
-                        sc[i][0] = __byte_perm(f, f, 0x1010);
+                        sc[i] = scales_to_f16(lds8(blk + off_ks(D) + (tok + 2 * i) * 4 + t4));
                     }
                 }
 #pragma unroll
@@ -274,8 +264,8 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                     codes_to_f16(kw[1][w], x1);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        x0[j] = mul_f16x2(x0[j], sc[0][w >> 1]);
-                        x1[j] = mul_f16x2(x1[j], sc[1][w >> 1]);
+                        x0[j] = w < 2 ? mul_low(x0[j], sc[0]) : mul_high(x0[j], sc[0]);
+                        x1[j] = w < 2 ? mul_low(x1[j], sc[1]) : mul_high(x1[j], sc[1]);
                     }
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh)
@@ -292,7 +282,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
             if (edge) {
                 const int tok = key0 + 4 * (g >> 1) + (g & 1);
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                for (int mt = 0; mt < kBlocks; ++mt)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -302,13 +292,15 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                         }
             }
             // ---- running maximum and weights
-            uint32_t pf[NT][PARTS][2][2];
+            uint32_t pf[NT][PARTS][kBlocks][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float top[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    top[j] = fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]), fmaxf(s[1][nt][j], s[1][nt][j + 2]));
+                    top[j] = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+                    for (int mt = 1; mt < kBlocks; ++mt) top[j] = fmaxf(top[j], fmaxf(s[mt][nt][j], s[mt][nt][j + 2]));
                     top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 4));
                     top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
                     top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
@@ -331,7 +323,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) off[j] = kLift - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
+                for (int mt = 0; mt < kBlocks; ++mt) {
                     float w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -351,8 +343,8 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
             }
             // ---- O^T += V^T P^T: lane (g, t4) holds channels (D / 8) g ... of keys 4 t4 .. 4 t4 + 3
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                if (mt == 1 && !two) continue;
+            for (int mt = 0; mt < kBlocks; ++mt) {
+                if (mt >= blocks) continue;
                 const uint32_t blk = buf + mt * BB;
                 constexpr int W = D / 64;  // code words per key and lane
                 uint32_t vw[4][W], sv;
@@ -475,7 +467,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
     if (lane == 0) a.jobs[me] = dead ? make_int4(-1, 0, 0, 0) : job;
 }
 
-constexpr int smem_bytes(int d) { return kWarps * kStages * 2 * block_bytes(d); }
+constexpr int smem_bytes(int d) { return kWarps * stages(d) * kBlocks * block_bytes(d); }
 
 template <int D, int NT, bool F32>
 cudaError_t launch_attn(const Cache4AttnArgs &a, int sms, cudaStream_t st) {

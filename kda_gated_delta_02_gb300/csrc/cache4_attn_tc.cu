@@ -107,20 +107,6 @@ __device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
         : "memory");
 }
 
-// Polls until the phase with this parity is over, at most `limit` times.
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\n.reg .u32 n;\nmov.u32 n, %3;\n"
-        "AGAIN:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n@p bra DONE;\n"
-        "sub.u32 n, n, 1;\nsetp.ne.u32 p, n, 0;\n@p bra AGAIN;\nsetp.ne.u32 p, n, n;\n"
-        "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(limit)
-        : "memory");
-    return ok != 0;
-}
-
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }

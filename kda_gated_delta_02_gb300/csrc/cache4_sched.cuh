@@ -56,6 +56,20 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     return r;
 }
 
+// Polls until the phase with this parity is over, at most `limit` times.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .u32 n;\nmov.u32 n, %3;\n"
+        "AGAIN:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n@p bra DONE;\n"
+        "sub.u32 n, n, 1;\nsetp.ne.u32 p, n, 0;\n@p bra AGAIN;\nsetp.ne.u32 p, n, n;\n"
+        "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(limit)
+        : "memory");
+    return ok != 0;
+}
+
 // A request as the schedule sees it.
 struct Req {
     int q0, n, len;  // first query row, new tokens, keys
