@@ -43,6 +43,7 @@ using namespace cache4;
 // of up to 168 registers.
 constexpr int kTile = 64;                // keys per tile
 constexpr int kBlocks = kTile / 16;      // blocks per tile
+constexpr int kLead = 2;                 // an item's start and end, in tiles
 constexpr int kWarps = 12;               // workers per CTA
 constexpr int stages(int d) { return d == 128 ? 2 : 4; }  // tiles in flight per worker: 221 KB
 constexpr float kLift = 15.f; // weights are 2^(s - max + kLift), at most 2^15 of f16's 65504
@@ -79,7 +80,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     // neighbouring workers sit on different SMs, so that few units spread over all of them
     const int me = warp * gridDim.x + blockIdx.x;
-    Walk<ROWS, kTile> walk(a);
+    Walk<ROWS, kTile, kLead> walk(a);
     walk.begin(a, s_prefix, me, gridDim.x * kWarps);
     int4 job = make_int4(-1, 0, 0, 0);
     const uint32_t ring = smem_addr(smem) + warp * (kStages * STAGE);
@@ -480,7 +481,7 @@ cudaError_t launch_attn(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
 
 template <int D, int NT, bool F32>
 cudaError_t launch_merge(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
-    return merge_shares<D, 8 * NT, kTile, F32>(a, cache4_attn_workers(sms), kLift, st);
+    return merge_shares<D, 8 * NT, kTile, kLead, F32>(a, cache4_attn_workers(sms), kLift, st);
 }
 
 }  // namespace

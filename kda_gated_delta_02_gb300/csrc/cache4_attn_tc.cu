@@ -37,6 +37,7 @@ namespace {
 using namespace cache4;
 
 constexpr int kTile = 128;    // keys per tile
+constexpr int kLead = 5;      // an item's start and end, in tiles
 constexpr float kLift = 7.f;  // weights are at most 2^(kLift + kSlack)
 constexpr float kSlack = 8.f;
 
@@ -254,7 +255,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 0) umma::tmem_alloc(sb + C::off_misc, 512);
-    Walk<C::ROWS, kTile> walk(a);
+    Walk<C::ROWS, kTile, kLead> walk(a);
     const int me = blockIdx.x;
     walk.begin(a, reinterpret_cast<long long *>(smem), me, gridDim.x);
     umma::fence_before();
@@ -791,10 +792,10 @@ cudaError_t launch_cache4_attn_tc(const Cache4AttnArgs &a, int d, long long rows
 }
 cudaError_t launch_cache4_merge_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, cudaStream_t st) {
     if (rows > 128)
-        return d == 128 ? merge_shares<128, 256, kTile, false>(a, sms, kLift, st)
-                        : merge_shares<64, 256, kTile, false>(a, sms, kLift, st);
-    return d == 128 ? merge_shares<128, 128, kTile, false>(a, sms, kLift, st)
-                    : merge_shares<64, 128, kTile, false>(a, sms, kLift, st);
+        return d == 128 ? merge_shares<128, 256, kTile, kLead, false>(a, sms, kLift, st)
+                        : merge_shares<64, 256, kTile, kLead, false>(a, sms, kLift, st);
+    return d == 128 ? merge_shares<128, 128, kTile, kLead, false>(a, sms, kLift, st)
+                    : merge_shares<64, 128, kTile, kLead, false>(a, sms, kLift, st);
 }
 
 }  // namespace kda

@@ -8,7 +8,9 @@
 // request or many short ones load the SMs alike.  Row tiles of a request
 // count as many units as its widest one; they are taken from both ends in
 // turn (0, last, 1, last - 1, ...), so that under a causal mask neighbours
-// share the load.
+// share the load.  An item counts LEAD units more than it has key tiles: what
+// its start and end cost, so that ranges of many short items are not the last
+// to finish.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -74,11 +76,11 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t lim
 struct Req {
     int q0, n, len;  // first query row, new tokens, keys
     int rows, row_tiles;
-    int units;       // key tiles of every row tile (the widest one's)
+    int units;       // key tiles of every row tile (the widest one's), and LEAD
     bool ok;
 };
 
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int LEAD>
 __device__ __forceinline__ Req request(const Cache4AttnArgs &a, int r, int G) {
     Req q;
     const int c0 = a.cu_seqlens[r], c1 = a.cu_seqlens[r + 1], len = a.seq_len[r];
@@ -94,7 +96,7 @@ __device__ __forceinline__ Req request(const Cache4AttnArgs &a, int r, int G) {
         const long long span = ((long long)a.window + (ROWS - 1) / G + 1) / TILE + 2;
         if (span < t) t = (int)span;
     }
-    q.units = t > 0 ? t : 1;  // a row tile that sees nothing is still written
+    q.units = (t > 0 ? t : 1) + LEAD;  // a row tile that sees nothing is still written
     return q;
 }
 
@@ -106,7 +108,7 @@ struct Item {
     __device__ __forceinline__ bool whole() const { return starts && ends; }
 };
 
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int LEAD>
 struct Walk {
     int G;
     int r, h, i, unit;          // the next item and its unit
@@ -127,7 +129,7 @@ struct Walk {
         bool bad = false;
 #pragma unroll 1
         for (int k = r_lo; k < r_hi; ++k) {
-            const Req e = request<ROWS, TILE>(a, k, G);
+            const Req e = request<ROWS, TILE, LEAD>(a, k, G);
             bad |= !e.ok;
             x += (long long)e.row_tiles * a.Hkv * e.units;
         }
@@ -159,7 +161,7 @@ struct Walk {
         long long off = u - prefix[lo];
 #pragma unroll 1
         for (;; ++r) {
-            q = request<ROWS, TILE>(a, r, G);
+            q = request<ROWS, TILE, LEAD>(a, r, G);
             const long long units = (long long)q.row_tiles * a.Hkv * q.units;
             if (off < units) break;
             off -= units;
@@ -179,7 +181,7 @@ struct Walk {
                 if (++h == a.Hkv) {
                     h = 0;
 #pragma unroll 1
-                    do q = request<ROWS, TILE>(a, ++r, G);
+                    do q = request<ROWS, TILE, LEAD>(a, ++r, G);
                     while (q.row_tiles == 0);
                 }
             }
@@ -195,8 +197,8 @@ struct Walk {
         const int key_lo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
         const int tile_lo = key_lo / TILE;
         const int tiles = max(0, (it.pos1 + TILE) / TILE - tile_lo);  // none where pos1 < 0
-        it.first = tile_lo + min(unit, tiles);
-        it.last = tile_lo + min(unit1, tiles);
+        it.first = tile_lo + min(max(unit - LEAD, 0), tiles);
+        it.last = tile_lo + min(max(unit1 - LEAD, 0), tiles);
         it.starts = unit == 0;
         it.ends = unit1 == q.units;
         u += unit1 - unit;
@@ -243,7 +245,7 @@ struct Sum {
     }
 };
 
-template <int D, int ROWS, int TILE, bool F32>
+template <int D, int ROWS, int TILE, int LEAD, bool F32>
 __global__ void __launch_bounds__(256)
 cache4_merge_kernel(const Cache4AttnArgs a, int workers, float lift) {
     constexpr int C = D / 32, W = kMergeWorkers;
@@ -263,7 +265,7 @@ cache4_merge_kernel(const Cache4AttnArgs a, int workers, float lift) {
         const int n = job.w - w0 + 1;
         const bool wide = n > 16;
         if (!wide && k % 8 != warp) continue;
-        const Req q = request<ROWS, TILE>(a, job.x, G);
+        const Req q = request<ROWS, TILE, LEAD>(a, job.x, G);
         const int rr = job.z * ROWS + row;
         if (rr >= q.rows) continue;  // the same in every warp
         const float *first = a.parts + ((size_t)w0 * 2 + 1) * step, *later = a.parts + (size_t)w0 * 2 * step;
@@ -309,7 +311,7 @@ cache4_merge_kernel(const Cache4AttnArgs a, int workers, float lift) {
 // lets the merge kernel's CTAs be placed as this kernel's leave
 __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
-template <int D, int ROWS, int TILE, bool F32>
+template <int D, int ROWS, int TILE, int LEAD, bool F32>
 cudaError_t merge_shares(const Cache4AttnArgs &a, int workers, float lift, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((workers + kMergeWorkers - 1) / kMergeWorkers), ROWS);
@@ -320,7 +322,7 @@ cudaError_t merge_shares(const Cache4AttnArgs &a, int workers, float lift, cudaS
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache4_merge_kernel<D, ROWS, TILE, F32>, a, workers, lift);
+    return cudaLaunchKernelEx(&cfg, cache4_merge_kernel<D, ROWS, TILE, LEAD, F32>, a, workers, lift);
 }
 
 }  // namespace cache4
