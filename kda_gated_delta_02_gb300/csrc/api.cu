@@ -1296,21 +1296,39 @@ int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_
     const int sms = sm_count();
     char *ws = static_cast<char *>(workspace);
     kda::Cache4AttnArgs a{q, q_stride, static_cast<const uint8_t *>(cache), block_table, seq_len, cu_seqlens, k_scale,
-                          v_scale, o, lse, R, T, Hq, Hkv, max_pages, num_pages, shift, window, scale, status,
+                          v_scale, o, lse, R, T, Hq, Hkv, max_pages, num_pages, shift, window, scale, 0, 0, status,
                           reinterpret_cast<int4 *>(ws),
                           reinterpret_cast<float *>(ws + (size_t)kda::cache4_attn_workers(sms) * sizeof(int4))};
+    // rows: (query, head of the group) pairs of a request and key head.  Up to
+    // kFewRows go to the warps' kernel, more (of bf16 queries) to the tcgen05
+    // one, request by request: a batch of single tokens and prompt chunks
+    // runs both.  Only one is launched where all requests are of one kind: by
+    // the bound, or because T shows that every request has max_new queries.
+    constexpr int kFewRows = 16, kAll = 0x7fffffff;
     const bool bf16 = in_dtype == KDA_DTYPE_BF16;
-    const long long rows = (long long)(max_new > 0 && max_new < T ? max_new : T) * (Hq / Hkv);
+    const long long most = max_new > 0 && max_new < T ? max_new : T;
+    const long long rows = most * (Hq / Hkv);
+    const bool many = bf16 && rows > kFewRows, few = !many || most * R != T;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool tc = bf16 && rows > 16;
-    cudaError_t e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st, [&] {
-        return tc ? kda::launch_cache4_attn_tc(a, d, rows, sms, st) : kda::launch_cache4_attn(a, d, bf16, rows, sms, st);
-    });
-    if (e == cudaSuccess)
-        e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st, [&] {
-            return tc ? kda::launch_cache4_merge_tc(a, d, rows, sms, st)
-                      : kda::launch_cache4_merge(a, d, bf16, rows, sms, st);
-        });
+    cudaError_t e = cudaSuccess;
+    if (few) {
+        a.rows_above = 0;
+        a.rows_to = many ? kFewRows : kAll;
+        const long long width = many ? kFewRows : rows;
+        e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st,
+                         [&] { return kda::launch_cache4_attn(a, d, bf16, width, sms, st); });
+        if (e == cudaSuccess)
+            e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st,
+                             [&] { return kda::launch_cache4_merge(a, d, bf16, width, sms, st); });
+    }
+    if (many && e == cudaSuccess) {
+        a.rows_above = few ? kFewRows : 0;
+        a.rows_to = kAll;
+        e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st, [&] { return kda::launch_cache4_attn_tc(a, d, rows, sms, st); });
+        if (e == cudaSuccess)
+            e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st,
+                             [&] { return kda::launch_cache4_merge_tc(a, d, rows, sms, st); });
+    }
     return cuda_status(e);
 }
 

@@ -89,7 +89,8 @@ __device__ __forceinline__ Req request(const Cache4AttnArgs &a, int r, int G) {
     q.n = q.ok ? c1 - c0 : 0;
     q.len = q.ok ? len : 0;
     q.rows = q.n * G;
-    q.row_tiles = (q.rows + ROWS - 1) / ROWS;
+    // a call runs as one or two kernels; each takes the requests whose rows are in its range
+    q.row_tiles = q.rows > a.rows_above && q.rows <= a.rows_to ? (q.rows + ROWS - 1) / ROWS : 0;
     int t = (q.len + TILE - 1) / TILE;
     if (a.window > 0) {
         // a row tile spans up to (ROWS - 1) / G + 2 tokens

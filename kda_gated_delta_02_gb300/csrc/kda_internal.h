@@ -223,6 +223,7 @@ struct Cache4AttnArgs {
     float *lse;                   // [T][Hq] or null
     int R, T, Hq, Hkv, max_pages, num_pages, page_shift, window;
     float scale;
+    int rows_above, rows_to;      // requests with more rows than the first and at most the second
     uint32_t *status;
     // work split over the key axis (cache4_attn_workspace): one job record per
     // worker, and two partial results (rows x (d + 2) f32) per worker
