@@ -1314,7 +1314,8 @@ int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_
     if (few) {
         a.rows_above = 0;
         a.rows_to = many ? kFewRows : kAll;
-        const long long width = many ? kFewRows : rows;
+        // (beside longer requests most of the few rows are single tokens: a group's heads)
+        const long long width = many ? Hq / Hkv : rows;
         e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st,
                          [&] { return kda::launch_cache4_attn(a, d, bf16, width, sms, st); });
         if (e == cudaSuccess)
