@@ -46,6 +46,13 @@ constexpr int kBlocks = kTile / 16;      // blocks per tile
 constexpr int kLead = 2;                 // an item's start and end, in tiles
 constexpr int kWarps = 12;               // workers per CTA
 constexpr int stages(int d) { return d == 128 ? 2 : 4; }  // tiles in flight per worker: 221 KB
+// The first wait for a tile's copy: a test build (KDA_TEST_SHORT_FIRST_WAIT) gives up on it
+// at once, to exercise the way out.
+#ifdef KDA_TEST_SHORT_FIRST_WAIT
+constexpr uint32_t kFirstWait = 0;
+#else
+constexpr uint32_t kFirstWait = kWaitLimit;
+#endif
 constexpr float kLift = 15.f; // weights are 2^(s - max + kLift), at most 2^15 of f16's 65504
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -216,7 +223,7 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
 
 #pragma unroll 1
         for (int tile = first; tile < last; ++tile) {
-            if (!__all_sync(0xffffffffu, poll(bars + stage * 8, phase, kWaitLimit))) {
+            if (!__all_sync(0xffffffffu, poll(bars + stage * 8, phase, tile == first ? kFirstWait : kWaitLimit))) {
                 dead = true;
                 if (lane == 0 && a.status) atomicOr(a.status, KDA_STATUS_TIMEOUT);
                 // the copies in flight end before the warp leaves

@@ -38,6 +38,13 @@ using namespace cache4;
 
 constexpr int kTile = 128;    // keys per tile
 constexpr int kLead = 5;      // an item's start and end, in tiles
+// The first wait for scores: a test build (KDA_TEST_SHORT_FIRST_WAIT) gives up on it
+// at once, to exercise the way out.
+#ifdef KDA_TEST_SHORT_FIRST_WAIT
+constexpr uint32_t kFirstWait = 0;
+#else
+constexpr uint32_t kFirstWait = kWaitLimit;
+#endif
 constexpr float kLift = 7.f;  // weights are at most 2^(kLift + kSlack)
 constexpr float kSlack = 8.f;
 
@@ -265,12 +272,18 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
 
     // a bounded wait that gives up when any role has; `wait` for whole warps,
     // whose lanes then agree
-    auto wait1 = [&](int i, uint32_t parity) {
-        if (poll(bar(i), parity & 1, kWaitLimit)) return true;
+    auto wait1 = [&](int i, uint32_t parity, uint32_t limit = kWaitLimit) {
+#pragma unroll 1
+        for (uint32_t n = 0; n < limit; n += 4096) {
+            if (poll(bar(i), parity & 1, 4096)) return true;
+            if (misc[1]) return false;
+        }
         misc[1] = 1;
         return false;
     };
-    auto wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait1(i, parity)) != 0; };
+    auto wait = [&](int i, uint32_t parity, uint32_t limit = kWaitLimit) {
+        return __all_sync(0xffffffffu, wait1(i, parity, limit)) != 0;
+    };
 
     Item it;
     if (warp < C::SOFT) {
@@ -318,7 +331,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
 #pragma unroll 1
                 for (int tile = it.first; tile < it.last; ++tile, ++n) {
                     if (QT == 1 && (int)(n & 1) != t) continue;
-                    if (!wait(C::b_s_full + t, mine++)) return;
+                    if (!wait(C::b_s_full + t, mine++, n == 0 ? kFirstWait : kWaitLimit)) return;
                     umma::fence_after();
                     if (idle) {
                         // no row of this warp is there: its weights may be anything (rows do not mix)
@@ -639,7 +652,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         if (misc[1]) {
             // copies in flight end before the CTA leaves
             for (uint32_t i = raws > C::RAWS ? raws - C::RAWS : 0; i < raws; ++i)
-                umma::mbar_wait(bar(C::b_raw_full + i % C::RAWS), (i / C::RAWS) & 1, kWaitLimit);
+                poll(bar(C::b_raw_full + i % C::RAWS), (i / C::RAWS) & 1, kWaitLimit);
         }
     } else if (warp == C::SOFT + C::DEQ + 1) {
         // ------------------------------------------------------------ products
@@ -716,7 +729,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         work();
         // products in flight end before the CTA leaves
         commit(bar(C::b_drain), lead);
-        wait1(C::b_drain, 0);
+        poll(bar(C::b_drain), 0, kWaitLimit);
     } else if (QT == 1) {
         // ------------------------------------------------------------ queries: D / 8 lanes per row, ahead of the item
         constexpr int LANES = D / 8, STEP = 64 / LANES, BATCH = 8;

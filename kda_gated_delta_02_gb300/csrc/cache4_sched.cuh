@@ -60,6 +60,7 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 
 // Polls until the phase with this parity is over, at most `limit` times.
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
+    if (limit == 0) return false;
     uint32_t ok;
     asm volatile(
         "{\n.reg .pred p;\n.reg .u32 n;\nmov.u32 n, %3;\n"

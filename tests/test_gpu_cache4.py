@@ -373,3 +373,87 @@ def test_bad_lengths_and_pages_are_refused(new):
         o = kda.cache4_attention(c.q.cuda(), cache, t2, lengths, cu, page, status=st)
         assert st.item() == kda.STATUS_BAD_PAGE
         assert torch.equal(o[:new], want[:new]) and torch.equal(o[2 * new:], want[2 * new:])
+
+
+@pytest.mark.parametrize("window", [0, 33])
+def test_batches_of_single_tokens_and_chunks(window):
+    """Requests of few rows and of many in one call, through both kernels, in every order of sizes."""
+    lengths = [70, 300, 1, 129, 500, 64, 200, 31]
+    new = [1, 40, 1, 3, 200, 1, 9, 4]
+    for Hq, H, d, page in ((8, 1, 128, 64), (12, 4, 64, 16), (5, 1, 64, 32)):
+        c = Case(lengths, new, Hq, H, d, page, seed=Hq + window)
+        c.check(window=window)
+        c.check(window=window, max_new=200)
+        c.check(window=window, max_new=5)  # too low a bound picks another split, not another result
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_on_16_byte_boundaries(dtype):
+    """Rows that are 16-byte but not 32-byte aligned (the wide accesses need 32)."""
+    T, H, d, page = 37, 3, 64, 16
+    step = 8 if dtype == "bf16" else 4
+    g = torch.Generator().manual_seed(21)
+    wide = torch.randn(T, 2 * H * d + step, generator=g).to(DT[dtype]).cuda()
+    k, v = wide[:, step:step + H * d].view(T, H, d), wide[:, step + H * d:].view(T, H, d)
+    cache, slots = kda.cache4_alloc(3, H, page, d), torch.arange(T, dtype=torch.int32, device="cuda")
+    kda.cache4_append(k, v, slots, cache, page)
+    ko, vo = kda.cache4_read(cache, slots, page, d, dtype=DT[dtype])
+    assert np.array_equal(to64(ko), ref.held(k.float().cpu().numpy()))
+    assert np.array_equal(to64(vo), ref.held(v.float().cpu().numpy()))
+    # read into outputs on 16-byte boundaries, through the C ABI
+    lib, n = kda.load_library(), T * H * d
+    out = torch.zeros(2 * n + 3 * step, dtype=DT[dtype], device="cuda")
+    po, at = out[step:step + n], out[2 * step + n:2 * step + 2 * n]
+    assert lib.kda_cache4_read(cache.data_ptr(), slots.data_ptr(), T, H, d, 3, page, None, None, 0 if dtype == "bf16" else 1,
+                               po.data_ptr(), at.data_ptr(), None, kda._stream(None)) == 0
+    assert torch.equal(po.view(T, H, d), ko) and torch.equal(at.view(T, H, d), vo)
+    assert (out[:step] == 0).all() and (out[step + n:2 * step + n] == 0).all() and (out[2 * step + 2 * n:] == 0).all()
+
+
+@pytest.mark.parametrize("new", [1, 12, 50])
+def test_nothing_is_written_outside_the_outputs(new):
+    """Cache, outputs and workspace lie between bands of a sentinel byte."""
+    def guarded(like, pad=4096):
+        whole = torch.full((like.nbytes + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
+        view = whole[pad:pad + like.nbytes].view(like.dtype).view(like.shape)
+        view.copy_(like)
+        return whole, view
+
+    def intact(whole, pad=4096):
+        return bool((whole[:pad] == 0xA5).all() and (whole[-pad:] == 0xA5).all())
+
+    c = Case([400, 33, 90], [new] * 3, 8, 2, 128, 16, seed=23, extra_pages=0)
+    want = c.run(return_lse=True)
+    w_cache, cache = guarded(c.cache)
+    kda.cache4_append(c.k.bfloat16().cuda(), c.v.bfloat16().cuda(), c.slots, cache, 16)
+    assert intact(w_cache) and torch.equal(cache, c.cache)
+    w_out, out = guarded(torch.zeros_like(want[0]))
+    w_lse, lse = guarded(torch.zeros_like(want[1]))
+    need = kda.cache4_attention_workspace_size(3, 3 * new, 8, 2, 128)
+    w_ws, ws = guarded(torch.zeros(need, dtype=torch.uint8, device="cuda"))
+    kda.cache4_attention(c.q.cuda(), cache, *c.args[1:], out=out, lse=lse, return_lse=True, workspace=ws)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert intact(w_out) and intact(w_lse) and intact(w_ws) and intact(w_cache)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_wait_that_runs_out_is_reported(new):
+    """A build whose first wait gives up at once (copies, or products, in flight): the call sets KDA_STATUS_TIMEOUT and
+    returns, the stream completes, and the ordinary library is right on the same inputs afterwards."""
+    import ctypes
+
+    from kda_gated_delta_02_gb300 import build
+    test_lib, main = ctypes.CDLL(build.build_variant("shortwait", ["KDA_TEST_SHORT_FIRST_WAIT"])), kda.load_library()
+    f = test_lib.kda_cache4_attention
+    f.restype, f.argtypes = main.kda_cache4_attention.restype, main.kda_cache4_attention.argtypes
+    c = Case([900, 300], [new, new], 8, 2, 128, 16, seed=24)
+    cache, table, lengths, cu, page = c.args
+    q, st = c.q.cuda(), status_word()
+    out = torch.zeros_like(q)
+    ws = torch.empty(kda.cache4_attention_workspace_size(2, 2 * new, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    assert f(q.data_ptr(), cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), cu.data_ptr(), 2, 2 * new, 8, 2, 128,
+             cache.shape[0], page, table.shape[1], new, 0, 128 ** -0.5, 8 * 128, None, None, out.data_ptr(), None, 0,
+             ws.data_ptr(), ws.nbytes, st.data_ptr(), kda._stream(None)) == 0
+    torch.cuda.synchronize()
+    assert st.item() & kda.STATUS_TIMEOUT
+    c.check(max_new=new)
