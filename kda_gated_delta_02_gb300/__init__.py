@@ -589,10 +589,9 @@ def page_plan(context_len, new_len, page_count, block_table, free_pages, free_co
         raise KDAError("tokens must not be negative")
     with _on(stream):
         lib = load_library()
-        dev = block_table.device
-        cu, seq = torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev)
-        slots, pos = torch.empty(T, dtype=i32, device=dev), torch.empty(T, dtype=i32, device=dev)
-        count, free = torch.empty(R, dtype=i32, device=dev), torch.empty(1, dtype=i32, device=dev)
+        dev, like = block_table.device, torch.empty_like
+        cu, slots = torch.empty(R + 1, dtype=i32, device=dev), torch.empty(T, dtype=i32, device=dev)
+        seq, pos, count, free = like(context_len), like(slots), like(page_count), like(free_count)
         rc = lib.kda_page_plan(_ptr(context_len), _ptr(new_len), _ptr(page_count), _ptr(block_table), _ptr(free_pages),
                                _ptr(free_count), R, B, free_pages.shape[0], int(page_size), T, cu.data_ptr(),
                                seq.data_ptr(), slots.data_ptr(), pos.data_ptr(), count.data_ptr(), free.data_ptr(),
@@ -632,7 +631,7 @@ def cache4_read(cache, slots, page_size, d, dtype=torch.bfloat16, k_scale=None, 
     _check_scales(k_scale, v_scale, Hkv)
     with _on(stream):
         k = torch.empty((n, Hkv, d), dtype=dtype, device=cache.device)
-        v = torch.empty((n, Hkv, d), dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
         rc = load_library().kda_cache4_read(_ptr(cache), _ptr(slots), n, Hkv, d, P, int(page_size), _ptr(k_scale),
                                             _ptr(v_scale), _in_dtype(k), k.data_ptr(), v.data_ptr(), _ptr(status),
                                             _stream(stream))
