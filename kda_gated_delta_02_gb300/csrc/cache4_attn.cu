@@ -23,7 +23,7 @@
 // second f16 part for 32-bit queries, and so are the queries (scaled by a
 // power of two per row), so that only that rounding separates the result from
 // fp32.  A worker whose share cuts a row tile's keys leaves (max, sum, sum of
-// weighted values), and cache4_merge_kernel joins the shares in key order.
+// weighted values), and kda_cache4_merge_kernel joins the shares in key order.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-cache4_attn_kernel(const Cache4AttnArgs a) {
+kda_cache4_attn_kernel(const Cache4AttnArgs a) {
     constexpr int ROWS = 8 * NT, KS = D / 16, BB = block_bytes(D), STAGE = kBlocks * BB, kStages = stages(D);
     constexpr int PARTS = F32 ? 2 : 1;  // f16 parts of a query or weight
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -329,13 +329,15 @@ cache4_attn_kernel(const Cache4AttnArgs a) {
                 }
                 float off[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) off[j] = kLift - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
+                for (int j = 0; j < 2; ++j) off[j] = (F32 ? 0.f : kLift) - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
 #pragma unroll
                 for (int mt = 0; mt < kBlocks; ++mt) {
                     float w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         w[j] = exp2_fast(fmaf(s[mt][nt][j], fac[nt][j & 1], off[j & 1]));
+                        // 32-bit calls: an exponent near 15 would carry four bits less than one near 0
+                        if constexpr (F32) w[j] *= 32768.f;
                         l[nt][j & 1] += w[j];
                     }
 #pragma unroll
@@ -479,7 +481,7 @@ constexpr int smem_bytes(int d) { return kWarps * stages(d) * kBlocks * block_by
 
 template <int D, int NT, bool F32>
 cudaError_t launch_attn(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
-    auto kernel = cache4_attn_kernel<D, NT, F32>;
+    auto kernel = kda_cache4_attn_kernel<D, NT, F32>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(D));
     if (e != cudaSuccess) return e;
     kernel<<<sms, kWarps * 32, smem_bytes(D), st>>>(a);

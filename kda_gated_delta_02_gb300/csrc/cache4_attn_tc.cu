@@ -227,7 +227,7 @@ __device__ __forceinline__ void store_query(uint32_t addr, const uint4 &w, float
 
 template <int D, int QT>
 __global__ void __launch_bounds__((Cfg<D, QT>::THREADS), 1)
-cache4_attn_tc_kernel(const Cache4AttnArgs a) {
+kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     using C = Cfg<D, QT>;
     constexpr int BB = block_bytes(D), KS = D / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -783,7 +783,7 @@ cache4_attn_tc_kernel(const Cache4AttnArgs a) {
 
 template <int D, int QT>
 cudaError_t launch(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
-    auto kernel = cache4_attn_tc_kernel<D, QT>;
+    auto kernel = kda_cache4_attn_tc_kernel<D, QT>;
     constexpr int bytes = Cfg<D, QT>::SMEM;
     static_assert(bytes <= 232448, "shared memory of one CTA");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);

@@ -137,7 +137,7 @@ __device__ __forceinline__ uint8_t *block_of(const Cache4RowsArgs &a, int slot, 
 
 template <int D, bool BF16, bool SCALED>
 __global__ void __launch_bounds__(256)
-cache4_append_kernel(Cache4RowsArgs a) {
+kda_cache4_append_kernel(Cache4RowsArgs a) {
     constexpr int GROUPS = D / 16;  // lanes of a token and head: 8 or 4 neighbours in a warp
     const uint32_t th = blockIdx.x * (256 / GROUPS) + threadIdx.x / GROUPS;  // below 2^32 (checked at the launch)
     const int grp = threadIdx.x % GROUPS;
@@ -200,7 +200,7 @@ __device__ __forceinline__ void store_values(void *base, size_t elem, uint2 code
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256)
-cache4_read_kernel(Cache4RowsArgs a) {
+kda_cache4_read_kernel(Cache4RowsArgs a) {
     constexpr int GROUPS = D / 16;
     const uint32_t th = blockIdx.x * (256 / GROUPS) + threadIdx.x / GROUPS;
     const int grp = threadIdx.x % GROUPS;
@@ -229,9 +229,9 @@ cudaError_t launch(const Cache4RowsArgs &a, cudaStream_t st) {
     const long long th = (long long)a.T * a.Hkv, per = 256 / (D / 16);
     if (th + per > 0xffffffffLL) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)((th + per - 1) / per);
-    if constexpr (READ) cache4_read_kernel<D, BF16><<<grid, 256, 0, st>>>(a);
-    else if (a.k_scale || a.v_scale) cache4_append_kernel<D, BF16, true><<<grid, 256, 0, st>>>(a);
-    else cache4_append_kernel<D, BF16, false><<<grid, 256, 0, st>>>(a);
+    if constexpr (READ) kda_cache4_read_kernel<D, BF16><<<grid, 256, 0, st>>>(a);
+    else if (a.k_scale || a.v_scale) kda_cache4_append_kernel<D, BF16, true><<<grid, 256, 0, st>>>(a);
+    else kda_cache4_append_kernel<D, BF16, false><<<grid, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 

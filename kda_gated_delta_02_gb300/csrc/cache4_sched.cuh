@@ -249,7 +249,7 @@ struct Sum {
 
 template <int D, int ROWS, int TILE, int LEAD, bool F32>
 __global__ void __launch_bounds__(256)
-cache4_merge_kernel(const Cache4AttnArgs a, int workers, float lift) {
+kda_cache4_merge_kernel(const Cache4AttnArgs a, int workers, float lift) {
     constexpr int C = D / 32, W = kMergeWorkers;
     __shared__ float s_l[8], s_y[8][D];
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -324,7 +324,7 @@ cudaError_t merge_shares(const Cache4AttnArgs &a, int workers, float lift, cudaS
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache4_merge_kernel<D, ROWS, TILE, LEAD, F32>, a, workers, lift);
+    return cudaLaunchKernelEx(&cfg, kda_cache4_merge_kernel<D, ROWS, TILE, LEAD, F32>, a, workers, lift);
 }
 
 }  // namespace cache4

@@ -57,7 +57,7 @@ __device__ __forceinline__ int find(const int *starts, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kThreads)
-page_plan_kernel(PagePlanArgs a) {
+kda_page_plan_kernel(PagePlanArgs a) {
     __shared__ long long warp_sums[32];
     __shared__ int s_row[kThreads + 1], s_base[kThreads + 1], s_ctx[kThreads], s_held[kThreads];
     __shared__ int s_used;
@@ -151,7 +151,7 @@ cudaError_t launch_page_plan(const PagePlanArgs &a, int sms, cudaStream_t st) {
     long grid = ((long)a.T + threads - 1) / threads;
     const long most = 2L * sms * kThreads / threads;
     grid = grid < 1 ? 1 : grid > most ? most : grid;
-    page_plan_kernel<<<(unsigned)grid, threads, 0, st>>>(a);
+    kda_page_plan_kernel<<<(unsigned)grid, threads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
