@@ -143,7 +143,14 @@ kda_cache4_append_kernel(Cache4RowsArgs a) {
     const int grp = threadIdx.x % GROUPS;
     const uint32_t t = th / (uint32_t)a.Hkv, h = th - t * (uint32_t)a.Hkv;
     const bool live = t < (uint32_t)a.T;
-    const int slot = live ? __ldg(a.slots + t) : -1;
+    // the rows are asked for beside their slot, not after it (a row without one is read in vain)
+    Group<BF16> k, v;
+    int slot = -1;
+    if (live) {
+        slot = __ldg(a.slots + t);
+        k.load(a.k, (size_t)t * a.k_stride + h * D + grp * 16, a.wide);
+        v.load(a.v, (size_t)t * a.v_stride + h * D + grp * 16, a.wide);
+    }
     const bool in_range = slot < a.num_slots;
     if (live && !in_range && a.status) atomicOr(a.status, KDA_STATUS_BAD_PAGE);
     const bool write = slot >= 0 && in_range;
@@ -151,9 +158,6 @@ kda_cache4_append_kernel(Cache4RowsArgs a) {
     uint32_t ks = 0, vs = 0;
     bool finite = true;
     if (write) {
-        Group<BF16> k, v;
-        k.load(a.k, (size_t)t * a.k_stride + h * D + grp * 16, a.wide);
-        v.load(a.v, (size_t)t * a.v_stride + h * D + grp * 16, a.wide);
         finite = quantise<BF16, SCALED>(k, SCALED && a.k_scale ? a.k_scale[h] : 1.f, kc, ks);
         finite = quantise<BF16, SCALED>(v, SCALED && a.v_scale ? a.v_scale[h] : 1.f, vc, vs) && finite;
     }
