@@ -580,8 +580,10 @@ int kda_cache4_read(const void *cache, const int32_t *slots, int n, int Hkv, int
  *             i of n sees positions up to seq_len[r] - n + i, and with window
  *             > 0 only the last `window` of those.  A query that sees nothing
  *             gets o = 0 and lse = -inf.
- *  max_new    an upper bound of the requests' new tokens (0: T).  It picks the
- *             kernel's tile; a request with more is still computed.
+ *  max_new    an upper bound of the requests' new tokens (0: T).  Requests of
+ *             up to 16 (query, head of a group) rows and those of more run in
+ *             two kernels; the bound says which are needed and how wide a tile
+ *             is.  A request with more queries is still computed.
  *  o          device [T][Hq][d], in_dtype.  lse: device f32 [T][Hq] or NULL,
  *             the natural log of the sum of e^{scale q.k}.
  *  workspace  at least kda_cache4_attention_workspace_size(...) bytes.

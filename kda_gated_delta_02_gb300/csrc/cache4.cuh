@@ -1,6 +1,6 @@
 // cache4.cuh -- the paged 4-bit key/value cache: format arithmetic and the
 // conversions shared by its kernels (page_plan.cu, cache4_rows.cu,
-// cache4_attn.cu).
+// cache4_attn.cu, cache4_attn_tc.cu).
 //
 // cache [pages][Hkv][page_size / 16 blocks][block bytes].  A block holds 16
 // tokens of one head, in four parts one after the other:

@@ -9,8 +9,9 @@
 // row is a (token, head of the group) pair and rows of a request and key head
 // are cut into row tiles.
 //
-// Memory bounds the few-row case (9 d / 8 bytes per key and head against
-// 4 d flops per row).  Every warp is a worker of its own: it takes an equal,
+// This file: few rows (single tokens, up to 16 rows; 32-bit queries of any
+// number).  Memory bounds that, 9 d / 8 bytes per key and head against 4 d
+// flops per row.  Every warp is a worker of its own: it takes an equal,
 // contiguous share of all (request, key head, row tile, key tile) units in
 // that order, keeps its own ring of key tiles filled by bulk copies and meets
 // no barrier.  A key tile goes from shared memory to registers once, the
@@ -24,6 +25,13 @@
 // power of two per row), so that only that rounding separates the result from
 // fp32.  A worker whose share cuts a row tile's keys leaves (max, sum, sum of
 // weighted values), and kda_cache4_merge_kernel joins the shares in key order.
+//
+// Measured at d = 128, 96 query heads on 12 key heads (device time): 256
+// single tokens over up to 8K keys (1.86 GB) 315 us, 5.9 TB/s, 87 % of the
+// measured copy bandwidth; one token over 1M keys (1.81 GB) 298 us, 90 %; one
+// over 1,003 keys 10.7 us.  After the copies comes instruction issue (57 %
+// busy, the conversion's pipe 48 %): 530 warp instructions per 32 keys, of
+// which the conversion of the codes is 290 and the products 32.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -4,25 +4,46 @@
 // Same operator and division of the work as cache4_attn.cu, with row tiles of
 // QT x 128 rows and key tiles of 128.  One persistent CTA per SM, warps by
 // role:
-//   producer   1 warp   bulk copies of 64 keys at a time into a raw ring
-//   dequant    12 - 4 QT warps, half for the keys and half for the values: codes
-//                       and scales -> f16 (exact), into the swizzled shared-
+//   softmax    8 warps  a thread per row of one of two score tiles: maximum,
+//                       weights (f16, lifted by 2^kLift), sum, and the
+//                       accumulator's rescaling; the epilogue
+//   dequant    4 or 8   half for the keys and half for the values: codes and
+//                       scales -> f16 (exact), into the swizzled shared-
 //                       memory operands K (K-major) and V (N-major)
+//   producer   1 warp   bulk copies of 64 keys at a time into a raw ring
 //   products   1 warp   S = Q K^T into tensor memory, O += P V with P read
 //                       from tensor memory (it takes the place of S)
-//   queries    2 warps  the next item's query rows, scaled, as f16
-//   softmax    8 warps  a thread per row and tile (or stream): maximum, weights (f16, lifted by
-//                       2^kLift), sum, and the accumulator's rescaling
-// The running maximum that the weights refer to moves only when it would rise
-// by more than 2^8, so the accumulator (in tensor memory) is rescaled a few
-// times per row tile; f16 holds the weights of up to 2^15 that this allows.
-// With QT = 2 the two row tiles take turns: one's products run while the
-// other's softmax does.  With QT = 1 the next tile's S is formed in a second
-// buffer meanwhile.
+//   queries    2 warps  QT = 1: the next item's query rows, scaled, as f16
+//                       (QT = 2: the softmax threads, a row each)
+// There are two score tiles S and two accumulators O in tensor memory (all
+// 512 columns at d = 128).  With QT = 2 they belong to two row tiles, whose
+// products and softmax take turns.  With QT = 1 (up to 128 rows) they belong
+// to the even and the odd key tiles of the one row tile: two streams with
+// maximum, sum and accumulator of their own, joined at the item's end.
 //
-// What bounds it: at QT = 2 the products (1,024 cycles of the tensor pipe per
-// 128 x 128 pair of tiles at d = 128) and, close by, shared memory, which
-// carries the converted operands in (64 KB per key tile) and out.
+// The running maximum that the weights refer to moves only when it would rise
+// by more than 2^8, so the accumulator is rescaled a few times per item; f16
+// holds the weights of up to 2^15 that this allows.
+//
+// What bounds it.  QT = 2: the products take 2,048 cycles of the tensor pipe
+// per 256 rows x 128 keys at d = 128; a row tile's chain (scores, two passes
+// over them, weights, O, next scores) makes that 3,250.  632 GFLOP of prompt
+// chunks (2 x 2,048 queries of 32 heads over up to 16K keys): 486 us on the
+// device, 1.30 PFLOP/s, 67 % of the measured bf16 rate.  QT = 1: shared
+// memory, through which a key tile moves 213 KB (raw bytes in and out 45,
+// operands in 64, operand reads 96, of it Q's 128 rows 32): 1,660 cycles at
+// 128 bytes a cycle of the 1,950 that a tile takes.  64 requests of up to 8
+// queries x 96 heads (752 MB): 306 us on the device, 36 % of the measured
+// copy bandwidth.
+//
+// Measured on the way (us, the two calls above): one thread issuing the
+// products from a divergent branch, operands moved to uniform registers for
+// each, 591 / 451, the whole warp with an elected lane 483 / 420; one stream
+// for QT = 1 420, two 352; 145 KB of code, which overran the instruction
+// cache, 997 / 817, the roles rolled up 597 / 463.  Slower and left out:
+// copies of keys and values apart (1,152 bytes each) 406 for QT = 1; weights
+// against a stale maximum held in registers until it is checked, which wants
+// over 200 registers.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
