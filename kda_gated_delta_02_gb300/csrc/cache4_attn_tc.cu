@@ -73,13 +73,14 @@ template <int D, int QT>
 struct Cfg {
     // Whole warpgroups by role, whose registers are shared out anew at the start:
     // a CTA of 16 warps is launched with 128 a thread, one of 20 with 96.  With
-    // one row tile memory bounds the call and conversion gets two warpgroups.
+    // two row tiles a softmax thread holds its row's 128 scores; with one,
+    // memory bounds the call and conversion gets two warpgroups.
     static constexpr int SOFT = 8, DEQ = QT == 2 ? 4 : 8, WARPS = SOFT + DEQ + 4, THREADS = WARPS * 32;
     static constexpr int R_LAUNCH = QT == 2 ? 128 : 96;
-    static constexpr int R_SOFT = QT == 2 ? 144 : 112, R_DEQ = QT == 2 ? 128 : 80, R_MISC = 96;
+    static constexpr int R_SOFT = QT == 2 ? 176 : 112, R_DEQ = QT == 2 ? 96 : 80, R_MISC = QT == 2 ? 64 : 96;
     // the others give up what the softmax warpgroups take, and nobody waits for more than there is
     static_assert(R_SOFT >= R_LAUNCH && R_DEQ <= R_LAUNCH && R_MISC <= R_LAUNCH, "who takes and who gives registers");
-    static_assert(2 * R_SOFT + DEQ / 4 * R_DEQ + R_MISC <= WARPS / 4 * R_LAUNCH, "registers of the CTA");
+    static_assert(SOFT / 4 * R_SOFT + DEQ / 4 * R_DEQ + R_MISC <= WARPS / 4 * R_LAUNCH, "registers of the CTA");
     static constexpr int ROWS = 128 * QT;
     static constexpr int OPERAND = 128 * D * 2;       // 128 rows of f16
     static constexpr int RAW = 4 * block_bytes(D);    // 64 keys
@@ -96,7 +97,8 @@ struct Cfg {
     static constexpr int off_misc = off_bar + BARS * 8;  // TMEM address, dead flag
     static constexpr int off_ml = off_misc + 16;         // maxima and sums of the two streams
     static constexpr int off_fac = off_ml + 2 * 128 * 8; // factors of the rows' scores, two items
-    static constexpr int SMEM = off_fac + 2 * ROWS * 4;
+    static constexpr int off_item = (off_fac + 2 * ROWS * 4 + 15) & ~15;  // the softmax warps' place in the work
+    static constexpr int SMEM = off_item + SOFT * 176;
     // tensor memory columns: S (and P over it) 2 x 128, O 2 x D
     static constexpr int t_o = 256;
 };
@@ -175,12 +177,13 @@ __device__ __forceinline__ void hold(uint32_t (&r)[32]) {
           "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
 }
 
-__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&s)[2][32]) {
-    ld32_async(taddr, s[0]);
-    ld32_async(taddr + 32, s[1]);
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&s)[N][32]) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) ld32_async(taddr + c * 32, s[c]);
     umma::wait_ld();
-    hold(s[0]);
-    hold(s[1]);
+#pragma unroll
+    for (int c = 0; c < N; ++c) hold(s[c]);
 }
 __device__ __forceinline__ void st32b(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
@@ -192,13 +195,17 @@ __device__ __forceinline__ void st32b(uint32_t taddr, const uint32_t (&r)[32]) {
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void st16_async(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
-        "tcgen05.wait::st.sync.aligned;\n" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+            taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    st16_async(taddr, r);
+    asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
@@ -309,27 +316,50 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     Item it;
     if (warp < C::SOFT) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::R_SOFT));
-        // ------------------------------------------------------------ softmax: a thread per row and stream
-        const int t = warp >> 2, lane_base = (warp & 3) * 32, r = lane_base + lane;
-        const int my = (QT == 2 ? t * 128 : 0) + r;
+        // ------------------------------------------------------------ softmax: a thread per row of a score tile
+        // scores per load: a load from tensor memory takes about 200 cycles beside the products, however wide
+        constexpr int CHUNK = QT == 2 ? 128 : 64;
+        const int t = warp >> 2, lane_base = (warp & 3) * 32, r = lane_base + lane, my = (QT == 2 ? t * 128 : 0) + r;
         const uint32_t tq = tmem + ((uint32_t)lane_base << 16), ts = tq + t * 128, to = tq + C::t_o + t * D;
         uint32_t n = 0, mine = 0, items = 0;  // key tiles so far, those of this stream, items with key tiles
-        int4 job = make_int4(-1, 0, 0, 0);
+        // The place in the work lives in shared memory, a copy per warp: its
+        // twenty-odd registers are needed between items only.
+        struct Place {
+            Walk<C::ROWS, kTile, kLead> walk;
+            Item it;
+            int4 job;
+            int more;
+        };
+        static_assert(sizeof(Place) <= 176, "room of a warp's place");
+        Place &at = *reinterpret_cast<Place *>(smem + C::off_item + warp * 176);
+        if (lane == 0) {
+            at.walk = walk;
+            at.job = make_int4(-1, 0, 0, 0);
+        }
         auto work = [&]() {
-            while (walk.next(a, it)) {
-                const Req &q = walk.q;
-                const int rr = it.row0 + my;
-                const bool valid = rr < q.rows, idle = it.row0 + my - lane >= q.rows;
-                const int tok = min(rr, q.rows - 1) / G, x = valid ? rr % G : 0;
-                const size_t head = (size_t)(q.q0 + tok) * a.Hq + it.h * G + x;
-                const bool some = it.last > it.first;
+            while (true) {
+                __syncwarp();
+                if (lane == 0) {
+                    Walk<C::ROWS, kTile, kLead> w = at.walk;
+                    Item next;
+                    at.more = w.next(a, next);
+                    at.it = next;
+                    if (at.more && next.starts && !next.ends) at.job = make_int4(next.r, next.h, next.rt, w.last_worker());
+                    at.walk = w;
+                }
+                __syncwarp();
+                if (!at.more) break;
+                const int tile0 = at.it.first, tile1 = at.it.last;
+                const bool some = tile1 > tile0;
+                const int rows = at.walk.q.rows, rr = at.it.row0 + my, tok = min(rr, rows - 1) / G;
+                const bool valid = rr < rows, idle = rr - lane >= rows;
                 float m = -INFINITY, l = 0.f, fac = 1.f;
-                const float base = a.scale * kLog2e * (a.k_scale ? a.k_scale[it.h] : 1.f);
                 if (QT == 2 && some) {
-                    // this thread's query row (its warps' last products have read the row before)
+                    // this thread's query row (its score tile's last products have read the row before)
+                    const float base = a.scale * kLog2e * (a.k_scale ? a.k_scale[at.it.h] : 1.f);
                     const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                                     (size_t)(q.q0 + tok) * a.q_stride +
-                                                                     (size_t)(it.h * G + x) * D);
+                                                                     (size_t)(at.walk.q.q0 + tok) * a.q_stride +
+                                                                     (size_t)(at.it.h * G + (valid ? rr % G : 0)) * D);
                     uint4 w[D / 8];
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) w[i] = __ldg(p + i);
@@ -346,11 +376,11 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     arrive(bar(C::b_q_full));
                 }
                 // positions this row sees (a padding row sees what the last row does), and what the whole warp sees
-                const int sees = q.len - q.n + tok;
+                const int sees = at.walk.q.len - at.walk.q.n + tok;
                 const int see_lo = __reduce_min_sync(0xffffffffu, sees), see_hi = __reduce_max_sync(0xffffffffu, sees);
                 bool begun = false;
 #pragma unroll 1
-                for (int tile = it.first; tile < it.last; ++tile, ++n) {
+                for (int tile = tile0; tile < tile1; ++tile, ++n) {
                     if (QT == 1 && (int)(n & 1) != t) continue;
                     if (!wait(C::b_s_full + t, mine++, n == 0 ? kFirstWait : kWaitLimit)) return;
                     umma::fence_after();
@@ -378,14 +408,14 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         }
                         wait_st();
                     }
-                    uint32_t s[2][32];
+                    uint32_t s[CHUNK / 32][32];
                     float top = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        load64(ts + c * 64, s);
+                    for (int c = 0; c < 128 / CHUNK; ++c) {
+                        load_scores(ts + c * CHUNK, s);
                         float tops[4] = {top, top, top, top};
 #pragma unroll
-                        for (int i = 0; i < 64; i += 2)
+                        for (int i = 0; i < CHUNK; i += 2)
                             tops[i / 2 % 4] = fmaxf(tops[i / 2 % 4], fmaxf(__uint_as_float(s[i / 32][i % 32]),
                                                                            __uint_as_float(s[i / 32][i % 32 + 1])));
                         top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
@@ -417,28 +447,40 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     const float off = kLift - (m == -INFINITY ? 0.f : m);
                     const float2 fac2 = make_float2(fac, fac), off2 = make_float2(off, off);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    // the weights take the place of columns of S that have been read; the products may start on
-                    // the first half
-                    auto half = [&](int c, const uint32_t(&s0)[32], const uint32_t(&s1)[32]) {
-                        uint32_t p[32];
+                    // the weights take the place of columns of S that have been read; the products may start on the
+                    // first half
+                    auto weights = [&](int column, const uint32_t(&v)[32]) {
+                        uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const uint32_t(&v)[32] = i < 16 ? s0 : s1;
-                            const float2 y = __ffma2_rn(
-                                make_float2(__uint_as_float(v[i % 16 * 2]), __uint_as_float(v[i % 16 * 2 + 1])), fac2, off2);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 y =
+                                __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), fac2, off2);
                             const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
                             sum[i & 1] = __fadd2_rn(sum[i & 1], e);
                             p[i] = pack_f16(e.x, e.y);
                         }
-                        st32b(ts + c * 32, p);
+                        st16_async(ts + column, p);
+                    };
+                    auto release = [&](int half) {
                         wait_st();
                         umma::fence_before();
-                        arrive(bar(C::b_p_full + 2 * t + c));
+                        arrive(bar(C::b_p_full + 2 * t + half));
                     };
+                    if constexpr (QT == 2) {
+                        weights(0, s[0]);
+                        weights(16, s[1]);
+                        release(0);
+                        weights(32, s[CHUNK / 32 - 2]);
+                        weights(48, s[CHUNK / 32 - 1]);
+                        release(1);
+                    } else {
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        load64(ts + c * 64, s);
-                        half(c, s[0], s[1]);
+                        for (int c = 0; c < 2; ++c) {
+                            load_scores(ts + c * 64, s);
+                            weights(c * 32, s[0]);
+                            weights(c * 32 + 16, s[1]);
+                            release(c);
+                        }
                     }
                     sum[0] = __fadd2_rn(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
@@ -464,12 +506,14 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     fo[0] = exp2_fast(m0 - ref), fo[1] = exp2_fast(m1 - ref);
                     l = fo[0] * l0 + fo[1] * l1;
                     // a stream without a tile has no sum in tensor memory
-                    if (it.last - it.first == 1) fo[((n - 1) & 1) ^ 1] = -1.f;
+                    if (tile1 - tile0 == 1) fo[((n - 1) & 1) ^ 1] = -1.f;
                 }
                 const bool none = !some || (m == -INFINITY && l == 0.f);
-                const bool whole = it.whole();
-                const float f = none ? 0.f : whole ? (a.v_scale ? a.v_scale[it.h] : 1.f) / l : 1.f;
-                float *part = a.parts + ((size_t)me * 2 + (it.starts ? 1 : 0)) * ((size_t)C::ROWS * (D + 2));
+                const bool whole = at.it.whole();
+                const float f = none ? 0.f : whole ? (a.v_scale ? a.v_scale[at.it.h] : 1.f) / l : 1.f;
+                const int row = at.it.row0 + my, token = row / G;
+                const size_t head = (size_t)(at.walk.q.q0 + token) * a.Hq + at.it.h * G + (row - token * G);
+                float *part = a.parts + ((size_t)me * 2 + (at.it.starts ? 1 : 0)) * ((size_t)C::ROWS * (D + 2));
                 if (valid && whole && a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(l) - kLift) * kLn2;
                 if (valid && !whole) {
                     part[my] = none ? -INFINITY : m;
@@ -517,7 +561,6 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         for (int i = 0; i < 4; ++i) p[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
-                if (it.starts && !whole) job = make_int4(it.r, it.h, it.rt, walk.last_worker());
                 // the reads of O come before the next item's products: those of a row tile of two follow the
                 // weights of its own warps, those of two streams wait until both streams have read
                 umma::fence_before();
@@ -528,7 +571,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
             }
         };
         work();
-        if (tid == 0) a.jobs[me] = misc[1] ? make_int4(-1, 0, 0, 0) : job;
+        if (tid == 0) a.jobs[me] = misc[1] ? make_int4(-1, 0, 0, 0) : at.job;
     } else if (warp < C::SOFT + C::DEQ) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::R_DEQ));
         // ------------------------------------------------------------ dequant
