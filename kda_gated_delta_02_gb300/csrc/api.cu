@@ -1238,6 +1238,7 @@ int kda_cache4_append(const void *k, const void *v, const int32_t *slot_map, voi
     if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return KDA_ERR_ALIGNMENT;
     if (int rc = row_stride(k_stride, (long long)Hkv * d, in_dtype)) return rc;
     if (int rc = row_stride(v_stride, (long long)Hkv * d, in_dtype)) return rc;
+    if ((long long)T * Hkv > 0xfffff000LL) return KDA_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return KDA_OK;
     const long long size = in_dtype == KDA_DTYPE_BF16 ? 2 : 4;
     kda::Cache4RowsArgs a{k, v, k_stride, v_stride, nullptr, nullptr, slot_map, static_cast<uint8_t *>(cache), k_scale,
@@ -1257,6 +1258,7 @@ int kda_cache4_read(const void *cache, const int32_t *slots, int n, int Hkv, int
     if (int rc = cache4_shape(Hkv, d, num_pages, page_size, out_dtype, &shift)) return rc;
     if (!cache || (n > 0 && (!k || !v || !slots))) return KDA_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return KDA_ERR_ALIGNMENT;
+    if ((long long)n * Hkv > 0xfffff000LL) return KDA_ERR_UNSUPPORTED_SHAPE;
     if (n == 0) return KDA_OK;
     kda::Cache4RowsArgs a{nullptr, nullptr, 0, 0, k, v, slots,
                           const_cast<uint8_t *>(static_cast<const uint8_t *>(cache)), k_scale, v_scale, n, Hkv,
@@ -1284,7 +1286,7 @@ int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_
     if (R < 1 || T < 0 || max_pages < 1 || max_new < 0 || window < 0) return KDA_ERR_INVALID_ARG;
     if (int rc = cache4_shape(Hkv, d, num_pages, page_size, in_dtype, &shift)) return rc;
     if (Hq < 1 || Hq % Hkv || ((long long)max_pages << shift) > 0x7fffffffLL ||
-        (long long)T * (Hq / Hkv) > 0x7fffffffLL)
+        (long long)T * (Hq / Hkv) > 0x7fffff00LL)
         return KDA_ERR_UNSUPPORTED_SHAPE;
     if (!cache || !block_table || !seq_len || !cu_seqlens || (T > 0 && (!q || !o))) return KDA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(workspace)) return KDA_ERR_ALIGNMENT;

@@ -143,7 +143,7 @@ template <int D, bool BF16, bool SCALED>
 __global__ void __launch_bounds__(256)
 kda_cache4_append_kernel(Cache4RowsArgs a) {
     constexpr int GROUPS = D / 16;  // lanes of a token and head: 8 or 4 neighbours in a warp
-    const uint32_t th = blockIdx.x * (256 / GROUPS) + threadIdx.x / GROUPS;  // below 2^32 (checked at the launch)
+    const uint32_t th = blockIdx.x * (256 / GROUPS) + threadIdx.x / GROUPS;  // below 2^32
     const int grp = threadIdx.x % GROUPS;
     const uint32_t t = th / (uint32_t)a.Hkv, h = th - t * (uint32_t)a.Hkv;
     const bool live = t < (uint32_t)a.T;
@@ -234,8 +234,7 @@ kda_cache4_read_kernel(Cache4RowsArgs a) {
 
 template <bool READ, int D, bool BF16>
 cudaError_t launch(const Cache4RowsArgs &a, cudaStream_t st) {
-    const long long th = (long long)a.T * a.Hkv, per = 256 / (D / 16);
-    if (th + per > 0xffffffffLL) return cudaErrorInvalidValue;
+    const long long th = (long long)a.T * a.Hkv, per = 256 / (D / 16);  // th below 2^32 - 2^12 (checked by the caller)
     const unsigned grid = (unsigned)((th + per - 1) / per);
     if constexpr (READ) kda_cache4_read_kernel<D, BF16><<<grid, 256, 0, st>>>(a);
     else if (a.k_scale || a.v_scale) kda_cache4_append_kernel<D, BF16, true><<<grid, 256, 0, st>>>(a);

@@ -103,7 +103,7 @@ def test_abi_refuses_before_any_launch():
 
     assert append(d=32) == -2 and append(page=8) == -2 and append(T=-1) == -1 and append(k=None) == -1 and append(slots=None) == -1
     assert append(k=p + 2) == -3 and append(ks=120) == -1 and append(vs=132) == -3 and append(dt=1, ks=130) == -3
-    assert append(T=0) == 0
+    assert append(T=0) == 0 and append(T=2 ** 31 - 1, H=3, ks=192, vs=192) == -2 and attn(T=2 ** 31 - 1) == -2
 
     def read(out=p, n=3, P=2):
         return lib.kda_cache4_read(p, p, n, 2, 64, P, 16, None, None, 0, out, p, None, None)

@@ -282,12 +282,14 @@ def test_a_marked_token_reaches_only_queries_that_see_it(n, dtype):
     assert torch.equal(o[:n - 2], clean[:n - 2])
 
 
-def test_queries_that_are_not_finite_stay_alone():
-    c = Case([50, 20], [4, 1], 4, 1, 64, 16, seed=16)
-    clean = c.run()
+@pytest.mark.parametrize("n", [4, 40])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_queries_that_are_not_finite_stay_alone(n, what):
+    c = Case([50, 20], [n, 1], 4, 1, 64, 16, seed=16)
+    clean = c.run(max_new=n)
     q = c.q.clone()
-    q[1, 2, 3] = float("nan")
-    o = c.run(q=q)
+    q[1, 2, 3] = what
+    o = c.run(q=q, max_new=n)
     assert o[1, 2].isnan().all()
     o[1, 2] = clean[1, 2]
     assert torch.equal(o, clean)
