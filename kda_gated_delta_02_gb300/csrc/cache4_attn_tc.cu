@@ -25,25 +25,32 @@
 // by more than 2^8, so the accumulator is rescaled a few times per item; f16
 // holds the weights of up to 2^15 that this allows.
 //
-// What bounds it.  QT = 2: the products take 2,048 cycles of the tensor pipe
-// per 256 rows x 128 keys at d = 128; a row tile's chain (scores, two passes
-// over them, weights, O, next scores) makes that 3,250.  632 GFLOP of prompt
-// chunks (2 x 2,048 queries of 32 heads over up to 16K keys): 486 us on the
-// device, 1.30 PFLOP/s, 67 % of the measured bf16 rate.  QT = 1: shared
-// memory, through which a key tile moves 213 KB (raw bytes in and out 45,
-// operands in 64, operand reads 96, of it Q's 128 rows 32): 1,660 cycles at
-// 128 bytes a cycle of the 1,950 that a tile takes.  64 requests of up to 8
-// queries x 96 heads (752 MB): 306 us on the device, 36 % of the measured
-// copy bandwidth.
+// What bounds it.  The products take 1,028 cycles of the tensor pipe per 128
+// rows x 128 keys at d = 128.  QT = 2: a row tile's chain (its products, the
+// scores' way to registers, weights, O, next scores) is longer than the other
+// tile's products hide: about 2,650 cycles per 256 rows x 128 keys where the
+// pipe wants 2,056.  632 GFLOP of prompt chunks (2 x 2,048 queries of 32
+// heads over up to 16K keys): 436 us with the join, 1.45 PFLOP/s, 75 % of
+// the measured bf16 rate.  QT = 1: the keys are converted for up to 128 rows
+// only, and the chains of the two streams and of the conversion (about 1,100
+// cycles of a warp per tile and as many of waiting for bytes and free
+// operands), all longer than the pipe's 1,028 cycles, make 2,200 per tile
+// together.  With either the weights' or the conversion's arithmetic taken
+// out 11 % and 14 % are gained, with both 28 %; without the copies, or with
+// half of the raw stages, nothing changes: not memory but the waits between
+// roles bound it.  64 requests of up to 8 queries x 96 heads (752 MB, a third
+// of it by the other kernel): 299 us, 37 % of the measured copy bandwidth.
 //
 // Measured on the way (us, the two calls above): one thread issuing the
 // products from a divergent branch, operands moved to uniform registers for
 // each, 591 / 451, the whole warp with an elected lane 483 / 420; one stream
 // for QT = 1 420, two 352; 145 KB of code, which overran the instruction
-// cache, 997 / 817, the roles rolled up 597 / 463.  Slower and left out:
-// copies of keys and values apart (1,152 bytes each) 406 for QT = 1; weights
-// against a stale maximum held in registers until it is checked, which wants
-// over 200 registers.
+// cache, 997 / 817, the roles rolled up 597 / 463; the maximum formed by the
+// tensor-memory load instead of by the threads 480 / 306 to 466 / 302; QT =
+// 2's registers shared out 176 / 96 / 64 (144 bytes spilled) 466, 192 / 72 /
+// 56 437, 200 / 64 / 48 (4 bytes) 428, 208 / 48 / 48 435.  Slower and left
+// out: copies of keys and values apart (1,152 bytes each) 406 for QT = 1;
+// half of a row's scores kept from maximum to weights for QT = 1, 312.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -73,11 +80,11 @@ template <int D, int QT>
 struct Cfg {
     // Whole warpgroups by role, whose registers are shared out anew at the start:
     // a CTA of 16 warps is launched with 128 a thread, one of 20 with 96.  With
-    // two row tiles a softmax thread holds its row's 128 scores; with one,
-    // memory bounds the call and conversion gets two warpgroups.
+    // two row tiles a softmax thread holds its row's 128 scores; with one
+    // there is half as much to weigh per key, and conversion gets two warpgroups.
     static constexpr int SOFT = 8, DEQ = QT == 2 ? 4 : 8, WARPS = SOFT + DEQ + 4, THREADS = WARPS * 32;
     static constexpr int R_LAUNCH = QT == 2 ? 128 : 96;
-    static constexpr int R_SOFT = QT == 2 ? 176 : 112, R_DEQ = QT == 2 ? 96 : 80, R_MISC = QT == 2 ? 64 : 96;
+    static constexpr int R_SOFT = QT == 2 ? 200 : 128, R_DEQ = QT == 2 ? 64 : 72, R_MISC = QT == 2 ? 48 : 80;
     // the others give up what the softmax warpgroups take, and nobody waits for more than there is
     static_assert(R_SOFT >= R_LAUNCH && R_DEQ <= R_LAUNCH && R_MISC <= R_LAUNCH, "who takes and who gives registers");
     static_assert(SOFT / 4 * R_SOFT + DEQ / 4 * R_DEQ + R_MISC <= WARPS / 4 * R_LAUNCH, "registers of the CTA");
@@ -177,13 +184,35 @@ __device__ __forceinline__ void hold(uint32_t (&r)[32]) {
           "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
 }
 
+// the same, and their largest (NaN where all are, as fmaxf): the load forms it on its way
+__device__ __forceinline__ void ld32_max_async(uint32_t taddr, uint32_t (&r)[32], float &top) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=f"(top)
+        : "r"(taddr)
+        : "memory");
+}
+
+// 32 N scores of this thread's row; returns their largest
 template <int N>
-__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&s)[N][32]) {
+__device__ __forceinline__ float load_scores(uint32_t taddr, uint32_t (&s)[N][32]) {
+    float top[N];
 #pragma unroll
-    for (int c = 0; c < N; ++c) ld32_async(taddr + c * 32, s[c]);
+    for (int c = 0; c < N; ++c) ld32_max_async(taddr + c * 32, s[c], top[c]);
     umma::wait_ld();
 #pragma unroll
-    for (int c = 0; c < N; ++c) hold(s[c]);
+    for (int c = 0; c < N; ++c) {
+        hold(s[c]);
+        asm volatile("" : "+f"(top[c]) : : "memory");
+    }
+#pragma unroll
+    for (int c = 1; c < N; ++c) top[0] = fmaxf(top[0], top[c]);
+    return top[0];
 }
 __device__ __forceinline__ void st32b(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
@@ -411,15 +440,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     uint32_t s[CHUNK / 32][32];
                     float top = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 128 / CHUNK; ++c) {
-                        load_scores(ts + c * CHUNK, s);
-                        float tops[4] = {top, top, top, top};
-#pragma unroll
-                        for (int i = 0; i < CHUNK; i += 2)
-                            tops[i / 2 % 4] = fmaxf(tops[i / 2 % 4], fmaxf(__uint_as_float(s[i / 32][i % 32]),
-                                                                           __uint_as_float(s[i / 32][i % 32 + 1])));
-                        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    }
+                    for (int c = 0; c < 128 / CHUNK; ++c) top = fmaxf(top, load_scores(ts + c * CHUNK, s));
                     // (the scores that have arrived came after the queries and their factors)
                     if (QT == 1 && !begun) fac = reinterpret_cast<volatile float *>(smem + C::off_fac)[(items & 1) * C::ROWS + my];
                     top *= fac;
