@@ -1273,8 +1273,8 @@ size_t kda_cache4_attention_workspace_size(int R, int T, int Hq, int Hkv, int d,
     if (R < 1 || T < 0 || Hq < 1 || Hkv < 1 || !dim_ok(d) || (in_dtype != KDA_DTYPE_BF16 && in_dtype != KDA_DTYPE_F32))
         return 0;
     const int sms = sm_count();
-    const size_t a = kda::cache4_attn_workspace(sms, d), b = kda::cache4_attn_tc_workspace(sms, d);
-    return align256(a > b ? a : b);
+    const size_t few = align256(kda::cache4_attn_workspace(sms, d));
+    return in_dtype == KDA_DTYPE_BF16 ? few + align256(kda::cache4_attn_tc_workspace(sms, d)) : few;
 }
 
 int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_table, const int32_t *seq_len,
@@ -1305,33 +1305,37 @@ int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_
     // kFewRows go to the warps' kernel, more (of bf16 queries) to the tcgen05
     // one, request by request: a batch of single tokens and prompt chunks
     // runs both.  Only one is launched where all requests are of one kind: by
-    // the bound, or because T shows that every request has max_new queries.
+    // the bound, by the group's heads, or because T shows that every request
+    // has max_new queries.
     constexpr int kFewRows = 16, kAll = 0x7fffffff;
     const bool bf16 = in_dtype == KDA_DTYPE_BF16;
     const long long most = max_new > 0 && max_new < T ? max_new : T;
-    const long long rows = most * (Hq / Hkv);
-    const bool many = bf16 && rows > kFewRows, few = !many || most * R != T;
+    const long long group = Hq / Hkv, rows = most * group;
+    const bool many = bf16 && rows > kFewRows, few = !many || (most * R != T && group <= kFewRows);
+    // (beside longer requests most of the few rows are single tokens: a group's heads)
+    const long long width = many ? group : rows;
+    a.rows_above = 0;
+    a.rows_to = many ? kFewRows : kAll;
+    kda::Cache4AttnArgs b = a;
+    // a workspace of its own: its CTAs take their places as the other kernel's leave
+    ws += align256(kda::cache4_attn_workspace(sms, d));
+    b.jobs = reinterpret_cast<int4 *>(ws);
+    b.parts = reinterpret_cast<float *>(ws + (size_t)sms * sizeof(int4));
+    b.rows_above = few ? kFewRows : 0;
+    b.rows_to = kAll;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (few) {
-        a.rows_above = 0;
-        a.rows_to = many ? kFewRows : kAll;
-        // (beside longer requests most of the few rows are single tokens: a group's heads)
-        const long long width = many ? Hq / Hkv : rows;
+    if (few)
         e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st,
                          [&] { return kda::launch_cache4_attn(a, d, bf16, width, sms, st); });
-        if (e == cudaSuccess)
-            e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st,
-                             [&] { return kda::launch_cache4_merge(a, d, bf16, width, sms, st); });
-    }
-    if (many && e == cudaSuccess) {
-        a.rows_above = few ? kFewRows : 0;
-        a.rows_to = kAll;
-        e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st, [&] { return kda::launch_cache4_attn_tc(a, d, rows, sms, st); });
-        if (e == cudaSuccess)
-            e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st,
-                             [&] { return kda::launch_cache4_merge_tc(a, d, rows, sms, st); });
-    }
+    if (many && e == cudaSuccess)
+        e = timed_launch(KDA_KERNEL_CACHE4_ATTN, st,
+                         [&] { return kda::launch_cache4_attn_tc(b, d, rows, sms, few, st); });
+    if (e == cudaSuccess)
+        e = timed_launch(KDA_KERNEL_CACHE4_MERGE, st, [&] {
+            return kda::launch_cache4_merge(a, b, d, bf16, few ? kda::cache4_attn_rows(bf16, width) : 0,
+                                            many ? kda::cache4_attn_tc_rows(rows) : 0, sms, st);
+        });
     return cuda_status(e);
 }
 

@@ -49,9 +49,9 @@ using namespace cache4;
 // across lanes, the schedule) was a sixth of the instructions at 32 keys, and
 // instruction issue is what comes after the copies here: 64 keys, in 12 warps
 // of up to 168 registers.
-constexpr int kTile = 64;                // keys per tile
+constexpr int kTile = FewRows::TILE;     // keys per tile
 constexpr int kBlocks = kTile / 16;      // blocks per tile
-constexpr int kLead = 2;                 // an item's start and end, in tiles
+constexpr int kLead = FewRows::LEAD;     // an item's start and end, in tiles
 constexpr int kWarps = 12;               // workers per CTA
 constexpr int stages(int d) { return d == 128 ? 2 : 4; }  // tiles in flight per worker: 221 KB
 // The first wait for a tile's copy: a test build (KDA_TEST_SHORT_FIRST_WAIT) gives up on it
@@ -61,7 +61,7 @@ constexpr uint32_t kFirstWait = 0;
 #else
 constexpr uint32_t kFirstWait = kWaitLimit;
 #endif
-constexpr float kLift = 15.f; // weights are 2^(s - max + kLift), at most 2^15 of f16's 65504
+constexpr float kLift = FewRows::LIFT;  // weights are 2^(s - max + kLift), at most 2^15 of f16's 65504
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -496,11 +496,6 @@ cudaError_t launch_attn(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int D, int NT, bool F32>
-cudaError_t launch_merge(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
-    return merge_shares<D, 8 * NT, kTile, kLead, F32>(a, cache4_attn_workers(sms), kLift, st);
-}
-
 }  // namespace
 
 int cache4_attn_workers(int sms) { return sms * kWarps; }
@@ -511,17 +506,17 @@ size_t cache4_attn_workspace(int sms, int d) {
 // 16 rows a tile when a request may have more than 8 (the keys' conversion to
 // f16 is then shared by two products); 32-bit queries have two f16 parts and
 // keep 8.
-#define KDA_ATTN(F)                                                                       \
-    const bool wide = bf16 && rows > 8;                                                   \
-    if (d == 128)                                                                         \
-        return !bf16 ? F<128, 1, true>(a, sms, st) : wide ? F<128, 2, false>(a, sms, st) : F<128, 1, false>(a, sms, st); \
-    return !bf16 ? F<64, 1, true>(a, sms, st) : wide ? F<64, 2, false>(a, sms, st) : F<64, 1, false>(a, sms, st);
+int cache4_attn_rows(bool bf16, long long rows) { return bf16 && rows > 8 ? 16 : 8; }
 
 cudaError_t launch_cache4_attn(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st) {
-    KDA_ATTN(launch_attn)
-}
-cudaError_t launch_cache4_merge(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st) {
-    KDA_ATTN(launch_merge)
+    const bool wide = cache4_attn_rows(bf16, rows) == 16;
+    if (d == 128)
+        return !bf16 ? launch_attn<128, 1, true>(a, sms, st)
+               : wide ? launch_attn<128, 2, false>(a, sms, st)
+                      : launch_attn<128, 1, false>(a, sms, st);
+    return !bf16 ? launch_attn<64, 1, true>(a, sms, st)
+           : wide ? launch_attn<64, 2, false>(a, sms, st)
+                  : launch_attn<64, 1, false>(a, sms, st);
 }
 
 }  // namespace kda

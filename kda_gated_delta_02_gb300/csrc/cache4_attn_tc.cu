@@ -39,7 +39,7 @@
 // out 11 % and 14 % are gained, with both 28 %; without the copies, or with
 // half of the raw stages, nothing changes: not memory but the waits between
 // roles bound it.  64 requests of up to 8 queries x 96 heads (752 MB, a third
-// of it by the other kernel): 299 us, 37 % of the measured copy bandwidth.
+// of it by the other kernel): 293 us, 38 % of the measured copy bandwidth.
 //
 // Measured on the way (us, the two calls above): one thread issuing the
 // products from a divergent branch, operands moved to uniform registers for
@@ -64,8 +64,8 @@ namespace {
 
 using namespace cache4;
 
-constexpr int kTile = 128;    // keys per tile
-constexpr int kLead = 5;      // an item's start and end, in tiles
+constexpr int kTile = ManyRows::TILE;    // keys per tile
+constexpr int kLead = ManyRows::LEAD;    // an item's start and end, in tiles
 // The first wait for scores: a test build (KDA_TEST_SHORT_FIRST_WAIT) gives up on it
 // at once, to exercise the way out.
 #ifdef KDA_TEST_SHORT_FIRST_WAIT
@@ -73,7 +73,7 @@ constexpr uint32_t kFirstWait = 0;
 #else
 constexpr uint32_t kFirstWait = kWaitLimit;
 #endif
-constexpr float kLift = 7.f;  // weights are at most 2^(kLift + kSlack)
+constexpr float kLift = ManyRows::LIFT;  // weights are at most 2^(kLift + kSlack)
 constexpr float kSlack = 8.f;
 
 template <int D, int QT>
@@ -864,17 +864,27 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     umma::fence_after();
     if (tid == 0 && misc[1] && a.status) atomicOr(a.status, KDA_STATUS_TIMEOUT);
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
+    wait_for_primary();
 }
 
 template <int D, int QT>
-cudaError_t launch(const Cache4AttnArgs &a, int sms, cudaStream_t st) {
+cudaError_t launch(const Cache4AttnArgs &a, int sms, bool beside, cudaStream_t st) {
     auto kernel = kda_cache4_attn_tc_kernel<D, QT>;
     constexpr int bytes = Cfg<D, QT>::SMEM;
     static_assert(bytes <= 232448, "shared memory of one CTA");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<sms, Cfg<D, QT>::THREADS, bytes, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sms);
+    cfg.blockDim = dim3(Cfg<D, QT>::THREADS);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = beside ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
@@ -884,16 +894,11 @@ size_t cache4_attn_tc_workspace(int sms, int d) {
 }
 
 // two row tiles at a time when a request may have more than 128 rows
-cudaError_t launch_cache4_attn_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, cudaStream_t st) {
-    if (rows > 128) return d == 128 ? launch<128, 2>(a, sms, st) : launch<64, 2>(a, sms, st);
-    return d == 128 ? launch<128, 1>(a, sms, st) : launch<64, 1>(a, sms, st);
-}
-cudaError_t launch_cache4_merge_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, cudaStream_t st) {
-    if (rows > 128)
-        return d == 128 ? merge_shares<128, 256, kTile, kLead, false>(a, sms, kLift, st)
-                        : merge_shares<64, 256, kTile, kLead, false>(a, sms, kLift, st);
-    return d == 128 ? merge_shares<128, 128, kTile, kLead, false>(a, sms, kLift, st)
-                    : merge_shares<64, 128, kTile, kLead, false>(a, sms, kLift, st);
+int cache4_attn_tc_rows(long long rows) { return rows > 128 ? 256 : 128; }
+
+cudaError_t launch_cache4_attn_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, bool beside, cudaStream_t st) {
+    if (cache4_attn_tc_rows(rows) == 256) return d == 128 ? launch<128, 2>(a, sms, beside, st) : launch<64, 2>(a, sms, beside, st);
+    return d == 128 ? launch<128, 1>(a, sms, beside, st) : launch<64, 1>(a, sms, beside, st);
 }
 
 }  // namespace kda

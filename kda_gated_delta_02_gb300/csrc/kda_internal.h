@@ -233,12 +233,18 @@ struct Cache4AttnArgs {
 // warps that share the work of a call, and the workspace they need
 int cache4_attn_workers(int sms);
 size_t cache4_attn_workspace(int sms, int d);
-// rows: an upper bound of the query rows (tokens x heads of a group) of one request
+// rows: an upper bound of the query rows (tokens x heads of a group) of one
+// request; _rows: the rows of a tile for it
+int cache4_attn_rows(bool bf16, long long rows);
 cudaError_t launch_cache4_attn(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st);
-cudaError_t launch_cache4_merge(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st);
 // The same on the tcgen05 tensor cores, for bf16 queries with many rows (cache4_attn_tc.cu).
 size_t cache4_attn_tc_workspace(int sms, int d);
-cudaError_t launch_cache4_attn_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, cudaStream_t st);
-cudaError_t launch_cache4_merge_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, cudaStream_t st);
+int cache4_attn_tc_rows(long long rows);
+// beside: CTAs start as those of the kernel launched before leave; they read
+// nothing that it writes, and end after it has
+cudaError_t launch_cache4_attn_tc(const Cache4AttnArgs &a, int d, long long rows, int sms, bool beside, cudaStream_t st);
+// Joins the shares of either or both (cache4_merge.cu); the rows of their tiles, 0 for one that did not run.
+cudaError_t launch_cache4_merge(const Cache4AttnArgs &few, const Cache4AttnArgs &many, int d, bool bf16, int few_rows,
+                                int many_rows, int sms, cudaStream_t st);
 
 }  // namespace kda
