@@ -10,7 +10,7 @@
 //   dequant    4 or 8   half for the keys and half for the values: codes and
 //                       scales -> f16 (exact), into the swizzled shared-
 //                       memory operands K (K-major) and V (N-major)
-//   producer   1 warp   bulk copies of 64 keys at a time into a raw ring
+//   producer   1 warp   bulk copies of 64 (QT = 1: 128) keys at a time into a raw ring
 //   products   1 warp   S = Q K^T into tensor memory, O += P V with P read
 //                       from tensor memory (it takes the place of S)
 //   queries    2 warps  QT = 1: the next item's query rows, scaled, as f16
@@ -28,18 +28,17 @@
 // What bounds it.  The products take 1,028 cycles of the tensor pipe per 128
 // rows x 128 keys at d = 128.  QT = 2: a row tile's chain (its products, the
 // scores' way to registers, weights, O, next scores) is longer than the other
-// tile's products hide: about 2,650 cycles per 256 rows x 128 keys where the
+// tile's products hide: about 2,800 cycles per 256 rows x 128 keys where the
 // pipe wants 2,056.  632 GFLOP of prompt chunks (2 x 2,048 queries of 32
-// heads over up to 16K keys): 436 us with the join, 1.45 PFLOP/s, 75 % of
-// the measured bf16 rate.  QT = 1: the keys are converted for up to 128 rows
-// only, and the chains of the two streams and of the conversion (about 1,100
-// cycles of a warp per tile and as many of waiting for bytes and free
-// operands), all longer than the pipe's 1,028 cycles, make 2,200 per tile
-// together.  With either the weights' or the conversion's arithmetic taken
-// out 11 % and 14 % are gained, with both 28 %; without the copies, or with
-// half of the raw stages, nothing changes: not memory but the waits between
-// roles bound it.  64 requests of up to 8 queries x 96 heads (752 MB, a third
-// of it by the other kernel): 293 us, 38 % of the measured copy bandwidth.
+// heads over up to 16K keys): 430 us with the join, 1.47 PFLOP/s, 76 % of
+// the measured bf16 rate; 371 without the softmax, 391 without the
+// conversion, 366 without both.  QT = 1: a key tile's conversion serves up to
+// 128 rows only, and it and the two streams' softmax share the SM's issue
+// slots beside products that the padded row tile makes as long as a full
+// one's.  64 requests of up to 8 queries x 96 heads (752 MB, a third of it by
+// the other kernel, 85 us): 279 us, 40 % of the measured copy bandwidth; 263
+// without the softmax, 255 without the conversion, 230 without both, which is
+// the pipe's time.  Memory bounds neither: copies taken out gain nothing.
 //
 // Measured on the way (us, the two calls above): one thread issuing the
 // products from a divergent branch, operands moved to uniform registers for
@@ -48,9 +47,12 @@
 // cache, 997 / 817, the roles rolled up 597 / 463; the maximum formed by the
 // tensor-memory load instead of by the threads 480 / 306 to 466 / 302; QT =
 // 2's registers shared out 176 / 96 / 64 (144 bytes spilled) 466, 192 / 72 /
-// 56 437, 200 / 64 / 48 (4 bytes) 428, 208 / 48 / 48 435.  Slower and left
+// 56 437, 200 / 64 / 48 (4 bytes) 428, 208 / 48 / 48 435; raw stages of 128
+// keys for QT = 1, with half of the waits of those of 64, 295 to 279.  Slower and left
 // out: copies of keys and values apart (1,152 bytes each) 406 for QT = 1;
-// half of a row's scores kept from maximum to weights for QT = 1, 312.
+// half of a row's scores kept from maximum to weights for QT = 1, 312; the
+// accumulator rescaled after the first weights instead of before them 441 for
+// QT = 2; one arrival per warp instead of per thread 437 for QT = 2.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -90,8 +92,8 @@ struct Cfg {
     static_assert(SOFT / 4 * R_SOFT + DEQ / 4 * R_DEQ + R_MISC <= WARPS / 4 * R_LAUNCH, "registers of the CTA");
     static constexpr int ROWS = 128 * QT;
     static constexpr int OPERAND = 128 * D * 2;       // 128 rows of f16
-    static constexpr int RAW = 4 * block_bytes(D);    // 64 keys
-    static constexpr int RAWS = QT == 2 ? 3 : 6;      // raw stages
+    static constexpr int KEYS = QT == 2 ? 64 : 128;   // keys of a raw stage
+    static constexpr int RAW = KEYS / 16 * block_bytes(D), RAWS = 3;
     static constexpr int off_q = 0, off_k = QT * OPERAND, off_v = off_k + 2 * OPERAND, off_raw = off_v + 2 * OPERAND;
     static constexpr int off_bar = off_raw + RAWS * RAW;
     // barriers: raw full / empty, K and V full / empty, S full, P full (two halves), O done, Q full /
@@ -604,13 +606,13 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         // Keys: four lanes per key; lane g takes the channel groups g and (d =
         // 128) g + 4, so the eight lanes of a 128-byte store row write eight
         // different chunks.
-        constexpr int K_ROWS = THR / 4, K_STEPS = 64 / K_ROWS * NK;       // keys per pass; conversions per 64 keys
+        constexpr int K_ROWS = THR / 4, K_STEPS = C::KEYS / K_ROWS * NK;       // keys per pass; conversions per stage
         // Values: sixteen lanes per block and group, a key each.
-        constexpr int PAIRS = THR / 16, V_STEPS = 4 * NG / PAIRS;         // (block, group) pairs per pass
+        constexpr int PAIRS = THR / 16, V_STEPS = C::KEYS / 16 * NG / PAIRS;         // (block, group) pairs per pass
         constexpr int SPLIT = NG > PAIRS ? NG / PAIRS : 1;                // passes over the groups of a block
         constexpr int V_BLKS = PAIRS > NG ? PAIRS / NG : 1;               // blocks per pass
         uint32_t codes, scale, out0, out1;
-        int blk_key;  // key of the first conversion in its 64
+        int blk_key;  // key of the first conversion in its stage
         if (for_keys) {
             const int key = e >> 2, g = e & 3;
             codes = (key >> 4) * BB + (key & 15) * (D / 2) + g * 8;
@@ -632,7 +634,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                 for (int tile = it.first; tile < it.last; ++tile, ++n) {
                     if (!wait(b_empty + (n & 1), (n >> 1) + 1)) return;
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half, ++raws) {
+                    for (int half = 0; half < kTile / C::KEYS; ++half, ++raws) {
                         const uint32_t ri = raws % C::RAWS;
                         if (!wait(C::b_raw_full + ri, raws / C::RAWS)) return;
                         const uint32_t raw = sb + C::off_raw + ri * C::RAW;
@@ -657,7 +659,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         } else {
                             const uint32_t out = sb + C::off_v + (n & 1) * C::OPERAND + half * (8 * NK * 1024);
                             // past the end the bytes are anything, NaN scales too: a zero weight does not undo that
-                            const int left = walk.q.len - (tile * kTile + half * 64 + blk_key);
+                            const int left = walk.q.len - (tile * kTile + half * C::KEYS + blk_key);
 #pragma unroll
                             for (int p = 0; p < V_STEPS; p += BATCH) {
 #pragma unroll
@@ -691,7 +693,8 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
     if (warp == C::SOFT + C::DEQ) {
         // ------------------------------------------------------------ producer
         uint32_t raws = 0;
-        const int chunk = a.page_shift < 6 ? 1 << (a.page_shift - 4) : 4;  // blocks per copy
+        constexpr int BLOCKS = C::KEYS / 16;
+        const int chunk = min(1 << (a.page_shift - 4), BLOCKS);  // blocks per copy
         auto work = [&]() {
             while (walk.next(a, it)) {
                 const int32_t *table = a.block_table + (size_t)it.r * a.max_pages;
@@ -700,14 +703,14 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
 #pragma unroll 1
                 for (int tile = it.first; tile < it.last; ++tile)
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half, ++raws) {
+                    for (int half = 0; half < kTile / C::KEYS; ++half, ++raws) {
                         const uint32_t ri = raws % C::RAWS;
-                        const int key0 = tile * kTile + half * 64, key = key0 + lane * chunk * 16;
+                        const int key0 = tile * kTile + half * C::KEYS, key = key0 + lane * chunk * 16;
                         // blocks of this lane's copy that hold keys
                         const int left = (walk.q.len - key + 15) >> 4;
-                        const int mine = lane * chunk < 4 ? min(max(left, 0), chunk) : 0;
+                        const int mine = lane * chunk < BLOCKS ? min(max(left, 0), chunk) : 0;
                         const int page0 = key0 >> a.page_shift;
-                        if (page0 + 3 >= from + held) {
+                        if (page0 + BLOCKS - 1 >= from + held) {
                             from = page0, held = 32;
                             entry = 0;
                             if (from + lane < pages) {
