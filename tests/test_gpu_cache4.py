@@ -459,3 +459,28 @@ def test_a_wait_that_runs_out_is_reported(new):
     torch.cuda.synchronize()
     assert st.item() & kda.STATUS_TIMEOUT
     c.check(max_new=new)
+
+
+@pytest.mark.parametrize("Hq,H,d", [(16, 1, 128), (17, 1, 64), (34, 2, 128), (48, 1, 64)])
+def test_ragged_batches_at_the_widest_group_of_few_rows(Hq, H, d):
+    """Single tokens, none and several beside one another, where a group's heads are as many as the few-row kernel takes,
+    and more."""
+    Case([70, 40, 300, 1, 129], [1, 0, 8, 1, 2], Hq, H, d, 32, seed=Hq).check(max_new=8)
+
+
+def test_calls_in_a_row_on_one_workspace():
+    """Kernels of a call start while its others end; those of the next call on the same workspace do not."""
+    cases = [Case([900, 64, 300, 2000, 33], [1, 40, 1, 5, 2], 8, 1, 128, 64, seed=31),
+             Case([129, 1500, 40, 700], [100, 1, 1, 300], 8, 1, 128, 64, seed=32)]
+    alone = [c.run() for c in cases]
+    R, T = 5, max(c.q.shape[0] for c in cases)
+    ws = torch.empty(kda.cache4_attention_workspace_size(R, T, 8, 1, 128), dtype=torch.uint8, device="cuda")
+    q = [c.q.cuda() for c in cases]
+    outs = [[torch.empty_like(x) for x in q] for _ in range(10)]
+    torch.cuda.synchronize()
+    for o in outs:
+        for c, x, out in zip(cases, q, o):
+            kda.cache4_attention(x, *c.args, out=out, workspace=ws)
+    for o in outs:
+        for a, b in zip(o, alone):
+            assert torch.equal(a, b)
