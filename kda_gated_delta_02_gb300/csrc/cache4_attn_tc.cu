@@ -104,8 +104,11 @@ struct Cfg {
                          b_q_empty = b_k_full + 17, b_o_free = b_k_full + 18, b_pair = b_k_full + 19,
                          b_drain = b_k_full + 20, BARS = b_k_full + 21;
     static constexpr int off_misc = off_bar + BARS * 8;  // TMEM address, dead flag
-    static constexpr int off_ml = off_misc + 16;         // maxima and sums of the two streams
-    static constexpr int off_fac = off_ml + 2 * 128 * 8; // factors of the rows' scores, two items
+    // maxima and sums of the two streams, in two places that items take in turn: a stream without a tile
+    // of the next item waits for nothing before it writes that item's, and the other may still be reading
+    static constexpr int PAIR_PLACES = 2;
+    static constexpr int off_ml = off_misc + 16;
+    static constexpr int off_fac = off_ml + PAIR_PLACES * 2 * 128 * 8; // factors of the rows' scores, two items
     static constexpr int off_item = (off_fac + 2 * ROWS * 4 + 15) & ~15;  // the softmax warps' place in the work
     static constexpr int SMEM = off_item + SOFT * 176;
     // tensor memory columns: S (and P over it) 2 x 128, O 2 x D
@@ -515,7 +518,8 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                 // with one row tile the streams' results are joined: each takes half the channels
                 float fo[2] = {1.f, 1.f};
                 if (QT == 1 && some) {
-                    volatile float2 *ml = reinterpret_cast<volatile float2 *>(smem + C::off_ml);
+                    volatile float2 *ml =
+                        reinterpret_cast<volatile float2 *>(smem + C::off_ml) + items % C::PAIR_PLACES * (2 * 128);
                     ml[t * 128 + r].x = begun ? m : -INFINITY;
                     ml[t * 128 + r].y = l;
                     umma::fence_before();
@@ -523,7 +527,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     if (!wait(C::b_pair, items)) return;
                     umma::fence_after();
                     const float m0 = ml[r].x, m1 = ml[128 + r].x, l0 = ml[r].y, l1 = ml[128 + r].y;
-                    // (both have read before either writes again: the next item's Q is complete only after both)
+                    // (a stream writes here again two items on, which takes the other's arrival for the item between)
                     m = fmaxf(m0, m1);
                     const float ref = m == -INFINITY ? 0.f : m;
                     fo[0] = exp2_fast(m0 - ref), fo[1] = exp2_fast(m1 - ref);
