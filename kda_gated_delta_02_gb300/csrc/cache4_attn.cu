@@ -178,7 +178,7 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                 see[nt][j] = rr < q.rows ? q.len - q.n + rr / G : -1;
             }
 
-        float m[NT][2], l[NT][2], acc[NT][KS][4];
+        float m[NT][2], l[NT][2], acc[NT][KS][4];  // (m: the largest score, without its factor)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
@@ -320,12 +320,13 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                     top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 4));
                     top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
                     top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-                    top[j] = fmaxf(m[nt][j], top[j] * fac[nt][j]);
+                    top[j] = fmaxf(m[nt][j], top[j]);
                 }
                 if (__any_sync(0xffffffffu, top[0] > m[nt][0] || top[1] > m[nt][1])) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float shrink = top[j] == -INFINITY ? 1.f : exp2_fast(m[nt][j] - top[j]);
+                        const float shrink =
+                            top[j] == -INFINITY ? 1.f : exp2_fast(scaled(m[nt][j], fac[nt][j]) - scaled(top[j], fac[nt][j]));
                         l[nt][j] *= shrink;
 #pragma unroll
                         for (int i = 0; i < KS; ++i) {
@@ -335,9 +336,22 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                         m[nt][j] = top[j];
                     }
                 }
-                float off[2];
+                float off[2], sub[2];
+                bool far = false;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) off[j] = (F32 ? 0.f : kLift) - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
+                for (int j = 0; j < 2; ++j) {
+                    const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j], at = scaled(ref, fac[nt][j]);
+                    const bool big = fabsf(at) >= kFar;
+                    far = far || big;
+                    sub[j] = big ? ref : 0.f;
+                    off[j] = (F32 ? 0.f : kLift) - (big ? 0.f : at);
+                }
+                if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+                    for (int mt = 0; mt < kBlocks; ++mt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[mt][nt][j] -= sub[j & 1];
+                }
 #pragma unroll
                 for (int mt = 0; mt < kBlocks; ++mt) {
                     float w[4];
@@ -458,7 +472,7 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                         }
                     }
                     if (a.lse && g == 0)
-                        a.lse[head] = none ? -INFINITY : (m[nt][j] + log2f(l[nt][j]) - kLift) * kLn2;
+                        a.lse[head] = none ? -INFINITY : (scaled(m[nt][j], fac[nt][j]) + log2f(l[nt][j]) - kLift) * kLn2;
                 }
         } else {
             // part 1 starts a row tile that goes on, part 0 continues one
@@ -470,7 +484,7 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                 for (int j = 0; j < 2; ++j) {
                     const int row = nt * 8 + 2 * t4 + j;
                     if (g == 0) {
-                        w[row] = m[nt][j];
+                        w[row] = scaled(m[nt][j], fac[nt][j]);
                         w[ROWS + row] = l[nt][j];
                     }
                     float4 *p = reinterpret_cast<float4 *>(w + 2 * ROWS + row * D + g * (D / 8));

@@ -443,20 +443,26 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         wait_st();
                     }
                     uint32_t s[CHUNK / 32][32];
-                    float top = -INFINITY;
+                    float off;
+                    // where the maximum is far from zero it is taken from the scores in tensor memory, and they are loaded again
 #pragma unroll 1
-                    for (int c = 0; c < 128 / CHUNK; ++c) top = fmaxf(top, load_scores(ts + c * CHUNK, s));
-                    // (the scores that have arrived came after the queries and their factors)
-                    if (QT == 1 && !begun) fac = reinterpret_cast<volatile float *>(smem + C::off_fac)[(items & 1) * C::ROWS + my];
-                    top *= fac;
-                    if (!begun) {
-                        m = top;
+                    for (bool lowered = false;; lowered = true) {
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < 128 / CHUNK; ++c) top = fmaxf(top, load_scores(ts + c * CHUNK, s));
+                        if (lowered) break;
+                        // (the scores that have arrived came after the queries and their factors)
+                        if (QT == 1 && !begun)
+                            fac = reinterpret_cast<volatile float *>(smem + C::off_fac)[(items & 1) * C::ROWS + my];
+                        if (!begun) m = top;
                         begun = true;
-                    } else {
+                        const bool rise = (top - m) * fac > kSlack;  // (false where both are -inf)
+                        const float low = scaled(m == -INFINITY ? 0.f : m, fac);
+                        off = kLift - low;
+                        if (!__any_sync(0xffffffffu, rise || fabsf(low) >= kFar)) break;
                         // (this stream's last product onto O came before the scores that have arrived)
-                        const bool rise = top > m + kSlack || (m == -INFINITY && top > m);
                         if (__any_sync(0xffffffffu, rise)) {
-                            const float f = rise ? exp2_fast(m - top) : 1.f;
+                            const float f = rise ? exp2_fast(scaled(m, fac) - scaled(top, fac)) : 1.f;
                             l *= f;
                             if (rise) m = top;
 #pragma unroll 1
@@ -469,8 +475,24 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                                 st16(to + c * 16, u);
                             }
                         }
+                        const float ref = m == -INFINITY ? 0.f : m;
+                        const bool big = fabsf(scaled(ref, fac)) >= kFar;
+                        off = kLift - (big ? 0.f : scaled(ref, fac));
+                        if (!__any_sync(0xffffffffu, big)) break;
+                        const float sub = big ? ref : 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t v[32];
+                            ld32_async(ts + c * 32, v);
+                            umma::wait_ld();
+                            hold(v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) - sub);
+                            st32b(ts + c * 32, v);
+                        }
+                        wait_st();
+                        if (QT == 1) break;
                     }
-                    const float off = kLift - (m == -INFINITY ? 0.f : m);
                     const float2 fac2 = make_float2(fac, fac), off2 = make_float2(off, off);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     // the weights take the place of columns of S that have been read; the products may start on the
@@ -503,7 +525,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
 #pragma unroll 1
                         for (int c = 0; c < 2; ++c) {
                             load_scores(ts + c * 64, s);
-                            weights(c * 32, s[0]);
+                                weights(c * 32, s[0]);
                             weights(c * 32 + 16, s[1]);
                             release(c);
                         }
@@ -511,6 +533,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     sum[0] = __fadd2_rn(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                 }
+                m = scaled(m, fac);
                 if (some) {
                     if (mine > 0 && !wait(C::b_o_done + t, mine - 1)) return;
                     umma::fence_after();
@@ -520,7 +543,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                 if (QT == 1 && some) {
                     volatile float2 *ml =
                         reinterpret_cast<volatile float2 *>(smem + C::off_ml) + items % C::PAIR_PLACES * (2 * 128);
-                    ml[t * 128 + r].x = begun ? m : -INFINITY;
+                    ml[t * 128 + r].x = m;
                     ml[t * 128 + r].y = l;
                     umma::fence_before();
                     arrive(bar(C::b_pair));

@@ -25,6 +25,16 @@ namespace cache4 {
 
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A weight is 2^(score * factor + (lift - maximum * factor)), one multiply-add.
+// The rounding of the maximum and of the offset lifts the largest weight by a
+// step of fp32 at the maximum, 2^-3 at most below this, which f16 has room
+// for.  From here on (where a score's own rounding is a factor of 2^(1/16) and
+// more) the maximum is taken from the scores first, so that no weight is above
+// 2^lift and the largest is never lost.
+constexpr float kFar = 1048576.f;
+// A maximum with its factor, rounded as it stands: two of the same value cancel
+// (fused into a difference they would leave the product's rounding).
+__device__ __forceinline__ float scaled(float top, float fac) { return __fmul_rn(top, fac); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;

@@ -1,6 +1,8 @@
 """The paged 4-bit cache on the GPU: rows in and out against the format's
 definition, and attention against a 64-bit reference on the cache's own bytes,
 with per-element bounds from the kernel's roundings (cache4_ref)."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
@@ -484,3 +486,36 @@ def test_calls_in_a_row_on_one_workspace():
     for o in outs:
         for a, b in zip(o, alone):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("power", [15, 20, 21, 24, 40])
+@pytest.mark.parametrize("lengths,new,Hq,H,d", [([150, 33, 7000], [1, 3, 1], 8, 2, 128), ([300, 20], [40, 20], 2, 1, 64),
+                                                ([333, 9000], [90, 40], 6, 2, 128)])
+def test_scores_far_apart(lengths, new, Hq, H, d, power, dtype):
+    """Scores of 2^power and more: one key takes all where the next is further away than the scores' rounding, the output
+    is then its value (the weight's rounding to f16 for bf16 calls, then the output's own), and every row is finite and
+    no larger than the largest value."""
+    c = Case(lengths, new, Hq, H, d, 32, dtype, seed=power + d, gain=2.0 ** power)
+    o, lse = c.run(return_lse=True, max_new=max(new))
+    keys, values = ref.decode(c.cache.cpu().numpy(), d)
+    want, want_lse, _, _, top = c.want()
+    o, lse, q, G, clear = to64(o), to64(lse), to64(c.q), Hq // H, 0
+    assert np.isfinite(o).all() and np.isfinite(lse).all()
+    err = top * 2.0 ** -17  # of a score (cache4_ref.attention_bounds)
+    assert np.all(np.abs(lse - want_lse) <= err + 2.0 ** -19 * (1 + np.abs(want_lse)))
+    rel = 2.0 ** -8 + 2.0 ** -11 if dtype == "bf16" else 2.0 ** -19
+    for r, (n, L) in enumerate(zip(new, lengths)):
+        pages = c.table[r, :-(-L // 32)]
+        for h in range(H):
+            k, v = (t[pages, h].reshape(-1, d)[:L] for t in (keys, values))
+            largest = np.maximum.accumulate(np.abs(v))
+            for i, x in itertools.product(range(n), range(h * G, h * G + G)):
+                row, sees = c.cu[r] + i, L - n + i + 1
+                s = k[:sees] @ q[row, x] * d ** -0.5
+                assert np.all(np.abs(o[row, x]) <= (1 + rel) * largest[sees - 1])
+                first, second = np.argmax(s), np.sort(s)[-2] if sees > 1 else -np.inf
+                if s[first] - second > 4 * err[row, x] + 40:  # e^-40 is below f16's smallest weight
+                    clear += 1
+                    assert np.all(np.abs(o[row, x] - v[first]) <= rel * np.abs(v[first]) + 2.0 ** -30)
+    assert clear > 0
