@@ -112,9 +112,9 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
         uint32_t qf[NT][PARTS][KS][2];
         float fac[NT][2];
         // the sign (and a zero) of the scale goes into the queries: the factor stays positive, so that it may
-        // follow the maximum and a masked score stays -inf
+        // follow the maximum and a masked score stays -inf (a scale that is NaN makes the queries NaN)
         const float base = a.scale * kLog2e * (a.k_scale ? a.k_scale[h] : 1.f);
-        const float sign = base < 0.f ? -1.f : base == 0.f ? 0.f : 1.f;
+        const float sign = base < 0.f ? -1.f : base > 0.f ? 1.f : base;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int rr = row0 + nt * 8 + g;

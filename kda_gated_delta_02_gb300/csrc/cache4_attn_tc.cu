@@ -263,8 +263,8 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
 
 // A query row goes in scaled by a power of two that brings its largest element
 // to [2^8, 2^9), as f16; its scores get the inverse and the softmax scale as a
-// factor.  The sign (and a zero) of the scale goes into the row, so that the
-// factor is positive and may follow the maximum.
+// factor.  The sign of the scale (a zero and NaN as well) goes into the row, so
+// that the factor is positive and may follow the maximum.
 __device__ __forceinline__ uint32_t magnitude(const uint4 &w) {  // of eight bf16, which orders as an integer
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
     uint32_t top = 0;
@@ -274,7 +274,7 @@ __device__ __forceinline__ uint32_t magnitude(const uint4 &w) {  // of eight bf1
 }
 __device__ __forceinline__ int exponent(uint32_t top) { return min(max((int)(top >> 23), 9), 253); }
 __device__ __forceinline__ float scale_up(float base, int ex) {
-    return (base < 0.f ? -1.f : base == 0.f ? 0.f : 1.f) * __uint_as_float((uint32_t)(262 - ex) << 23);
+    return (base < 0.f ? -1.f : base > 0.f ? 1.f : base) * __uint_as_float((uint32_t)(262 - ex) << 23);
 }
 __device__ __forceinline__ float factor(float base, int ex) {
     return fmaxf(fabsf(base) * __uint_as_float((uint32_t)(ex - 8) << 23), 1e-37f);

@@ -519,3 +519,22 @@ def test_scores_far_apart(lengths, new, Hq, H, d, power, dtype):
                     clear += 1
                     assert np.all(np.abs(o[row, x] - v[first]) <= rel * np.abs(v[first]) + 2.0 ** -30)
     assert clear > 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [2, 40, 200])
+def test_scales_that_are_not_finite_are_seen(n, dtype):
+    """A scale of NaN, or a head's key scale: every row that sees a key is NaN there, and a row that sees none is zero."""
+    c = Case([90, 260], [100, n], 4, 2, 64, 16, dtype, seed=41)
+    seen = torch.ones(100 + n, dtype=torch.bool)
+    seen[:10] = False  # 90 keys, 100 queries
+    o, lse = c.run(return_lse=True, scale=float("nan"))
+    assert o[seen].isnan().all() and lse[seen].isnan().all()
+    assert (o[~seen] == 0).all() and torch.isneginf(lse[~seen]).all()
+    o = c.run(scale=float("inf"))
+    assert o[seen].isnan().all() and (o[~seen] == 0).all()
+    clean = c.run()
+    c.ks = dev([1.0, float("nan")], torch.float32)
+    o, lse = c.run(return_lse=True)
+    assert o[seen][:, 2:].isnan().all() and lse[seen][:, 2:].isnan().all()
+    assert torch.equal(o[:, :2], clean[:, :2]) and (o[~seen] == 0).all()
