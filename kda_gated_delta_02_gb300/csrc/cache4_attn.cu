@@ -161,7 +161,8 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                     qf[nt][0][ks][b] = pack_f16(lo, hi);
                     if constexpr (F32) {
                         const float2 w = unpack_f16(qf[nt][0][ks][b]);
-                        qf[nt][PARTS - 1][ks][b] = pack_f16(lo - w.x, hi - w.y);
+                        // (an infinity has no second part: it stays one)
+                        qf[nt][PARTS - 1][ks][b] = pack_f16(lo == w.x ? 0.f : lo - w.x, hi == w.y ? 0.f : hi - w.y);
                     }
                 }
             // this lane's accumulator columns are rows 2 t4 and 2 t4 + 1
@@ -445,7 +446,7 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                     const int rr = row0 + nt * 8 + 2 * t4 + j;
                     if (rr >= q.rows) continue;
                     const size_t head = (size_t)(q.q0 + rr / G) * a.Hq + h * G + rr % G;
-                    const bool none = m[nt][j] == -INFINITY && l[nt][j] == 0.f;
+                    const bool none = see[nt][j] < 0;
                     const float inv = none ? 0.f : vs / l[nt][j];
                     float y[D / 8];
 #pragma unroll

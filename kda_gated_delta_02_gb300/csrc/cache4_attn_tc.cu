@@ -558,7 +558,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                     // a stream without a tile has no sum in tensor memory
                     if (tile1 - tile0 == 1) fo[((n - 1) & 1) ^ 1] = -1.f;
                 }
-                const bool none = !some || (m == -INFINITY && l == 0.f);
+                const bool none = !some || sees < 0;
                 const bool whole = at.it.whole();
                 const float f = none ? 0.f : whole ? (a.v_scale ? a.v_scale[at.it.h] : 1.f) / l : 1.f;
                 const int row = at.it.row0 + my, token = row / G;

@@ -98,7 +98,7 @@ __device__ __forceinline__ void join(const Cache4AttnArgs &a, int workers, int w
             }
         }
         const size_t head = (size_t)(q.q0 + rr / G) * a.Hq + job.y * G + rr % G;
-        const bool none = m == -INFINITY && sum.l == 0.f;
+        const bool none = q.len - q.n + rr / G < 0;  // sees no key (scores of -inf alone are 0 / 0)
         const float inv = none ? 0.f : (a.v_scale ? a.v_scale[job.y] : 1.f) / sum.l;
 #pragma unroll
         for (int c = 0; c < C; c += 2) {

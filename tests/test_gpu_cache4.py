@@ -538,3 +538,21 @@ def test_scales_that_are_not_finite_are_seen(n, dtype):
     o, lse = c.run(return_lse=True)
     assert o[seen][:, 2:].isnan().all() and lse[seen][:, 2:].isnan().all()
     assert torch.equal(o[:, :2], clean[:, :2]) and (o[~seen] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,new", [([1, 40], [1, 2]), ([5000], [1]), ([100, 6000], [40, 30]), ([500], [300])])
+def test_scores_of_minus_infinity_alone_are_not_an_empty_row(lengths, new, dtype):
+    """A query whose scores are all -inf has o = 0 / 0, not the zero of a query that sees nothing."""
+    c = Case(lengths, new, 4, 2, 64, 16, dtype, seed=42)
+    c.k[:, :, 5] = -3.0
+    kda.cache4_append(c.k.bfloat16().cuda(), c.v.bfloat16().cuda(), c.slots, c.cache, 16)
+    clean, lse0 = c.run(return_lse=True)
+    q = c.q.clone()
+    q[0, 1, 5] = float("inf")
+    q[-1, 2, 5] = float("inf")
+    o, lse = c.run(q=q, return_lse=True)
+    for at in ((0, 1), (q.shape[0] - 1, 2)):
+        assert o[at].isnan().all() and torch.isneginf(lse[at])
+        o[at], lse[at] = clean[at], lse0[at]
+    assert torch.equal(o, clean) and torch.equal(lse, lse0)
