@@ -530,9 +530,10 @@ int kda_decode_verify_replay_ragged(void *state, void *conv_tail, const float *c
  *  seq_len       device int32 [R], context_len + new_len.
  *  slot_map, positions  device int32 [T]: slot and position of every new
  *                token, packed by cu_seqlens; -1 past the last one.
- *  page_count_out [R], free_count_out [1]: the counts after the call (other
- *                buffers than page_count and free_count: many blocks read
- *                those).
+ *  page_count_out [R], free_count_out [1]: the counts after the call.
+ * No output overlaps an input or another output (many blocks read the inputs
+ * while others write), so context_len is not advanced in place either:
+ * KDA_ERR_INVALID_ARG.
  * A request whose lengths are negative, that does not fit max_pages, or whose
  * rows end past T sets KDA_STATUS_BAD_SEQLENS; one whose pages are not there
  * sets KDA_STATUS_NO_PAGES, and so do all later ones that need a page.  Such

@@ -1205,7 +1205,21 @@ int kda_page_plan(const int32_t *context_len, const int32_t *new_len, const int3
     if (!context_len || !new_len || !page_count || !block_table || !free_count || !cu_seqlens || !seq_len ||
         !page_count_out || !free_count_out || (num_free > 0 && !free_pages) || (T > 0 && (!slot_map || !positions)))
         return KDA_ERR_INVALID_ARG;
-    if (page_count_out == page_count || free_count_out == free_count) return KDA_ERR_INVALID_ARG;
+    // many blocks read the inputs while others write: no output overlaps an input or another output
+    const struct { const int32_t *p; long long n; } out[] = {
+        {block_table, (long long)R * max_pages}, {cu_seqlens, R + 1LL}, {seq_len, R}, {slot_map, T}, {positions, T},
+        {page_count_out, R}, {free_count_out, 1}}, in[] = {
+        {context_len, R}, {new_len, R}, {page_count, R}, {free_pages, num_free}, {free_count, 1}};
+    auto meet = [](auto &x, auto &y) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+        return x.n > 0 && y.n > 0 && a < b + 4 * (uintptr_t)y.n && b < a + 4 * (uintptr_t)x.n;
+    };
+    for (auto &x : out) {
+        for (auto &y : in)
+            if (meet(x, y)) return KDA_ERR_INVALID_ARG;
+        for (auto &y : out)
+            if (&x != &y && meet(x, y)) return KDA_ERR_INVALID_ARG;
+    }
     kda::PagePlanArgs a{context_len, new_len, page_count, free_pages, free_count, block_table, R, max_pages, num_free,
                         shift, T, cu_seqlens, seq_len, slot_map, positions, page_count_out, free_count_out, status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -117,6 +117,30 @@ def test_abi_refuses_before_any_launch():
     assert plan(count_out=p) == -1 and plan(free_out=p) == -1  # in place is not allowed
 
 
+def test_plan_refuses_outputs_over_inputs():
+    """Every output over every input and every other output: from the start, and by one element at either end."""
+    lib = kda.load_library()
+    R, B, F, T, page = 3, 4, 9, 7, 16
+    sizes = dict(context_len=R, new_len=R, page_count=R, block_table=R * B, free_pages=F, free_count=1, cu_seqlens=R + 1,
+                 seq_len=R, slot_map=T, positions=T, page_count_out=R, free_count_out=1)
+    names = list(sizes)
+    buf = ctypes.create_string_buffer(4 * sum(sizes.values()) + 4096)
+    at, start = {}, (ctypes.addressof(buf) + 2047) & ~15
+    for n in names:  # back to back
+        at[n], start = start, start + 4 * sizes[n]
+    outputs = names[6:] + ["block_table"]
+
+    def plan(at):
+        return lib.kda_page_plan(*(at[n] for n in names[:6]), R, B, F, page, T, *(at[n] for n in names[6:]), None, None)
+
+    for o in outputs:
+        for n in names:
+            if n == o:
+                continue
+            for shift in (0, sizes[n] - 1, -(sizes[o] - 1)):
+                assert plan({**at, o: at[n] + 4 * shift}) == -1, (o, n, shift)
+
+
 def test_reference_rounding():
     """The reference's nearest() and quantise() on values whose answers are known."""
     assert [ref.E2M1[ref.nearest(np.array(x), ref.E2M1)] for x in (0.25, 0.26, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 5.1, 9.0)] == \
