@@ -193,13 +193,14 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
         // ---- ring: block table entries, 32 at a time, one per lane; a copy is
         // what a page holds of the tile, issued by a lane of its own
         const int32_t *table = a.block_table + (size_t)it.r * a.max_pages;
-        const int pages = (q.len + (1 << a.page_shift) - 1) >> a.page_shift;
+        const int pages = (int)(((uint32_t)q.len + (1u << a.page_shift) - 1) >> a.page_shift);
         const int chunk = a.page_shift < 6 ? 1 << (a.page_shift - 4) : kBlocks;  // blocks per copy
         const uint8_t *base_h = a.cache + (((size_t)h << (a.page_shift - 4)) * BB);
         const size_t page_bytes = (((size_t)a.Hkv << (a.page_shift - 4)) * BB);
         int from = 0, held = 0, entry = 0;
         auto fill = [&](int tile, uint32_t st) {
-            const int key0 = tile * kTile, key = key0 + lane * chunk * 16, page0 = key0 >> a.page_shift;
+            const int key0 = tile * kTile, page0 = key0 >> a.page_shift;
+            const uint32_t key = (uint32_t)key0 + lane * chunk * 16;  // (past the last key in lanes without a copy)
             if (page0 + kBlocks > from + held) {
                 from = page0, held = 32, entry = 0;
                 if (from + lane < pages) {
@@ -211,14 +212,14 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                 }
                 __syncwarp();
             }
-            const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - from) & 31);
+            const int page = __shfl_sync(0xffffffffu, entry, ((int)(key >> a.page_shift) - from) & 31);
             const int all = min(kBlocks, (q.len - key0 + 15) >> 4);  // blocks with keys
             const uint32_t bar = bars + st * 8;
             if (lane == 0) umma::mbar_expect_tx(bar, all * BB);
             __syncwarp();
             const int mine = min(chunk, all - lane * chunk);
             if (mine > 0) {
-                const int blk = (key & ((1 << a.page_shift) - 1)) >> 4;
+                const int blk = (key & ((1u << a.page_shift) - 1)) >> 4;
                 umma::bulk_load(ring + st * STAGE + lane * chunk * BB, base_h + page * page_bytes + blk * BB, mine * BB, bar);
             }
         };
@@ -295,7 +296,7 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                 }
             }
             // ---- masks: only tiles that some row of the tile does not see whole
-            const bool edge = key0 + kTile > pos0 + 1 || (a.window > 0 && key0 <= pos1 - a.window);
+            const bool edge = key0 > pos0 + 1 - kTile || (a.window > 0 && key0 <= pos1 - a.window);
             if (edge) {
                 const int tok = key0 + 4 * (g >> 1) + (g & 1);
 #pragma unroll
@@ -393,9 +394,9 @@ kda_cache4_attn_kernel(const Cache4AttnArgs a) {
                         vw[i][0] = lds32(blk + off_vc(D) + (g >> 1) * 128 + (t4 * 4 + i) * 8 + (g & 1) * 4);
                     sv = lds32(blk + off_vs(D) + (g >> 1) * 16 + t4 * 4);
                 }
-                if (key0 + kTile > q.len) {
+                if (key0 > q.len - kTile) {
                     // keys past the end hold anything, NaN scales too: a zero weight does not undo that
-                    const int over = key0 + mt * 16 + t4 * 4 + 4 - q.len;
+                    const int over = key0 - q.len + mt * 16 + t4 * 4 + 4;
                     if (over > 0) sv = over >= 4 ? 0u : sv & (0xffffffffu >> (8 * over));
                 }
                 const uint32_t s01 = scales_to_f16(sv & 0xffffu), s23 = scales_to_f16(sv >> 16);

@@ -426,7 +426,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         continue;
                     }
                     const int key0 = tile * kTile;
-                    if (key0 + kTile > see_lo + 1 || (a.window > 0 && key0 <= see_hi - a.window)) {
+                    if (key0 > see_lo + 1 - kTile || (a.window > 0 && key0 <= see_hi - a.window)) {
                         // hidden columns become -inf where they are; few tiles have any
                         const int hi = sees - key0, lo = a.window > 0 ? hi - a.window : -1;
 #pragma unroll 1
@@ -725,16 +725,17 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
         auto work = [&]() {
             while (walk.next(a, it)) {
                 const int32_t *table = a.block_table + (size_t)it.r * a.max_pages;
-                const int pages = (walk.q.len + (1 << a.page_shift) - 1) >> a.page_shift;
+                const int pages = (int)(((uint32_t)walk.q.len + (1u << a.page_shift) - 1) >> a.page_shift);
                 int from = 0, entry = 0, held = 0;  // 32 table entries, one per lane, from page `from` on
 #pragma unroll 1
                 for (int tile = it.first; tile < it.last; ++tile)
 #pragma unroll 1
                     for (int half = 0; half < kTile / C::KEYS; ++half, ++raws) {
                         const uint32_t ri = raws % C::RAWS;
-                        const int key0 = tile * kTile + half * C::KEYS, key = key0 + lane * chunk * 16;
+                        const int key0 = tile * kTile + half * C::KEYS;
+                        const uint32_t key = (uint32_t)key0 + lane * chunk * 16;  // (past the last one in lanes without a copy)
                         // blocks of this lane's copy that hold keys
-                        const int left = (walk.q.len - key + 15) >> 4;
+                        const int left = (walk.q.len - key0 - lane * chunk * 16 + 15) >> 4;
                         const int mine = lane * chunk < BLOCKS ? min(max(left, 0), chunk) : 0;
                         const int page0 = key0 >> a.page_shift;
                         if (page0 + BLOCKS - 1 >= from + held) {
@@ -749,13 +750,13 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                             }
                             __syncwarp();
                         }
-                        const int page = __shfl_sync(0xffffffffu, entry, ((key >> a.page_shift) - from) & 31);
+                        const int page = __shfl_sync(0xffffffffu, entry, ((int)(key >> a.page_shift) - from) & 31);
                         const int all = __reduce_add_sync(0xffffffffu, mine);
                         if (!wait(C::b_raw_empty + ri, raws / C::RAWS + 1)) return;
                         if (lane == 0) umma::mbar_expect_tx(bar(C::b_raw_full + ri), all * BB);
                         __syncwarp();
                         if (mine > 0) {
-                            const int blk = (key & ((1 << a.page_shift) - 1)) >> 4;
+                            const int blk = (key & ((1u << a.page_shift) - 1)) >> 4;
                             const uint8_t *src = a.cache + ((((size_t)page * a.Hkv + it.h) << (a.page_shift - 4)) + blk) * BB;
                             umma::bulk_load(sb + C::off_raw + ri * C::RAW + lane * chunk * BB, src, mine * BB,
                                             bar(C::b_raw_full + ri));

@@ -102,7 +102,7 @@ __device__ __forceinline__ Req request(const Cache4AttnArgs &a, int r, int G) {
     q.rows = q.n * G;
     // a call runs as one or two kernels; each takes the requests whose rows are in its range
     q.row_tiles = q.rows > a.rows_above && q.rows <= a.rows_to ? (q.rows + ROWS - 1) / ROWS : 0;
-    int t = (q.len + TILE - 1) / TILE;
+    int t = (int)(((uint32_t)q.len + TILE - 1) / TILE);  // (lengths go up to 2^31 - 16)
     if (a.window > 0) {
         // a row tile spans up to (ROWS - 1) / G + 2 tokens
         const long long span = ((long long)a.window + (ROWS - 1) / G + 1) / TILE + 2;
@@ -208,7 +208,7 @@ struct Walk {
         it.pos1 = q.len - q.n + row1 / G;
         const int key_lo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
         const int tile_lo = key_lo / TILE;
-        const int tiles = max(0, (it.pos1 + TILE) / TILE - tile_lo);  // none where pos1 < 0
+        const int tiles = it.pos1 < 0 ? 0 : it.pos1 / TILE + 1 - tile_lo;
         it.first = tile_lo + min(max(unit - LEAD, 0), tiles);
         it.last = tile_lo + min(max(unit1 - LEAD, 0), tiles);
         it.starts = unit == 0;

@@ -556,3 +556,25 @@ def test_scores_of_minus_infinity_alone_are_not_an_empty_row(lengths, new, dtype
         assert o[at].isnan().all() and torch.isneginf(lse[at])
         o[at], lse[at] = clean[at], lse0[at]
     assert torch.equal(o, clean) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 40, 200])
+def test_the_longest_lengths(new, dtype):
+    """2^31 - 16 keys, the longest that a block table of 16-token pages stands for: the last keys within a window as in a
+    short request, and (single tokens) all of them, on one page again and again."""
+    pages = 2 ** 27 - 1
+    c = Case([496], [new], 1, 1, 64, 16, dtype, seed=51)  # ends as the long one does within a tile
+    table = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    table[0, -31:] = c.args[1][0, :31]
+    table[0, :-31] = c.args[1][0, 0]
+    st, cu, q = status_word(), c.args[3], c.q.cuda()
+    o, lse = kda.cache4_attention(q, c.cache, table, dev([pages * 16]), cu, 16, window=100, return_lse=True, status=st)
+    want, want_lse = c.run(window=100, return_lse=True)
+    assert st.item() == 0 and near(o, want) and (lse - want_lse).abs().max() <= 2.0 ** -16 * (1 + want_lse.abs().max())
+    if new == 1:
+        o, lse = kda.cache4_attention(0 * q, c.cache, table, dev([pages * 16]), cu, 16, return_lse=True)
+        _, v = kda.cache4_read(c.cache, c.args[1][0, 0] * 16 + torch.arange(16, device="cuda").int(), 16, 64, torch.float32)
+        # equal weights: the mean over the page that all but 31 of 2^27 entries name
+        assert (lse - np.log(pages * 16.0)).abs().max() <= 2.0 ** -16
+        assert ((o[0] - v.mean(0)).abs() <= 2.0 ** -8 * v.abs().mean(0) + 2.0 ** -16).all()
