@@ -141,6 +141,19 @@ def test_plan_refuses_outputs_over_inputs():
                 assert plan({**at, o: at[n] + 4 * shift}) == -1, (o, n, shift)
 
 
+def test_the_current_stream_without_torchs_internal_function(monkeypatch):
+    class Stream:
+        cuda_stream = 0x1234
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(kda, "_raw_stream", None, raising=False)
+    assert kda._stream(None) == 0x1234 and kda._stream(Stream) == 0x1234
+    monkeypatch.setattr(kda, "_raw_stream", lambda device: 0x100 + device, raising=False)
+    assert kda._stream(None) == 0x103
+
+
 def test_reference_rounding():
     """The reference's nearest() and quantise() on values whose answers are known."""
     assert [ref.E2M1[ref.nearest(np.array(x), ref.E2M1)] for x in (0.25, 0.26, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 5.1, 9.0)] == \
