@@ -22,7 +22,6 @@
 namespace kda {
 namespace cache4 {
 
-constexpr int kBlockTokens = 16;
 constexpr uint32_t kScaleNaN = 0x7F;  // e4m3 NaN: the key scales of a token whose key or value is not finite
 
 __host__ __device__ constexpr int block_bytes(int d) { return 16 * (d + d / 8); }

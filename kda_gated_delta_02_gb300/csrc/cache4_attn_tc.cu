@@ -104,12 +104,12 @@ struct Cfg {
                          b_q_empty = b_k_full + 17, b_o_free = b_k_full + 18, b_pair = b_k_full + 19,
                          b_drain = b_k_full + 20, BARS = b_k_full + 21;
     static constexpr int off_misc = off_bar + BARS * 8;  // TMEM address, dead flag
-    // maxima and sums of the two streams, in two places that items take in turn: a stream without a tile
+    // QT = 1: maxima and sums of the two streams, in two places that items take in turn: a stream without a tile
     // of the next item waits for nothing before it writes that item's, and the other may still be reading
     static constexpr int PAIR_PLACES = 2;
     static constexpr int off_ml = off_misc + 16;
-    static constexpr int off_fac = off_ml + PAIR_PLACES * 2 * 128 * 8; // factors of the rows' scores, two items
-    static constexpr int off_item = (off_fac + 2 * ROWS * 4 + 15) & ~15;  // the softmax warps' place in the work
+    static constexpr int off_fac = off_ml + (QT == 1 ? PAIR_PLACES * 2 * 128 * 8 : 0);  // factors of the rows' scores, two items
+    static constexpr int off_item = (off_fac + (QT == 1 ? 2 * ROWS * 4 : 0) + 15) & ~15;  // the softmax warps' place in the work
     static constexpr int SMEM = off_item + SOFT * 176;
     // tensor memory columns: S (and P over it) 2 x 128, O 2 x D
     static constexpr int t_o = 256;
@@ -809,7 +809,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
 #pragma unroll
                 for (int t = 0; t < QT; ++t) scores(t, n, QT == 2 ? t : n & 1);
                 commit(bar(C::b_k_empty + (n & 1)), lead);
-                if (tiles == 1) commit(bar(C::b_q_empty), lead);
+                if (QT == 1 && tiles == 1) commit(bar(C::b_q_empty), lead);
 #pragma unroll 1
                 for (int j = 0; j < tiles; ++j, ++n) {
                     if (QT == 1 && j + 1 < tiles) {
@@ -835,10 +835,7 @@ kda_cache4_attn_tc_kernel(const Cache4AttnArgs a) {
                         }
                     }
                     commit(bar(C::b_v_empty + (n & 1)), lead);
-                    if (QT == 2 && j + 1 < tiles) {
-                        commit(bar(C::b_k_empty + ((n + 1) & 1)), lead);
-                        if (j + 2 == tiles) commit(bar(C::b_q_empty), lead);
-                    }
+                    if (QT == 2 && j + 1 < tiles) commit(bar(C::b_k_empty + ((n + 1) & 1)), lead);
                 }
             }
         };
