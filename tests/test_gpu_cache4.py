@@ -578,3 +578,142 @@ def test_the_longest_lengths(new, dtype):
         # equal weights: the mean over the page that all but 31 of 2^27 entries name
         assert (lse - np.log(pages * 16.0)).abs().max() <= 2.0 ** -16
         assert ((o[0] - v.mean(0)).abs() <= 2.0 ** -8 * v.abs().mean(0) + 2.0 ** -16).all()
+
+
+def shares(c, rows, tile, lead, workers, window):
+    """(items that one worker holds whole, those of one key tile that follow another of its items with key tiles), as the
+    kernels divide the work: items request by request, head by head, row tiles from both ends in turn; every worker
+    takes an equal, contiguous range of their units."""
+    H, G = c.cache.shape[1], c.q.shape[1] // c.cache.shape[1]
+    items = []  # units, key tiles
+    for L, n in zip(c.lengths, c.new):
+        count, t = -(-n * G // rows), -(-L // tile)
+        if window:
+            t = min(t, (window + (rows - 1) // G + 1) // tile + 2)
+        for _, i in itertools.product(range(H), range(count)):
+            rt = count - 1 - i // 2 if i % 2 else i // 2
+            first, last = L - n + rt * rows // G, L - n + (min(n * G, (rt + 1) * rows) - 1) // G
+            low = max(0, first - window + 1) // tile if window else 0
+            items.append((max(t, 1) + lead, last // tile + 1 - low if last >= 0 else 0))
+    share = max(1, -(-sum(u for u, _ in items) // workers))
+    at, whole, short, tiles_before = 0, 0, 0, {}
+    for units, tiles in items:
+        a, b = at // share, (at + units - 1) // share
+        whole += a == b
+        short += a == b and tiles == 1 and a in tiles_before
+        if tiles:
+            tiles_before[b] = True
+        at += units
+    return whole, short
+
+
+KINDS = ["few8", "few16", "f32", "many128", "many256"]  # by the rows of a tile; f32 has 8
+
+
+def crowd(kind, d, window=0, **kw):
+    """A batch of so many requests that workers go from item to item, and what check() takes: rows come out of the
+    attention kernels themselves, contexts of one tile, of odd tiles and of none follow one another."""
+    R, H, G, most = dict(few8=(1500, 3, 2, 1), few16=(1000, 2, 8, 2), f32=(400, 2, 3, 9), many128=(110, 4, 3, 40),
+                         many256=(70, 3, 2, 120))[kind]
+    r = np.random.default_rng(R + d + window)
+    lengths = np.where(r.random(R) < 0.4, r.integers(0, 70, R), r.integers(1, 300, R)).tolist()
+    least = {"many128": 6, "many256": 70}.get(kind, 1)  # more than 16 rows, more than 128 rows
+    new = r.integers(least, most + 1, R).tolist()
+    c = Case(lengths, new, H * G, H, d, 16, "f32" if kind == "f32" else "bf16", seed=R + d, ks=[0.5, 4.0, 1.0, 2.0][:H],
+             vs=[1.0, 2.0 ** -6, 3.0, 1.0][:H], **kw)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows, tile, lead, workers = {"few8": (8, 64, 2, 12 * sms), "few16": (16, 64, 2, 12 * sms), "f32": (8, 64, 2, 12 * sms),
+                                 "many128": (128, 128, 5, sms), "many256": (256, 128, 5, sms)}[kind]
+    whole, short = shares(c, rows, tile, lead, workers, window)
+    assert whole >= R // 2 and short >= R // 8
+    return c, dict(window=window, max_new=most)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", KINDS)
+def test_workers_that_hold_whole_items(kind, d, window):
+    c, how = crowd(kind, d, window)
+    o, lse = c.check(**how)
+    for _ in range(3):
+        again = c.run(return_lse=True, **how)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+def positions(c):
+    """Of every query row."""
+    return torch.cat([torch.arange(L - n, L) for L, n in zip(c.lengths, c.new)])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_whole_items_whose_scores_are_minus_infinity(kind):
+    """As test_scores_of_minus_infinity_alone_are_not_an_empty_row, in rows that no join makes; their neighbours keep
+    their bits."""
+    c, how = crowd(kind, 64)
+    c.k[:, :, 5] = -3.0
+    kda.cache4_append(c.k.bfloat16().cuda(), c.v.bfloat16().cuda(), c.slots, c.cache, 16, k_scale=c.ks, v_scale=c.vs)
+    clean, lse0 = c.run(return_lse=True, **how)
+    q = c.q.clone()
+    q[::7, 1, 5] = float("inf")
+    o, lse = c.run(q=q, return_lse=True, **how)
+    seen = (positions(c)[::7] >= 0).cuda()
+    assert o[::7, 1][seen].isnan().all() and (o[::7, 1][~seen] == 0).all() and torch.isneginf(lse[::7, 1]).all()
+    o[::7, 1], lse[::7, 1] = clean[::7, 1], lse0[::7, 1]
+    assert torch.equal(o, clean) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("power", [22, 30])
+@pytest.mark.parametrize("kind", KINDS)
+def test_whole_items_of_scores_far_apart(kind, power):
+    """Every row is finite and within its values' range at scores of 2^power, and a query that sees one key gets its value
+    (bounds as in test_scores_far_apart)."""
+    c, how = crowd(kind, 128, gain=2.0 ** power)
+    o, lse = c.run(return_lse=True, **how)
+    o, lse, at = to64(o), to64(lse), positions(c).numpy()
+    rel = 2.0 ** -19 if kind == "f32" else 2.0 ** -8 + 2.0 ** -11
+    assert np.isfinite(o).all() and np.isfinite(lse[at >= 0]).all() and np.isneginf(lse[at < 0]).all()
+    _, values = ref.decode(c.cache.cpu().numpy(), c.d)
+    values, G, ones = values * to64(c.vs)[:, None, None], c.q.shape[1] // c.cache.shape[1], 0
+    for r, (n, L) in enumerate(zip(c.new, c.lengths)):
+        v = values[c.table[r, :-(-L // 16)]].swapaxes(0, 1).reshape(values.shape[1], -1, c.d)[:, :L]
+        largest = np.maximum.accumulate(np.abs(v), axis=1)
+        for i in range(n):
+            row, pos = c.cu[r] + i, L - n + i
+            if pos < 0:
+                assert np.all(o[row] == 0)
+                continue
+            assert np.all(np.abs(o[row]) <= (1 + rel) * np.repeat(largest[:, pos], G, axis=0))
+            if pos == 0:
+                ones += 1
+                only = np.repeat(v[:, 0], G, axis=0)
+                assert np.all(np.abs(o[row] - only) <= rel * np.abs(only))
+    assert ones > 0
+
+
+@pytest.mark.parametrize("lengths,new", [([900, 300], [40, 25]), ([900, 300], [200, 30]), ([900, 300, 77], [1, 40, 2]),
+                                         ([900, 4000, 77], [1, 200, 1])])
+def test_graphs_of_the_many_row_kernel_and_of_both(lengths, new):
+    """Replays of the tcgen05 kernel with its join, and of both kernels with theirs, give the call's bits; the inputs change
+    between replays."""
+    c = Case(lengths, new, 8, 2, 128, 64, seed=61)
+    q, side = c.q.cuda(), torch.cuda.Stream()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ws = torch.empty(kda.cache4_attention_workspace_size(len(new), sum(new), 8, 2, 128), dtype=torch.uint8, device="cuda")
+    call = lambda: kda.cache4_attention(q, *c.args, max_new=max(new), out=out, lse=lse, return_lse=True, workspace=ws)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    side.synchronize()
+    for i in range(3):
+        q.copy_(torch.roll(c.q, i, 1))
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = c.run(q=torch.roll(c.q, i, 1), max_new=max(new), return_lse=True)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
