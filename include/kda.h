@@ -510,8 +510,8 @@ int kda_decode_verify_replay_ragged(void *state, void *conv_tail, const float *c
  *             * page_size < 2^31.  Negative slots are skipped.
  * k_scale, v_scale  device f32 [Hkv] or NULL (1): the cache's units, the same
  *             in every call on it.  A power of two keeps the division exact.
- * A token whose key or value holds a NaN or an infinity in some head is
- * marked in that head: queries that see it come out NaN, others are not
+ * A token whose key or value holds a NaN or an infinity in some head (or has
+ * no quotient by its scale: 0 / 0, a scale of NaN) is marked in that head: queries that see it come out NaN, others are not
  * touched, and KDA_STATUS_NOT_FINITE is set.
  */
 

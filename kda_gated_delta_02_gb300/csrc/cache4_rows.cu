@@ -106,8 +106,12 @@ __device__ __forceinline__ bool quantise(const Group<BF16> &g, float head_scale,
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             x[i] = g.pair(i);
-            if constexpr (SCALED) x[i].x = x[i].x / head_scale, x[i].y = x[i].y / head_scale;
             finite = finite && fabsf(x[i].x) <= 3.402823466e38f && fabsf(x[i].y) <= 3.402823466e38f;
+            if constexpr (SCALED) {
+                // (a quotient past fp32 saturates as any other; 0 / 0 and a scale of NaN have none)
+                x[i].x = x[i].x / head_scale, x[i].y = x[i].y / head_scale;
+                finite = finite && x[i].x == x[i].x && x[i].y == x[i].y;
+            }
             top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
         }
     }

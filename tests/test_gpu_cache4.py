@@ -717,3 +717,26 @@ def test_graphs_of_the_many_row_kernel_and_of_both(lengths, new):
         torch.cuda.synchronize()
         want = c.run(q=torch.roll(c.q, i, 1), max_new=max(new), return_lse=True)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_quotients_past_fp32_saturate():
+    """Finite rows whose quotient by the head's scale overflows hold the largest value with their sign and mark nothing; a
+    scale that is NaN marks its head's tokens."""
+    T, H, d, page = 3, 2, 64, 16
+    k = torch.ones(T, H, d)
+    k[1, 0] = -1e30
+    k[1, 0, 20:30] = 1e3
+    v, scale = torch.randn(T, H, d), torch.tensor([2.0 ** -40, 1.0])
+    cache, st = kda.cache4_alloc(1, H, page, d), status_word()
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    how = dict(k_scale=scale.cuda(), status=st)
+    kda.cache4_append(k.cuda(), v.cuda(), slots, cache, page, **how)
+    ko, vo = kda.cache4_read(cache, slots, page, d, dtype=torch.float32, **how)
+    assert st.item() == 0
+    want = np.float32(2688) * np.sign(k[:, 0].numpy()) * np.float32(2.0 ** -40)
+    assert np.array_equal(to64(ko)[:, 0], want.astype(np.float64)) and np.array_equal(to64(ko)[:, 1], ref.held(k.numpy())[:, 1])
+    assert np.array_equal(to64(vo), ref.held(v.numpy()))
+    how["k_scale"] = torch.tensor([1.0, float("nan")], device="cuda")
+    kda.cache4_append(k.cuda(), v.cuda(), slots, cache, page, **how)
+    _, vo = kda.cache4_read(cache, slots, page, d, dtype=torch.float32)
+    assert st.item() == kda.STATUS_NOT_FINITE and vo[:, 1].isnan().all() and not vo[:, 0].isnan().any()
