@@ -511,8 +511,9 @@ int kda_decode_verify_replay_ragged(void *state, void *conv_tail, const float *c
  * k_scale, v_scale  device f32 [Hkv] or NULL (1): the cache's units, the same
  *             in every call on it.  A power of two keeps the division exact.
  * A token whose key or value holds a NaN or an infinity in some head (or has
- * no quotient by its scale: 0 / 0, a scale of NaN) is marked in that head: queries that see it come out NaN, others are not
- * touched, and KDA_STATUS_NOT_FINITE is set.
+ * no quotient by its scale: 0 / 0, a scale of NaN) is marked in that head:
+ * queries that see it come out NaN, others are not touched, and
+ * KDA_STATUS_NOT_FINITE is set.
  */
 
 /*
@@ -586,8 +587,11 @@ int kda_cache4_read(const void *cache, const int32_t *slots, int n, int Hkv, int
  *             two kernels; the bound says which are needed and how wide a tile
  *             is.  A request with more queries is still computed.
  *  o          device [T][Hq][d], in_dtype.  lse: device f32 [T][Hq] or NULL,
- *             the natural log of the sum of e^{scale q.k}.
- *  workspace  at least kda_cache4_attention_workspace_size(...) bytes.
+ *             the natural log of the sum of e^{scale q.k}.  Rows past
+ *             cu_seqlens[R], and those of a request that is skipped, are not
+ *             written.  Neither overlaps an input.
+ *  workspace  at least kda_cache4_attention_workspace_size(...) bytes (places for
+ *             the workers' shares: by d, in_dtype and the device alone).
  * Products take f16 operands with fp32 accumulation: keys and values exactly
  * as the cache holds them, queries scaled by a power of two per row, weights
  * rounded to 11 bits; 32-bit queries and their weights in two f16 parts each.

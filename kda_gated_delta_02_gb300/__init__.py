@@ -660,7 +660,9 @@ def cache4_attention(q, cache, block_table, seq_len, cu_seqlens, page_size, scal
     `window` of them when that is not 0).  scale defaults to d ** -0.5.
     max_new is an upper bound of the requests' query counts (0: T).  q's rows
     may lie further apart than Hq * d.  Returns o [T, Hq, d] in q's dtype, and
-    lse f32 [T, Hq] with return_lse."""
+    lse f32 [T, Hq] with return_lse.  Rows past the last request (of a padded
+    batch) are not written: they keep what `out` held, and are uninitialised
+    where the call makes it."""
     if q.dim() != 3 or block_table.dim() != 2:
         raise KDAError("q must be [T, Hq, d] and block_table [R, max_pages]")
     T, Hq, d = q.shape

@@ -1321,8 +1321,9 @@ int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_
     // runs both.  Only one is launched where all requests are of one kind: by
     // the bound, by the group's heads, or because T shows that every request
     // has max_new queries.  64 requests of 1 to 8 queries, 8 heads a group,
-    // take 290 us with no rows in the warps' kernel, 284 with up to 8, 279
-    // with 16, 289 with 24 and 303 with 32.
+    // d = 128, take 290 us with no rows in the warps' kernel, 284 with up to 8,
+    // 279 with 16, 289 with 24 and 303 with 32.  Other groups, d = 64 and
+    // windows follow the same rule without measurements of their own.
     constexpr int kFewRows = 16, kAll = 0x7fffffff;
     const bool bf16 = in_dtype == KDA_DTYPE_BF16;
     const long long most = max_new > 0 && max_new < T ? max_new : T;

@@ -27,10 +27,10 @@
 // weighted values), and kda_cache4_merge_kernel joins the shares in key order.
 //
 // Measured at d = 128, 96 query heads on 12 key heads (device time): 256
-// single tokens over up to 8K keys (1.86 GB) 315 us, 5.9 TB/s, 87 % of the
-// measured copy bandwidth; one token over 1M keys (1.81 GB) 298 us, 90 %; one
-// over 1,003 keys 10.7 us.  After the copies comes instruction issue (57 %
-// busy, the conversion's pipe 48 %): 530 warp instructions per 32 keys, of
+// single tokens over up to 8K keys (1.86 GB) 314 us, 5.9 TB/s, 88 % of the
+// measured copy bandwidth; one token over 1M keys (1.81 GB) 301 us, 89 %; one
+// over 1,003 keys 11.2 us.  After the copies comes instruction issue (57 %
+// busy, the conversion's pipe 49 %): 534 warp instructions per 32 keys, of
 // which the conversion of the codes is 290 and the products 32.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -520,8 +520,10 @@ size_t cache4_attn_workspace(int sms, int d) {
 }
 
 // 16 rows a tile when a request may have more than 8 (the keys' conversion to
-// f16 is then shared by two products); 32-bit queries have two f16 parts and
-// keep 8.
+// f16 is then shared by two products: 131 MB of two-token requests at 8 heads
+// a group 67 us, in tiles of 8 rows 71).  32-bit queries have two f16 parts and
+// keep 8: with 16 a batch of 9 x up to 45 queries, d = 64, took 26.1 us instead
+// of 23.8, having half the units.
 int cache4_attn_rows(bool bf16, long long rows) { return bf16 && rows > 8 ? 16 : 8; }
 
 cudaError_t launch_cache4_attn(const Cache4AttnArgs &a, int d, bool bf16, long long rows, int sms, cudaStream_t st) {

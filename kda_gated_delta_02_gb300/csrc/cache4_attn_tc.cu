@@ -30,21 +30,21 @@
 // scores' way to registers, weights, O, next scores) is longer than the other
 // tile's products hide: about 2,800 cycles per 256 rows x 128 keys where the
 // pipe wants 2,056.  632 GFLOP of prompt chunks (2 x 2,048 queries of 32
-// heads over up to 16K keys): 430 us with the join, 1.47 PFLOP/s, 76 % of
-// the measured bf16 rate; 371 without the softmax, 391 without the
+// heads over up to 16K keys), by call: 430 us with the join, 1.47 PFLOP/s,
+// 76 % of the measured bf16 rate; 371 without the softmax, 391 without the
 // conversion, 366 without both.  QT = 1: a key tile's conversion serves up to
 // 128 rows only, and it and the two streams' softmax share the SM's issue
 // slots beside products that the padded row tile makes as long as a full
 // one's.  64 requests of up to 8 queries x 96 heads (752 MB, a third of it by
-// the other kernel, 85 us): 279 us, 40 % of the measured copy bandwidth; 263
+// the other kernel, 90 us alone): 277 us, 40 % of the measured copy bandwidth; 263
 // without the softmax, 255 without the conversion, 230 without both, which is
 // the pipe's time.  Memory bounds neither: copies taken out gain nothing.
 //
 // Measured on the way (us, the two calls above): one thread issuing the
 // products from a divergent branch, operands moved to uniform registers for
 // each, 591 / 451, the whole warp with an elected lane 483 / 420; one stream
-// for QT = 1 420, two 352; 145 KB of code, which overran the instruction
-// cache, 997 / 817, the roles rolled up 597 / 463; the maximum formed by the
+// for QT = 1 420, two 352; the roles' loops unrolled, with instruction
+// fetch the first cause of stalls, 997 / 817, rolled up 597 / 463; the maximum formed by the
 // tensor-memory load instead of by the threads 480 / 306 to 466 / 302; QT =
 // 2's registers shared out 176 / 96 / 64 (144 bytes spilled) 466, 192 / 72 /
 // 56 437, 200 / 64 / 48 (4 bytes) 428, 208 / 48 / 48 435; raw stages of 128

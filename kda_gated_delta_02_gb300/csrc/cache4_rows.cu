@@ -6,10 +6,14 @@
 // A thread takes one group of a token and head, of the key and of the value:
 // 32 bytes in per row at bf16, 8 bytes of codes and one scale out.  Memory
 // bounds it: 2 x (2 or 4) bytes read and 2 x 9/16 bytes written per channel.
-// Rows of 32K tokens x 12 heads x 128 at slots in random order: 258 MB each
-// way, append 51 us (5.1 TB/s, 75 % of the measured copy bandwidth), read
-// 50 us (76 %); a value's codes and scales of one token lie in 16 sectors of
-// 32 bytes, which neighbouring tokens share and scattered ones do not.
+// Rows of 32K tokens x 12 heads x 128, 258 MB each way, other rows each time,
+// by call.  Slots in random order: append 66 us (3.9 TB/s, 58 % of the measured
+// copy bandwidth), read 54 us (71 %).  Slots in order: 49 and 43 us (78 and
+// 88 %).  The difference is sectors of 32 bytes: a value of one token lies in
+// 12 of them (its codes in 8, its scales in 4), of which it fills a quarter
+// and a sixteenth; neighbouring tokens share them and scattered ones do not.
+// (The same rows written again and again take 48 us at random slots: the L2
+// cache holds some of them.)
 //
 // A token whose key or value is not finite in a head is marked there: its key
 // scales are NaN and its value is zero, so every query that sees it comes out

@@ -224,6 +224,8 @@ struct Walk {
 
 // What the two attention kernels' shares are made with: keys per tile, an
 // item's start and end in tiles, and the power of two that lifts the weights.
+// (Leads of 0 / 0, 2 / 2, 4 / 1 and 6 / 3 measured on ragged single tokens and
+// verify windows at d = 128: 2 and 5 took 341 to 314 and 354 to 311 us.)
 struct FewRows {
     static constexpr int TILE = 64, LEAD = 2;
     static constexpr float LIFT = 15.f;
