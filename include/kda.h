@@ -54,6 +54,9 @@ extern "C" {
 #define KDA_CONV_NONE 0
 #define KDA_CONV_SILU 1
 
+#define KDA_NORM_RMS 0
+#define KDA_NORM_LAYER 1
+
 #define KDA_CP_OFF 0
 #define KDA_CP_ON 1
 #define KDA_CP_AUTO (-1)
@@ -86,7 +89,13 @@ extern "C" {
 #define KDA_KERNEL_CACHE4_READ 14    /* kda_cache4_read */
 #define KDA_KERNEL_CACHE4_ATTN 15    /* kda_cache4_attention */
 #define KDA_KERNEL_CACHE4_MERGE 16   /* kda_cache4_attention: shares of a long key axis joined */
-#define KDA_KERNEL_KINDS 17
+#define KDA_KERNEL_NORM 17           /* kda_norm_fwd, kda_norm_bwd */
+#define KDA_KERNEL_CONV 18           /* kda_conv_fwd, kda_conv_bwd, kda_conv_step */
+#define KDA_KERNEL_SCAN 19           /* kda_scan_fwd, kda_scan_step: the walk */
+#define KDA_KERNEL_SCAN_SEGMENT 20   /* kda_scan_fwd, kda_scan_bwd: segments' own states, and their chain */
+#define KDA_KERNEL_SCAN_BWD 21       /* kda_scan_bwd: the walk back */
+#define KDA_KERNEL_SUMS 22           /* backward calls: partial sums added up */
+#define KDA_KERNEL_KINDS 23
 
 /* Human-readable name of a return status. Never NULL. */
 const char *kda_status_string(int status);
@@ -607,6 +616,141 @@ int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_
                          const float *v_scale, void *o, float *lse, int in_dtype, void *workspace,
                          size_t workspace_bytes, uint32_t *status, void *stream);
 size_t kda_cache4_attention_workspace_size(int R, int T, int Hq, int Hkv, int d, int in_dtype);
+
+/*
+ * What stands around a recurrence: the norm of its outputs (or of a layer's
+ * inputs), the short convolution of its inputs, and a second recurrence, the
+ * selective state space scan.  These have no counterpart on the pages except
+ * where the fused verify (kda_decode_verify_replay) contains them: its conv and
+ * its output norm are kda_conv_step and kda_norm_fwd of single tokens, and
+ * kda_conv_fwd leaves the tail that it continues from.
+ *
+ * Rows.  Tensors called rows hold a row per token; a row is contiguous and rows
+ * lie a stride (in elements, at least the row's length) apart, so they may be
+ * parts of a fused projection.  Any address and stride of whole elements is
+ * taken; where all of a call's rows start on 16-byte boundaries (and the channels of a
+ * group are a multiple of 16 bytes) wider accesses run.  Other tensors are contiguous and
+ * start on 16-byte boundaries.  dtype is bf16 or f32.  Outputs overlap neither
+ * inputs nor one another (kda_norm_*: y may be x, and dx may be x or dy, row for
+ * row): KDA_ERR_INVALID_ARG.  Sums, statistics and states are fp32; an output
+ * is rounded once.  The same inputs give the same bits.
+ * Sequences: cu_seqlens device int32 [N + 1], N >= 1, T <= 2^30.  A sequence
+ * whose ends are not in order or not in [0, T] sets KDA_STATUS_BAD_SEQLENS, and
+ * its outputs and those of the sequences behind it are unspecified.  Rows of no
+ * sequence, as behind the last, are not written.
+ */
+
+/*
+ * Norm of rows: y = (x - m) / sqrt(var + eps) weight + bias (KDA_NORM_LAYER) or
+ * y = x / sqrt(mean(x^2) + eps) weight + bias (KDA_NORM_RMS).
+ *  x, y       rows of d (1 to 16384).
+ *  weight, bias  device f32 [d] or NULL (1, 0).
+ */
+int kda_norm_fwd(const void *x, const float *weight, const float *bias, long long rows, int d,
+                 long long x_stride, long long y_stride, float eps, int kind, void *y, int dtype,
+                 void *stream);
+
+/*
+ * Its gradients, from x and dy alone.
+ *  dx         rows of d.
+ *  dweight, dbias  device f32 [d] or NULL (not computed).
+ *  workspace  at least kda_norm_bwd_workspace_size(...) bytes; not used without dweight and dbias.
+ */
+int kda_norm_bwd(const void *x, const void *dy, const float *weight, long long rows, int d,
+                 long long x_stride, long long dy_stride, long long dx_stride, float eps, int kind,
+                 void *dx, float *dweight, float *dbias, int dtype, void *workspace,
+                 size_t workspace_bytes, void *stream);
+size_t kda_norm_bwd_workspace_size(long long rows, int d, int dtype);
+
+/*
+ * Short causal convolution over packed sequences, as the fused verify has it:
+ *     p_t = bias + sum_j w[c][j] x_{t - (W - 1) + j},   y_t = p_t, or p_t sigmoid(p_t)
+ *  x, y       rows of C, T of them.
+ *  w          device f32 [C][W], W from 1 to 4; bias f32 [C] or NULL.
+ *  tail       rows of C, [N][W - 1] of them: the rows before each sequence, oldest
+ *             first, tail_stride apart; or NULL (zeros).
+ *  tail_out   the same of each sequence's end, or NULL.  A sequence shorter than
+ *             W - 1 keeps part of its tail; one without tokens all of it.
+ *  conv_act   KDA_CONV_NONE or KDA_CONV_SILU.
+ */
+int kda_conv_fwd(const void *x, const int32_t *cu_seqlens, const float *w, const float *bias,
+                 const void *tail, int N, int T, int C, int W, long long x_stride,
+                 long long tail_stride, long long y_stride, long long tail_out_stride, int conv_act,
+                 void *y, void *tail_out, int dtype, uint32_t *status, void *stream);
+
+/*
+ * Its gradients.
+ *  dy         rows of C, of dtype dy_dtype: dtype, or f32 beside bf16 (what
+ *             kda_chunk_bwd leaves).
+ *  dtail_out  device f32 [N][W - 1][C], the gradient of tail_out, or NULL.
+ *  dx         rows of C.  dw, dbias: device f32 [C][W], [C], or NULL (not computed).
+ *  dtail      device f32 [N][W - 1][C], the gradient of tail, or NULL.
+ *  workspace  at least kda_conv_bwd_workspace_size(...) bytes; not used without dw and dbias.
+ */
+int kda_conv_bwd(const void *x, const int32_t *cu_seqlens, const float *w, const float *bias,
+                 const void *tail, const void *dy, const float *dtail_out, int N, int T, int C, int W,
+                 long long x_stride, long long tail_stride, long long dy_stride, long long dx_stride,
+                 int conv_act, void *dx, float *dw, float *dbias, float *dtail, int dtype,
+                 int dy_dtype, void *workspace, size_t workspace_bytes, uint32_t *status,
+                 void *stream);
+size_t kda_conv_bwd_workspace_size(int T, int C, int W);
+
+/* One token for each of R requests: y from x and the tail (rows of C, [R][W - 1] of them), which
+ * moves on in place. */
+int kda_conv_step(const void *x, const float *w, const float *bias, void *tail, int R, int C, int W,
+                  long long x_stride, long long tail_stride, long long y_stride, int conv_act, void *y,
+                  int dtype, void *stream);
+
+/*
+ * Selective state space scan over packed sequences.  Per channel c of D and
+ * state n of S, with v = dt + dt_bias, delta = ln(1 + e^v) (v itself without
+ * dt_softplus) and g = c / (D / G):
+ *     h_t = e^{delta_t A[c][n]} h_{t-1} + delta_t x_t B_t[g][n]
+ *     y_t = (sum_n C_t[g][n] h_t + skip[c] x_t) z_t sigmoid(z_t)
+ *  x, dt, z, y  rows of D; z may be NULL (no gate).
+ *  B, C       rows of [G][S].  S: 8, 16, 32 or 64; G divides D.
+ *  A          device f32 [D][S] (negative in use).  skip, dt_bias: f32 [D] or NULL (0).
+ *  initial_state, final_state  device f32 [N][D][S] or NULL (zero; not written).
+ *  saved      NULL, or kda_scan_saved_size(...) bytes for kda_scan_bwd: the state
+ *             before every eighth token of a sequence.
+ *  workspace  at least kda_scan_workspace_size(...) bytes (0: none needed): the
+ *             states of the segments that few or uneven sequences are cut into.
+ */
+int kda_scan_fwd(const void *x, const void *dt, const float *A, const void *B, const void *C,
+                 const float *skip, const void *z, const float *dt_bias, const int32_t *cu_seqlens,
+                 int N, int T, int D, int G, int S, long long x_stride, long long dt_stride,
+                 long long B_stride, long long C_stride, long long z_stride, long long y_stride,
+                 const float *initial_state, float *final_state, int dt_softplus, void *y,
+                 float *saved, int dtype, void *workspace, size_t workspace_bytes, uint32_t *status,
+                 void *stream);
+size_t kda_scan_workspace_size(int N, int T, int D, int G, int S);
+size_t kda_scan_saved_size(int N, int T, int D, int S);
+
+/*
+ * Its gradients, from the same inputs and what kda_scan_fwd saved.
+ *  dy         rows of D.  dfinal_state: device f32 [N][D][S], the gradient of
+ *             final_state, or NULL.
+ *  dx, ddt, dz  device [T][D]; dB, dC: [T][G][S]; of dtype.  dz as z.
+ *  dA         device f32 [D][S]; dskip, ddt_bias: f32 [D] or NULL.
+ *  dinitial_state  device f32 [N][D][S] or NULL.
+ */
+int kda_scan_bwd(const void *x, const void *dt, const float *A, const void *B, const void *C,
+                 const float *skip, const void *z, const float *dt_bias, const int32_t *cu_seqlens,
+                 const void *dy, const float *dfinal_state, const float *saved, int N, int T, int D,
+                 int G, int S, long long x_stride, long long dt_stride, long long B_stride,
+                 long long C_stride, long long z_stride, long long dy_stride, int dt_softplus,
+                 void *dx, void *ddt, float *dA, void *dB, void *dC, float *dskip, void *dz,
+                 float *ddt_bias, float *dinitial_state, int dtype, void *workspace,
+                 size_t workspace_bytes, uint32_t *status, void *stream);
+size_t kda_scan_bwd_workspace_size(int N, int T, int D, int G, int S);
+
+/* One token for each of R requests (rows as above, R of them); state device f32 [R][D][S] moves on in
+ * place. */
+int kda_scan_step(const void *x, const void *dt, const float *A, const void *B, const void *C,
+                  const float *skip, const void *z, const float *dt_bias, float *state, int R, int D,
+                  int G, int S, long long x_stride, long long dt_stride, long long B_stride,
+                  long long C_stride, long long z_stride, long long y_stride, int dt_softplus, void *y,
+                  int dtype, void *stream);
 
 /*
  * Context-parallel prefill that allocates nothing.  (The pages have no

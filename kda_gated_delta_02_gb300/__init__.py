@@ -22,7 +22,8 @@ __all__ = ["chunk_fwd", "chunk_fwd_workspace_size", "chunk_fwd_prep_workspace_si
            "STATUS_BAD_ACCEPTED_LEN", "STATUS_SEGMENT_OVERFLOW", "STATUS_TIMEOUT", "STATUS_BAD_DRAFT_LEN",
            "KERNEL_FAMILIES", "chunk_bwd", "chunk_fwd_host", "kernel_timing_start",
            "kernel_timing_stop", "page_plan", "cache4_alloc", "cache4_append", "cache4_read", "cache4_attention",
-           "cache4_attention_workspace_size", "STATUS_NO_PAGES", "STATUS_BAD_PAGE", "STATUS_NOT_FINITE"]
+           "cache4_attention_workspace_size", "norm_fwd", "norm_bwd", "conv_fwd", "conv_bwd", "conv_step", "scan_fwd",
+           "scan_bwd", "scan_step", "NORM_RMS", "NORM_LAYER", "STATUS_NO_PAGES", "STATUS_BAD_PAGE", "STATUS_NOT_FINITE"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -31,6 +32,7 @@ _lib = None
 
 CP_OFF, CP_ON, CP_AUTO = 0, 1, -1
 CONV_NONE, CONV_SILU = 0, 1
+NORM_RMS, NORM_LAYER = 0, 1
 DTYPE_BF16, DTYPE_F32 = 0, 1
 STATUS_BAD_SEQLENS, STATUS_BAD_ACCEPTED_LEN, STATUS_SEGMENT_OVERFLOW = 1, 2, 4
 STATUS_TIMEOUT, STATUS_BAD_DRAFT_LEN = 8, 16
@@ -120,6 +122,17 @@ def load_library():
         lib.kda_cache4_attention.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, L, P, P, P, P, I, P, S, P, P]
         lib.kda_cache4_attention_workspace_size.restype = S
         lib.kda_cache4_attention_workspace_size.argtypes = [I, I, I, I, I, I]
+        for name, kinds in (
+                ("norm_fwd", "PPPLILLFIPIP"), ("norm_bwd", "PPPLILLLFIPPPIPSP"), ("conv_fwd", "PPPPPIIIILLLLIPPIPP"),
+                ("conv_bwd", "PPPPPPPIIIILLLLIPPPPIIPSPP"), ("conv_step", "PPPPIIILLLIPIP"),
+                ("scan_fwd", "PPPPPPPPPIIIIILLLLLLPPIPPIPSPP"), ("scan_bwd", "PPPPPPPPPPPPIIIIILLLLLLIPPPPPPPPPIPSPP"),
+                ("scan_step", "PPPPPPPPPIIIILLLLLLIPIP")):
+            f = getattr(lib, "kda_" + name)
+            f.restype, f.argtypes = I, [dict(P=P, I=I, L=L, F=F, S=S)[k] for k in kinds]
+        for name, kinds in (("norm_bwd_workspace", "LII"), ("conv_bwd_workspace", "III"), ("scan_workspace", "IIIII"),
+                            ("scan_saved", "IIII"), ("scan_bwd_workspace", "IIIII")):
+            f = getattr(lib, f"kda_{name}_size")
+            f.restype, f.argtypes = S, [dict(I=I, L=L)[k] for k in kinds]
         _lib = lib
         return lib
 
@@ -316,7 +329,8 @@ KERNEL_FAMILIES = ("kda_chunk_list_kernel", "kda_chunk_prep_kernel", "kda_chunk_
                    "kda_chunk_tc_kernel", "kda_chunk_kernel", "kda_compose_kernel", "kda_segment_table_kernel",
                    "kda_decode_verify_replay", "kda_chunk_bwd_kernel", "kda_bwd_walk_kernel",
                    "kda_bwd_chunk_kernel", "kda_bwd_compose_kernel", "kda_page_plan", "kda_cache4_append",
-                   "kda_cache4_read", "kda_cache4_attention", "kda_cache4_merge")
+                   "kda_cache4_read", "kda_cache4_attention", "kda_cache4_merge", "kda_norm", "kda_conv", "kda_scan",
+                   "kda_scan_segment", "kda_scan_bwd", "kda_sums")
 
 
 def chunk_fwd_host(q, k, v, g, beta, cu_seqlens, initial_state=None, output_final_state=True, scale=1.0,
@@ -694,3 +708,319 @@ def cache4_attention(q, cache, block_table, seq_len, cu_seqlens, page_size, scal
                                       _stream(stream))
         _check(rc, "kda_cache4_attention")
         return (out, lse) if return_lse else out
+
+
+# ------------------------------------------------------------------ norm, short convolution, selective scan
+class _Device:
+    """The device of a call's tensors as the current one, and the stream it launches on as the one that the tensors it
+    makes belong to (see _on)."""
+
+    def __init__(self, t, stream):
+        if not t.is_cuda:
+            raise KDAError("KDA calls take CUDA tensors")
+        self.device = t.device
+        self.guards = []
+        if stream is not None:
+            if stream.device != t.device:
+                raise KDAError(f"stream is on {stream.device}, the tensors on {t.device}")
+            self.guards.append(torch.cuda.stream(stream))
+        elif torch.cuda.current_device() != t.device.index:
+            self.guards.append(torch.cuda.device(t.device))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+    def flat(self, t, name, dtype=torch.float32, shape=None):
+        """Pointer of a contiguous tensor (None: null)."""
+        if t is None:
+            return None
+        if t.dtype != dtype:
+            raise KDAError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise KDAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != self.device:
+            raise KDAError(f"{name} must be on {self.device}, got {t.device}")
+        if not t.is_contiguous():
+            raise KDAError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def rows(self, t, name, dtype, shape):
+        """(pointer, stride in elements) of rows: the last axes of `shape` past the first are one contiguous row, rows may
+        lie further apart."""
+        if t is None:
+            return None, _width(shape)
+        if t.dtype != dtype:
+            raise KDAError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise KDAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != self.device:
+            raise KDAError(f"{name} must be on {self.device}, got {t.device}")
+        width, strides = 1, t.stride()
+        for n, s in zip(reversed(t.shape[1:]), reversed(strides[1:])):
+            if n != 1 and s != width:
+                raise KDAError(f"{name}'s rows must be contiguous")
+            width *= n
+        if t.shape[0] > 1 and strides[0] < width:
+            raise KDAError(f"{name}'s rows must not overlap")
+        return t.data_ptr(), strides[0] if t.shape[0] > 1 else width
+
+    def tails(self, t, name, dtype, shape):
+        """rows() of tails [N, W - 1, C]: all their N (W - 1) rows the same way apart."""
+        if t is None:
+            return None, shape[2]
+        N, m, C = shape
+        if t.shape != shape:
+            raise KDAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if m > 1 and N > 1 and t.stride(0) != m * t.stride(1):
+            raise KDAError(f"{name}'s rows must all lie the same way apart")
+        step = t.stride(1) if m > 1 else t.stride(0)
+        return self.rows(t.as_strided((N * m, C), (step, t.stride(2))) if N * m else t.view(0, C), name, dtype, (N * m, C))
+
+    def workspace(self, t, need):
+        """(pointer, bytes) of a workspace of `need` bytes: t where it is large enough, else a new one."""
+        if need == 0:
+            return None, 0
+        if t is None or t.nbytes < need:
+            t = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return self.flat(t, "workspace", t.dtype), t.nbytes
+
+
+def _width(shape):
+    n = 1
+    for k in shape[1:]:
+        n *= k
+    return n
+
+
+def _norm_rows(d, t, name, like):
+    """(pointer, stride) of rows [.., n]: contiguous, or two axes with rows apart."""
+    if t.dtype != like.dtype:
+        raise KDAError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.shape != like.shape:
+        raise KDAError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    if t.dim() != 2:
+        if not t.is_contiguous():
+            raise KDAError(f"{name} must be contiguous, or rows of two axes")
+        t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(0, t.shape[-1])
+    return d.rows(t, name, t.dtype, t.shape)
+
+
+def norm_fwd(x, weight=None, bias=None, eps=1e-6, kind=NORM_RMS, out=None, stream=None):
+    """Norm over the last axis (1 to 16384 channels) of x [.., n], bf16 or f32: with kind NORM_RMS x / sqrt(mean(x^2) +
+    eps), with NORM_LAYER (x - mean) / sqrt(var + eps), times weight and plus bias (f32 [n] or None).  x of two axes may
+    have its rows further apart.  out may be x."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise KDAError("x must be [.., n]")
+    dt, n = _in_dtype(x), x.shape[-1]
+    with _Device(x, stream) as d:
+        xp, xs = _norm_rows(d, x, "x", x)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        op, os_ = _norm_rows(d, out, "out", x)
+        rc = load_library().kda_norm_fwd(xp, d.flat(weight, "weight", shape=(n,)), d.flat(bias, "bias", shape=(n,)),
+                                         x.numel() // n, n, xs, os_, float(eps), int(kind), op, dt, _stream(stream))
+        _check(rc, "kda_norm_fwd")
+        return out
+
+
+def norm_bwd(x, dy, weight=None, eps=1e-6, kind=NORM_RMS, dx=None, want_dweight=True, want_dbias=False, workspace=None,
+             stream=None):
+    """Gradients of norm_fwd at x for dy: (dx in x's dtype, dweight f32 or None, dbias f32 or None).  dx may be x or dy."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise KDAError("x must be [.., n]")
+    dt, n = _in_dtype(x), x.shape[-1]
+    rows = x.numel() // n
+    with _Device(x, stream) as d:
+        lib = load_library()
+        xp, xs = _norm_rows(d, x, "x", x)
+        gp, gs = _norm_rows(d, dy, "dy", x)
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        op, os_ = _norm_rows(d, dx, "dx", x)
+        new = lambda want: torch.empty(n, dtype=torch.float32, device=x.device) if want else None
+        dw, db = new(want_dweight), new(want_dbias)
+        ws, nb = d.workspace(workspace, lib.kda_norm_bwd_workspace_size(rows, n, dt) if want_dweight or want_dbias else 0)
+        rc = lib.kda_norm_bwd(xp, gp, d.flat(weight, "weight", shape=(n,)), rows, n, xs, gs, os_, float(eps), int(kind), op,
+                              d.flat(dw, "dweight"), d.flat(db, "dbias"), dt, ws, nb, _stream(stream))
+        _check(rc, "kda_norm_bwd")
+        return dx, dw, db
+
+
+def _conv_shape(x, conv_w, cu_seqlens):
+    if x.dim() != 2 or conv_w.dim() != 2:
+        raise KDAError("x must be [T, C] and conv_w [C, W]")
+    if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2):
+        raise KDAError("cu_seqlens must be int32 [N + 1] with N >= 1")
+    return x.shape[0], x.shape[1], conv_w.shape[1]
+
+
+def conv_fwd(x, conv_w, cu_seqlens, bias=None, tail=None, output_tail=True, conv_act=CONV_SILU, out=None, tail_out=None,
+             status=None, stream=None):
+    """Short causal convolution of packed sequences: x [T, C] (bf16 or f32, rows may lie further apart), conv_w f32
+    [C, W] (W from 1 to 4), cu_seqlens int32 [N + 1], bias f32 [C]; tail [N, W - 1, C] in x's dtype holds the rows
+    before each sequence (None: zeros).  Returns (y [T, C], tail after each sequence [N, W - 1, C] or None): the conv_tail
+    that decode_verify_replay, conv_step and a following call continue from.  Rows of no sequence are not written."""
+    T, C, W = _conv_shape(x, conv_w, cu_seqlens)
+    N, dt = cu_seqlens.shape[0] - 1, _in_dtype(x)
+    with _Device(x, stream) as d:
+        if out is None:
+            out = torch.empty((T, C), dtype=x.dtype, device=x.device)
+        if tail_out is None and output_tail:
+            tail_out = torch.empty((N, W - 1, C), dtype=x.dtype, device=x.device)
+        xp, xs = d.rows(x, "x", x.dtype, (T, C))
+        yp, ys = d.rows(out, "out", x.dtype, (T, C))
+        tp, ts = d.tails(tail, "tail", x.dtype, (N, W - 1, C))
+        op, os_ = d.tails(tail_out, "tail_out", x.dtype, (N, W - 1, C))
+        rc = load_library().kda_conv_fwd(xp, d.flat(cu_seqlens, "cu_seqlens", torch.int32), d.flat(conv_w, "conv_w", shape=(C, W)),
+                                         d.flat(bias, "bias", shape=(C,)), tp, N, T, C, W, xs, ts, ys, os_, int(conv_act), yp, op,
+                                         dt, d.flat(status, "status", torch.int32), _stream(stream))
+        _check(rc, "kda_conv_fwd")
+        return out, tail_out
+
+
+def conv_bwd(x, conv_w, cu_seqlens, dy, bias=None, tail=None, dtail_out=None, conv_act=CONV_SILU, dx=None, workspace=None,
+             status=None, stream=None):
+    """Gradients of conv_fwd for dy [T, C] (x's dtype or f32, as chunk_bwd's are) and dtail_out f32 [N, W - 1, C] (or
+    None): (dx in x's dtype, dw f32 [C, W], dbias f32 [C] or None without bias, dtail f32 [N, W - 1, C] or None without tail)."""
+    T, C, W = _conv_shape(x, conv_w, cu_seqlens)
+    N, dt, f32 = cu_seqlens.shape[0] - 1, _in_dtype(x), torch.float32
+    if dy.dtype != x.dtype and dy.dtype != f32:
+        raise KDAError(f"dy must be {x.dtype} or {f32}, got {dy.dtype}")
+    with _Device(x, stream) as d:
+        lib = load_library()
+        if dx is None:
+            dx = torch.empty((T, C), dtype=x.dtype, device=x.device)
+        new = lambda *s: torch.empty(s, dtype=f32, device=x.device)
+        dw, db = new(C, W), new(C) if bias is not None else None
+        dtail = new(N, W - 1, C) if tail is not None else None
+        xp, xs = d.rows(x, "x", x.dtype, (T, C))
+        gp, gs = d.rows(dy, "dy", dy.dtype, (T, C))
+        op, os_ = d.rows(dx, "dx", x.dtype, (T, C))
+        tp, ts = d.tails(tail, "tail", x.dtype, (N, W - 1, C))
+        ws, nb = d.workspace(workspace, lib.kda_conv_bwd_workspace_size(T, C, W))
+        rc = lib.kda_conv_bwd(xp, d.flat(cu_seqlens, "cu_seqlens", torch.int32), d.flat(conv_w, "conv_w", shape=(C, W)),
+                              d.flat(bias, "bias", shape=(C,)), tp, gp, d.flat(dtail_out, "dtail_out", shape=(N, W - 1, C)), N, T,
+                              C, W, xs, ts, gs, os_, int(conv_act), op, d.flat(dw, "dw"), d.flat(db, "dbias"),
+                              d.flat(dtail, "dtail"), dt, _in_dtype(dy), ws, nb, d.flat(status, "status", torch.int32),
+                              _stream(stream))
+        _check(rc, "kda_conv_bwd")
+        return dx, dw, db, dtail
+
+
+def conv_step(x, conv_w, tail, bias=None, conv_act=CONV_SILU, out=None, stream=None):
+    """conv_fwd for one token of each request: x [R, C]; tail [R, W - 1, C] moves on in place.  Returns y [R, C]."""
+    R, C, W = _conv_shape(x, conv_w, None)
+    dt = _in_dtype(x)
+    with _Device(x, stream) as d:
+        if out is None:
+            out = torch.empty((R, C), dtype=x.dtype, device=x.device)
+        xp, xs = d.rows(x, "x", x.dtype, (R, C))
+        yp, ys = d.rows(out, "out", x.dtype, (R, C))
+        tp, ts = d.tails(tail, "tail", x.dtype, (R, W - 1, C))
+        rc = load_library().kda_conv_step(xp, d.flat(conv_w, "conv_w", shape=(C, W)), d.flat(bias, "bias", shape=(C,)), tp, R, C,
+                                          W, xs, ts, ys, int(conv_act), yp, dt, _stream(stream))
+        _check(rc, "kda_conv_step")
+        return out
+
+
+def _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias):
+    """The pointers and sizes that the scan's calls begin with: (pointers, (rows, D, G, S), strides)."""
+    if x.dim() != 2 or A.dim() != 2 or B.dim() != 3:
+        raise KDAError("x and dt must be [T, D], A [D, S], B and C [T, G, S]")
+    T, n = x.shape
+    G, S = B.shape[1:]
+    xp, xs = d.rows(x, "x", x.dtype, (T, n))
+    dtp, dts = d.rows(dt, "dt", x.dtype, (T, n))
+    zp, zs = d.rows(z, "z", x.dtype, (T, n))
+    bp, bs = d.rows(B, "B", x.dtype, (T, G, S))
+    cp, cs = d.rows(C, "C", x.dtype, (T, G, S))
+    ptrs = (xp, dtp, d.flat(A, "A", shape=(n, S)), bp, cp, d.flat(D, "D", shape=(n,)), zp, d.flat(dt_bias, "dt_bias", shape=(n,)))
+    return ptrs, (T, n, G, S), (xs, dts, bs, cs, zs)
+
+
+def _scan_sequences(cu_seqlens):
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise KDAError("cu_seqlens must be int32 [N + 1] with N >= 1")
+    return cu_seqlens.shape[0] - 1
+
+
+def scan_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, initial_state=None, output_final_state=True,
+             dt_softplus=True, save=False, out=None, final_state=None, saved=None, workspace=None, status=None, stream=None):
+    """Selective state space scan of packed sequences.  x, dt, z [T, D], B, C [T, G, S] (bf16 or f32, rows may lie further
+    apart; S 8, 16, 32 or 64, G divides D), A f32 [D, S], D and dt_bias f32 [D], initial_state f32 [N, D, S]:
+        delta = softplus(dt + dt_bias),  h = e^(delta A) h + delta x B,  y = (C h + D x) silu(z)
+    Returns (y [T, D], final_state f32 [N, D, S] or None), and with save the states that scan_bwd starts from (4 / 8 S
+    bytes per token and channel).  Rows of no sequence are not written."""
+    N, f32 = _scan_sequences(cu_seqlens), torch.float32
+    with _Device(x, stream) as d:
+        lib = load_library()
+        ptrs, (T, n, G, S), strides = _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias)
+        if out is None:
+            out = torch.empty((T, n), dtype=x.dtype, device=x.device)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N, n, S), dtype=f32, device=x.device)
+        if save:
+            need = lib.kda_scan_saved_size(N, T, n, S) // 4
+            if saved is None:
+                saved = torch.empty(need, dtype=f32, device=x.device)
+            elif saved.numel() < need:
+                raise KDAError(f"saved must hold {need} f32 values, got {saved.numel()}")
+        yp, ys = d.rows(out, "out", x.dtype, (T, n))
+        ws, nb = d.workspace(workspace, lib.kda_scan_workspace_size(N, T, n, G, S))
+        rc = lib.kda_scan_fwd(*ptrs, d.flat(cu_seqlens, "cu_seqlens", torch.int32), N, T, n, G, S, *strides, ys,
+                              d.flat(initial_state, "initial_state", shape=(N, n, S)),
+                              d.flat(final_state, "final_state", shape=(N, n, S)), int(bool(dt_softplus)), yp,
+                              d.flat(saved, "saved") if save else None, _in_dtype(x), ws, nb,
+                              d.flat(status, "status", torch.int32), _stream(stream))
+        _check(rc, "kda_scan_fwd")
+        return (out, final_state, saved) if save else (out, final_state)
+
+
+def scan_bwd(x, dt, A, B, C, cu_seqlens, dy, saved, D=None, z=None, dt_bias=None, initial_state=None, dfinal_state=None,
+             dt_softplus=True, workspace=None, status=None, stream=None):
+    """Gradients of scan_fwd, from its inputs, what it saved, dy [T, D] and dfinal_state f32 [N, D, S] (or None): (dx, ddt
+    [T, D], dA f32 [D, S], dB, dC [T, G, S], dD f32 [D], dz [T, D], ddt_bias f32 [D], dinitial_state f32 [N, D, S]), None
+    for what the call has not got.  dx, ddt, dB, dC and dz are of x's dtype."""
+    N, f32 = _scan_sequences(cu_seqlens), torch.float32
+    with _Device(x, stream) as d:
+        lib = load_library()
+        ptrs, (T, n, G, S), strides = _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias)
+        if initial_state is not None:
+            d.flat(initial_state, "initial_state", shape=(N, n, S))
+        need = lib.kda_scan_saved_size(N, T, n, S) // 4
+        if saved.numel() < need:
+            raise KDAError(f"saved must hold {need} f32 values, got {saved.numel()}")
+        gp, gs = d.rows(dy, "dy", x.dtype, (T, n))
+        new = lambda have, dtype, *s: torch.empty(s, dtype=dtype, device=x.device) if have is not None else None
+        dx, ddt, dz = new(x, x.dtype, T, n), new(x, x.dtype, T, n), new(z, x.dtype, T, n)
+        dB, dC, dA = new(x, x.dtype, T, G, S), new(x, x.dtype, T, G, S), new(x, f32, n, S)
+        dD, dbias, dh = new(D, f32, n), new(dt_bias, f32, n), new(initial_state, f32, N, n, S)
+        ws, nb = d.workspace(workspace, lib.kda_scan_bwd_workspace_size(N, T, n, G, S))
+        ptr = lambda t: None if t is None else t.data_ptr()
+        rc = lib.kda_scan_bwd(*ptrs, d.flat(cu_seqlens, "cu_seqlens", torch.int32), gp,
+                              d.flat(dfinal_state, "dfinal_state", shape=(N, n, S)), d.flat(saved, "saved"), N, T, n, G, S,
+                              *strides, gs, int(bool(dt_softplus)), ptr(dx), ptr(ddt), ptr(dA), ptr(dB), ptr(dC), ptr(dD),
+                              ptr(dz), ptr(dbias), ptr(dh), _in_dtype(x), ws, nb, d.flat(status, "status", torch.int32),
+                              _stream(stream))
+        _check(rc, "kda_scan_bwd")
+        return dx, ddt, dA, dB, dC, dD, dz, dbias, dh
+
+
+def scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus=True, out=None, stream=None):
+    """scan_fwd for one token of each request: x, dt, z [R, D], B, C [R, G, S]; state f32 [R, D, S] moves on in place.
+    Returns y [R, D]."""
+    with _Device(x, stream) as d:
+        ptrs, (R, n, G, S), strides = _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias)
+        if out is None:
+            out = torch.empty((R, n), dtype=x.dtype, device=x.device)
+        yp, ys = d.rows(out, "out", x.dtype, (R, n))
+        rc = load_library().kda_scan_step(*ptrs, d.flat(state, "state", shape=(R, n, S)), R, n, G, S, *strides, ys,
+                                          int(bool(dt_softplus)), yp, _in_dtype(x), _stream(stream))
+        _check(rc, "kda_scan_step")
+        return out

@@ -332,6 +332,61 @@ int copy_streams(CopyStreams *cs) {
     *cs = g_copy[dev];
     return KDA_OK;
 }
+// `rows` rows of `width` elements of `size` bytes, `stride` elements apart
+struct Rows {
+    const void *p;
+    long long rows, width, stride;
+    int size;
+    uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
+    uintptr_t bytes() const { return p && rows > 0 ? (uintptr_t)((rows - 1) * stride + width) * size : 0; }
+    bool on16() const { return !p || (!(begin() & 15u) && (rows < 2 || stride * size % 16 == 0)); }
+};
+inline Rows flat(const void *p, long long n, int size = 4) { return {p, p && n > 0 ? 1 : 0, n, n, size}; }
+
+// whether two of them share a byte; rows of one stride may lie side by side
+bool meet(const Rows &x, const Rows &y) {
+    const uintptr_t a = x.begin(), b = y.begin();
+    if (!x.bytes() || !y.bytes() || a >= b + y.bytes() || b >= a + x.bytes()) return false;
+    const uintptr_t s = (uintptr_t)x.stride * x.size, wx = (uintptr_t)x.width * x.size, wy = (uintptr_t)y.width * y.size;
+    if (x.rows < 2 || y.rows < 2 || s != (uintptr_t)y.stride * y.size) return true;
+    const uintptr_t d = b >= a ? (b - a) % s : (s - (a - b) % s) % s;  // y's column from x's
+    return d < wx || d + wy > s;
+}
+
+// outputs apart from inputs and from one another
+template <int I, int O>
+bool apart(const Rows (&in)[I], const Rows (&out)[O]) {
+    for (int o = 0; o < O; ++o) {
+        for (const Rows &x : in)
+            if (meet(x, out[o])) return false;
+        for (int q = o + 1; q < O; ++q)
+            if (meet(out[o], out[q])) return false;
+    }
+    return true;
+}
+
+// strides and element alignment of all of them
+template <int N>
+int rows_ok(const Rows (&r)[N]) {
+    for (const Rows &x : r) {
+        if (!x.p) continue;
+        if (x.stride < x.width) return KDA_ERR_INVALID_ARG;
+        if (x.begin() % x.size) return KDA_ERR_ALIGNMENT;
+    }
+    return KDA_OK;
+}
+
+template <int N>
+bool all_on16(const Rows (&r)[N]) {
+    for (const Rows &x : r)
+        if (!x.on16()) return false;
+    return true;
+}
+
+inline bool dtype_ok(int t) { return t == KDA_DTYPE_BF16 || t == KDA_DTYPE_F32; }
+inline int elem_size(int t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
+constexpr int kMaxTokens = 1 << 30, kMaxNorm = 16384, kMaxGridY = 65535;
+
 }  // namespace
 
 extern "C" {
@@ -1354,6 +1409,409 @@ int kda_cache4_attention(const void *q, const void *cache, const int32_t *block_
                                             many ? kda::cache4_attn_tc_rows(rows) : 0, sms, st);
         });
     return cuda_status(e);
+}
+
+// ------------------------------------------------------------------ norm, convolution, scan
+static int norm_args(kda::NormArgs &a, const void *x, const float *weight, long long rows, int d, float eps, int kind,
+                     int dtype) {
+    if (rows < 0 || d < 1 || !dtype_ok(dtype) || (kind != KDA_NORM_RMS && kind != KDA_NORM_LAYER)) return KDA_ERR_INVALID_ARG;
+    if (d > kMaxNorm || rows > (1LL << 40)) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (rows > 0 && !x) return KDA_ERR_INVALID_ARG;
+    a.x = x; a.weight = weight; a.rows = rows; a.d = d; a.eps = eps; a.layer = kind == KDA_NORM_LAYER;
+    return KDA_OK;
+}
+
+int kda_norm_fwd(const void *x, const float *weight, const float *bias, long long rows, int d, long long x_stride,
+                 long long y_stride, float eps, int kind, void *y, int dtype, void *stream) {
+    kda::NormArgs a = {};
+    if (int rc = norm_args(a, x, weight, rows, d, eps, kind, dtype)) return rc;
+    if (rows == 0) return KDA_OK;
+    if (!y) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(dtype);
+    const Rows r[] = {{x, rows, d, x_stride, e}, {y, rows, d, y_stride, e}};
+    if (int rc = rows_ok(r)) return rc;
+    if (!aligned16(weight) || !aligned16(bias)) return KDA_ERR_ALIGNMENT;
+    const Rows in[] = {flat(weight, d), flat(bias, d)}, out[] = {r[1]};
+    if (!apart(in, out) || (meet(r[0], r[1]) && !(x == y && x_stride == y_stride))) return KDA_ERR_INVALID_ARG;
+    a.bias = bias; a.y = y; a.x_stride = x_stride; a.y_stride = y_stride;
+    a.wide = all_on16(r) && (long long)d * e % 16 == 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed_launch(KDA_KERNEL_NORM, st, [&] {
+        return kda::launch_norm(a, dtype == KDA_DTYPE_BF16, false, sm_count(), st);
+    }));
+}
+
+size_t kda_norm_bwd_workspace_size(long long rows, int d, int dtype) {
+    kda::NormArgs a = {};
+    if (norm_args(a, &a, nullptr, rows, d, 0.f, KDA_NORM_RMS, dtype)) return 0;
+    // the more blocks of the two forms
+    size_t most = 0;
+    for (int wide = 0; wide < 2; ++wide) {
+        a.wide = wide;
+        if (wide && (long long)d * elem_size(dtype) % 16) break;
+        const size_t n = kda::norm_bwd_blocks(a, dtype == KDA_DTYPE_BF16, sm_count());
+        most = n > most ? n : most;
+    }
+    return align256(most * 2 * d * sizeof(float));
+}
+
+int kda_norm_bwd(const void *x, const void *dy, const float *weight, long long rows, int d, long long x_stride,
+                 long long dy_stride, long long dx_stride, float eps, int kind, void *dx, float *dweight, float *dbias,
+                 int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    kda::NormArgs a = {};
+    if (int rc = norm_args(a, x, weight, rows, d, eps, kind, dtype)) return rc;
+    if (rows > 0 && (!dy || !dx)) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(dtype);
+    const Rows r[] = {{x, rows, d, x_stride, e}, {dy, rows, d, dy_stride, e}, {dx, rows, d, dx_stride, e}};
+    if (rows > 0)
+        if (int rc = rows_ok(r)) return rc;
+    if (!aligned16(weight) || !aligned16(dweight) || !aligned16(dbias) || !aligned16(workspace)) return KDA_ERR_ALIGNMENT;
+    const bool sums = dweight || dbias;
+    const size_t need = kda_norm_bwd_workspace_size(rows, d, dtype);
+    if (sums && need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+    const Rows in[] = {flat(weight, d)};
+    const Rows out[] = {r[2], flat(dweight, d), flat(dbias, d), flat(sums ? workspace : nullptr, (long long)need, 1)};
+    const Rows more[] = {out[1], out[2], out[3]}, rows_in[] = {r[0], r[1]};
+    if (!apart(in, out) || !apart(rows_in, more) || (meet(r[0], r[2]) && !(x == dx && x_stride == dx_stride)) ||
+        (meet(r[1], r[2]) && !(dy == dx && dy_stride == dx_stride)))
+        return KDA_ERR_INVALID_ARG;
+    a.dy = dy; a.dx = dx; a.x_stride = x_stride; a.dy_stride = dy_stride; a.dx_stride = dx_stride;
+    a.wide = all_on16(r) && (long long)d * e % 16 == 0;
+    a.parts = sums ? static_cast<float *>(workspace) : nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
+    if (rows > 0)
+        err = timed_launch(KDA_KERNEL_NORM, st, [&] {
+            return kda::launch_norm(a, dtype == KDA_DTYPE_BF16, true, sm_count(), st);
+        });
+    if (sums && err == cudaSuccess) {
+        kda::SumRowsArgs s = {a.parts, rows > 0 ? kda::norm_bwd_blocks(a, dtype == KDA_DTYPE_BF16, sm_count()) : 0, 2 * d,
+                              {dweight, dbias, nullptr}, {0, d, 2 * d, 2 * d}, {1, 1, 1}};
+        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, st); });
+    }
+    return cuda_status(err);
+}
+
+// shape checks shared by the convolution's calls (R requests of one token: T = R)
+static int conv_shape(int N, int T, int C, int W, int act, int dtype) {
+    if (N < 1 || T < 0 || C < 1 || !dtype_ok(dtype) || (act != KDA_CONV_NONE && act != KDA_CONV_SILU)) return KDA_ERR_INVALID_ARG;
+    if (W < 1 || W > 4) return KDA_ERR_INVALID_ARG;
+    if (T > kMaxTokens || N > kMaxTokens || C > (1 << 22)) return KDA_ERR_UNSUPPORTED_SHAPE;
+    return KDA_OK;
+}
+
+int kda_conv_fwd(const void *x, const int32_t *cu_seqlens, const float *w, const float *bias, const void *tail, int N,
+                 int T, int C, int W, long long x_stride, long long tail_stride, long long y_stride,
+                 long long tail_out_stride, int conv_act, void *y, void *tail_out, int dtype, uint32_t *status,
+                 void *stream) {
+    if (int rc = conv_shape(N, T, C, W, conv_act, dtype)) return rc;
+    if (!cu_seqlens || !w || (T > 0 && (!x || !y))) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(dtype);
+    const long long tails = (long long)N * (W - 1);
+    if (tails == 0) tail = nullptr, tail_out = nullptr;
+    const Rows r[] = {{T > 0 ? x : nullptr, T, C, x_stride, e}, {tail, tails, C, tail_stride, e}, {T > 0 ? y : nullptr, T, C, y_stride, e},
+                      {tail_out, tails, C, tail_out_stride, e}};
+    if (int rc = rows_ok(r)) return rc;
+    if (!aligned16(w) || !aligned16(bias) || !aligned16(cu_seqlens)) return KDA_ERR_ALIGNMENT;
+    const Rows in[] = {r[0], r[1], flat(w, (long long)C * W), flat(bias, C), flat(cu_seqlens, N + 1LL)}, out[] = {r[2], r[3]};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    kda::ConvArgs a = {};
+    a.x = x; a.tail = tail; a.cu_seqlens = cu_seqlens; a.w = w; a.bias = bias; a.y = y; a.tail_out = tail_out;
+    a.x_stride = x_stride; a.tail_stride = tail_stride; a.y_stride = y_stride; a.tail_out_stride = tail_out_stride;
+    a.N = N; a.T = T; a.C = C; a.act = conv_act == KDA_CONV_SILU; a.status = status;
+    a.wide = all_on16(r) && (long long)C * e % 16 == 0;
+    a.run = kda::conv_run(T, C, a.wide ? 16 / e : 1, false, sm_count());
+    a.runs = (T + a.run - 1) / a.run;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed_launch(KDA_KERNEL_CONV, st, [&] { return kda::launch_conv(a, W, 0, bf16, bf16, st); }));
+}
+
+size_t kda_conv_bwd_workspace_size(int T, int C, int W) {
+    if (conv_shape(1, T, C, W, KDA_CONV_NONE, KDA_DTYPE_F32)) return 0;
+    // runs are no shorter, and so no more, with four channels a thread than with one
+    const int run = kda::conv_run(T, C, 4, true, sm_count());
+    return align256((size_t)((T + run - 1) / run) * (W + 1) * C * sizeof(float));
+}
+
+int kda_conv_bwd(const void *x, const int32_t *cu_seqlens, const float *w, const float *bias, const void *tail,
+                 const void *dy, const float *dtail_out, int N, int T, int C, int W, long long x_stride,
+                 long long tail_stride, long long dy_stride, long long dx_stride, int conv_act, void *dx, float *dw,
+                 float *dbias, float *dtail, int dtype, int dy_dtype, void *workspace, size_t workspace_bytes,
+                 uint32_t *status, void *stream) {
+    if (int rc = conv_shape(N, T, C, W, conv_act, dtype)) return rc;
+    if (dy_dtype != dtype && dy_dtype != KDA_DTYPE_F32) return KDA_ERR_INVALID_ARG;
+    if (!cu_seqlens || !w || (T > 0 && (!x || !dy || !dx))) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(dtype);
+    const long long tails = (long long)N * (W - 1);
+    if (tails == 0) tail = nullptr, dtail_out = nullptr, dtail = nullptr;
+    const bool any = T > 0, sums = dw || dbias;
+    const Rows r[] = {{any ? x : nullptr, T, C, x_stride, e}, {tail, tails, C, tail_stride, e},
+                      {any ? dy : nullptr, T, C, dy_stride, elem_size(dy_dtype)}, {any ? dx : nullptr, T, C, dx_stride, e}};
+    if (int rc = rows_ok(r)) return rc;
+    if (!aligned16(w) || !aligned16(bias) || !aligned16(cu_seqlens) || !aligned16(dtail_out) || !aligned16(dw) ||
+        !aligned16(dbias) || !aligned16(dtail) || !aligned16(workspace))
+        return KDA_ERR_ALIGNMENT;
+    const size_t need = kda_conv_bwd_workspace_size(T, C, W);
+    if (sums && need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+    const Rows in[] = {r[0], r[1], r[2], flat(w, (long long)C * W), flat(bias, C), flat(cu_seqlens, N + 1LL),
+                       flat(dtail_out, tails * C)};
+    const Rows out[] = {r[3], flat(dw, (long long)C * W), flat(dbias, C), flat(dtail, tails * C),
+                        flat(sums ? workspace : nullptr, (long long)need, 1)};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    kda::ConvArgs a = {};
+    a.x = x; a.tail = tail; a.dy = dy; a.cu_seqlens = cu_seqlens; a.w = w; a.bias = bias; a.dx = dx;
+    a.x_stride = x_stride; a.tail_stride = tail_stride; a.dy_stride = dy_stride; a.dx_stride = dx_stride;
+    a.dtail_out = dtail_out; a.dtail = dtail; a.parts = sums ? static_cast<float *>(workspace) : nullptr;
+    a.N = N; a.T = T; a.C = C; a.act = conv_act == KDA_CONV_SILU; a.status = status;
+    a.wide = all_on16(r) && (long long)C * e % 16 == 0;
+    a.run = kda::conv_run(T, C, 4, true, sm_count());
+    a.runs = (T + a.run - 1) / a.run;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t err = timed_launch(KDA_KERNEL_CONV, st, [&] {
+        return kda::launch_conv(a, W, 1, dtype == KDA_DTYPE_BF16, dy_dtype == KDA_DTYPE_BF16, st);
+    });
+    if (sums && err == cudaSuccess) {
+        kda::SumRowsArgs s = {a.parts, a.runs, (W + 1) * C, {dw, dbias, nullptr}, {0, W * C, (W + 1) * C, (W + 1) * C}, {W, 1, 1}};
+        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, st); });
+    }
+    return cuda_status(err);
+}
+
+int kda_conv_step(const void *x, const float *w, const float *bias, void *tail, int R, int C, int W, long long x_stride,
+                  long long tail_stride, long long y_stride, int conv_act, void *y, int dtype, void *stream) {
+    if (int rc = conv_shape(R, R, C, W, conv_act, dtype)) return rc;
+    const long long tails = (long long)R * (W - 1);
+    if (!x || !w || !y || (tails && !tail)) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(dtype);
+    if (tails == 0) tail = nullptr;
+    const Rows r[] = {{x, R, C, x_stride, e}, {tail, tails, C, tail_stride, e}, {y, R, C, y_stride, e}};
+    if (int rc = rows_ok(r)) return rc;
+    if (!aligned16(w) || !aligned16(bias)) return KDA_ERR_ALIGNMENT;
+    const Rows in[] = {r[0], flat(w, (long long)C * W), flat(bias, C)}, out[] = {r[1], r[2]};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    if ((long long)R * ((C + 127) / 128) > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    kda::ConvArgs a = {};
+    a.x = x; a.w = w; a.bias = bias; a.y = y; a.tail_out = tail;
+    a.x_stride = x_stride; a.y_stride = y_stride; a.tail_out_stride = tail_stride;
+    a.N = R; a.C = C; a.act = conv_act == KDA_CONV_SILU;
+    a.wide = all_on16(r) && (long long)C * e % 16 == 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed_launch(KDA_KERNEL_CONV, st, [&] { return kda::launch_conv(a, W, 2, bf16, bf16, st); }));
+}
+
+static int scan_shape(int N, int T, int D, int G, int S, int dtype) {
+    if (N < 1 || T < 0 || D < 1 || G < 1 || D % G || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
+    if ((S != 8 && S != 16 && S != 32 && S != 64) || T > kMaxTokens || N > kMaxTokens || D > (1 << 22) ||
+        (long long)D * S + 2LL * D > 0x7fffffffLL ||
+        (long long)G * ((D / G + kda::scan_bwd_channels(S) - 1) / kda::scan_bwd_channels(S)) > kMaxGridY)
+        return KDA_ERR_UNSUPPORTED_SHAPE;
+    return KDA_OK;
+}
+
+// Tokens of a segment (a multiple of 16), or 0 for whole sequences.  Where the
+// sequences' blocks cover the SMs, only sequences of over four times the mean length
+// are cut; else all are, for about `fill` blocks per SM.
+static int scan_segment(int N, int T, int D, int G, int S, bool backward) {
+    if (T < 512 || N > kMaxGridY) return 0;
+    const int ch = backward ? kda::scan_bwd_channels(S) : kda::scan_channels(S), sms = sm_count();
+    const long long tiles = (long long)G * ((D / G + ch - 1) / ch), enough = backward ? 2LL * sms : sms + sms / 2;
+    long long seg;
+    if (N * tiles >= enough) {
+        seg = 4LL * T / N;
+        if (seg < 1024) seg = 1024;
+    } else {
+        const long long parts = (4LL * sms + tiles - 1) / tiles;
+        seg = (T + parts - 1) / parts;
+        if (seg < 128) seg = 128;
+    }
+    seg = (seg + 15) / 16 * 16;
+    return seg >= T ? 0 : (int)seg;
+}
+
+namespace {
+struct ScanLayout {
+    int seg, units;
+    size_t state, sum, parts, bc, total;  // offsets of the segments' states and sums, partial sums
+};
+ScanLayout scan_layout(int N, int T, int D, int G, int S, bool backward) {
+    ScanLayout L = {};
+    L.seg = scan_segment(N, T, D, G, S, backward);
+    L.units = kda::scan_units(N, T, L.seg);
+    size_t o = 0;
+    if (L.seg) {
+        L.state = o;
+        o = align256(o + (size_t)L.units * D * S * 4);
+        L.sum = o;
+        o = align256(o + (size_t)L.units * D * 4);
+    }
+    if (backward) {
+        const int ch = kda::scan_bwd_channels(S);
+        L.parts = o;
+        o = align256(o + (size_t)L.units * ((size_t)D * S + 2 * D) * 4);
+        L.bc = o;
+        o = align256(o + (size_t)((D / G + ch - 1) / ch) * T * G * 2 * S * 4);
+    }
+    L.total = o;
+    return L;
+}
+}  // namespace
+
+size_t kda_scan_workspace_size(int N, int T, int D, int G, int S) {
+    return scan_shape(N, T, D, G, S, KDA_DTYPE_F32) ? 0 : scan_layout(N, T, D, G, S, false).total;
+}
+
+size_t kda_scan_saved_size(int N, int T, int D, int S) {
+    return scan_shape(N, T, D, 1, S, KDA_DTYPE_F32) ? 0 : ((size_t)(T / kda::kScanSaveEvery) + N) * D * S * 4;
+}
+
+size_t kda_scan_bwd_workspace_size(int N, int T, int D, int G, int S) {
+    return scan_shape(N, T, D, G, S, KDA_DTYPE_F32) ? 0 : scan_layout(N, T, D, G, S, true).total;
+}
+
+// the fields that a scan's calls share
+static kda::ScanArgs scan_args(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *skip,
+                               const void *z, const float *dt_bias, int N, int T, int D, int G, long long x_stride,
+                               long long dt_stride, long long B_stride, long long C_stride, long long z_stride, int softplus) {
+    kda::ScanArgs a = {};
+    a.x = x; a.dt = dt; a.A = A; a.B = B; a.C = C; a.Dskip = skip; a.z = z; a.dt_bias = dt_bias;
+    a.x_stride = x_stride; a.dt_stride = dt_stride; a.b_stride = B_stride; a.c_stride = C_stride; a.z_stride = z_stride;
+    a.N = N; a.T = T; a.D = D; a.G = G; a.dt_softplus = softplus != 0;
+    return a;
+}
+
+int kda_scan_fwd(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *skip, const void *z,
+                 const float *dt_bias, const int32_t *cu_seqlens, int N, int T, int D, int G, int S, long long x_stride,
+                 long long dt_stride, long long B_stride, long long C_stride, long long z_stride, long long y_stride,
+                 const float *initial_state, float *final_state, int dt_softplus, void *y, float *saved, int dtype,
+                 void *workspace, size_t workspace_bytes, uint32_t *status, void *stream) {
+    if (int rc = scan_shape(N, T, D, G, S, dtype)) return rc;
+    const bool any = T > 0;
+    if (!A || !cu_seqlens || (any && (!x || !dt || !B || !C || !y))) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(dtype);
+    const long long GS = (long long)G * S, DS = (long long)D * S;
+    const Rows r[] = {{any ? x : nullptr, T, D, x_stride, e}, {any ? dt : nullptr, T, D, dt_stride, e},
+                      {any ? z : nullptr, T, D, z_stride, e}, {any ? B : nullptr, T, GS, B_stride, e},
+                      {any ? C : nullptr, T, GS, C_stride, e}, {any ? y : nullptr, T, D, y_stride, e}};
+    if (int rc = rows_ok(r)) return rc;
+    if (!aligned16(A) || !aligned16(skip) || !aligned16(dt_bias) || !aligned16(cu_seqlens) || !aligned16(initial_state) ||
+        !aligned16(final_state) || !aligned16(saved) || !aligned16(workspace))
+        return KDA_ERR_ALIGNMENT;
+    const ScanLayout L = scan_layout(N, T, D, G, S, false);
+    if (L.total && (!workspace || workspace_bytes < L.total)) return KDA_ERR_WORKSPACE;
+    const Rows in[] = {r[0], r[1], r[2], r[3], r[4], flat(A, DS), flat(skip, D), flat(dt_bias, D), flat(cu_seqlens, N + 1LL),
+                       flat(initial_state, N * DS)};
+    const Rows out[] = {r[5], flat(final_state, N * DS), flat(saved, (long long)(kda_scan_saved_size(N, T, D, S) / 4)),
+                        flat(L.total ? workspace : nullptr, (long long)L.total, 1)};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    kda::ScanArgs a = scan_args(x, dt, A, B, C, skip, z, dt_bias, N, T, D, G, x_stride, dt_stride, B_stride, C_stride, z_stride, dt_softplus);
+    a.cu_seqlens = cu_seqlens; a.initial_state = initial_state; a.final_state = final_state; a.y = y; a.y_stride = y_stride;
+    a.saved = saved; a.status = status; a.seg = L.seg;
+    const Rows copied[] = {r[0], r[1], r[2]};
+    a.wide = all_on16(copied) && (long long)(D / G) * e % 16 == 0;
+    char *ws = static_cast<char *>(workspace);
+    a.seg_state = reinterpret_cast<float *>(ws + L.state);
+    a.seg_sum = reinterpret_cast<float *>(ws + L.sum);
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    const int sms = sm_count();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
+    if (L.seg) {
+        err = timed_launch(KDA_KERNEL_SCAN_SEGMENT, st, [&] { return kda::launch_scan(a, S, kda::SCAN_FORWARD, bf16, sms, st); });
+        if (err == cudaSuccess)
+            err = timed_launch(KDA_KERNEL_SCAN_SEGMENT, st, [&] { return kda::launch_scan_chain(a, S, false, st); });
+    }
+    if (err == cudaSuccess)
+        err = timed_launch(KDA_KERNEL_SCAN, st, [&] { return kda::launch_scan(a, S, kda::SCAN_WALK, bf16, sms, st); });
+    return cuda_status(err);
+}
+
+int kda_scan_bwd(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *skip, const void *z,
+                 const float *dt_bias, const int32_t *cu_seqlens, const void *dy, const float *dfinal_state,
+                 const float *saved, int N, int T, int D, int G, int S, long long x_stride, long long dt_stride,
+                 long long B_stride, long long C_stride, long long z_stride, long long dy_stride, int dt_softplus, void *dx,
+                 void *ddt, float *dA, void *dB, void *dC, float *dskip, void *dz, float *ddt_bias, float *dinitial_state,
+                 int dtype, void *workspace, size_t workspace_bytes, uint32_t *status, void *stream) {
+    if (int rc = scan_shape(N, T, D, G, S, dtype)) return rc;
+    const bool any = T > 0;
+    if (!A || !cu_seqlens || !saved || !dA || (any && (!x || !dt || !B || !C || !dy || !dx || !ddt || !dB || !dC || (z && !dz))))
+        return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(dtype);
+    const long long GS = (long long)G * S, DS = (long long)D * S;
+    const Rows r[] = {{any ? x : nullptr, T, D, x_stride, e}, {any ? dt : nullptr, T, D, dt_stride, e},
+                      {any ? z : nullptr, T, D, z_stride, e}, {any ? dy : nullptr, T, D, dy_stride, e},
+                      {any ? B : nullptr, T, GS, B_stride, e}, {any ? C : nullptr, T, GS, C_stride, e}};
+    if (int rc = rows_ok(r)) return rc;
+    for (const void *p : {(const void *)A, (const void *)skip, (const void *)dt_bias, (const void *)cu_seqlens,
+                          (const void *)dfinal_state, (const void *)saved, (const void *)dx, (const void *)ddt, (const void *)dA,
+                          (const void *)dB, (const void *)dC, (const void *)dskip, (const void *)dz, (const void *)ddt_bias,
+                          (const void *)dinitial_state, (const void *)workspace})
+        if (!aligned16(p)) return KDA_ERR_ALIGNMENT;
+    const ScanLayout L = scan_layout(N, T, D, G, S, true);
+    if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+    const long long TD = (long long)T * D;
+    if (!z) dz = nullptr;
+    const Rows in[] = {r[0], r[1], r[2], r[3], r[4], r[5], flat(A, DS), flat(skip, D), flat(dt_bias, D),
+                       flat(cu_seqlens, N + 1LL), flat(dfinal_state, N * DS),
+                       flat(saved, (long long)(kda_scan_saved_size(N, T, D, S) / 4))};
+    const Rows out[] = {flat(dx, TD, e), flat(ddt, TD, e), flat(dz, TD, e), flat(dB, T * GS, e), flat(dC, T * GS, e),
+                        flat(dA, DS), flat(dskip, D), flat(ddt_bias, D), flat(dinitial_state, N * DS),
+                        flat(workspace, (long long)L.total, 1)};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    kda::ScanArgs a = scan_args(x, dt, A, B, C, skip, z, dt_bias, N, T, D, G, x_stride, dt_stride, B_stride, C_stride, z_stride, dt_softplus);
+    a.cu_seqlens = cu_seqlens; a.dy = dy; a.dy_stride = dy_stride; a.dfinal = dfinal_state;
+    a.saved = const_cast<float *>(saved);
+    a.dx = dx; a.ddt = ddt; a.dz = dz; a.dB = dB; a.dC = dC; a.dstate = dinitial_state; a.status = status; a.seg = L.seg;
+    const Rows copied[] = {r[0], r[1], r[2], r[3]};
+    a.wide = all_on16(copied) && (long long)(D / G) * e % 16 == 0;
+    char *ws = static_cast<char *>(workspace);
+    a.seg_state = reinterpret_cast<float *>(ws + L.state);
+    a.seg_sum = reinterpret_cast<float *>(ws + L.sum);
+    a.parts = reinterpret_cast<float *>(ws + L.parts);
+    a.bc_parts = reinterpret_cast<float *>(ws + L.bc);
+    const bool bf16 = dtype == KDA_DTYPE_BF16;
+    const int sms = sm_count();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
+    if (L.seg) {
+        err = timed_launch(KDA_KERNEL_SCAN_SEGMENT, st, [&] { return kda::launch_scan(a, S, kda::SCAN_REVERSE, bf16, sms, st); });
+        if (err == cudaSuccess)
+            err = timed_launch(KDA_KERNEL_SCAN_SEGMENT, st, [&] { return kda::launch_scan_chain(a, S, true, st); });
+    }
+    if (err == cudaSuccess) err = timed_launch(KDA_KERNEL_SCAN_BWD, st, [&] { return kda::launch_scan_bwd(a, S, bf16, st); });
+    if (err == cudaSuccess) err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_scan_bc(a, S, bf16, st); });
+    if (err == cudaSuccess) {
+        const int n = (int)DS;
+        kda::SumRowsArgs s = {a.parts, L.units, n + 2 * D, {dA, dskip, ddt_bias}, {0, n, n + D, n + 2 * D}, {1, 1, 1}};
+        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, st); });
+    }
+    return cuda_status(err);
+}
+
+int kda_scan_step(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *skip, const void *z,
+                  const float *dt_bias, float *state, int R, int D, int G, int S, long long x_stride, long long dt_stride,
+                  long long B_stride, long long C_stride, long long z_stride, long long y_stride, int dt_softplus, void *y,
+                  int dtype, void *stream) {
+    if (int rc = scan_shape(R, R, D, G, S, dtype)) return rc;
+    if (!x || !dt || !A || !B || !C || !state || !y) return KDA_ERR_INVALID_ARG;
+    const int e = elem_size(dtype);
+    const long long GS = (long long)G * S, DS = (long long)D * S;
+    const Rows r[] = {{x, R, D, x_stride, e}, {dt, R, D, dt_stride, e}, {z, R, D, z_stride, e}, {B, R, GS, B_stride, e},
+                      {C, R, GS, C_stride, e}, {y, R, D, y_stride, e}};
+    if (int rc = rows_ok(r)) return rc;
+    if (!aligned16(A) || !aligned16(skip) || !aligned16(dt_bias) || !aligned16(state)) return KDA_ERR_ALIGNMENT;
+    const Rows in[] = {r[0], r[1], r[2], r[3], r[4], flat(A, DS), flat(skip, D), flat(dt_bias, D)}, out[] = {r[5], flat(state, R * DS)};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    if ((long long)R * ((D + 1024 / S - 1) / (1024 / S)) > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED_SHAPE;
+    kda::ScanArgs a = scan_args(x, dt, A, B, C, skip, z, dt_bias, R, R, D, G, x_stride, dt_stride, B_stride, C_stride, z_stride, dt_softplus);
+    a.state = state; a.y = y; a.y_stride = y_stride;
+    const Rows pair[] = {r[3], r[4]};
+    a.wide = all_on16(pair);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(timed_launch(KDA_KERNEL_SCAN, st, [&] {
+        return kda::launch_scan(a, S, kda::SCAN_STEP, dtype == KDA_DTYPE_BF16, sm_count(), st);
+    }));
 }
 
 int kda_kernel_timing_start(void) {

@@ -247,4 +247,81 @@ cudaError_t launch_cache4_attn_tc(const Cache4AttnArgs &a, int d, long long rows
 cudaError_t launch_cache4_merge(const Cache4AttnArgs &few, const Cache4AttnArgs &many, int d, bool bf16, int few_rows,
                                 int many_rows, int sms, cudaStream_t st);
 
+// RMS and layer norm of rows (norm.cu).
+struct NormArgs {
+    const void *x, *dy;           // rows of d elements, x_stride / dy_stride elements apart
+    const float *weight, *bias;   // [d] or null
+    void *y, *dx;
+    long long rows, x_stride, dy_stride, y_stride, dx_stride;
+    int d;
+    float eps;
+    bool layer, wide;             // wide: every row starts on a 16-byte boundary
+    float *parts;                 // backward: [blocks][2][d] sums of dy n and dy, or null
+};
+int norm_bwd_blocks(const NormArgs &a, bool bf16, int sms);
+cudaError_t launch_norm(const NormArgs &a, bool bf16, bool backward, int sms, cudaStream_t st);
+
+// Sums over the rows of parts [rows][width]: columns [begin[k], begin[k + 1])
+// are a table [cols[k]][..], whose transpose goes to out[k] (or nowhere).
+struct SumRowsArgs {
+    static constexpr int kOuts = 3;
+    const float *parts;
+    long long rows;
+    int width;
+    float *out[kOuts];
+    int begin[kOuts + 1], cols[kOuts];
+};
+cudaError_t launch_sum_rows(const SumRowsArgs &a, cudaStream_t st);
+
+// Short causal convolution (conv.cu).
+struct ConvArgs {
+    const void *x, *tail, *dy;    // rows of C channels, strides in elements; tail [N][W - 1] rows or null
+    long long x_stride, tail_stride, dy_stride;
+    const int32_t *cu_seqlens;    // [N + 1]
+    const float *w, *bias;        // [C][W], [C] or null
+    void *y, *tail_out, *dx;      // (single tokens: tail_out is the tail, in place)
+    long long y_stride, tail_out_stride, dx_stride;
+    const float *dtail_out;       // [N][W - 1][C] or null
+    float *dtail;                 // [N][W - 1][C] or null
+    float *parts;                 // backward: [runs][W + 1][C] sums for dw and dbias, or null
+    int N, T, C, run, runs;       // runs of `run` tokens
+    bool act, wide;               // wide: every row starts on a 16-byte boundary
+    uint32_t *status;
+};
+// what: 0 forward, 1 backward, 2 single tokens (N of them)
+cudaError_t launch_conv(const ConvArgs &a, int W, int what, bool bf16, bool dy_bf16, cudaStream_t st);
+int conv_run(int T, int C, int v, bool backward, int sms);
+
+// Selective state space scan (scan.cu, scan_bwd.cu).
+constexpr int kScanSaveEvery = 8;  // tokens between saved states
+struct ScanArgs {
+    const void *x, *dt, *B, *C, *z, *dy;  // rows, strides in elements; z may be null
+    long long x_stride, dt_stride, b_stride, c_stride, z_stride, dy_stride;
+    const float *A, *Dskip, *dt_bias;     // [D][S], [D] or null, [D] or null
+    const int32_t *cu_seqlens;            // [N + 1]
+    const float *initial_state, *dfinal;  // [N][D][S] or null
+    float *final_state, *state;           // [N][D][S]; state: in place (single tokens)
+    void *y;
+    long long y_stride;
+    float *saved;                         // [floor(T / 8) + N][D][S]: the state before every eighth token, or null
+    float *seg_state, *seg_sum;           // [units][D][S], [units][D]
+    int N, T, D, G, seg;                  // seg: tokens of a segment, 0 for whole sequences
+    bool dt_softplus, wide;               // wide: 16-byte copies of rows (single tokens: of B and C)
+    uint32_t *status;
+    // backward
+    void *dx, *ddt, *dz;                  // [T][D]
+    float *dstate;                        // [N][D][S] or null
+    float *bc_parts;                      // [channel tiles][T][G][2 S]
+    float *parts;                         // [units][D S + 2 D]: sums for dA, dD and ddt_bias
+    void *dB, *dC;                        // [T][G][S]
+};
+enum ScanWhat : int { SCAN_WALK = 0, SCAN_FORWARD = 1, SCAN_REVERSE = 2, SCAN_STEP = 3 };
+int scan_units(int N, int T, int seg);
+int scan_channels(int S);      // channels of a block
+int scan_bwd_channels(int S);  // channels of a block of the backward
+cudaError_t launch_scan(const ScanArgs &a, int S, int what, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_scan_chain(const ScanArgs &a, int S, bool reverse, cudaStream_t st);
+cudaError_t launch_scan_bwd(const ScanArgs &a, int S, bool bf16, cudaStream_t st);
+cudaError_t launch_scan_bc(const ScanArgs &a, int S, bool bf16, cudaStream_t st);
+
 }  // namespace kda

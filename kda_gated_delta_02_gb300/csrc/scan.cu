@@ -1,0 +1,373 @@
+// scan.cu -- the selective state space recurrence over packed sequences, and
+// single tokens.  Per channel c and state n, with v = dt + dt_bias, d = ln(1 + e^v):
+//
+//   h_t = e^{d_t A[c][n]} h_{t-1} + d_t x_t B_t[n],   y_t = (sum_n C_t[n] h_t + D[c] x_t) z_t sigmoid(z_t)
+//
+// What bounds it: instructions.  A token and channel costs 8 bytes (bf16 x,
+// dt, z, y) and, with 16 states, 16 exponentials and 32 pairs of packed fp32
+// operations: about 0.6 cycles of an SM, where 8 bytes take 0.34.
+//
+// A thread keeps a channel (16 states of it; more states take 2 or 4
+// neighbouring lanes), so the sum over n needs no exchange and a channel's
+// d and x no shared copies.  States lie in pairs for the packed operations.  A
+// block of 128 threads walks its tokens 16 at a time: x, dt and z of the next
+// 16 come by cp.async while these are worked on, and B and C (the same for all
+// channels of a group) are widened to 32 bits once per block, so that a thread
+// reads them as 16-byte broadcasts.
+//
+// The recurrence is serial along a sequence.  Where sequences times channels
+// do not fill the GPU, or one sequence is far longer than the mean, they are
+// cut into segments: a first kernel forms every segment's own end state from
+// zero and its sum of d (the segment's decay is e^{A sum d}, exactly), a second
+// chains these, and the walk then starts each segment from its true state.  The
+// first kernel costs about 0.8 of the walk, so the cut has to buy more.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_internal.h"
+#include "layer.cuh"
+#include "scan.cuh"
+
+namespace kda {
+namespace {
+using namespace layer;
+using namespace scan;
+
+constexpr int kTile = 16;  // tokens of a tile (a multiple of kSaveEvery)
+
+enum Mode : int {
+    WALK = 0,     // outputs, final and saved states
+    FORWARD = 1,  // a segment's end state from zero, and its sum of d
+    REVERSE = 2,  // the same backwards: what reaches its start of the gradients dy C
+};
+
+template <bool BF16, int S>
+struct Layout {
+    static constexpr int LN = S > 16 ? S / 16 : 1, M = S / LN, CH = kThreads / LN;
+    static constexpr int raw = kTile * CH * (BF16 ? 2 : 4);  // bytes of one tensor's tile
+    static constexpr int bytes = 2 * 3 * raw + 2 * kTile * 2 * S * 4;
+};
+
+template <bool BF16, int S, int MODE, bool VEC>
+__global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
+    using E = Elem<BF16>;
+    using L = Layout<BF16, S>;
+    constexpr int LN = L::LN, M = L::M, CH = L::CH;
+    extern __shared__ __align__(16) unsigned char smem[];
+    E *raw = reinterpret_cast<E *>(smem);                            // [2][3][kTile][CH]
+    float *bc = reinterpret_cast<float *>(smem + 2 * 3 * L::raw);    // [2][kTile][2 S]: B, then C
+    const int tid = threadIdx.x, ch = tid / LN, ln = tid % LN;
+    const Segment g = segment_of(a.cu_seqlens, a.N, a.T, a.seg, blockIdx.x);
+    if (MODE == WALK && tid == 0 && blockIdx.y == 0) check_sequence(a, blockIdx.x);
+    if (g.s < 0) return;
+    if (MODE == FORWARD && g.last) return;
+    if (MODE == REVERSE && g.first) return;
+    const int per = a.D / a.G, tiles = (per + CH - 1) / CH;
+    const int grp = blockIdx.y / tiles, c_in = (blockIdx.y - grp * tiles) * CH;  // first channel, in its group
+    const int c0 = grp * per + c_in, left = per - c_in;                          // channels from c0 on in the group
+    const bool live = ch < left;
+    const int c = c0 + (live ? ch : 0);
+
+    const E *src[3] = {static_cast<const E *>(MODE == REVERSE ? a.dy : a.x), static_cast<const E *>(a.dt),
+                       static_cast<const E *>(a.z)};
+    const long long stride[3] = {MODE == REVERSE ? a.dy_stride : a.x_stride, a.dt_stride, a.z_stride};
+    const bool third = MODE != FORWARD && a.z != nullptr;
+    const E *Bp = static_cast<const E *>(MODE == REVERSE ? a.C : a.B) + (size_t)grp * S;
+    const E *Cp = static_cast<const E *>(a.C) + (size_t)grp * S;
+    const long long b_stride = MODE == REVERSE ? a.c_stride : a.b_stride;
+
+    float2 A2[M / 2], h2[M / 2];
+    {
+        const float4 *p = reinterpret_cast<const float4 *>(a.A + (size_t)c * S + ln * M);
+        const float *h0 = nullptr;
+        if (MODE == WALK) h0 = g.first ? (a.initial_state ? a.initial_state + (size_t)g.s * a.D * S : nullptr)
+                                       : a.seg_state + (size_t)blockIdx.x * a.D * S;
+        const float4 *q = reinterpret_cast<const float4 *>(h0 + (h0 ? (size_t)c * S + ln * M : 0));
+#pragma unroll
+        for (int i = 0; i < M / 4; ++i) {
+            const float4 v = p[i];
+            A2[2 * i] = make_float2(v.x * kLog2e, v.y * kLog2e);
+            A2[2 * i + 1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+            const float4 w = h0 ? q[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            h2[2 * i] = make_float2(w.x, w.y);
+            h2[2 * i + 1] = make_float2(w.z, w.w);
+        }
+    }
+    const float skip = MODE == WALK && a.Dskip ? a.Dskip[c] : 0.f, bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+    float sum = 0.f;
+    const int count = g.t1 - g.t0, steps = (count + kTile - 1) / kTile;
+    auto token = [&](int r) { return MODE == REVERSE ? g.t1 - 1 - r : g.t0 + r; };
+
+    auto stage = [&](int i) {
+        E *dst = raw + (i & 1) * 3 * kTile * CH;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (k == 2 && !third) break;
+            if constexpr (VEC) {
+                constexpr int EPC = BF16 ? 8 : 4, PER_ROW = CH / EPC;
+#pragma unroll
+                for (int e = tid; e < kTile * PER_ROW; e += kThreads) {
+                    const int r = e / PER_ROW, o = (e % PER_ROW) * EPC, at = i * kTile + r;
+                    const bool ok = at < count && o < left;
+                    const E *p = src[k] + (ok ? token(at) * stride[k] + c0 + o : 0);
+                    cp_async16(dst + (k * kTile + r) * CH + o, p, ok);
+                }
+            } else {
+                for (int e = tid; e < kTile * CH; e += kThreads) {
+                    const int r = e / CH, o = e % CH, at = i * kTile + r;
+                    if (at < count && o < left) dst[(k * kTile + r) * CH + o] = src[k][token(at) * stride[k] + c0 + o];
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    constexpr int BCN = (kTile * 2 * S + kThreads - 1) / kThreads;
+    float bcr[BCN];
+    auto bc_load = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < BCN; ++k) {
+            const int e = tid + k * kThreads, r = e / (2 * S), n = e % (2 * S), at = i * kTile + r;
+            bcr[k] = 0.f;
+            if (at >= count) continue;
+            if (n < S) bcr[k] = (float)Bp[token(at) * b_stride + n];
+            else if (MODE == WALK) bcr[k] = (float)Cp[token(at) * a.c_stride + n - S];
+        }
+    };
+    auto bc_store = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < BCN; ++k) bc[(i & 1) * kTile * 2 * S + tid + k * kThreads] = bcr[k];
+    };
+
+    if (steps > 0) {
+        stage(0);
+        bc_load(0);
+        bc_store(0);
+    }
+    for (int i = 0; i < steps; ++i) {
+        cp_async_wait_all();
+        __syncthreads();
+        const bool more = i + 1 < steps;
+        if (more) {
+            stage(i + 1);
+            bc_load(i + 1);
+        }
+        const E *xs = raw + (i & 1) * 3 * kTile * CH + ch, *ds = xs + kTile * CH, *zs = ds + kTile * CH;
+        const float *bt = bc + (i & 1) * kTile * 2 * S + ln * M;
+        const int rows = min(kTile, count - i * kTile);
+#pragma unroll 2
+        for (int r = 0; r < rows; ++r) {
+            const int t = token(i * kTile + r);
+            float x = (float)xs[r * CH], v = (float)ds[r * CH] + bias;
+            const float d = a.dt_softplus ? softplus(v) : v;
+            if constexpr (MODE == WALK) {
+                if (a.saved && (r % kSaveEvery) == 0 && live) {
+                    const long long slot = g.slot + (t - g.t0) / kSaveEvery;
+                    float4 *p = reinterpret_cast<float4 *>(a.saved + ((size_t)slot * a.D + c) * S + ln * M);
+#pragma unroll
+                    for (int k = 0; k < M / 4; ++k) p[k] = make_float4(h2[2 * k].x, h2[2 * k].y, h2[2 * k + 1].x, h2[2 * k + 1].y);
+                }
+            }
+            if constexpr (MODE == REVERSE) {
+                if (third) x *= silu((float)zs[r * CH]);
+            }
+            if constexpr (MODE != WALK) sum += d;
+            const float2 dd = make_float2(d, d), in = MODE == REVERSE ? make_float2(x, x) : make_float2(d * x, d * x);
+            float2 y2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float4 *b4 = reinterpret_cast<const float4 *>(bt + r * 2 * S), *c4 = reinterpret_cast<const float4 *>(bt + r * 2 * S + S);
+#pragma unroll
+            for (int k = 0; k < M / 4; ++k) {
+                const float4 B4 = b4[k];
+                float4 C4;
+                if constexpr (MODE == WALK) C4 = c4[k];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int n = 2 * k + e;
+                    const float2 arg = __fmul2_rn(A2[n], dd);
+                    const float2 dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
+                    const float2 b = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
+                    if constexpr (MODE == REVERSE) {
+                        h2[n] = __fmul2_rn(dec, __ffma2_rn(b, in, h2[n]));
+                    } else {
+                        h2[n] = __ffma2_rn(dec, h2[n], __fmul2_rn(in, b));
+                    }
+                    if constexpr (MODE == WALK)
+                        y2[e] = __ffma2_rn(e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y), h2[n], y2[e]);
+                }
+            }
+            if constexpr (MODE == WALK) {
+                const float2 ys = __fadd2_rn(y2[0], y2[1]);
+                float y = ys.x + ys.y;
+#pragma unroll
+                for (int o = 1; o < LN; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                y = fmaf(skip, x, y);
+                if (third) y *= silu((float)zs[r * CH]);
+                if (live && ln == 0) static_cast<E *>(a.y)[t * a.y_stride + c] = (E)y;
+            }
+        }
+        if (more) bc_store(i + 1);
+    }
+    if (!live) return;
+    float *out = nullptr;
+    if (MODE == WALK) out = g.last && a.final_state ? a.final_state + (size_t)g.s * a.D * S : nullptr;
+    else out = a.seg_state + (size_t)blockIdx.x * a.D * S;
+    if (MODE != WALK && ln == 0) a.seg_sum[(size_t)blockIdx.x * a.D + c] = sum;
+    if (!out) return;
+    float4 *p = reinterpret_cast<float4 *>(out + (size_t)c * S + ln * M);
+#pragma unroll
+    for (int k = 0; k < M / 4; ++k) p[k] = make_float4(h2[2 * k].x, h2[2 * k].y, h2[2 * k + 1].x, h2[2 * k + 1].y);
+}
+
+// The segments' own states chained: seg_state[u] becomes the state at the
+// start of segment u (reverse: the gradient at its end).  A thread per state.
+__global__ void __launch_bounds__(256) kda_scan_chain_kernel(ScanArgs a, int S, bool reverse) {
+    const int s = blockIdx.y;
+    const long long e = (long long)blockIdx.x * 256 + threadIdx.x, size = (long long)a.D * S;
+    const int b0 = a.cu_seqlens[s], b1 = a.cu_seqlens[s + 1];
+    if (e >= size || b0 < 0 || b1 < b0 || b1 > a.T) return;
+    const int count = (int)(((long long)b1 - b0 + a.seg - 1) / a.seg);
+    if (count < 2) return;
+    const int c = (int)(e / S);
+    const long long u0 = b0 / a.seg + s;
+    const float A = a.A[e] * kLog2e;
+    // e^{A sum d} in two halves, so that only a product that is out of range is
+    auto chain = [&](float h, long long u, float own) {
+        const float k = exp2f(0.5f * (A * a.seg_sum[u * a.D + c]));
+        return h == 0.f ? own : fmaf(h * k, k, own);
+    };
+    float *st = a.seg_state + e;
+    if (!reverse) {
+        float h = a.initial_state ? a.initial_state[s * size + e] : 0.f, own = st[u0 * size];
+        for (int j = 0; j + 1 < count; ++j) {
+            h = chain(h, u0 + j, own);
+            if (j + 2 < count) own = st[(u0 + j + 1) * size];
+            st[(u0 + j + 1) * size] = h;
+        }
+    } else {
+        float h = a.dfinal ? a.dfinal[s * size + e] : 0.f;
+        for (int j = count - 1; j > 0; --j) {
+            const float own = st[(u0 + j) * size];
+            st[(u0 + j) * size] = h;
+            h = chain(h, u0 + j, own);
+        }
+        st[u0 * size] = h;
+    }
+}
+
+// One token per request, states in place.  Bytes bound it: 8 of state for a
+// state, where 16 states share the channel's 8 (bf16) of x, dt, z and y.  A
+// thread takes four neighbouring states (16 bytes), a channel S / 4 lanes that
+// add up its output, and a block walks `rows` requests with the rates A in
+// registers, four requests' states in flight.
+template <bool BF16, int S>
+__global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int rows) {
+    using E = Elem<BF16>;
+    constexpr int LANES = S / 4, U = 4;
+    const int ln = threadIdx.x % LANES, per = a.D / a.G;
+    const int blocks = (a.D + 256 / LANES - 1) / (256 / LANES), chunk = (int)blockIdx.x / blocks;
+    const int at = ((int)blockIdx.x - chunk * blocks) * (256 / LANES) + threadIdx.x / LANES;
+    const bool live = at < a.D;
+    const int c = live ? at : a.D - 1, grp = c / per;
+    float4 A = reinterpret_cast<const float4 *>(a.A + (size_t)c * S)[ln];
+    A.x *= kLog2e, A.y *= kLog2e, A.z *= kLog2e, A.w *= kLog2e;
+    const float skip = a.Dskip ? a.Dskip[c] : 0.f, bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+    const E *x = static_cast<const E *>(a.x) + c, *dt = static_cast<const E *>(a.dt) + c, *z = static_cast<const E *>(a.z) + c;
+    const E *B = static_cast<const E *>(a.B) + (size_t)grp * S + 4 * ln, *C = static_cast<const E *>(a.C) + (size_t)grp * S + 4 * ln;
+    const int r0 = chunk * rows, r1 = min(r0 + rows, a.N);
+    for (int r = r0; r < r1; r += U) {
+        float4 h[U];
+        float xv[U], dv[U], zv[U], bv[U][4], cv[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = min(r + u, r1 - 1);
+            h[u] = reinterpret_cast<const float4 *>(a.state + ((size_t)q * a.D + c) * S)[ln];
+            xv[u] = (float)x[q * a.x_stride];
+            dv[u] = (float)dt[q * a.dt_stride] + bias;
+            zv[u] = a.z ? (float)z[q * a.z_stride] : 0.f;
+            if (a.wide) {
+                Vec<BF16, 4> vb, vc;
+                vb.load(B + q * a.b_stride);
+                vc.load(C + q * a.c_stride);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bv[u][i] = vb.get(i), cv[u][i] = vc.get(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bv[u][i] = (float)B[q * a.b_stride + i], cv[u][i] = (float)C[q * a.c_stride + i];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r + u >= r1) break;
+            const float d = a.dt_softplus ? softplus(dv[u]) : dv[u], in = d * xv[u];
+            h[u].x = fmaf(exp2_fast(A.x * d), h[u].x, in * bv[u][0]);
+            h[u].y = fmaf(exp2_fast(A.y * d), h[u].y, in * bv[u][1]);
+            h[u].z = fmaf(exp2_fast(A.z * d), h[u].z, in * bv[u][2]);
+            h[u].w = fmaf(exp2_fast(A.w * d), h[u].w, in * bv[u][3]);
+            float y = fmaf(cv[u][0], h[u].x, cv[u][1] * h[u].y) + fmaf(cv[u][2], h[u].z, cv[u][3] * h[u].w);
+#pragma unroll
+            for (int o = 1; o < LANES; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            if (!live) continue;
+            reinterpret_cast<float4 *>(a.state + ((size_t)(r + u) * a.D + c) * S)[ln] = h[u];
+            if (ln == 0) {
+                y = fmaf(skip, xv[u], y);
+                if (a.z) y *= silu(zv[u]);
+                static_cast<E *>(a.y)[(r + u) * a.y_stride + c] = (E)y;
+            }
+        }
+    }
+}
+
+template <bool BF16, int S, int MODE, bool VEC>
+cudaError_t launch_scan_t(const ScanArgs &a, cudaStream_t st) {
+    using L = Layout<BF16, S>;
+    auto kern = kda_scan_kernel<BF16, S, MODE, VEC>;
+    if (L::bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
+        if (e != cudaSuccess) return e;
+    }
+    const int per = a.D / a.G, tiles = (per + L::CH - 1) / L::CH;
+    kern<<<dim3(scan_units(a.N, a.T, a.seg), a.G * tiles), kThreads, L::bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool BF16, int S>
+cudaError_t launch_scan_s(const ScanArgs &a, int what, int sms, cudaStream_t st) {
+    if (what == SCAN_STEP) {
+        const int blocks = (a.D + 1024 / S - 1) / (1024 / S);
+        // requests of a block: the rates are read once for them, while the grid covers the SMs twice
+        int rows = 16;
+        while (rows > 1 && (long long)blocks * ((a.N + rows - 1) / rows) < 16LL * sms) rows /= 2;
+        kda_scan_step_kernel<BF16, S><<<blocks * ((a.N + rows - 1) / rows), 256, 0, st>>>(a, rows);
+        return cudaGetLastError();
+    }
+    if (a.wide) {
+        if (what == SCAN_FORWARD) return launch_scan_t<BF16, S, FORWARD, true>(a, st);
+        if (what == SCAN_REVERSE) return launch_scan_t<BF16, S, REVERSE, true>(a, st);
+        return launch_scan_t<BF16, S, WALK, true>(a, st);
+    }
+    if (what == SCAN_FORWARD) return launch_scan_t<BF16, S, FORWARD, false>(a, st);
+    if (what == SCAN_REVERSE) return launch_scan_t<BF16, S, REVERSE, false>(a, st);
+    return launch_scan_t<BF16, S, WALK, false>(a, st);
+}
+
+}  // namespace
+
+int scan_units(int N, int T, int seg) { return seg ? T / seg + N : N; }
+
+int scan_channels(int S) { return S > 16 ? kThreads * 16 / S : kThreads; }
+
+cudaError_t launch_scan(const ScanArgs &a, int S, int what, bool bf16, int sms, cudaStream_t st) {
+    switch (S) {
+        case 8: return bf16 ? launch_scan_s<true, 8>(a, what, sms, st) : launch_scan_s<false, 8>(a, what, sms, st);
+        case 16: return bf16 ? launch_scan_s<true, 16>(a, what, sms, st) : launch_scan_s<false, 16>(a, what, sms, st);
+        case 32: return bf16 ? launch_scan_s<true, 32>(a, what, sms, st) : launch_scan_s<false, 32>(a, what, sms, st);
+        default: return bf16 ? launch_scan_s<true, 64>(a, what, sms, st) : launch_scan_s<false, 64>(a, what, sms, st);
+    }
+}
+
+cudaError_t launch_scan_chain(const ScanArgs &a, int S, bool reverse, cudaStream_t st) {
+    const long long size = (long long)a.D * S;
+    kda_scan_chain_kernel<<<dim3((unsigned)((size + 255) / 256), a.N), 256, 0, st>>>(a, S, reverse);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

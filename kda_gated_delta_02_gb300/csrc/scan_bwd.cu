@@ -1,0 +1,363 @@
+// scan_bwd.cu -- gradients of the selective scan, from the states that the
+// forward saved before every eighth token.  With e_t the gradient of the
+// gated sum, e_t = dy_t z_t sigmoid(z_t), and l_t the gradient of h_t, last token first:
+//
+//   l_t = C_t e_t + a_{t+1} l_{t+1},  a_t = e^{d_t A}
+//   dx_t = d_t sum_n l_t B_t + D e_t,   dd_t = x_t sum_n l_t B_t + sum_n l_t A a_t h_{t-1},   ddt = dd (1 - e^{-d})
+//   dB_t = sum over channels of l_t d_t x_t,  dC_t = sum over channels of e_t h_t
+//   dA = sum_t d_t l_t a_t h_{t-1},  dD = sum_t e_t x_t,  dz_t = dy_t (sum_n C_t h_t + D x_t) sigma'(z_t)
+//
+// What bounds it: instructions and shared memory, as the forward only more so:
+// 13 packed operations and two exponentials per state, and the sums of dB
+// and dC over channels.  A warp is a block.  A thread keeps 2 channels of 16
+// states (so that it adds two channels of those sums in registers), runs the
+// eight tokens from the saved state forward with every second state kept in
+// shared memory, then backward: of the two tokens that share a kept state H,
+// the later one goes forward from it (a H, a H + b) and the earlier one back
+// (H, H - b), neither with an operation more.  The sums over the warp's
+// channels go through shared memory, four floats at a time: 8 stores, 8 loads
+// and 26 additions and exchanges per token, where exchanges alone would take
+// 124.  They leave as a partial row per warp, token and group; a second
+// kernel adds them up in order.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_internal.h"
+#include "layer.cuh"
+#include "scan.cuh"
+
+namespace kda {
+namespace {
+using namespace layer;
+using namespace scan;
+
+constexpr int K = kSaveEvery;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int S>
+struct Layout {
+    static constexpr int LN = S > 16 ? S / 16 : 1, M = S / LN, PAIRS = 32 / LN, CH = 2 * PAIRS;
+    static constexpr int V4 = 2 * M / 4;           // float4s of a thread's states, and of its dB and dC
+    static constexpr int hist = K / 2 * V4 * 32;   // float4s
+    static constexpr int red = V4 * 32;            // float4s
+    static constexpr int vals = 5 * K * 32;        // float2s
+    static constexpr int bytes = 16 * (hist + red) + 8 * vals + 4 * K * 2 * S;
+};
+
+template <bool BF16>
+struct Pair {
+    float2 v;
+    __device__ __forceinline__ void load(const Elem<BF16> *p, bool vec, bool two, bool one) {
+        v = make_float2(0.f, 0.f);
+        if (vec) {
+            if (!one) return;
+            Vec<BF16, 2> r;
+            r.load(p);
+            v = make_float2(r.get(0), r.get(1));
+        } else {
+            if (one) v.x = (float)p[0];
+            if (two) v.y = (float)p[1];
+        }
+    }
+    static __device__ __forceinline__ void store(Elem<BF16> *p, float2 v, bool vec, bool two, bool one) {
+        if (vec) {
+            if (!one) return;
+            Vec<BF16, 2> r;
+            const float f[2] = {v.x, v.y};
+            r.set(f);
+            r.store(p);
+        } else {
+            if (one) p[0] = (Elem<BF16>)v.x;
+            if (two) p[1] = (Elem<BF16>)v.y;
+        }
+    }
+};
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+template <bool BF16, int S, bool VEC>
+__global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
+    using E = Elem<BF16>;
+    using L = Layout<S>;
+    constexpr int LN = L::LN, M = L::M, V4 = L::V4;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float4 *hist = reinterpret_cast<float4 *>(smem);                    // [K / 2][V4][32]
+    float4 *red = hist + L::hist;                                       // [V4][32]
+    float2 *vals = reinterpret_cast<float2 *>(red + L::red);            // [5][K][32], a thread's own
+    float *bc = reinterpret_cast<float *>(vals + L::vals);              // [K][2 S]
+    const int lane = threadIdx.x, ln = lane / L::PAIRS, cl = lane % L::PAIRS;
+    const Segment g = segment_of(a.cu_seqlens, a.N, a.T, a.seg, blockIdx.x);
+    if (lane == 0 && blockIdx.y == 0) check_sequence(a, blockIdx.x);
+    const int per = a.D / a.G, tiles = (per + L::CH - 1) / L::CH;
+    const int grp = blockIdx.y / tiles, tile = blockIdx.y - grp * tiles;
+    const int at = tile * L::CH + 2 * cl, c = grp * per + (at < per ? at : 0);  // the thread's first channel
+    const bool one = at < per, two = at + 1 < per;
+    const int c1 = two ? c + 1 : c;
+    const size_t DS = (size_t)a.D * S;
+
+    float2 A2[2][M / 2], carry[2][M / 2], dA[2][M / 2];
+    const float *from = nullptr;
+    if (g.s >= 0)
+        from = g.first && g.last ? (a.dfinal ? a.dfinal + g.s * DS : nullptr) : a.seg_state + blockIdx.x * DS;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const size_t o = (size_t)(q ? c1 : c) * S + ln * M;
+#pragma unroll
+        for (int i = 0; i < M / 4; ++i) {
+            const float4 v = reinterpret_cast<const float4 *>(a.A + o)[i];
+            A2[q][2 * i] = make_float2(v.x * kLog2e, v.y * kLog2e), A2[q][2 * i + 1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+            const float4 w = from && (q ? two : one) ? reinterpret_cast<const float4 *>(from + o)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            carry[q][2 * i] = make_float2(w.x, w.y), carry[q][2 * i + 1] = make_float2(w.z, w.w);
+            dA[q][2 * i] = dA[q][2 * i + 1] = make_float2(0.f, 0.f);
+        }
+    }
+    const float2 skip = a.Dskip ? make_float2(a.Dskip[c], a.Dskip[c1]) : both(0.f);
+    const float2 bias = a.dt_bias ? make_float2(a.dt_bias[c], a.dt_bias[c1]) : both(0.f);
+    float2 dD = both(0.f), dbias = both(0.f);
+    const E *xp = static_cast<const E *>(a.x) + c, *dtp = static_cast<const E *>(a.dt) + c;
+    const E *zp = static_cast<const E *>(a.z) + c, *dyp = static_cast<const E *>(a.dy) + c;
+    const E *Bp = static_cast<const E *>(a.B) + (size_t)grp * S, *Cp = static_cast<const E *>(a.C) + (size_t)grp * S;
+    E *dxp = static_cast<E *>(a.dx) + c, *ddtp = static_cast<E *>(a.ddt) + c, *dzp = static_cast<E *>(a.dz) + c;
+    const int count = g.s < 0 ? 0 : g.t1 - g.t0;
+
+    for (int i = (count + K - 1) / K - 1; i >= 0; --i) {
+        const int t0 = g.t0 + i * K, rows = min(K, g.t1 - t0);
+        // the eight tokens' values, at this thread's own places: d, x, e, 1 - e^{-d}, dy sigma'(z)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            Pair<BF16> x, v, e, z;
+            const bool in1 = one && k < rows, in2 = two && k < rows;
+            const long long t = k < rows ? t0 + k : t0;
+            x.load(xp + t * a.x_stride, VEC, in2, in1);
+            v.load(dtp + t * a.dt_stride, VEC, in2, in1);
+            e.load(dyp + t * a.dy_stride, VEC, in2, in1);
+            if (a.z) z.load(zp + t * a.z_stride, VEC, in2, in1);
+            v.v.x += bias.x, v.v.y += bias.y;
+            float2 d = v.v, s = both(1.f), dz = both(0.f);
+            if (a.dt_softplus) {
+                d = make_float2(softplus(v.v.x), softplus(v.v.y));
+                s = make_float2(sigmoid(v.v.x), sigmoid(v.v.y));
+            }
+            if (a.z) {
+                const float2 sg = make_float2(sigmoid(z.v.x), sigmoid(z.v.y));
+                dz = make_float2(e.v.x * (sg.x * fmaf(z.v.x, 1.f - sg.x, 1.f)), e.v.y * (sg.y * fmaf(z.v.y, 1.f - sg.y, 1.f)));
+                e.v = make_float2(e.v.x * (z.v.x * sg.x), e.v.y * (z.v.y * sg.y));
+            }
+            float2 *p = vals + k * 32 + lane;
+            p[0] = d, p[K * 32] = x.v, p[2 * K * 32] = e.v, p[3 * K * 32] = s, p[4 * K * 32] = dz;
+        }
+        __syncwarp();  // B and C of the previous tokens have been read
+        for (int n = lane; n < K * 2 * S; n += 32) {
+            const int k = n / (2 * S), m = n % (2 * S);
+            const long long t = t0 + (k < rows ? k : 0);
+            bc[n] = m < S ? (float)Bp[t * a.b_stride + m] : (float)Cp[t * a.c_stride + m - S];
+        }
+        float2 h[2][M / 2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float4 *p = reinterpret_cast<const float4 *>(a.saved + (size_t)(g.slot + i) * DS + (size_t)(q ? c1 : c) * S + ln * M);
+#pragma unroll
+            for (int n = 0; n < M / 4; ++n) {
+                const float4 v = p[n];
+                h[q][2 * n] = make_float2(v.x, v.y), h[q][2 * n + 1] = make_float2(v.z, v.w);
+            }
+        }
+        __syncwarp();
+        // forward, the states after tokens 0, 2, 4 and 6 kept
+#pragma unroll 1
+        for (int k = 0; k < min(rows, K - 1); ++k) {
+            const float2 d = vals[k * 32 + lane], x = vals[(K + k) * 32 + lane];
+            const float4 *b4 = reinterpret_cast<const float4 *>(bc + k * 2 * S + ln * M);
+#pragma unroll
+            for (int n = 0; n < M / 4; ++n) {
+                const float4 B4 = b4[n];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float2 dq = both(q ? d.y : d.x), in = both(q ? d.y * x.y : d.x * x.x);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 arg = __fmul2_rn(A2[q][2 * n + e], dq), b = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
+                        h[q][2 * n + e] = __ffma2_rn(make_float2(exp2_fast(arg.x), exp2_fast(arg.y)), h[q][2 * n + e], __fmul2_rn(in, b));
+                    }
+                    if ((k & 1) == 0)
+                        hist[((k >> 1) * V4 + q * (M / 4) + n) * 32 + lane] =
+                            make_float4(h[q][2 * n].x, h[q][2 * n].y, h[q][2 * n + 1].x, h[q][2 * n + 1].y);
+                }
+            }
+        }
+        // backward
+#pragma unroll 1
+        for (int k = rows - 1; k >= 0; --k) {
+            const bool odd = k & 1;
+            const float2 d = vals[k * 32 + lane], x = vals[(K + k) * 32 + lane], ev = vals[(2 * K + k) * 32 + lane];
+            const float4 *b4 = reinterpret_cast<const float4 *>(bc + k * 2 * S + ln * M), *c4 = b4 + S / 4;
+            float2 lB[2] = {both(0.f), both(0.f)}, lA[2] = {both(0.f), both(0.f)}, y[2] = {both(0.f), both(0.f)};
+#pragma unroll
+            for (int n = 0; n < M / 4; ++n) {
+                const float4 B4 = b4[n], C4 = c4[n];
+                float2 sB[2], sC[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float4 H4 = hist[((k >> 1) * V4 + q * (M / 4) + n) * 32 + lane];
+                    const float2 dq = both(q ? d.y : d.x), in = both(q ? d.y * x.y : d.x * x.x), eq = both(q ? ev.y : ev.x);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 A = A2[q][2 * n + e], arg = __fmul2_rn(A, dq), dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
+                        const float2 B = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
+                        const float2 C = e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y);
+                        const float2 H = e ? make_float2(H4.z, H4.w) : make_float2(H4.x, H4.y);
+                        const float2 b = __fmul2_rn(in, B);
+                        float2 ah, hk;
+                        if (odd) ah = __fmul2_rn(dec, H), hk = __fadd2_rn(ah, b);
+                        else hk = H, ah = __fadd2_rn(H, make_float2(-b.x, -b.y));
+                        const float2 l = __ffma2_rn(C, eq, carry[q][2 * n + e]);
+                        const float2 u = __fmul2_rn(l, ah);
+                        carry[q][2 * n + e] = __fmul2_rn(dec, l);
+                        lB[q] = __ffma2_rn(l, B, lB[q]);
+                        lA[q] = __ffma2_rn(u, A, lA[q]);
+                        dA[q][2 * n + e] = __ffma2_rn(dq, u, dA[q][2 * n + e]);
+                        y[q] = __ffma2_rn(C, hk, y[q]);
+                        sB[e] = q ? __ffma2_rn(l, in, sB[e]) : __fmul2_rn(l, in);
+                        sC[e] = q ? __ffma2_rn(hk, eq, sC[e]) : __fmul2_rn(hk, eq);
+                    }
+                }
+                red[n * 32 + lane] = make_float4(sB[0].x, sB[0].y, sB[1].x, sB[1].y);
+                red[(M / 4 + n) * 32 + lane] = make_float4(sC[0].x, sC[0].y, sC[1].x, sC[1].y);
+            }
+            __syncwarp();
+            // Row v of `red` is four outputs of all lanes.  A lane adds up a row over the PART lanes of its
+            // part (rotated, so that eight neighbours read eight places), and parts of one ln are joined.
+            {
+                constexpr int PARTS = 32 / V4, PART = 32 / PARTS, JOIN = PARTS / LN;
+                const int v = lane / PARTS, part = lane % PARTS;
+                const float4 *p = red + v * 32 + part * PART;
+                float2 f0 = both(0.f), f1 = both(0.f);
+#pragma unroll
+                for (int j = 0; j < PART; ++j) {
+                    const float4 w = p[(j + lane) % PART];
+                    f0 = __fadd2_rn(f0, make_float2(w.x, w.y)), f1 = __fadd2_rn(f1, make_float2(w.z, w.w));
+                }
+                // output n of the lane's part: B for rows below M / 4, C above
+                const int which = v >= M / 4, n0 = (part / JOIN) * M + (v - which * (M / 4)) * 4;
+                float *out = a.bc_parts + (((size_t)tile * a.T + t0 + k) * a.G + grp) * (2 * S) + which * S + n0;
+                if constexpr (JOIN >= 2) {  // two lanes: each keeps two of the four
+                    const bool up = part & 1;
+                    const float2 send = up ? f0 : f1;
+                    float2 mine = up ? f1 : f0;
+                    mine.x += __shfl_xor_sync(0xffffffffu, send.x, 1), mine.y += __shfl_xor_sync(0xffffffffu, send.y, 1);
+                    if constexpr (JOIN >= 4) {
+                        const bool up2 = part & 2;
+                        const float s2 = up2 ? mine.x : mine.y;
+                        float m2 = up2 ? mine.y : mine.x;
+                        m2 += __shfl_xor_sync(0xffffffffu, s2, 2);
+                        if constexpr (JOIN >= 8) m2 += __shfl_xor_sync(0xffffffffu, m2, 4);
+                        if (JOIN < 8 || (part & 4) == 0) out[(up ? 2 : 0) + (up2 ? 1 : 0)] = m2;
+                    } else {
+                        out[up ? 2 : 0] = mine.x, out[up ? 3 : 1] = mine.y;
+                    }
+                } else {
+                    out[0] = f0.x, out[1] = f0.y, out[2] = f1.x, out[3] = f1.y;
+                }
+            }
+            // the token's own gradients
+            float sB0 = lB[0].x + lB[0].y, sB1 = lB[1].x + lB[1].y, sA0 = lA[0].x + lA[0].y, sA1 = lA[1].x + lA[1].y;
+            float y0 = y[0].x + y[0].y, y1 = y[1].x + y[1].y;
+#pragma unroll
+            for (int o = L::PAIRS; o < 32; o <<= 1) {
+                sB0 += __shfl_xor_sync(0xffffffffu, sB0, o), sB1 += __shfl_xor_sync(0xffffffffu, sB1, o);
+                sA0 += __shfl_xor_sync(0xffffffffu, sA0, o), sA1 += __shfl_xor_sync(0xffffffffu, sA1, o);
+                y0 += __shfl_xor_sync(0xffffffffu, y0, o), y1 += __shfl_xor_sync(0xffffffffu, y1, o);
+            }
+            const float2 sg = vals[(3 * K + k) * 32 + lane];
+            const float2 dx = make_float2(fmaf(d.x, sB0, skip.x * ev.x), fmaf(d.y, sB1, skip.y * ev.y));
+            const float2 dd = make_float2(fmaf(x.x, sB0, kLn2 * sA0) * sg.x, fmaf(x.y, sB1, kLn2 * sA1) * sg.y);
+            dD.x = fmaf(ev.x, x.x, dD.x), dD.y = fmaf(ev.y, x.y, dD.y);
+            dbias.x += dd.x, dbias.y += dd.y;
+            if (ln == 0) {
+                const size_t t = (size_t)(t0 + k) * a.D;
+                Pair<BF16>::store(dxp + t, dx, VEC, two, one);
+                Pair<BF16>::store(ddtp + t, dd, VEC, two, one);
+                if (a.z) {
+                    const float2 dz = vals[(4 * K + k) * 32 + lane];
+                    Pair<BF16>::store(dzp + t, make_float2(dz.x * fmaf(skip.x, x.x, y0), dz.y * fmaf(skip.y, x.y, y1)), VEC, two, one);
+                }
+            }
+            __syncwarp();  // `red` has been read
+        }
+    }
+    // the unit's sums, zero where it has no tokens
+    float *parts = a.parts + blockIdx.x * (DS + 2 * (size_t)a.D);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        if (!(q ? two : one)) continue;
+        const size_t o = (size_t)(c + q) * S + ln * M;
+#pragma unroll
+        for (int n = 0; n < M / 2; ++n) *reinterpret_cast<float2 *>(parts + o + 2 * n) = dA[q][n];
+        if (g.first && a.dstate) {
+#pragma unroll
+            for (int n = 0; n < M / 2; ++n) *reinterpret_cast<float2 *>(a.dstate + g.s * DS + o + 2 * n) = carry[q][n];
+        }
+        if (ln == 0) parts[DS + c + q] = q ? dD.y : dD.x, parts[DS + a.D + c + q] = q ? dbias.y : dbias.x;
+    }
+}
+
+// dB and dC of a token and group: the channel tiles' partial rows in order.  A
+// warp per token and group; rows of no sequence are left as they were.
+template <bool BF16>
+__global__ void __launch_bounds__(256) kda_scan_bc_kernel(ScanArgs a, int S, int tiles) {
+    using E = Elem<BF16>;
+    const long long tg = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, t = (int)(tg / a.G), grp = (int)(tg - (long long)t * a.G);
+    if (t >= a.T) return;
+    const int s = find_sequence(a.cu_seqlens, a.N, t);
+    if (s >= a.N || a.cu_seqlens[s] > t || a.cu_seqlens[s] < 0 || a.cu_seqlens[s + 1] > a.T) return;
+    const size_t step = (size_t)a.T * a.G * 2 * S, at = ((size_t)t * a.G + grp) * S;
+    for (int n = lane; n < 2 * S; n += 32) {
+        const float *p = a.bc_parts + 2 * at + n;
+        float sum = 0.f;
+        int i = 0;
+        for (; i + 8 <= tiles; i += 8) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = p[(i + k) * step];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += v[k];
+        }
+        for (; i < tiles; ++i) sum += p[i * step];
+        if (n < S) static_cast<E *>(a.dB)[at + n] = (E)sum;
+        else static_cast<E *>(a.dC)[at + n - S] = (E)sum;
+    }
+}
+
+template <bool BF16, int S>
+cudaError_t launch_s(const ScanArgs &a, cudaStream_t st) {
+    using L = Layout<S>;
+    auto kern = a.wide ? kda_scan_bwd_kernel<BF16, S, true> : kda_scan_bwd_kernel<BF16, S, false>;
+    const int per = a.D / a.G, tiles = (per + L::CH - 1) / L::CH;
+    kern<<<dim3(scan_units(a.N, a.T, a.seg), a.G * tiles), 32, L::bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int scan_bwd_channels(int S) { return S > 16 ? 64 * 16 / S : 64; }
+
+cudaError_t launch_scan_bwd(const ScanArgs &a, int S, bool bf16, cudaStream_t st) {
+    switch (S) {
+        case 8: return bf16 ? launch_s<true, 8>(a, st) : launch_s<false, 8>(a, st);
+        case 16: return bf16 ? launch_s<true, 16>(a, st) : launch_s<false, 16>(a, st);
+        case 32: return bf16 ? launch_s<true, 32>(a, st) : launch_s<false, 32>(a, st);
+        default: return bf16 ? launch_s<true, 64>(a, st) : launch_s<false, 64>(a, st);
+    }
+}
+
+cudaError_t launch_scan_bc(const ScanArgs &a, int S, bool bf16, cudaStream_t st) {
+    const int per = a.D / a.G, tiles = (per + scan_bwd_channels(S) - 1) / scan_bwd_channels(S);
+    const unsigned grid = (unsigned)(((long long)a.T * a.G + 7) / 8);
+    if (grid == 0) return cudaSuccess;
+    if (bf16) kda_scan_bc_kernel<true><<<grid, 256, 0, st>>>(a, S, tiles);
+    else kda_scan_bc_kernel<false><<<grid, 256, 0, st>>>(a, S, tiles);
+    return cudaGetLastError();
+}
+
+}  // namespace kda
