@@ -1597,6 +1597,8 @@ int kda_conv_step(const void *x, const float *w, const float *bias, void *tail, 
     a.x_stride = x_stride; a.y_stride = y_stride; a.tail_out_stride = tail_stride;
     a.N = R; a.C = C; a.act = conv_act == KDA_CONV_SILU;
     a.wide = all_on16(r) && (long long)C * e % 16 == 0;
+    a.run = kda::conv_step_run(R, C, a.wide ? 16 / e : 1, sm_count());
+    a.runs = (R + a.run - 1) / a.run;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(timed_launch(KDA_KERNEL_CONV, st, [&] { return kda::launch_conv(a, W, 2, bf16, bf16, st); }));
 }
@@ -1616,13 +1618,13 @@ static int scan_shape(int N, int T, int D, int G, int S, int dtype) {
 static int scan_segment(int N, int T, int D, int G, int S, bool backward) {
     if (T < 512 || N > kMaxGridY) return 0;
     const int ch = backward ? kda::scan_bwd_channels(S) : kda::scan_channels(S), sms = sm_count();
-    const long long tiles = (long long)G * ((D / G + ch - 1) / ch), enough = backward ? 2LL * sms : sms + sms / 2;
+    const long long tiles = (long long)G * ((D / G + ch - 1) / ch), enough = backward ? 4LL * sms : 2LL * sms;
     long long seg;
     if (N * tiles >= enough) {
         seg = 4LL * T / N;
         if (seg < 1024) seg = 1024;
     } else {
-        const long long parts = (4LL * sms + tiles - 1) / tiles;
+        const long long parts = (7LL * sms + tiles - 1) / tiles;
         seg = (T + parts - 1) / parts;
         if (seg < 128) seg = 128;
     }

@@ -44,6 +44,43 @@ __device__ __forceinline__ Walk next_sequence(const int32_t *cu, int N, int T, i
     return {N, 0x7fffffff, 0x7fffffff};
 }
 
+// a row of pairs of channels, as loaded from p or zero
+template <bool BF16, int V>
+__device__ __forceinline__ void load_pairs(float2 (&x)[(V + 1) / 2], const Elem<BF16> *p, bool live) {
+    Vec<BF16, V> r;
+    if (live) r.load(p);
+    else r.zero();
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) x[i] = r.pair(i);
+}
+
+// taps [pairs][W] and bias of channels c .. c + V - 1
+template <int V, int W>
+__device__ __forceinline__ void load_taps(float2 (&w)[(V + 1) / 2][W], float2 (&bias)[(V + 1) / 2], const float *wp,
+                                          const float *bp, int c) {
+    float t[(V + 1) / 2 * 2][W];
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2 * 2; ++i) {
+        const float *p = wp + (long long)(c + (i < V ? i : 0)) * W;
+        if constexpr (W == 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p);
+            t[i][0] = q.x, t[i][1] = q.y, t[i][2] = q.z, t[i][3] = q.w;
+        } else if constexpr (W == 2) {
+            const float2 q = *reinterpret_cast<const float2 *>(p);
+            t[i][0] = q.x, t[i][1] = q.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) t[i][j] = p[j];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[i][j] = make_float2(t[2 * i][j], t[2 * i + 1][j]);
+        bias[i] = bp ? make_float2(bp[c + 2 * i], V > 1 ? bp[c + 2 * i + 1] : 0.f) : both(0.f);
+    }
+}
+
 template <bool BF16, int V>
 __device__ __forceinline__ void load_row(Vec<BF16, V> &r, const Elem<BF16> *p, bool live) {
     if (live) r.load(p);
@@ -81,23 +118,18 @@ __global__ void __launch_bounds__(kThreads) kda_conv_fwd_kernel(ConvArgs a) {
     const int ta = (int)blockIdx.x * a.run, tb = min(ta + a.run, a.T);
     const int s_first = find_sequence(a.cu_seqlens, a.N, ta);
     if (!live) return;
-    float w[V][W], bias[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[i][j] = a.w[(long long)(c + i) * W + j];
-        bias[i] = a.bias ? a.bias[c + i] : 0.f;
-    }
+    constexpr int P = (V + 1) / 2;
+    float2 w[P][W], bias[P], win[W][P];  // taps; rows t - (W - 1) .. t
+    load_taps<V, W>(w, bias, a.w, a.bias, c);
     E *y = static_cast<E *>(a.y) + c;
     Walk q = next_sequence(a.cu_seqlens, a.N, a.T, s_first, ta);
-    Vec<BF16, V> win[W];  // rows t - (W - 1) .. t
-    // the rows before token t of sequence q into win[0 .. W - 2]
+    // the rows before token t of sequence q
     auto fill = [&](int t) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int pos = t - q.a - (W - 1) + j;
-            if (pos >= 0) win[j].load(x + (long long)(q.a + pos) * a.x_stride);
-            else load_row(win[j], tail + ((long long)q.s * (W - 1) + pos + W - 1) * a.tail_stride, a.tail != nullptr);
+            if (pos >= 0) load_pairs<BF16, V>(win[j], x + (long long)(q.a + pos) * a.x_stride, true);
+            else load_pairs<BF16, V>(win[j], tail + ((long long)q.s * (W - 1) + pos + W - 1) * a.tail_stride, a.tail != nullptr);
         }
     };
     if (q.a <= ta) fill(ta);
@@ -117,20 +149,18 @@ __global__ void __launch_bounds__(kThreads) kda_conv_fwd_kernel(ConvArgs a) {
             }
             if (t < q.a) continue;  // rows of no sequence
             if (t == q.a && t > ta) fill(t);
-            win[W - 1] = next[u];
-            float o[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float p = bias[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = fmaf(w[i][j], win[j].get(i), p);
-                o[i] = a.act ? silu(p) : p;
-            }
             Vec<BF16, V> out;
-            out.set(o);
-            out.store(y + (long long)t * a.y_stride);
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
+            for (int i = 0; i < P; ++i) {
+                win[W - 1][i] = next[u].pair(i);
+                float2 p = bias[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j][i], p);
+                out.set_pair(i, a.act ? silu2(p) : p);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+            }
+            out.store(y + (long long)t * a.y_stride);
         }
     }
 }
@@ -168,25 +198,24 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
     if (!live) return;
     const G *dy = static_cast<const G *>(a.dy) + c;
     E *dx = static_cast<E *>(a.dx) + c;
-    float w[V][W], bias[V], dw[V][W], db[V];
+    constexpr int P = (V + 1) / 2;
+    float2 w[P][W], bias[P], dw[P][W], db[P], win[W][P], g[W][P];  // g: gradients q of tokens t - (W - 1) .. t
+    load_taps<V, W>(w, bias, a.w, a.bias, c);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < P; ++i) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[i][j] = a.w[(long long)(c + i) * W + j], dw[i][j] = 0.f;
-        bias[i] = a.bias ? a.bias[c + i] : 0.f;
-        db[i] = 0.f;
+        for (int j = 0; j < W; ++j) dw[i][j] = both(0.f);
+        db[i] = both(0.f);
     }
     Walk q = next_sequence(a.cu_seqlens, a.N, a.T, s_first, ta);
-    Vec<BF16, V> win[W];
-    float g[W][V];  // gradients q of tokens t - (W - 1) .. t of the sequence
     auto fill = [&](int t) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int pos = t - q.a - (W - 1) + j;
-            if (pos >= 0) win[j].load(x + (long long)(q.a + pos) * a.x_stride);
-            else load_row(win[j], tail + ((long long)q.s * (W - 1) + pos + W - 1) * a.tail_stride, a.tail != nullptr);
+            if (pos >= 0) load_pairs<BF16, V>(win[j], x + (long long)(q.a + pos) * a.x_stride, true);
+            else load_pairs<BF16, V>(win[j], tail + ((long long)q.s * (W - 1) + pos + W - 1) * a.tail_stride, a.tail != nullptr);
 #pragma unroll
-            for (int i = 0; i < V; ++i) g[j][i] = 0.f;
+            for (int i = 0; i < P; ++i) g[j][i] = both(0.f);
         }
     };
     // the gradient of the row e = t - (W - 1), to which g[k] is the token k after
@@ -195,30 +224,37 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
     auto emit = [&](int e, int last) {
         const bool in_tail = e < q.a;
         if (in_tail ? (!a.dtail || q.a < ta) : (e < ta || e >= tb)) return;
-        float o[V];
+        float2 o[P];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            o[i] = 0.f;
+        for (int i = 0; i < P; ++i) {
+            o[i] = both(0.f);
 #pragma unroll
-            for (int k = 0; k < W; ++k) o[i] = fmaf(w[i][W - 1 - k], g[k][i], o[i]);
-            if (last >= 0 && a.dtail_out) o[i] += a.dtail_out[((long long)q.s * (W - 1) + last) * a.C + c + i];
+            for (int k = 0; k < W; ++k) o[i] = __ffma2_rn(w[i][W - 1 - k], g[k][i], o[i]);
+            if (last >= 0 && a.dtail_out) {
+                const float *p = a.dtail_out + ((long long)q.s * (W - 1) + last) * a.C + c + 2 * i;
+                o[i].x += p[0];
+                if (V > 1) o[i].y += p[1];
+            }
         }
         if (in_tail) {
+            float *p = a.dtail + ((long long)q.s * (W - 1) + e - q.a + W - 1) * a.C + c;
 #pragma unroll
-            for (int i = 0; i < V; ++i) a.dtail[((long long)q.s * (W - 1) + e - q.a + W - 1) * a.C + c + i] = o[i];
+            for (int i = 0; i < P; ++i) {
+                p[2 * i] = o[i].x;
+                if (V > 1) p[2 * i + 1] = o[i].y;
+            }
         } else {
             Vec<BF16, V> out;
-            out.set(o);
+#pragma unroll
+            for (int i = 0; i < P; ++i) out.set_pair(i, o[i]);
             out.store(dx + (long long)e * a.dx_stride);
         }
     };
     auto shift = [&] {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            win[j] = win[j + 1];
+        for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) g[j][i] = g[j + 1][i];
-        }
+            for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i], g[j][i] = g[j + 1][i];
     };
     if (q.a <= ta) fill(ta);
     constexpr int U = 4;
@@ -242,22 +278,21 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
             }
             if (t < q.a || (t >= tb && q.a >= tb)) continue;  // rows of no sequence, or of one after the run's
             if (t == q.a && t > ta) fill(t);
-            win[W - 1] = next[u];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float d = dnext[u].get(i);
+            for (int i = 0; i < P; ++i) {
+                win[W - 1][i] = next[u].pair(i);
+                float2 d = dnext[u].pair(i);
                 if (a.act) {
-                    float p = bias[i];
+                    float2 p = bias[i];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) p = fmaf(w[i][j], win[j].get(i), p);
-                    const float sg = sigmoid(p);
-                    d *= sg * fmaf(p, 1.f - sg, 1.f);
+                    for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j][i], p);
+                    d = __fmul2_rn(d, dsilu2(p, sigmoid2(p)));
                 }
                 g[W - 1][i] = d;
                 if (t < tb) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) dw[i][j] = fmaf(d, win[j].get(i), dw[i][j]);
-                    db[i] += d;
+                    for (int j = 0; j < W; ++j) dw[i][j] = __ffma2_rn(d, win[j][i], dw[i][j]);
+                    db[i] = __fadd2_rn(db[i], d);
                 }
             }
             emit(t - (W - 1), -1);
@@ -266,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) g[W - 1][i] = 0.f;
+                    for (int i = 0; i < P; ++i) g[W - 1][i] = both(0.f);
                     emit(t - (W - 1) + 1 + j, j);
                     shift();
                 }
@@ -276,38 +311,46 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
     if (!a.parts) return;
     float *out = a.parts + (long long)blockIdx.x * (W + 1) * a.C + c;  // [W + 1][C]
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int j = 0; j < W; ++j) out[(long long)j * a.C + i] = dw[i][j];
-        out[(long long)W * a.C + i] = db[i];
-    }
+        for (int i = 0; i < P; ++i) {
+            const float2 v = j < W ? dw[i][j < W ? j : 0] : db[i];
+            out[(long long)j * a.C + 2 * i] = v.x;
+            if (V > 1) out[(long long)j * a.C + 2 * i + 1] = v.y;
+        }
 }
 
-// One token per request; tail [R][W - 1][C] moves on in place.
+// One token per request; tail [R][W - 1][C] moves on in place.  A block takes
+// `run` requests, so that the taps (16 bytes a channel, as many as two bf16
+// tails) are read once for them.
 template <bool BF16, int V, int W>
 __global__ void __launch_bounds__(kThreads) kda_conv_step_kernel(ConvArgs a) {
     using E = Elem<BF16>;
-    const int tiles = (a.C + kThreads * V - 1) / (kThreads * V), r = (int)blockIdx.x / tiles;
-    const int c = (((int)blockIdx.x - r * tiles) * kThreads + threadIdx.x) * V;
+    constexpr int P = (V + 1) / 2;
+    const int tiles = (a.C + kThreads * V - 1) / (kThreads * V), chunk = (int)blockIdx.x / tiles;
+    const int c = (((int)blockIdx.x - chunk * tiles) * kThreads + threadIdx.x) * V;
     if (c >= a.C) return;
-    E *tail = static_cast<E *>(a.tail_out) + (long long)r * (W - 1) * a.tail_out_stride + c;
-    Vec<BF16, V> win[W];
+    float2 w[P][W], bias[P];
+    load_taps<V, W>(w, bias, a.w, a.bias, c);
+    const int r1 = min((chunk + 1) * a.run, a.N);
+#pragma unroll 2
+    for (int r = chunk * a.run; r < r1; ++r) {
+        E *tail = static_cast<E *>(a.tail_out) + (long long)r * (W - 1) * a.tail_out_stride + c;
+        Vec<BF16, V> win[W], out;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j].load(tail + j * a.tail_out_stride);
-    win[W - 1].load(static_cast<const E *>(a.x) + (long long)r * a.x_stride + c);
-    float o[V];
+        for (int j = 0; j < W - 1; ++j) win[j].load(tail + j * a.tail_out_stride);
+        win[W - 1].load(static_cast<const E *>(a.x) + (long long)r * a.x_stride + c);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float p = a.bias ? a.bias[c + i] : 0.f;
+        for (int i = 0; i < P; ++i) {
+            float2 p = bias[i];
 #pragma unroll
-        for (int j = 0; j < W; ++j) p = fmaf(a.w[(long long)(c + i) * W + j], win[j].get(i), p);
-        o[i] = a.act ? silu(p) : p;
+            for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j].pair(i), p);
+            out.set_pair(i, a.act ? silu2(p) : p);
+        }
+        out.store(static_cast<E *>(a.y) + (long long)r * a.y_stride + c);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[j + 1].store(tail + j * a.tail_out_stride);
     }
-    Vec<BF16, V> out;
-    out.set(o);
-    out.store(static_cast<E *>(a.y) + (long long)r * a.y_stride + c);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j + 1].store(tail + j * a.tail_out_stride);
 }
 
 template <int W>
@@ -329,7 +372,7 @@ cudaError_t launch_w(const ConvArgs &a, int what, bool bf16, bool dy_bf16, cudaS
         else if (a.wide) kda_conv_bwd_kernel<false, false, 4, W><<<g4, kThreads, 0, st>>>(a);
         else kda_conv_bwd_kernel<false, false, 1, W><<<g1, kThreads, 0, st>>>(a);
     } else {
-        const unsigned R = (unsigned)a.N;
+        const unsigned R = (unsigned)a.runs;
         if (bf16 && a.wide) kda_conv_step_kernel<true, 8, W><<<R * tiles(8), kThreads, 0, st>>>(a);
         else if (bf16) kda_conv_step_kernel<true, 1, W><<<R * tiles(1), kThreads, 0, st>>>(a);
         else if (a.wide) kda_conv_step_kernel<false, 4, W><<<R * tiles(4), kThreads, 0, st>>>(a);
@@ -346,6 +389,14 @@ int conv_run(int T, int C, int v, bool backward, int sms) {
     const long long tiles = (C + kThreads * v - 1) / (kThreads * v);
     int run = backward ? 128 : 64;
     while (run > 8 && tiles * ((T + run - 1) / run) < 8LL * sms) run /= 2;
+    return run;
+}
+
+// Requests of a block of single tokens: up to 8, while every SM has 16 blocks
+int conv_step_run(int R, int C, int v, int sms) {
+    const long long tiles = (C + kThreads * v - 1) / (kThreads * v);
+    int run = 8;
+    while (run > 1 && tiles * ((R + run - 1) / run) < 16LL * sms) run /= 2;
     return run;
 }
 

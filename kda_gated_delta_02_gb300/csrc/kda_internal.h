@@ -291,6 +291,7 @@ struct ConvArgs {
 // what: 0 forward, 1 backward, 2 single tokens (N of them)
 cudaError_t launch_conv(const ConvArgs &a, int W, int what, bool bf16, bool dy_bf16, cudaStream_t st);
 int conv_run(int T, int C, int v, bool backward, int sms);
+int conv_step_run(int R, int C, int v, int sms);
 
 // Selective state space scan (scan.cu, scan_bwd.cu).
 constexpr int kScanSaveEvery = 8;  // tokens between saved states

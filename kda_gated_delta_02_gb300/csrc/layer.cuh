@@ -57,6 +57,19 @@ struct Vec {
         if constexpr (!BF16) return __uint_as_float(w[i]);
         else return (i & 1) ? __uint_as_float(w[i >> 1] & 0xffff0000u) : __uint_as_float(w[i >> 1] << 16);
     }
+    // elements 2 i and 2 i + 1 (of one element: it and 0)
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (V == 1) return make_float2(get(0), 0.f);
+        else return make_float2(get(2 * i), get(2 * i + 1));
+    }
+    __device__ __forceinline__ void set_pair(int i, float2 x) {
+        if constexpr (!BF16) {
+            w[V == 1 ? 0 : 2 * i] = __float_as_uint(x.x);
+            if constexpr (V > 1) w[2 * i + 1] = __float_as_uint(x.y);
+        } else {
+            w[i] = pack_bf16(x.x, x.y);
+        }
+    }
     __device__ __forceinline__ void set(const float (&x)[V]) {
         if constexpr (!BF16) {
 #pragma unroll
@@ -81,9 +94,48 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f +
 // x sigmoid(x); -inf gives NaN, as the product does
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
-// softplus, ln(1 + e^v), to a unit in the last place or two: the steps of a scan
-// add up what is off here over the tokens that a state remembers
-__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
+// Pairs of the packed fp32 operations
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+    const float2 t = __fmul2_rn(x, both(-1.4426950408889634f));
+    const float2 d = __fadd2_rn(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
+    return make_float2(__fdividef(1.f, d.x), __fdividef(1.f, d.y));
+}
+__device__ __forceinline__ float2 silu2(float2 x) { return __fmul2_rn(x, sigmoid2(x)); }
+// its derivative, from x and its sigmoid
+__device__ __forceinline__ float2 dsilu2(float2 x, float2 s) {
+    return __fmul2_rn(s, __ffma2_rn(x, __fadd2_rn(both(1.f), make_float2(-s.x, -s.y)), both(1.f)));
+}
+
+// ln(1 + e^v) = max(v, 0) + ln(1 + e), e = e^{-|v|} <= 1, and
+// ln(1 + e) = 2 atanh(q) = 2 (q + q^3 / 3 + q^5 / 5 + ...), q = e / (2 + e) <= 1 / 3:
+// no branch, and small values keep their relative precision (2^-21), which the
+// steps of a scan need: they add up what is off here over the tokens that a
+// state remembers.  The product |v| log2(e) is carried in two parts.
+// *sig: e^v / (1 + e^v), its derivative.
+__device__ __forceinline__ float softplus(float v, float *sig = nullptr) {
+    float t = -fabsf(v);
+    t = t < -104.f ? -104.f : t;  // (e is 0 from there on; infinities would give NaN below)
+    const float hi = t * 1.4426950408889634f;
+    const float lo = fmaf(t, 1.4426950408889634f, -hi) + t * 1.9259629911266175e-8f;
+    float e = exp2_fast(hi);
+    e = fmaf(e, lo * 0.6931471805599453f, e);
+    const float q = __fdividef(e, 2.f + e), w = q * q;
+    // (seven terms: the next one is below 2^-26 of the sum)
+    float s = fmaf(w, 1.f / 13.f, 1.f / 11.f);
+    s = fmaf(w, s, 1.f / 9.f);
+    s = fmaf(w, s, 1.f / 7.f);
+    s = fmaf(w, s, 1.f / 5.f);
+    s = fmaf(w, s, 1.f / 3.f);
+    s = fmaf(w, s, 1.f);
+    if (sig) {
+        const float r = __fdividef(1.f, 1.f + e);
+        *sig = v >= 0.f ? r : e * r;
+    }
+    return fmaf(2.f * q, s, fmaxf(v, 0.f));
+}
+
+__device__ __forceinline__ void prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
 
 // The first s in [0, N) for which past(s) holds (N if there is none), past
 // being false up to some s and true from there on.  Each round asks for 32

@@ -33,7 +33,8 @@ namespace {
 using namespace layer;
 using namespace scan;
 
-constexpr int kTile = 16;  // tokens of a tile (a multiple of kSaveEvery)
+constexpr int kTile = 16;  // tokens of a tile
+constexpr int GROUP = kSaveEvery;
 
 enum Mode : int {
     WALK = 0,     // outputs, final and saved states
@@ -154,54 +155,66 @@ __global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
         const E *xs = raw + (i & 1) * 3 * kTile * CH + ch, *ds = xs + kTile * CH, *zs = ds + kTile * CH;
         const float *bt = bc + (i & 1) * kTile * 2 * S + ln * M;
         const int rows = min(kTile, count - i * kTile);
-#pragma unroll 2
-        for (int r = 0; r < rows; ++r) {
-            const int t = token(i * kTile + r);
-            float x = (float)xs[r * CH], v = (float)ds[r * CH] + bias;
-            const float d = a.dt_softplus ? softplus(v) : v;
+        // eight tokens at a time: their steps, the recurrence, their outputs.  Past the end the step is 0:
+        // decay 1 and nothing added.
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += GROUP) {
+            float d[GROUP], in[GROUP], y[GROUP];
+#pragma unroll
+            for (int r = 0; r < GROUP; ++r) {
+                const bool ok = r0 + r < rows;
+                float x = (float)xs[(r0 + r) * CH];
+                const float v = (float)ds[(r0 + r) * CH] + bias;
+                d[r] = ok ? (a.dt_softplus ? softplus(v) : v) : 0.f;
+                if (MODE == REVERSE && third) x *= silu((float)zs[(r0 + r) * CH]);
+                in[r] = ok ? (MODE == REVERSE ? x : d[r] * x) : 0.f;
+                if (MODE != WALK) sum += d[r];
+            }
             if constexpr (MODE == WALK) {
-                if (a.saved && (r % kSaveEvery) == 0 && live) {
-                    const long long slot = g.slot + (t - g.t0) / kSaveEvery;
+                if (a.saved && live) {
+                    const long long slot = g.slot + (i * kTile + r0) / kSaveEvery;
                     float4 *p = reinterpret_cast<float4 *>(a.saved + ((size_t)slot * a.D + c) * S + ln * M);
 #pragma unroll
                     for (int k = 0; k < M / 4; ++k) p[k] = make_float4(h2[2 * k].x, h2[2 * k].y, h2[2 * k + 1].x, h2[2 * k + 1].y);
                 }
             }
-            if constexpr (MODE == REVERSE) {
-                if (third) x *= silu((float)zs[r * CH]);
-            }
-            if constexpr (MODE != WALK) sum += d;
-            const float2 dd = make_float2(d, d), in = MODE == REVERSE ? make_float2(x, x) : make_float2(d * x, d * x);
-            float2 y2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const float4 *b4 = reinterpret_cast<const float4 *>(bt + r * 2 * S), *c4 = reinterpret_cast<const float4 *>(bt + r * 2 * S + S);
 #pragma unroll
-            for (int k = 0; k < M / 4; ++k) {
-                const float4 B4 = b4[k];
-                float4 C4;
-                if constexpr (MODE == WALK) C4 = c4[k];
+            for (int r = 0; r < GROUP; ++r) {
+                const float2 dd = make_float2(d[r], d[r]), ii = make_float2(in[r], in[r]);
+                float2 y2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float4 *b4 = reinterpret_cast<const float4 *>(bt + (r0 + r) * 2 * S), *c4 = b4 + S / 4;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int n = 2 * k + e;
-                    const float2 arg = __fmul2_rn(A2[n], dd);
-                    const float2 dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
-                    const float2 b = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
-                    if constexpr (MODE == REVERSE) {
-                        h2[n] = __fmul2_rn(dec, __ffma2_rn(b, in, h2[n]));
-                    } else {
-                        h2[n] = __ffma2_rn(dec, h2[n], __fmul2_rn(in, b));
+                for (int k = 0; k < M / 4; ++k) {
+                    const float4 B4 = b4[k];
+                    float4 C4;
+                    if constexpr (MODE == WALK) C4 = c4[k];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int n = 2 * k + e;
+                        const float2 arg = __fmul2_rn(A2[n], dd);
+                        const float2 dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
+                        const float2 b = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
+                        if constexpr (MODE == REVERSE) h2[n] = __fmul2_rn(dec, __ffma2_rn(b, ii, h2[n]));
+                        else h2[n] = __ffma2_rn(dec, h2[n], __fmul2_rn(ii, b));
+                        if constexpr (MODE == WALK)
+                            y2[e] = __ffma2_rn(e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y), h2[n], y2[e]);
                     }
-                    if constexpr (MODE == WALK)
-                        y2[e] = __ffma2_rn(e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y), h2[n], y2[e]);
+                }
+                if constexpr (MODE == WALK) {
+                    const float2 ys = __fadd2_rn(y2[0], y2[1]);
+                    y[r] = ys.x + ys.y;
                 }
             }
             if constexpr (MODE == WALK) {
-                const float2 ys = __fadd2_rn(y2[0], y2[1]);
-                float y = ys.x + ys.y;
 #pragma unroll
-                for (int o = 1; o < LN; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                y = fmaf(skip, x, y);
-                if (third) y *= silu((float)zs[r * CH]);
-                if (live && ln == 0) static_cast<E *>(a.y)[t * a.y_stride + c] = (E)y;
+                for (int r = 0; r < GROUP; ++r) {
+#pragma unroll
+                    for (int o = 1; o < LN; o <<= 1) y[r] += __shfl_xor_sync(0xffffffffu, y[r], o);
+                    y[r] = fmaf(skip, (float)xs[(r0 + r) * CH], y[r]);
+                    if (third) y[r] *= silu((float)zs[(r0 + r) * CH]);
+                    if (live && ln == 0 && r0 + r < rows)
+                        static_cast<E *>(a.y)[(long long)(g.t0 + i * kTile + r0 + r) * a.y_stride + c] = (E)y[r];
+                }
             }
         }
         if (more) bc_store(i + 1);
@@ -219,6 +232,8 @@ __global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
 
 // The segments' own states chained: seg_state[u] becomes the state at the
 // start of segment u (reverse: the gradient at its end).  A thread per state.
+// The decay e^{A sum d} is applied in two halves, so that a product in range
+// is not lost to a factor out of it.
 __global__ void __launch_bounds__(256) kda_scan_chain_kernel(ScanArgs a, int S, bool reverse) {
     const int s = blockIdx.y;
     const long long e = (long long)blockIdx.x * 256 + threadIdx.x, size = (long long)a.D * S;
@@ -229,27 +244,27 @@ __global__ void __launch_bounds__(256) kda_scan_chain_kernel(ScanArgs a, int S, 
     const int c = (int)(e / S);
     const long long u0 = b0 / a.seg + s;
     const float A = a.A[e] * kLog2e;
-    // e^{A sum d} in two halves, so that only a product that is out of range is
-    auto chain = [&](float h, long long u, float own) {
-        const float k = exp2f(0.5f * (A * a.seg_sum[u * a.D + c]));
-        return h == 0.f ? own : fmaf(h * k, k, own);
-    };
-    float *st = a.seg_state + e;
-    if (!reverse) {
-        float h = a.initial_state ? a.initial_state[s * size + e] : 0.f, own = st[u0 * size];
-        for (int j = 0; j + 1 < count; ++j) {
-            h = chain(h, u0 + j, own);
-            if (j + 2 < count) own = st[(u0 + j + 1) * size];
-            st[(u0 + j + 1) * size] = h;
+    float *st = a.seg_state + u0 * size + e;
+    const float *sum = a.seg_sum + u0 * a.D + c;
+    const float *first = reverse ? a.dfinal : a.initial_state;
+    float h = first ? first[s * size + e] : 0.f;
+    // eight segments' loads at a time, then their chain
+    constexpr int U = 8;
+    for (int j0 = 0; j0 < count; j0 += U) {
+        float own[U], k[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int j = min(j0 + i, count - 1), u = reverse ? count - 1 - j : j;
+            own[i] = st[u * size];
+            k[i] = exp2f(0.5f * (A * sum[(long long)u * a.D]));
         }
-    } else {
-        float h = a.dfinal ? a.dfinal[s * size + e] : 0.f;
-        for (int j = count - 1; j > 0; --j) {
-            const float own = st[(u0 + j) * size];
-            st[(u0 + j) * size] = h;
-            h = chain(h, u0 + j, own);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int j = j0 + i, u = reverse ? count - 1 - j : j;
+            if (j >= count) break;
+            st[u * size] = h;
+            h = h == 0.f ? own[i] : fmaf(h * k[i], k[i], own[i]);
         }
-        st[u0 * size] = h;
     }
 }
 

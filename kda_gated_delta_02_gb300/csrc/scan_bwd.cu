@@ -22,6 +22,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kda_internal.h"
 #include "layer.cuh"
 #include "scan.cuh"
@@ -73,8 +75,6 @@ struct Pair {
     }
 };
 
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
 template <bool BF16, int S, bool VEC>
 __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
     using E = Elem<BF16>;
@@ -120,6 +120,26 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
     E *dxp = static_cast<E *>(a.dx) + c, *ddtp = static_cast<E *>(a.ddt) + c, *dzp = static_cast<E *>(a.dz) + c;
     const int count = g.s < 0 ? 0 : g.t1 - g.t0;
 
+    // the eight tokens before are brought into L2 while these are worked on
+    auto ahead = [&](long long t) {
+        const int k = lane % K, what = lane / K, c0 = grp * per + tile * L::CH;
+        const E *rows[4] = {static_cast<const E *>(a.x), static_cast<const E *>(a.dt), static_cast<const E *>(a.dy), static_cast<const E *>(a.z)};
+        const long long strides[4] = {a.x_stride, a.dt_stride, a.dy_stride, a.z_stride};
+        const E *row = rows[0];
+        long long stride = strides[0];
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+            if (what == j) row = rows[j], stride = strides[j];
+        if (row) {
+#pragma unroll
+            for (int o = 0; o < L::CH; o += 128 / (int)sizeof(E))
+                if (tile * L::CH + o < per) prefetch(row + (t + k) * stride + c0 + o);
+        }
+        if (what < 2) prefetch(what ? Cp + (t + k) * a.c_stride : Bp + (t + k) * a.b_stride);
+        if (lane * 32 < L::CH * S && tile * L::CH + lane * 32 / S < per)
+            prefetch(a.saved + (size_t)(g.slot + (t - g.t0) / K) * DS + (size_t)c0 * S + lane * 32);
+    };
+
     for (int i = (count + K - 1) / K - 1; i >= 0; --i) {
         const int t0 = g.t0 + i * K, rows = min(K, g.t1 - t0);
         // the eight tokens' values, at this thread's own places: d, x, e, 1 - e^{-d}, dy sigma'(z)
@@ -134,10 +154,7 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
             if (a.z) z.load(zp + t * a.z_stride, VEC, in2, in1);
             v.v.x += bias.x, v.v.y += bias.y;
             float2 d = v.v, s = both(1.f), dz = both(0.f);
-            if (a.dt_softplus) {
-                d = make_float2(softplus(v.v.x), softplus(v.v.y));
-                s = make_float2(sigmoid(v.v.x), sigmoid(v.v.y));
-            }
+            if (a.dt_softplus) d = make_float2(softplus(v.v.x, &s.x), softplus(v.v.y, &s.y));
             if (a.z) {
                 const float2 sg = make_float2(sigmoid(z.v.x), sigmoid(z.v.y));
                 dz = make_float2(e.v.x * (sg.x * fmaf(z.v.x, 1.f - sg.x, 1.f)), e.v.y * (sg.y * fmaf(z.v.y, 1.f - sg.y, 1.f)));
@@ -146,6 +163,7 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
             float2 *p = vals + k * 32 + lane;
             p[0] = d, p[K * 32] = x.v, p[2 * K * 32] = e.v, p[3 * K * 32] = s, p[4 * K * 32] = dz;
         }
+        if (i > 0) ahead(t0 - K);
         __syncwarp();  // B and C of the previous tokens have been read
         for (int n = lane; n < K * 2 * S; n += 32) {
             const int k = n / (2 * S), m = n % (2 * S);
@@ -185,12 +203,13 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                 }
             }
         }
-        // backward
-#pragma unroll 1
-        for (int k = rows - 1; k >= 0; --k) {
-            const bool odd = k & 1;
+        // backward, two tokens to a kept state
+        auto back = [&](auto later, int k) {
+            constexpr bool LATER = decltype(later)::value;
             const float2 d = vals[k * 32 + lane], x = vals[(K + k) * 32 + lane], ev = vals[(2 * K + k) * 32 + lane];
             const float4 *b4 = reinterpret_cast<const float4 *>(bc + k * 2 * S + ln * M), *c4 = b4 + S / 4;
+            const float2 dq[2] = {both(d.x), both(d.y)}, in[2] = {both(d.x * x.x), both(d.y * x.y)}, eq[2] = {both(ev.x), both(ev.y)};
+            const float2 minus[2] = {both(-in[0].x), both(-in[1].x)};
             float2 lB[2] = {both(0.f), both(0.f)}, lA[2] = {both(0.f), both(0.f)}, y[2] = {both(0.f), both(0.f)};
 #pragma unroll
             for (int n = 0; n < M / 4; ++n) {
@@ -199,26 +218,23 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const float4 H4 = hist[((k >> 1) * V4 + q * (M / 4) + n) * 32 + lane];
-                    const float2 dq = both(q ? d.y : d.x), in = both(q ? d.y * x.y : d.x * x.x), eq = both(q ? ev.y : ev.x);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float2 A = A2[q][2 * n + e], arg = __fmul2_rn(A, dq), dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
+                        const float2 A = A2[q][2 * n + e], arg = __fmul2_rn(A, dq[q]), dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
                         const float2 B = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
                         const float2 C = e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y);
                         const float2 H = e ? make_float2(H4.z, H4.w) : make_float2(H4.x, H4.y);
-                        const float2 b = __fmul2_rn(in, B);
-                        float2 ah, hk;
-                        if (odd) ah = __fmul2_rn(dec, H), hk = __fadd2_rn(ah, b);
-                        else hk = H, ah = __fadd2_rn(H, make_float2(-b.x, -b.y));
-                        const float2 l = __ffma2_rn(C, eq, carry[q][2 * n + e]);
+                        const float2 ah = LATER ? __fmul2_rn(dec, H) : __ffma2_rn(minus[q], B, H);
+                        const float2 hk = LATER ? __ffma2_rn(in[q], B, ah) : H;
+                        const float2 l = __ffma2_rn(C, eq[q], carry[q][2 * n + e]);
                         const float2 u = __fmul2_rn(l, ah);
                         carry[q][2 * n + e] = __fmul2_rn(dec, l);
                         lB[q] = __ffma2_rn(l, B, lB[q]);
                         lA[q] = __ffma2_rn(u, A, lA[q]);
-                        dA[q][2 * n + e] = __ffma2_rn(dq, u, dA[q][2 * n + e]);
+                        dA[q][2 * n + e] = __ffma2_rn(dq[q], u, dA[q][2 * n + e]);
                         y[q] = __ffma2_rn(C, hk, y[q]);
-                        sB[e] = q ? __ffma2_rn(l, in, sB[e]) : __fmul2_rn(l, in);
-                        sC[e] = q ? __ffma2_rn(hk, eq, sC[e]) : __fmul2_rn(hk, eq);
+                        sB[e] = q ? __ffma2_rn(l, in[q], sB[e]) : __fmul2_rn(l, in[q]);
+                        sC[e] = q ? __ffma2_rn(hk, eq[q], sC[e]) : __fmul2_rn(hk, eq[q]);
                     }
                 }
                 red[n * 32 + lane] = make_float4(sB[0].x, sB[0].y, sB[1].x, sB[1].y);
@@ -283,6 +299,11 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                 }
             }
             __syncwarp();  // `red` has been read
+        };
+#pragma unroll 1
+        for (int k = (rows - 1) & ~1; k >= 0; k -= 2) {
+            if (k + 1 < rows) back(std::true_type(), k + 1);
+            back(std::false_type(), k);
         }
     }
     // the unit's sums, zero where it has no tokens
