@@ -1606,8 +1606,8 @@ int kda_conv_step(const void *x, const float *w, const float *bias, void *tail, 
 static int scan_shape(int N, int T, int D, int G, int S, int dtype) {
     if (N < 1 || T < 0 || D < 1 || G < 1 || D % G || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
     if ((S != 8 && S != 16 && S != 32 && S != 64) || T > kMaxTokens || N > kMaxTokens || D > (1 << 22) ||
-        (long long)D * S + 2LL * D > 0x7fffffffLL ||
-        (long long)G * ((D / G + kda::scan_bwd_channels(S) - 1) / kda::scan_bwd_channels(S)) > kMaxGridY)
+        (long long)D * S + 2LL * D > 0x7fffff00LL ||
+        (long long)G * ((D / G + kda::scan_channels(S) - 1) / kda::scan_channels(S)) > kMaxGridY)
         return KDA_ERR_UNSUPPORTED_SHAPE;
     return KDA_OK;
 }
@@ -1651,7 +1651,7 @@ ScanLayout scan_layout(int N, int T, int D, int G, int S, bool backward) {
     if (backward) {
         const int ch = kda::scan_bwd_channels(S);
         L.parts = o;
-        o = align256(o + (size_t)L.units * ((size_t)D * S + 2 * D) * 4);
+        o = align256(o + (size_t)L.units * kda::scan_parts_width(D, S) * 4);
         L.bc = o;
         o = align256(o + (size_t)((D / G + ch - 1) / ch) * T * G * 2 * S * 4);
     }
@@ -1710,7 +1710,8 @@ int kda_scan_fwd(const void *x, const void *dt, const float *A, const void *B, c
     kda::ScanArgs a = scan_args(x, dt, A, B, C, skip, z, dt_bias, N, T, D, G, x_stride, dt_stride, B_stride, C_stride, z_stride, dt_softplus);
     a.cu_seqlens = cu_seqlens; a.initial_state = initial_state; a.final_state = final_state; a.y = y; a.y_stride = y_stride;
     a.saved = saved; a.status = status; a.seg = L.seg;
-    const Rows copied[] = {r[0], r[1], r[2]};
+    const Rows copied[] = {r[0], r[1], r[2]}, pair[] = {r[3], r[4]};
+    a.wide_bc = all_on16(pair);
     a.wide = all_on16(copied) && (long long)(D / G) * e % 16 == 0;
     char *ws = static_cast<char *>(workspace);
     a.seg_state = reinterpret_cast<float *>(ws + L.state);
@@ -1765,7 +1766,8 @@ int kda_scan_bwd(const void *x, const void *dt, const float *A, const void *B, c
     a.cu_seqlens = cu_seqlens; a.dy = dy; a.dy_stride = dy_stride; a.dfinal = dfinal_state;
     a.saved = const_cast<float *>(saved);
     a.dx = dx; a.ddt = ddt; a.dz = dz; a.dB = dB; a.dC = dC; a.dstate = dinitial_state; a.status = status; a.seg = L.seg;
-    const Rows copied[] = {r[0], r[1], r[2], r[3]};
+    const Rows copied[] = {r[0], r[1], r[2], r[3]}, pair[] = {r[4], r[5]};
+    a.wide_bc = all_on16(pair);
     a.wide = all_on16(copied) && (long long)(D / G) * e % 16 == 0;
     char *ws = static_cast<char *>(workspace);
     a.seg_state = reinterpret_cast<float *>(ws + L.state);
@@ -1785,7 +1787,7 @@ int kda_scan_bwd(const void *x, const void *dt, const float *A, const void *B, c
     if (err == cudaSuccess) err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_scan_bc(a, S, bf16, st); });
     if (err == cudaSuccess) {
         const int n = (int)DS;
-        kda::SumRowsArgs s = {a.parts, L.units, n + 2 * D, {dA, dskip, ddt_bias}, {0, n, n + D, n + 2 * D}, {1, 1, 1}};
+        kda::SumRowsArgs s = {a.parts, L.units, (int)kda::scan_parts_width(D, S), {dA, dskip, ddt_bias}, {0, n, n + D, n + 2 * D}, {1, 1, 1}};
         err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, st); });
     }
     return cuda_status(err);
@@ -1809,7 +1811,7 @@ int kda_scan_step(const void *x, const void *dt, const float *A, const void *B, 
     kda::ScanArgs a = scan_args(x, dt, A, B, C, skip, z, dt_bias, R, R, D, G, x_stride, dt_stride, B_stride, C_stride, z_stride, dt_softplus);
     a.state = state; a.y = y; a.y_stride = y_stride;
     const Rows pair[] = {r[3], r[4]};
-    a.wide = all_on16(pair);
+    a.wide_bc = all_on16(pair);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(timed_launch(KDA_KERNEL_SCAN, st, [&] {
         return kda::launch_scan(a, S, kda::SCAN_STEP, dtype == KDA_DTYPE_BF16, sm_count(), st);

@@ -307,15 +307,18 @@ struct ScanArgs {
     float *saved;                         // [floor(T / 8) + N][D][S]: the state before every eighth token, or null
     float *seg_state, *seg_sum;           // [units][D][S], [units][D]
     int N, T, D, G, seg;                  // seg: tokens of a segment, 0 for whole sequences
-    bool dt_softplus, wide;               // wide: 16-byte copies of rows (single tokens: of B and C)
+    bool dt_softplus;
+    bool wide, wide_bc;                   // rows of channels on 16-byte boundaries; four of B and C at a time
     uint32_t *status;
     // backward
     void *dx, *ddt, *dz;                  // [T][D]
     float *dstate;                        // [N][D][S] or null
     float *bc_parts;                      // [channel tiles][T][G][2 S]
-    float *parts;                         // [units][D S + 2 D]: sums for dA, dD and ddt_bias
+    float *parts;                         // [units][scan_parts_width]: sums for dA [D][S], dD and ddt_bias [D]
     void *dB, *dC;                        // [T][G][S]
 };
+// floats of a unit's sums, whole 16 bytes
+constexpr size_t scan_parts_width(int D, int S) { return ((size_t)D * S + 2 * (size_t)D + 3) / 4 * 4; }
 enum ScanWhat : int { SCAN_WALK = 0, SCAN_FORWARD = 1, SCAN_REVERSE = 2, SCAN_STEP = 3 };
 int scan_units(int N, int T, int seg);
 int scan_channels(int S);      // channels of a block

@@ -7,9 +7,12 @@
 // dt, z, y) and, with 16 states, 16 exponentials and 32 pairs of packed fp32
 // operations: about 0.6 cycles of an SM, where 8 bytes take 0.34.
 //
-// A thread keeps a channel (16 states of it; more states take 2 or 4
-// neighbouring lanes), so the sum over n needs no exchange and a channel's
-// d and x no shared copies.  States lie in pairs for the packed operations.  A
+// A thread keeps 8 states of a channel, in pairs for the packed operations; S / 8
+// neighbouring lanes share a channel.  Of eight tokens each of these lanes
+// forms the steps, and at the end the outputs, of its own 8 / (S / 8): the steps go round by
+// shuffles, and the lanes' shares of the outputs are added on the way to
+// their token's lane.  (A channel to a thread took as many instructions but
+// half the warps at twice the registers, and 5 cycles an instruction.)  A
 // block of 128 threads walks its tokens 16 at a time: x, dt and z of the next
 // 16 come by cp.async while these are worked on, and B and C (the same for all
 // channels of a group) are widened to 32 bits once per block, so that a thread
@@ -44,16 +47,16 @@ enum Mode : int {
 
 template <bool BF16, int S>
 struct Layout {
-    static constexpr int LN = S > 16 ? S / 16 : 1, M = S / LN, CH = kThreads / LN;
+    static constexpr int M = 8, LN = S / M, CH = kThreads / LN;
     static constexpr int raw = kTile * CH * (BF16 ? 2 : 4);  // bytes of one tensor's tile
     static constexpr int bytes = 2 * 3 * raw + 2 * kTile * 2 * S * 4;
 };
 
 template <bool BF16, int S, int MODE, bool VEC>
-__global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, 7) kda_scan_kernel(ScanArgs a) {
     using E = Elem<BF16>;
     using L = Layout<BF16, S>;
-    constexpr int LN = L::LN, M = L::M, CH = L::CH;
+    constexpr int LN = L::LN, M = L::M, CH = L::CH, OWN = GROUP / LN;  // tokens of a lane's own in a group
     extern __shared__ __align__(16) unsigned char smem[];
     E *raw = reinterpret_cast<E *>(smem);                            // [2][3][kTile][CH]
     float *bc = reinterpret_cast<float *>(smem + 2 * 3 * L::raw);    // [2][kTile][2 S]: B, then C
@@ -68,14 +71,7 @@ __global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
     const int c0 = grp * per + c_in, left = per - c_in;                          // channels from c0 on in the group
     const bool live = ch < left;
     const int c = c0 + (live ? ch : 0);
-
-    const E *src[3] = {static_cast<const E *>(MODE == REVERSE ? a.dy : a.x), static_cast<const E *>(a.dt),
-                       static_cast<const E *>(a.z)};
-    const long long stride[3] = {MODE == REVERSE ? a.dy_stride : a.x_stride, a.dt_stride, a.z_stride};
     const bool third = MODE != FORWARD && a.z != nullptr;
-    const E *Bp = static_cast<const E *>(MODE == REVERSE ? a.C : a.B) + (size_t)grp * S;
-    const E *Cp = static_cast<const E *>(a.C) + (size_t)grp * S;
-    const long long b_stride = MODE == REVERSE ? a.c_stride : a.b_stride;
 
     float2 A2[M / 2], h2[M / 2];
     {
@@ -97,46 +93,57 @@ __global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
     const float skip = MODE == WALK && a.Dskip ? a.Dskip[c] : 0.f, bias = a.dt_bias ? a.dt_bias[c] : 0.f;
     float sum = 0.f;
     const int count = g.t1 - g.t0, steps = (count + kTile - 1) / kTile;
-    auto token = [&](int r) { return MODE == REVERSE ? g.t1 - 1 - r : g.t0 + r; };
+    // row r of the walk: forward from the first token, or backward from the last
+    auto token = [&](int r) { return (long long)(MODE == REVERSE ? g.t1 - 1 - r : g.t0 + r); };
 
     auto stage = [&](int i) {
         E *dst = raw + (i & 1) * 3 * kTile * CH;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             if (k == 2 && !third) break;
+            const E *src = static_cast<const E *>(k == 0 ? (MODE == REVERSE ? a.dy : a.x) : k == 1 ? a.dt : a.z) + c0;
+            const long long stride = k == 0 ? (MODE == REVERSE ? a.dy_stride : a.x_stride) : k == 1 ? a.dt_stride : a.z_stride;
             if constexpr (VEC) {
                 constexpr int EPC = BF16 ? 8 : 4, PER_ROW = CH / EPC;
 #pragma unroll
                 for (int e = tid; e < kTile * PER_ROW; e += kThreads) {
                     const int r = e / PER_ROW, o = (e % PER_ROW) * EPC, at = i * kTile + r;
                     const bool ok = at < count && o < left;
-                    const E *p = src[k] + (ok ? token(at) * stride[k] + c0 + o : 0);
-                    cp_async16(dst + (k * kTile + r) * CH + o, p, ok);
+                    cp_async16(dst + (k * kTile + r) * CH + o, src + (ok ? token(at) * stride + o : 0), ok);
                 }
             } else {
                 for (int e = tid; e < kTile * CH; e += kThreads) {
                     const int r = e / CH, o = e % CH, at = i * kTile + r;
-                    if (at < count && o < left) dst[(k * kTile + r) * CH + o] = src[k][token(at) * stride[k] + c0 + o];
+                    if (at < count && o < left) dst[(k * kTile + r) * CH + o] = src[token(at) * stride + o];
                 }
             }
         }
         cp_async_commit();
     };
-    constexpr int BCN = (kTile * 2 * S + kThreads - 1) / kThreads;
-    float bcr[BCN];
+    // four neighbouring values of B and C at a time (REVERSE wants C alone)
+    constexpr int BCN = (kTile * 2 * S + 4 * kThreads - 1) / (4 * kThreads);
+    Vec<BF16, 4> bcr[BCN];
     auto bc_load = [&](int i) {
 #pragma unroll
         for (int k = 0; k < BCN; ++k) {
-            const int e = tid + k * kThreads, r = e / (2 * S), n = e % (2 * S), at = i * kTile + r;
-            bcr[k] = 0.f;
-            if (at >= count) continue;
-            if (n < S) bcr[k] = (float)Bp[token(at) * b_stride + n];
-            else if (MODE == WALK) bcr[k] = (float)Cp[token(at) * a.c_stride + n - S];
+            const int e = 4 * (tid + k * kThreads), r = e / (2 * S), n = e % (2 * S), at = i * kTile + r;
+            bcr[k].zero();
+            if (at >= count || (MODE == FORWARD && n >= S) || (MODE == REVERSE && n < S)) continue;
+            const E *p = static_cast<const E *>(n < S ? a.B : a.C) + token(at) * (n < S ? a.b_stride : a.c_stride) + grp * S + n % S;
+            if (a.wide_bc) {
+                bcr[k].load(p);
+            } else {
+                const float f[4] = {(float)p[0], (float)p[1], (float)p[2], (float)p[3]};
+                bcr[k].set(f);
+            }
         }
     };
     auto bc_store = [&](int i) {
 #pragma unroll
-        for (int k = 0; k < BCN; ++k) bc[(i & 1) * kTile * 2 * S + tid + k * kThreads] = bcr[k];
+        for (int k = 0; k < BCN; ++k)
+            if (tid + k * kThreads < kTile * 2 * S / 4)
+                reinterpret_cast<float4 *>(bc + (i & 1) * kTile * 2 * S)[tid + k * kThreads] =
+                    make_float4(bcr[k].get(0), bcr[k].get(1), bcr[k].get(2), bcr[k].get(3));
     };
 
     if (steps > 0) {
@@ -153,22 +160,27 @@ __global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
             bc_load(i + 1);
         }
         const E *xs = raw + (i & 1) * 3 * kTile * CH + ch, *ds = xs + kTile * CH, *zs = ds + kTile * CH;
-        const float *bt = bc + (i & 1) * kTile * 2 * S + ln * M;
+        const float *bt = bc + (i & 1) * kTile * 2 * S + ln * M + (MODE == REVERSE ? S : 0);
         const int rows = min(kTile, count - i * kTile);
-        // eight tokens at a time: their steps, the recurrence, their outputs.  Past the end the step is 0:
-        // decay 1 and nothing added.
+        // eight tokens at a time.  Past the end the step is 0: decay 1 and nothing added.
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += GROUP) {
-            float d[GROUP], in[GROUP], y[GROUP];
+            const int mine = r0 + ln * OWN;  // the lane's own tokens
+            float d[OWN], in[OWN], y[GROUP];
 #pragma unroll
-            for (int r = 0; r < GROUP; ++r) {
-                const bool ok = r0 + r < rows;
-                float x = (float)xs[(r0 + r) * CH];
-                const float v = (float)ds[(r0 + r) * CH] + bias;
-                d[r] = ok ? (a.dt_softplus ? softplus(v) : v) : 0.f;
-                if (MODE == REVERSE && third) x *= silu((float)zs[(r0 + r) * CH]);
-                in[r] = ok ? (MODE == REVERSE ? x : d[r] * x) : 0.f;
-                if (MODE != WALK) sum += d[r];
+            for (int j = 0; j < OWN; j += 2) {  // (two of them in packed operations)
+                constexpr int NEXT = OWN > 1 ? 1 : 0;
+                const int p = (mine + j) * CH, q = (mine + j + NEXT) * CH;
+                float2 x = make_float2((float)xs[p], (float)xs[q]), sig;
+                float2 v = __fadd2_rn(make_float2((float)ds[p], (float)ds[q]), both(bias));
+                if (a.dt_softplus) v = softplus2(v, sig);
+                if (mine + j >= rows) v.x = 0.f;
+                if (mine + j + NEXT >= rows) v.y = 0.f;
+                if (MODE == REVERSE && third) x = __fmul2_rn(x, silu2(make_float2((float)zs[p], (float)zs[q])));
+                if (MODE != REVERSE) x = __fmul2_rn(v, x);
+                d[j] = v.x, d[j + NEXT] = v.y;
+                in[j] = mine + j < rows ? x.x : 0.f, in[j + NEXT] = mine + j + NEXT < rows ? x.y : 0.f;
+                if (MODE != WALK) sum += NEXT ? v.x + v.y : v.x;
             }
             if constexpr (MODE == WALK) {
                 if (a.saved && live) {
@@ -180,8 +192,11 @@ __global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
             }
 #pragma unroll
             for (int r = 0; r < GROUP; ++r) {
-                const float2 dd = make_float2(d[r], d[r]), ii = make_float2(in[r], in[r]);
-                float2 y2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const int from = (tid & 31 & ~(LN - 1)) + r / OWN;
+                const float dr = LN > 1 ? __shfl_sync(0xffffffffu, d[r % OWN], from) : d[r % OWN];
+                const float ir = LN > 1 ? __shfl_sync(0xffffffffu, in[r % OWN], from) : in[r % OWN];
+                const float2 dd = both(dr), ii = both(ir);
+                float2 y2 = both(0.f);
                 const float4 *b4 = reinterpret_cast<const float4 *>(bt + (r0 + r) * 2 * S), *c4 = b4 + S / 4;
 #pragma unroll
                 for (int k = 0; k < M / 4; ++k) {
@@ -191,33 +206,45 @@ __global__ void __launch_bounds__(kThreads) kda_scan_kernel(ScanArgs a) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int n = 2 * k + e;
-                        const float2 arg = __fmul2_rn(A2[n], dd);
+                        const float2 arg = __ffma2_rn(A2[n], dd, both(kExp2Low));
                         const float2 dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
                         const float2 b = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
                         if constexpr (MODE == REVERSE) h2[n] = __fmul2_rn(dec, __ffma2_rn(b, ii, h2[n]));
                         else h2[n] = __ffma2_rn(dec, h2[n], __fmul2_rn(ii, b));
                         if constexpr (MODE == WALK)
-                            y2[e] = __ffma2_rn(e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y), h2[n], y2[e]);
+                            y2 = __ffma2_rn(e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y), h2[n], y2);
                     }
                 }
-                if constexpr (MODE == WALK) {
-                    const float2 ys = __fadd2_rn(y2[0], y2[1]);
-                    y[r] = ys.x + ys.y;
-                }
+                if constexpr (MODE == WALK) y[r] = y2.x + y2.y;
             }
             if constexpr (MODE == WALK) {
+                // the lanes' shares of eight outputs, each added up in its token's lane
 #pragma unroll
-                for (int r = 0; r < GROUP; ++r) {
+                for (int o = LN / 2, n = GROUP / 2; o > 0; o /= 2, n /= 2) {
+                    const bool up = ln & o;
 #pragma unroll
-                    for (int o = 1; o < LN; o <<= 1) y[r] += __shfl_xor_sync(0xffffffffu, y[r], o);
-                    y[r] = fmaf(skip, (float)xs[(r0 + r) * CH], y[r]);
-                    if (third) y[r] *= silu((float)zs[(r0 + r) * CH]);
-                    if (live && ln == 0 && r0 + r < rows)
-                        static_cast<E *>(a.y)[(long long)(g.t0 + i * kTile + r0 + r) * a.y_stride + c] = (E)y[r];
+                    for (int j = 0; j < n; ++j) {
+                        const float send = up ? y[j] : y[j + n], keep = up ? y[j + n] : y[j];
+                        y[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+                }
+                E *yp = static_cast<E *>(a.y) + token(i * kTile + mine) * a.y_stride + c;
+#pragma unroll
+                for (int j = 0; j < OWN; j += 2) {
+                    constexpr int NEXT = OWN > 1 ? 1 : 0;
+                    const int p = (mine + j) * CH, q = (mine + j + NEXT) * CH;
+                    float2 out = __ffma2_rn(both(skip), make_float2((float)xs[p], (float)xs[q]), make_float2(y[j], y[j + NEXT]));
+                    if (third) out = __fmul2_rn(out, silu2(make_float2((float)zs[p], (float)zs[q])));
+                    if (live && mine + j < rows) yp[j * a.y_stride] = (E)out.x;
+                    if (NEXT && live && mine + j + NEXT < rows) yp[(j + NEXT) * a.y_stride] = (E)out.y;
                 }
             }
         }
         if (more) bc_store(i + 1);
+    }
+    if constexpr (MODE != WALK) {
+#pragma unroll
+        for (int o = 1; o < LN; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
     if (!live) return;
     float *out = nullptr;
@@ -298,7 +325,7 @@ __global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int rows
             xv[u] = (float)x[q * a.x_stride];
             dv[u] = (float)dt[q * a.dt_stride] + bias;
             zv[u] = a.z ? (float)z[q * a.z_stride] : 0.f;
-            if (a.wide) {
+            if (a.wide_bc) {
                 Vec<BF16, 4> vb, vc;
                 vb.load(B + q * a.b_stride);
                 vc.load(C + q * a.c_stride);
@@ -313,10 +340,10 @@ __global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int rows
         for (int u = 0; u < U; ++u) {
             if (r + u >= r1) break;
             const float d = a.dt_softplus ? softplus(dv[u]) : dv[u], in = d * xv[u];
-            h[u].x = fmaf(exp2_fast(A.x * d), h[u].x, in * bv[u][0]);
-            h[u].y = fmaf(exp2_fast(A.y * d), h[u].y, in * bv[u][1]);
-            h[u].z = fmaf(exp2_fast(A.z * d), h[u].z, in * bv[u][2]);
-            h[u].w = fmaf(exp2_fast(A.w * d), h[u].w, in * bv[u][3]);
+            h[u].x = fmaf(exp2_fast(fmaf(A.x, d, kExp2Low)), h[u].x, in * bv[u][0]);
+            h[u].y = fmaf(exp2_fast(fmaf(A.y, d, kExp2Low)), h[u].y, in * bv[u][1]);
+            h[u].z = fmaf(exp2_fast(fmaf(A.z, d, kExp2Low)), h[u].z, in * bv[u][2]);
+            h[u].w = fmaf(exp2_fast(fmaf(A.w, d, kExp2Low)), h[u].w, in * bv[u][3]);
             float y = fmaf(cv[u][0], h[u].x, cv[u][1] * h[u].y) + fmaf(cv[u][2], h[u].z, cv[u][3] * h[u].w);
 #pragma unroll
             for (int o = 1; o < LANES; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
@@ -368,7 +395,7 @@ cudaError_t launch_scan_s(const ScanArgs &a, int what, int sms, cudaStream_t st)
 
 int scan_units(int N, int T, int seg) { return seg ? T / seg + N : N; }
 
-int scan_channels(int S) { return S > 16 ? kThreads * 16 / S : kThreads; }
+int scan_channels(int S) { return kThreads * 8 / S; }
 
 cudaError_t launch_scan(const ScanArgs &a, int S, int what, bool bf16, int sms, cudaStream_t st) {
     switch (S) {

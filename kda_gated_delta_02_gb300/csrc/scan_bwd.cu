@@ -7,18 +7,19 @@
 //   dB_t = sum over channels of l_t d_t x_t,  dC_t = sum over channels of e_t h_t
 //   dA = sum_t d_t l_t a_t h_{t-1},  dD = sum_t e_t x_t,  dz_t = dy_t (sum_n C_t h_t + D x_t) sigma'(z_t)
 //
-// What bounds it: instructions and shared memory, as the forward only more so:
-// 13 packed operations and two exponentials per state, and the sums of dB
-// and dC over channels.  A warp is a block.  A thread keeps 2 channels of 16
-// states (so that it adds two channels of those sums in registers), runs the
-// eight tokens from the saved state forward with every second state kept in
-// shared memory, then backward: of the two tokens that share a kept state H,
-// the later one goes forward from it (a H, a H + b) and the earlier one back
-// (H, H - b), neither with an operation more.  The sums over the warp's
-// channels go through shared memory, four floats at a time: 8 stores, 8 loads
-// and 26 additions and exchanges per token, where exchanges alone would take
-// 124.  They leave as a partial row per warp, token and group; a second
-// kernel adds them up in order.
+// What bounds it: instructions, as the forward only more so: 15 packed
+// operations and four exponentials (two of them the recomputed states') per pair of
+// states, and the sums of dB and dC over channels.  A thread keeps 2 channels of 8 states; S / 8 lanes
+// share a pair of channels, and the tokens' own work (steps, gates, outputs) is dealt
+// out to them.  The eight tokens from a saved state run forward with every
+// second state kept in shared memory, then backward: of the two tokens that
+// share a kept state H, the later one goes forward from it (a H, a H + b) and
+// the earlier one back (H - b, H), neither with an operation more.  The sums over channels
+// add two in a thread's registers, then go through shared memory, four floats
+// at a time: 4 stores, 4 loads and 20 additions and exchanges per token, where
+// exchanges alone would take 62.  A block's four warps add theirs once per eight
+// tokens, and a second kernel adds the blocks' in order.  Sums along the tokens (dA, dD,
+// ddt_bias) are taken over eight tokens first.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -36,14 +37,17 @@ using namespace scan;
 constexpr int K = kSaveEvery;
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int WARPS = kThreads / 32;
+
 template <int S>
 struct Layout {
-    static constexpr int LN = S > 16 ? S / 16 : 1, M = S / LN, PAIRS = 32 / LN, CH = 2 * PAIRS;
+    static constexpr int M = 8, LN = S / M, PAIRS = 32 / LN, CH = 2 * PAIRS * WARPS;
     static constexpr int V4 = 2 * M / 4;           // float4s of a thread's states, and of its dB and dC
-    static constexpr int hist = K / 2 * V4 * 32;   // float4s
-    static constexpr int red = V4 * 32;            // float4s
-    static constexpr int vals = 5 * K * 32;        // float2s
-    static constexpr int bytes = 16 * (hist + red) + 8 * vals + 4 * K * 2 * S;
+    static constexpr int hist = K / 2 * V4 * 32;   // float4s of a warp
+    static constexpr int red = V4 * 32;
+    static constexpr int vals = 5 * K * PAIRS;     // float2s of a warp
+    static constexpr int out = K * 2 * S;          // floats of a warp, and of B and C
+    static constexpr int bytes = WARPS * (16 * (hist + red) + 8 * vals + 4 * out) + 4 * out;
 };
 
 template <bool BF16>
@@ -76,21 +80,22 @@ struct Pair {
 };
 
 template <bool BF16, int S, bool VEC>
-__global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
     using E = Elem<BF16>;
     using L = Layout<S>;
-    constexpr int LN = L::LN, M = L::M, V4 = L::V4;
+    constexpr int LN = L::LN, M = L::M, V4 = L::V4, PAIRS = L::PAIRS, OWN = K / LN;
     extern __shared__ __align__(16) unsigned char smem[];
-    float4 *hist = reinterpret_cast<float4 *>(smem);                    // [K / 2][V4][32]
-    float4 *red = hist + L::hist;                                       // [V4][32]
-    float2 *vals = reinterpret_cast<float2 *>(red + L::red);            // [5][K][32], a thread's own
-    float *bc = reinterpret_cast<float *>(vals + L::vals);              // [K][2 S]
-    const int lane = threadIdx.x, ln = lane / L::PAIRS, cl = lane % L::PAIRS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = lane / PAIRS, pl = lane % PAIRS;
+    float4 *hist = reinterpret_cast<float4 *>(smem) + warp * L::hist;                              // [K / 2][V4][32]
+    float4 *red = reinterpret_cast<float4 *>(smem) + WARPS * L::hist + warp * L::red;              // [V4][32]
+    float2 *vals = reinterpret_cast<float2 *>(smem + 16 * WARPS * (L::hist + L::red)) + warp * L::vals;  // [5][K][PAIRS]
+    float *outs = reinterpret_cast<float *>(smem + WARPS * (16 * (L::hist + L::red) + 8 * L::vals));    // [WARPS][K][2 S]
+    float *bc = outs + WARPS * L::out;                                                             // [K][2 S]
     const Segment g = segment_of(a.cu_seqlens, a.N, a.T, a.seg, blockIdx.x);
-    if (lane == 0 && blockIdx.y == 0) check_sequence(a, blockIdx.x);
+    if (tid == 0 && blockIdx.y == 0) check_sequence(a, blockIdx.x);
     const int per = a.D / a.G, tiles = (per + L::CH - 1) / L::CH;
     const int grp = blockIdx.y / tiles, tile = blockIdx.y - grp * tiles;
-    const int at = tile * L::CH + 2 * cl, c = grp * per + (at < per ? at : 0);  // the thread's first channel
+    const int at = tile * L::CH + 2 * (warp * PAIRS + pl), c = grp * per + (at < per ? at : 0);  // the thread's first channel
     const bool one = at < per, two = at + 1 < per;
     const int c1 = two ? c + 1 : c;
     const size_t DS = (size_t)a.D * S;
@@ -108,7 +113,7 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
             A2[q][2 * i] = make_float2(v.x * kLog2e, v.y * kLog2e), A2[q][2 * i + 1] = make_float2(v.z * kLog2e, v.w * kLog2e);
             const float4 w = from && (q ? two : one) ? reinterpret_cast<const float4 *>(from + o)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
             carry[q][2 * i] = make_float2(w.x, w.y), carry[q][2 * i + 1] = make_float2(w.z, w.w);
-            dA[q][2 * i] = dA[q][2 * i + 1] = make_float2(0.f, 0.f);
+            dA[q][2 * i] = dA[q][2 * i + 1] = both(0.f);
         }
     }
     const float2 skip = a.Dskip ? make_float2(a.Dskip[c], a.Dskip[c1]) : both(0.f);
@@ -120,31 +125,28 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
     E *dxp = static_cast<E *>(a.dx) + c, *ddtp = static_cast<E *>(a.ddt) + c, *dzp = static_cast<E *>(a.dz) + c;
     const int count = g.s < 0 ? 0 : g.t1 - g.t0;
 
-    // the eight tokens before are brought into L2 while these are worked on
+    // the eight tokens from t on are brought into L2, while later ones are worked on
     auto ahead = [&](long long t) {
-        const int k = lane % K, what = lane / K, c0 = grp * per + tile * L::CH;
-        const E *rows[4] = {static_cast<const E *>(a.x), static_cast<const E *>(a.dt), static_cast<const E *>(a.dy), static_cast<const E *>(a.z)};
-        const long long strides[4] = {a.x_stride, a.dt_stride, a.dy_stride, a.z_stride};
-        const E *row = rows[0];
-        long long stride = strides[0];
-#pragma unroll
-        for (int j = 1; j < 4; ++j)
-            if (what == j) row = rows[j], stride = strides[j];
-        if (row) {
-#pragma unroll
-            for (int o = 0; o < L::CH; o += 128 / (int)sizeof(E))
-                if (tile * L::CH + o < per) prefetch(row + (t + k) * stride + c0 + o);
+        constexpr int LINE = 128 / (int)sizeof(E), LINES = (L::CH + LINE - 1) / LINE;
+        const int c0 = tile * L::CH;
+        for (int i = tid; i < 4 * K * LINES; i += kThreads) {
+            const int what = i / (K * LINES), k = i / LINES % K, o = c0 + i % LINES * LINE;
+            const void *base = what == 0 ? a.x : what == 1 ? a.dt : what == 2 ? a.dy : a.z;
+            const long long stride = what == 0 ? a.x_stride : what == 1 ? a.dt_stride : what == 2 ? a.dy_stride : a.z_stride;
+            if (base && o < per) prefetch(static_cast<const E *>(base) + (t + k) * stride + grp * per + o);
         }
-        if (what < 2) prefetch(what ? Cp + (t + k) * a.c_stride : Bp + (t + k) * a.b_stride);
-        if (lane * 32 < L::CH * S && tile * L::CH + lane * 32 / S < per)
-            prefetch(a.saved + (size_t)(g.slot + (t - g.t0) / K) * DS + (size_t)c0 * S + lane * 32);
+        if (tid < 2 * K) prefetch(tid < K ? Bp + (t + tid) * a.b_stride : Cp + (t + tid - K) * a.c_stride);
+        const float *st = a.saved + (size_t)(g.slot + (t - g.t0) / K) * DS + (size_t)(grp * per + c0) * S;
+        for (int i = tid * 32; i < L::CH * S; i += 32 * kThreads)
+            if (c0 + i / S < per) prefetch(st + i);
     };
 
     for (int i = (count + K - 1) / K - 1; i >= 0; --i) {
         const int t0 = g.t0 + i * K, rows = min(K, g.t1 - t0);
-        // the eight tokens' values, at this thread's own places: d, x, e, 1 - e^{-d}, dy sigma'(z)
+        // the tokens' values, dealt out to the lanes of a pair: d, x, e, d's derivative, dy sigma'(z)
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
+        for (int j = 0; j < OWN; ++j) {
+            const int k = ln * OWN + j;
             Pair<BF16> x, v, e, z;
             const bool in1 = one && k < rows, in2 = two && k < rows;
             const long long t = k < rows ? t0 + k : t0;
@@ -152,20 +154,18 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
             v.load(dtp + t * a.dt_stride, VEC, in2, in1);
             e.load(dyp + t * a.dy_stride, VEC, in2, in1);
             if (a.z) z.load(zp + t * a.z_stride, VEC, in2, in1);
-            v.v.x += bias.x, v.v.y += bias.y;
+            v.v = __fadd2_rn(v.v, bias);
             float2 d = v.v, s = both(1.f), dz = both(0.f);
-            if (a.dt_softplus) d = make_float2(softplus(v.v.x, &s.x), softplus(v.v.y, &s.y));
+            if (a.dt_softplus) d = softplus2(v.v, s);
             if (a.z) {
-                const float2 sg = make_float2(sigmoid(z.v.x), sigmoid(z.v.y));
-                dz = make_float2(e.v.x * (sg.x * fmaf(z.v.x, 1.f - sg.x, 1.f)), e.v.y * (sg.y * fmaf(z.v.y, 1.f - sg.y, 1.f)));
-                e.v = make_float2(e.v.x * (z.v.x * sg.x), e.v.y * (z.v.y * sg.y));
+                const float2 sg = sigmoid2(z.v);
+                dz = __fmul2_rn(e.v, dsilu2(z.v, sg));
+                e.v = __fmul2_rn(e.v, __fmul2_rn(z.v, sg));
             }
-            float2 *p = vals + k * 32 + lane;
-            p[0] = d, p[K * 32] = x.v, p[2 * K * 32] = e.v, p[3 * K * 32] = s, p[4 * K * 32] = dz;
+            float2 *p = vals + k * PAIRS + pl;
+            p[0] = d, p[K * PAIRS] = x.v, p[2 * K * PAIRS] = e.v, p[3 * K * PAIRS] = s, p[4 * K * PAIRS] = dz;
         }
-        if (i > 0) ahead(t0 - K);
-        __syncwarp();  // B and C of the previous tokens have been read
-        for (int n = lane; n < K * 2 * S; n += 32) {
+        for (int n = tid; n < K * 2 * S; n += kThreads) {
             const int k = n / (2 * S), m = n % (2 * S);
             const long long t = t0 + (k < rows ? k : 0);
             bc[n] = m < S ? (float)Bp[t * a.b_stride + m] : (float)Cp[t * a.c_stride + m - S];
@@ -180,22 +180,23 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                 h[q][2 * n] = make_float2(v.x, v.y), h[q][2 * n + 1] = make_float2(v.z, v.w);
             }
         }
-        __syncwarp();
+        if (i > 0) ahead(t0 - K);
+        __syncthreads();
         // forward, the states after tokens 0, 2, 4 and 6 kept
 #pragma unroll 1
         for (int k = 0; k < min(rows, K - 1); ++k) {
-            const float2 d = vals[k * 32 + lane], x = vals[(K + k) * 32 + lane];
+            const float2 d = vals[k * PAIRS + pl], x = vals[(K + k) * PAIRS + pl];
             const float4 *b4 = reinterpret_cast<const float4 *>(bc + k * 2 * S + ln * M);
+            const float2 dq[2] = {both(d.x), both(d.y)}, in[2] = {both(d.x * x.x), both(d.y * x.y)};
 #pragma unroll
             for (int n = 0; n < M / 4; ++n) {
                 const float4 B4 = b4[n];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float2 dq = both(q ? d.y : d.x), in = both(q ? d.y * x.y : d.x * x.x);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float2 arg = __fmul2_rn(A2[q][2 * n + e], dq), b = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
-                        h[q][2 * n + e] = __ffma2_rn(make_float2(exp2_fast(arg.x), exp2_fast(arg.y)), h[q][2 * n + e], __fmul2_rn(in, b));
+                        const float2 arg = __ffma2_rn(A2[q][2 * n + e], dq[q], both(kExp2Low)), b = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
+                        h[q][2 * n + e] = __ffma2_rn(make_float2(exp2_fast(arg.x), exp2_fast(arg.y)), h[q][2 * n + e], __fmul2_rn(in[q], b));
                     }
                     if ((k & 1) == 0)
                         hist[((k >> 1) * V4 + q * (M / 4) + n) * 32 + lane] =
@@ -203,10 +204,13 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                 }
             }
         }
-        // backward, two tokens to a kept state
-        auto back = [&](auto later, int k) {
+        float2 dAt[2][M / 2], dDt = both(0.f), dbt = both(0.f);
+#pragma unroll
+        for (int n = 0; n < M / 2; ++n) dAt[0][n] = dAt[1][n] = both(0.f);
+        // A token back: sums over the thread's states for (lB, lA, y) of both channels, and dB and dC.
+        auto back = [&](auto later, int k, float2 (&sums)[3]) {
             constexpr bool LATER = decltype(later)::value;
-            const float2 d = vals[k * 32 + lane], x = vals[(K + k) * 32 + lane], ev = vals[(2 * K + k) * 32 + lane];
+            const float2 d = vals[k * PAIRS + pl], x = vals[(K + k) * PAIRS + pl], ev = vals[(2 * K + k) * PAIRS + pl];
             const float4 *b4 = reinterpret_cast<const float4 *>(bc + k * 2 * S + ln * M), *c4 = b4 + S / 4;
             const float2 dq[2] = {both(d.x), both(d.y)}, in[2] = {both(d.x * x.x), both(d.y * x.y)}, eq[2] = {both(ev.x), both(ev.y)};
             const float2 minus[2] = {both(-in[0].x), both(-in[1].x)};
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                     const float4 H4 = hist[((k >> 1) * V4 + q * (M / 4) + n) * 32 + lane];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float2 A = A2[q][2 * n + e], arg = __fmul2_rn(A, dq[q]), dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
+                        const float2 A = A2[q][2 * n + e], arg = __ffma2_rn(A, dq[q], both(kExp2Low)), dec = make_float2(exp2_fast(arg.x), exp2_fast(arg.y));
                         const float2 B = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
                         const float2 C = e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y);
                         const float2 H = e ? make_float2(H4.z, H4.w) : make_float2(H4.x, H4.y);
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                         carry[q][2 * n + e] = __fmul2_rn(dec, l);
                         lB[q] = __ffma2_rn(l, B, lB[q]);
                         lA[q] = __ffma2_rn(u, A, lA[q]);
-                        dA[q][2 * n + e] = __ffma2_rn(dq[q], u, dA[q][2 * n + e]);
+                        dAt[q][2 * n + e] = __ffma2_rn(dq[q], u, dAt[q][2 * n + e]);
                         y[q] = __ffma2_rn(C, hk, y[q]);
                         sB[e] = q ? __ffma2_rn(l, in[q], sB[e]) : __fmul2_rn(l, in[q]);
                         sC[e] = q ? __ffma2_rn(hk, eq[q], sC[e]) : __fmul2_rn(hk, eq[q]);
@@ -240,9 +244,12 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                 red[n * 32 + lane] = make_float4(sB[0].x, sB[0].y, sB[1].x, sB[1].y);
                 red[(M / 4 + n) * 32 + lane] = make_float4(sC[0].x, sC[0].y, sC[1].x, sC[1].y);
             }
+            sums[0] = make_float2(lB[0].x + lB[0].y, lB[1].x + lB[1].y);
+            sums[1] = make_float2(lA[0].x + lA[0].y, lA[1].x + lA[1].y);
+            sums[2] = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
             __syncwarp();
-            // Row v of `red` is four outputs of all lanes.  A lane adds up a row over the PART lanes of its
-            // part (rotated, so that eight neighbours read eight places), and parts of one ln are joined.
+            // Row v of `red` is four outputs of all lanes.  A lane adds up a row over the PART lanes of its part
+            // (rotated, so that eight neighbours read eight places), and parts of one ln are joined.
             {
                 constexpr int PARTS = 32 / V4, PART = 32 / PARTS, JOIN = PARTS / LN;
                 const int v = lane / PARTS, part = lane % PARTS;
@@ -250,12 +257,12 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                 float2 f0 = both(0.f), f1 = both(0.f);
 #pragma unroll
                 for (int j = 0; j < PART; ++j) {
-                    const float4 w = p[(j + lane) % PART];
+                    const float4 w = p[(j + (part >> 1)) % PART];
                     f0 = __fadd2_rn(f0, make_float2(w.x, w.y)), f1 = __fadd2_rn(f1, make_float2(w.z, w.w));
                 }
-                // output n of the lane's part: B for rows below M / 4, C above
+                // outputs of the lane's part: B for rows below M / 4, C above
                 const int which = v >= M / 4, n0 = (part / JOIN) * M + (v - which * (M / 4)) * 4;
-                float *out = a.bc_parts + (((size_t)tile * a.T + t0 + k) * a.G + grp) * (2 * S) + which * S + n0;
+                float *out = outs + (warp * K + k) * 2 * S + which * S + n0;
                 if constexpr (JOIN >= 2) {  // two lanes: each keeps two of the four
                     const bool up = part & 1;
                     const float2 send = up ? f0 : f1;
@@ -272,51 +279,83 @@ __global__ void __launch_bounds__(32) kda_scan_bwd_kernel(ScanArgs a) {
                         out[up ? 2 : 0] = mine.x, out[up ? 3 : 1] = mine.y;
                     }
                 } else {
-                    out[0] = f0.x, out[1] = f0.y, out[2] = f1.x, out[3] = f1.y;
-                }
-            }
-            // the token's own gradients
-            float sB0 = lB[0].x + lB[0].y, sB1 = lB[1].x + lB[1].y, sA0 = lA[0].x + lA[0].y, sA1 = lA[1].x + lA[1].y;
-            float y0 = y[0].x + y[0].y, y1 = y[1].x + y[1].y;
-#pragma unroll
-            for (int o = L::PAIRS; o < 32; o <<= 1) {
-                sB0 += __shfl_xor_sync(0xffffffffu, sB0, o), sB1 += __shfl_xor_sync(0xffffffffu, sB1, o);
-                sA0 += __shfl_xor_sync(0xffffffffu, sA0, o), sA1 += __shfl_xor_sync(0xffffffffu, sA1, o);
-                y0 += __shfl_xor_sync(0xffffffffu, y0, o), y1 += __shfl_xor_sync(0xffffffffu, y1, o);
-            }
-            const float2 sg = vals[(3 * K + k) * 32 + lane];
-            const float2 dx = make_float2(fmaf(d.x, sB0, skip.x * ev.x), fmaf(d.y, sB1, skip.y * ev.y));
-            const float2 dd = make_float2(fmaf(x.x, sB0, kLn2 * sA0) * sg.x, fmaf(x.y, sB1, kLn2 * sA1) * sg.y);
-            dD.x = fmaf(ev.x, x.x, dD.x), dD.y = fmaf(ev.y, x.y, dD.y);
-            dbias.x += dd.x, dbias.y += dd.y;
-            if (ln == 0) {
-                const size_t t = (size_t)(t0 + k) * a.D;
-                Pair<BF16>::store(dxp + t, dx, VEC, two, one);
-                Pair<BF16>::store(ddtp + t, dd, VEC, two, one);
-                if (a.z) {
-                    const float2 dz = vals[(4 * K + k) * 32 + lane];
-                    Pair<BF16>::store(dzp + t, make_float2(dz.x * fmaf(skip.x, x.x, y0), dz.y * fmaf(skip.y, x.y, y1)), VEC, two, one);
+                    *reinterpret_cast<float4 *>(out) = make_float4(f0.x, f0.y, f1.x, f1.y);
                 }
             }
             __syncwarp();  // `red` has been read
         };
+        // a token's own gradients, from its sums over all states
+        auto finish = [&](int k, const float2 (&sums)[3]) {
+            const float2 *p = vals + k * PAIRS + pl;
+            const float2 d = p[0], x = p[K * PAIRS], ev = p[2 * K * PAIRS], sg = p[3 * K * PAIRS], dz = p[4 * K * PAIRS];
+            const float2 dx = __ffma2_rn(d, sums[0], __fmul2_rn(skip, ev));
+            const float2 dd = __fmul2_rn(__ffma2_rn(x, sums[0], __fmul2_rn(both(kLn2), sums[1])), sg);
+            dDt = __ffma2_rn(ev, x, dDt);
+            dbt = __fadd2_rn(dbt, dd);
+            const size_t t = (size_t)(t0 + k) * a.D;
+            Pair<BF16>::store(dxp + t, dx, VEC, two, one);
+            Pair<BF16>::store(ddtp + t, dd, VEC, two, one);
+            if (a.z) Pair<BF16>::store(dzp + t, __fmul2_rn(dz, __ffma2_rn(skip, x, sums[2])), VEC, two, one);
+        };
 #pragma unroll 1
         for (int k = (rows - 1) & ~1; k >= 0; k -= 2) {
-            if (k + 1 < rows) back(std::true_type(), k + 1);
-            back(std::false_type(), k);
+            const bool pair = k + 1 < rows;
+            float2 late[3], early[3];
+            if (pair) {
+                back(std::true_type(), k + 1, late);
+                if constexpr (LN == 1) finish(k + 1, late);
+            } else {
+                late[0] = late[1] = late[2] = both(0.f);
+            }
+            back(std::false_type(), k, early);
+            if constexpr (LN == 1) {
+                finish(k, early);
+            } else {
+                // the upper half of a pair's lanes takes the later token, the lower half the earlier one
+                const bool up = lane & 16;
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    const float2 send = up ? early[j] : late[j], keep = up ? late[j] : early[j];
+                    late[j] = make_float2(keep.x + __shfl_xor_sync(0xffffffffu, send.x, 16), keep.y + __shfl_xor_sync(0xffffffffu, send.y, 16));
+#pragma unroll
+                    for (int o = 8; o >= PAIRS; o >>= 1)
+                        late[j] = make_float2(late[j].x + __shfl_xor_sync(0xffffffffu, late[j].x, o),
+                                              late[j].y + __shfl_xor_sync(0xffffffffu, late[j].y, o));
+                }
+                if (ln % (LN / 2) == 0 && (pair || !up)) finish(k + up, late);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < M / 2; ++n) dA[0][n] = __fadd2_rn(dA[0][n], dAt[0][n]), dA[1][n] = __fadd2_rn(dA[1][n], dAt[1][n]);
+        dD = __fadd2_rn(dD, dDt), dbias = __fadd2_rn(dbias, dbt);
+        __syncthreads();
+        for (int n = tid; n < rows * 2 * S; n += kThreads) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) s += outs[w * L::out + n];
+            const int k = n / (2 * S), m = n % (2 * S);
+            a.bc_parts[(((size_t)tile * a.T + t0 + k) * a.G + grp) * (2 * S) + m] = s;
         }
     }
     // the unit's sums, zero where it has no tokens
-    float *parts = a.parts + blockIdx.x * (DS + 2 * (size_t)a.D);
+    if constexpr (LN > 1) {
+#pragma unroll
+        for (int o = 16; o >= PAIRS; o >>= 1) {
+            dD.x += __shfl_xor_sync(0xffffffffu, dD.x, o), dD.y += __shfl_xor_sync(0xffffffffu, dD.y, o);
+            dbias.x += __shfl_xor_sync(0xffffffffu, dbias.x, o), dbias.y += __shfl_xor_sync(0xffffffffu, dbias.y, o);
+        }
+    }
+    float *parts = a.parts + blockIdx.x * scan_parts_width(a.D, S);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         if (!(q ? two : one)) continue;
         const size_t o = (size_t)(c + q) * S + ln * M;
 #pragma unroll
-        for (int n = 0; n < M / 2; ++n) *reinterpret_cast<float2 *>(parts + o + 2 * n) = dA[q][n];
-        if (g.first && a.dstate) {
-#pragma unroll
-            for (int n = 0; n < M / 2; ++n) *reinterpret_cast<float2 *>(a.dstate + g.s * DS + o + 2 * n) = carry[q][n];
+        for (int n = 0; n < M / 4; ++n) {
+            *reinterpret_cast<float4 *>(parts + o + 4 * n) = make_float4(dA[q][2 * n].x, dA[q][2 * n].y, dA[q][2 * n + 1].x, dA[q][2 * n + 1].y);
+            if (g.first && a.dstate)
+                *reinterpret_cast<float4 *>(a.dstate + g.s * DS + o + 4 * n) =
+                    make_float4(carry[q][2 * n].x, carry[q][2 * n].y, carry[q][2 * n + 1].x, carry[q][2 * n + 1].y);
         }
         if (ln == 0) parts[DS + c + q] = q ? dD.y : dD.x, parts[DS + a.D + c + q] = q ? dbias.y : dbias.x;
     }
@@ -355,13 +394,17 @@ cudaError_t launch_s(const ScanArgs &a, cudaStream_t st) {
     using L = Layout<S>;
     auto kern = a.wide ? kda_scan_bwd_kernel<BF16, S, true> : kda_scan_bwd_kernel<BF16, S, false>;
     const int per = a.D / a.G, tiles = (per + L::CH - 1) / L::CH;
-    kern<<<dim3(scan_units(a.N, a.T, a.seg), a.G * tiles), 32, L::bytes, st>>>(a);
+    if (L::bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<dim3(scan_units(a.N, a.T, a.seg), a.G * tiles), kThreads, L::bytes, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int scan_bwd_channels(int S) { return S > 16 ? 64 * 16 / S : 64; }
+int scan_bwd_channels(int S) { return 2 * kThreads * 8 / S; }
 
 cudaError_t launch_scan_bwd(const ScanArgs &a, int S, bool bf16, cudaStream_t st) {
     switch (S) {
