@@ -95,8 +95,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // 1.0e-6), and the argument is a product that takes an addend for nothing.
 constexpr float kExp2Low = 0.25f * 5.9604645e-8f * 1.4426950f;
 
-// 1 / (1 + e^-x): the quotient of a sum past 2^126 comes out 0, as it should
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// (of 2^126 and more: 0)
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + e^-x): past e^-x = 2^126 it comes out 0, as it should
+__device__ __forceinline__ float sigmoid(float x) { return rcp_fast(1.f + __expf(-x)); }
 // x sigmoid(x); -inf gives NaN, as the product does
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
@@ -105,7 +112,7 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
     const float2 t = __fmul2_rn(x, both(-1.4426950408889634f));
     const float2 d = __fadd2_rn(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
-    return make_float2(__fdividef(1.f, d.x), __fdividef(1.f, d.y));
+    return make_float2(rcp_fast(d.x), rcp_fast(d.y));
 }
 __device__ __forceinline__ float2 silu2(float2 x) { return __fmul2_rn(x, sigmoid2(x)); }
 // its derivative, from x and its sigmoid
@@ -129,7 +136,7 @@ __device__ __forceinline__ float2 softplus2(float2 v, float2 &sig) {
     float2 e = make_float2(exp2_fast(hi.x), exp2_fast(hi.y));
     e = __ffma2_rn(e, __fmul2_rn(lo, both(0.6931471805599453f)), e);
     const float2 below = __fadd2_rn(e, both(2.f)), one = __fadd2_rn(e, both(1.f));
-    const float2 q = make_float2(__fdividef(e.x, below.x), __fdividef(e.y, below.y)), w = __fmul2_rn(q, q);
+    const float2 q = __fmul2_rn(e, make_float2(rcp_fast(below.x), rcp_fast(below.y))), w = __fmul2_rn(q, q);
     // (seven terms: the next one is below 2^-26 of the sum)
     float2 s = __ffma2_rn(w, both(1.f / 13.f), both(1.f / 11.f));
     s = __ffma2_rn(w, s, both(1.f / 9.f));
@@ -137,7 +144,7 @@ __device__ __forceinline__ float2 softplus2(float2 v, float2 &sig) {
     s = __ffma2_rn(w, s, both(1.f / 5.f));
     s = __ffma2_rn(w, s, both(1.f / 3.f));
     s = __ffma2_rn(w, s, both(1.f));
-    sig = make_float2(__fdividef(v.x >= 0.f ? 1.f : e.x, one.x), __fdividef(v.y >= 0.f ? 1.f : e.y, one.y));
+    sig = __fmul2_rn(make_float2(v.x >= 0.f ? 1.f : e.x, v.y >= 0.f ? 1.f : e.y), make_float2(rcp_fast(one.x), rcp_fast(one.y)));
     return __ffma2_rn(__fadd2_rn(q, q), s, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 __device__ __forceinline__ float softplus(float v) {

@@ -50,28 +50,25 @@ struct Layout {
     static constexpr int bytes = WARPS * (16 * (hist + red) + 8 * vals + 4 * out) + 4 * out;
 };
 
-template <bool BF16>
+// two neighbouring channels of a row, of which `one` and `two` say which are there
+template <bool BF16, bool VEC>
 struct Pair {
-    float2 v;
-    __device__ __forceinline__ void load(const Elem<BF16> *p, bool vec, bool two, bool one) {
-        v = make_float2(0.f, 0.f);
-        if (vec) {
-            if (!one) return;
-            Vec<BF16, 2> r;
-            r.load(p);
-            v = make_float2(r.get(0), r.get(1));
+    Vec<BF16, 2> r;
+    __device__ __forceinline__ void load(const Elem<BF16> *p, bool one, bool two) {
+        if constexpr (VEC) {
+            if (one) r.load(p);
+            else r.zero();
         } else {
-            if (one) v.x = (float)p[0];
-            if (two) v.y = (float)p[1];
+            const float f[2] = {one ? (float)p[0] : 0.f, two ? (float)p[1] : 0.f};
+            r.set(f);
         }
     }
-    static __device__ __forceinline__ void store(Elem<BF16> *p, float2 v, bool vec, bool two, bool one) {
-        if (vec) {
-            if (!one) return;
+    __device__ __forceinline__ float2 get() const { return r.pair(0); }
+    static __device__ __forceinline__ void store(Elem<BF16> *p, float2 v, bool one, bool two) {
+        if constexpr (VEC) {
             Vec<BF16, 2> r;
-            const float f[2] = {v.x, v.y};
-            r.set(f);
-            r.store(p);
+            r.set_pair(0, v);
+            if (one) r.store(p);
         } else {
             if (one) p[0] = (Elem<BF16>)v.x;
             if (two) p[1] = (Elem<BF16>)v.y;
@@ -119,8 +116,6 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
     const float2 skip = a.Dskip ? make_float2(a.Dskip[c], a.Dskip[c1]) : both(0.f);
     const float2 bias = a.dt_bias ? make_float2(a.dt_bias[c], a.dt_bias[c1]) : both(0.f);
     float2 dD = both(0.f), dbias = both(0.f);
-    const E *xp = static_cast<const E *>(a.x) + c, *dtp = static_cast<const E *>(a.dt) + c;
-    const E *zp = static_cast<const E *>(a.z) + c, *dyp = static_cast<const E *>(a.dy) + c;
     const E *Bp = static_cast<const E *>(a.B) + (size_t)grp * S, *Cp = static_cast<const E *>(a.C) + (size_t)grp * S;
     E *dxp = static_cast<E *>(a.dx) + c, *ddtp = static_cast<E *>(a.ddt) + c, *dzp = static_cast<E *>(a.dz) + c;
     const int count = g.s < 0 ? 0 : g.t1 - g.t0;
@@ -141,34 +136,49 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
             if (c0 + i / S < per) prefetch(st + i);
     };
 
-    for (int i = (count + K - 1) / K - 1; i >= 0; --i) {
+    // a lane's own tokens of the eight from t0 on: dt, x, dy and z as they come, asked for eight tokens ahead
+    Pair<BF16, VEC> raw[4][OWN];
+    auto load = [&](int t0, int rows) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w == 3 && !a.z) continue;
+            const long long stride = w == 0 ? a.dt_stride : w == 1 ? a.x_stride : w == 2 ? a.dy_stride : a.z_stride;
+            const E *p = static_cast<const E *>(w == 0 ? a.dt : w == 1 ? a.x : w == 2 ? a.dy : a.z) + c + (long long)(t0 + ln * OWN) * stride;
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) raw[w][j].load(p + j * stride, one && ln * OWN + j < rows, two && ln * OWN + j < rows);
+        }
+    };
+    const int last = (count + K - 1) / K - 1;
+    if (last >= 0) load(g.t0 + last * K, count - last * K);
+    for (int i = last; i >= 0; --i) {
         const int t0 = g.t0 + i * K, rows = min(K, g.t1 - t0);
         // the tokens' values, dealt out to the lanes of a pair: d, x, e, d's derivative, dy sigma'(z)
 #pragma unroll
         for (int j = 0; j < OWN; ++j) {
-            const int k = ln * OWN + j;
-            Pair<BF16> x, v, e, z;
-            const bool in1 = one && k < rows, in2 = two && k < rows;
-            const long long t = k < rows ? t0 + k : t0;
-            x.load(xp + t * a.x_stride, VEC, in2, in1);
-            v.load(dtp + t * a.dt_stride, VEC, in2, in1);
-            e.load(dyp + t * a.dy_stride, VEC, in2, in1);
-            if (a.z) z.load(zp + t * a.z_stride, VEC, in2, in1);
-            v.v = __fadd2_rn(v.v, bias);
-            float2 d = v.v, s = both(1.f), dz = both(0.f);
-            if (a.dt_softplus) d = softplus2(v.v, s);
+            const float2 v = __fadd2_rn(raw[0][j].get(), bias), x = raw[1][j].get();
+            float2 e = raw[2][j].get(), d = v, s = both(1.f), dz = both(0.f);
+            if (a.dt_softplus) d = softplus2(v, s);
             if (a.z) {
-                const float2 sg = sigmoid2(z.v);
-                dz = __fmul2_rn(e.v, dsilu2(z.v, sg));
-                e.v = __fmul2_rn(e.v, __fmul2_rn(z.v, sg));
+                const float2 z = raw[3][j].get(), sg = sigmoid2(z);
+                dz = __fmul2_rn(e, dsilu2(z, sg));
+                e = __fmul2_rn(e, __fmul2_rn(z, sg));
             }
-            float2 *p = vals + k * PAIRS + pl;
-            p[0] = d, p[K * PAIRS] = x.v, p[2 * K * PAIRS] = e.v, p[3 * K * PAIRS] = s, p[4 * K * PAIRS] = dz;
+            float2 *p = vals + (ln * OWN + j) * PAIRS + pl;
+            p[0] = d, p[K * PAIRS] = x, p[2 * K * PAIRS] = e, p[3 * K * PAIRS] = s, p[4 * K * PAIRS] = dz;
         }
-        for (int n = tid; n < K * 2 * S; n += kThreads) {
+        if (i > 0) load(t0 - K, K);
+        for (int n = 4 * tid; n < K * 2 * S; n += 4 * kThreads) {
             const int k = n / (2 * S), m = n % (2 * S);
             const long long t = t0 + (k < rows ? k : 0);
-            bc[n] = m < S ? (float)Bp[t * a.b_stride + m] : (float)Cp[t * a.c_stride + m - S];
+            const E *p = m < S ? Bp + t * a.b_stride + m : Cp + t * a.c_stride + m - S;
+            Vec<BF16, 4> v;
+            if (a.wide_bc) {
+                v.load(p);
+            } else {
+                const float f[4] = {(float)p[0], (float)p[1], (float)p[2], (float)p[3]};
+                v.set(f);
+            }
+            *reinterpret_cast<float4 *>(bc + n) = make_float4(v.get(0), v.get(1), v.get(2), v.get(3));
         }
         float2 h[2][M / 2];
 #pragma unroll
@@ -180,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
                 h[q][2 * n] = make_float2(v.x, v.y), h[q][2 * n + 1] = make_float2(v.z, v.w);
             }
         }
-        if (i > 0) ahead(t0 - K);
+        if (i > 1) ahead(t0 - 2 * K);
         __syncthreads();
         // forward, the states after tokens 0, 2, 4 and 6 kept
 #pragma unroll 1
@@ -292,10 +302,10 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
             const float2 dd = __fmul2_rn(__ffma2_rn(x, sums[0], __fmul2_rn(both(kLn2), sums[1])), sg);
             dDt = __ffma2_rn(ev, x, dDt);
             dbt = __fadd2_rn(dbt, dd);
-            const size_t t = (size_t)(t0 + k) * a.D;
-            Pair<BF16>::store(dxp + t, dx, VEC, two, one);
-            Pair<BF16>::store(ddtp + t, dd, VEC, two, one);
-            if (a.z) Pair<BF16>::store(dzp + t, __fmul2_rn(dz, __ffma2_rn(skip, x, sums[2])), VEC, two, one);
+            const size_t at = (size_t)(t0 + k) * a.D + c;
+            Pair<BF16, VEC>::store(static_cast<E *>(a.dx) + at, dx, one, two);
+            Pair<BF16, VEC>::store(static_cast<E *>(a.ddt) + at, dd, one, two);
+            if (a.z) Pair<BF16, VEC>::store(static_cast<E *>(a.dz) + at, __fmul2_rn(dz, __ffma2_rn(skip, x, sums[2])), one, two);
         };
 #pragma unroll 1
         for (int k = (rows - 1) & ~1; k >= 0; k -= 2) {
