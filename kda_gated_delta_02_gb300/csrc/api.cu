@@ -1624,7 +1624,7 @@ static int scan_segment(int N, int T, int D, int G, int S, bool backward) {
         seg = 4LL * T / N;
         if (seg < 1024) seg = 1024;
     } else {
-        const long long parts = tiles < 8LL * sms ? 8LL * sms / tiles : 1;
+        const long long parts = tiles < 16LL * sms ? 16LL * sms / tiles : 1;
         seg = (T + parts - 1) / parts;
         if (seg < 128) seg = 128;
     }
