@@ -1521,7 +1521,7 @@ int kda_conv_fwd(const void *x, const int32_t *cu_seqlens, const float *w, const
     a.x_stride = x_stride; a.tail_stride = tail_stride; a.y_stride = y_stride; a.tail_out_stride = tail_out_stride;
     a.N = N; a.T = T; a.C = C; a.act = conv_act == KDA_CONV_SILU; a.status = status;
     a.wide = all_on16(r) && (long long)C * e % 16 == 0;
-    a.run = kda::conv_run(T, C, a.wide ? 16 / e : 1, false, sm_count());
+    a.run = kda::conv_run(T, C, a.wide ? 4 : 1, false, sm_count());
     a.runs = (T + a.run - 1) / a.run;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(timed_launch(KDA_KERNEL_CONV, st, [&] { return kda::launch_conv(a, W, 0, bf16, bf16, st); }));

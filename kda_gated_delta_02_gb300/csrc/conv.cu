@@ -7,13 +7,16 @@
 //   q_t = dy_t y'(p_t),  dx_e = sum_k w[c][W - 1 - k] q_{e + k} (same sequence) + what the new tail passes back
 //   dw[c][j] = sum_t q_t x_{t - (W - 1) + j},  dbias = sum_t q_t
 //
-// What bounds it: bytes (x in, y out; backward x and dy in, dx out).  A thread
-// owns V neighbouring channels (16 bytes of the forward's row) and walks a run
-// of tokens, with the W - 1 rows behind it in registers; only those are read
-// twice, once per run (W - 1 rows in a run of 16 to 128, and the neighbouring
-// run has them in L2).  Runs do not stop at sequence ends, so short sequences
+// What bounds it: bytes (x in, y out; backward x and dy in, dx out), once the
+// instructions are few enough: about 10 per element forward, 19 backward, in packed pairs of
+// channels.  A thread owns four neighbouring channels and walks a run of tokens, with the
+// W - 1 rows behind it in registers and the next four rows asked for; only
+// W - 1 rows of a run of 8 to 128 are read twice, and the neighbouring run has
+// them in L2.  (Eight channels a thread had 118 registers and half the warps: 149 us
+// for 16384 tokens x 8192 channels.)  Runs do not stop at sequence ends, so short sequences
 // cost no threads: where one ends the window is filled from the next one's
-// tail.  The backward walks W - 1 tokens past its run, for the gradients that
+// tail, token by token; four tokens of one sequence go without such checks.
+// The backward walks W - 1 tokens past its run, for the gradients that
 // reach back into it.  Its sums for dw leave as one partial row per run and are
 // added up in a fixed order.
 #include <cuda_runtime.h>
@@ -27,6 +30,7 @@ namespace {
 using namespace layer;
 
 constexpr int kThreads = 128;
+constexpr int U = 4;          // rows asked for while as many are worked on
 constexpr int kTailRows = 8;  // sequences of a block that writes tails
 
 // the sequence a walk is in: tokens [a, b), b past the walk's end once there is none
@@ -41,7 +45,7 @@ __device__ __forceinline__ Walk next_sequence(const int32_t *cu, int N, int T, i
         const int a = cu[s], b = cu[s + 1];
         if (a >= 0 && a < b && b <= T && b > t) return {s, a, b};
     }
-    return {N, 0x7fffffff, 0x7fffffff};
+    return {N, 0x7fff0000, 0x7fff0000};  // past any T, with room for sums
 }
 
 // a row of pairs of channels, as loaded from p or zero
@@ -133,34 +137,55 @@ __global__ void __launch_bounds__(kThreads) kda_conv_fwd_kernel(ConvArgs a) {
         }
     };
     if (q.a <= ta) fill(ta);
-    constexpr int U = 4;  // rows in flight
-    for (int t0 = ta; t0 < tb; t0 += U) {
-        Vec<BF16, V> next[U];
+    // the output of the row that win[W - 1] holds, and the window moved on
+    auto token = [&](int t) {
+        Vec<BF16, V> out;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float2 p = bias[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j][i], p);
+            out.set_pair(i, a.act ? silu2(p) : p);
+        }
+        out.store(y + (long long)t * a.y_stride);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i];
+    };
+    Vec<BF16, V> next[U];
+    auto ask = [&](int t0) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (t0 + u < tb) next[u].load(x + (long long)(t0 + u) * a.x_stride);
+    };
+    ask(ta);
+#pragma unroll 1
+    for (int t0 = ta; t0 < tb; t0 += U) {
+        Vec<BF16, V> now[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + u;
-            if (t >= tb) break;
-            if (t >= q.b) {
-                q = next_sequence(a.cu_seqlens, a.N, a.T, q.s + 1, t);
-                if (q.a < t) fill(t);
+        for (int u = 0; u < U; ++u) now[u] = next[u];
+        ask(t0 + U);
+        if (q.a <= t0 && t0 + U <= min(tb, q.b)) {  // all of one sequence
+            if (t0 == q.a && t0 > ta) fill(t0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) win[W - 1][i] = now[u].pair(i);
+                token(t0 + u);
             }
-            if (t < q.a) continue;  // rows of no sequence
-            if (t == q.a && t > ta) fill(t);
-            Vec<BF16, V> out;
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                win[W - 1][i] = next[u].pair(i);
-                float2 p = bias[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j][i], p);
-                out.set_pair(i, a.act ? silu2(p) : p);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+        } else {
+#pragma unroll 1
+            for (int t = t0; t < min(t0 + U, tb); ++t) {
+                if (t >= q.b) {
+                    q = next_sequence(a.cu_seqlens, a.N, a.T, q.s + 1, t);
+                    if (q.a < t) fill(t);
+                }
+                if (t < q.a) continue;  // rows of no sequence
+                if (t == q.a && t > ta) fill(t);
+                load_pairs<BF16, V>(win[W - 1], x + (long long)t * a.x_stride, true);
+                token(t);
             }
-            out.store(y + (long long)t * a.y_stride);
         }
     }
 }
@@ -257,53 +282,83 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
             for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i], g[j][i] = g[j + 1][i];
     };
     if (q.a <= ta) fill(ta);
-    constexpr int U = 4;
+    // q of the token whose row win[W - 1] holds, from its dy in g[W - 1]
+    auto token = [&](bool own) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float2 d = g[W - 1][i];
+            if (a.act) {
+                float2 p = bias[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j][i], p);
+                d = __fmul2_rn(d, dsilu2(p, sigmoid2(p)));
+            }
+            g[W - 1][i] = d;
+            if (own) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[i][j] = __ffma2_rn(d, win[j][i], dw[i][j]);
+                db[i] = __fadd2_rn(db[i], d);
+            }
+        }
+    };
     const int end = min(tb + W - 1, a.T);  // the walk's own tokens end at tb
-    for (int t0 = ta; t0 < end; t0 += U) {
-        Vec<BF16, V> next[U];
-        Vec<DYBF16, V> dnext[U];
+    Vec<BF16, V> next[U];
+    Vec<DYBF16, V> dnext[U];
+    auto ask = [&](int t0) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t0 + u < end) {
+            if (t0 + u < tb) {
                 next[u].load(x + (long long)(t0 + u) * a.x_stride);
                 dnext[u].load(dy + (long long)(t0 + u) * a.dy_stride);
             }
+    };
+    ask(ta);
+#pragma unroll 1
+    for (int t0 = ta; t0 < end; t0 += U) {
+        Vec<BF16, V> now[U];
+        Vec<DYBF16, V> dnow[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + u;
-            if (t >= end) break;
-            if (t >= q.b) {
-                q = next_sequence(a.cu_seqlens, a.N, a.T, q.s + 1, t);
-                if (q.a < t) fill(t);
-            }
-            if (t < q.a || (t >= tb && q.a >= tb)) continue;  // rows of no sequence, or of one after the run's
-            if (t == q.a && t > ta) fill(t);
+        for (int u = 0; u < U; ++u) now[u] = next[u], dnow[u] = dnext[u];
+        ask(t0 + U);
+        if (max(ta, q.a) + W - 1 <= t0 && t0 + U <= tb && t0 + U < q.b) {  // all of one sequence and the run, and what they emit
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                win[W - 1][i] = next[u].pair(i);
-                float2 d = dnext[u].pair(i);
-                if (a.act) {
-                    float2 p = bias[i];
+            for (int u = 0; u < U; ++u) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j][i], p);
-                    d = __fmul2_rn(d, dsilu2(p, sigmoid2(p)));
+                for (int i = 0; i < P; ++i) win[W - 1][i] = now[u].pair(i), g[W - 1][i] = dnow[u].pair(i);
+                token(true);
+                Vec<BF16, V> out;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    float2 o = both(0.f);
+#pragma unroll
+                    for (int k = 0; k < W; ++k) o = __ffma2_rn(w[i][W - 1 - k], g[k][i], o);
+                    out.set_pair(i, o);
                 }
-                g[W - 1][i] = d;
-                if (t < tb) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[i][j] = __ffma2_rn(d, win[j][i], dw[i][j]);
-                    db[i] = __fadd2_rn(db[i], d);
-                }
+                out.store(dx + (long long)(t0 + u - (W - 1)) * a.dx_stride);
+                shift();
             }
-            emit(t - (W - 1), -1);
-            shift();
-            if (t == q.b - 1) {  // nothing follows: the last W - 1 rows
+        } else {
+#pragma unroll 1
+            for (int t = t0; t < min(t0 + U, end); ++t) {
+                if (t >= q.b) {
+                    q = next_sequence(a.cu_seqlens, a.N, a.T, q.s + 1, t);
+                    if (q.a < t) fill(t);
+                }
+                if (t < q.a || (t >= tb && q.a >= tb)) continue;  // rows of no sequence, or of one after the run's
+                if (t == q.a && t > ta) fill(t);
+                load_pairs<BF16, V>(win[W - 1], x + (long long)t * a.x_stride, true);
+                load_pairs<DYBF16, V>(g[W - 1], dy + (long long)t * a.dy_stride, true);
+                token(t < tb);
+                emit(t - (W - 1), -1);
+                shift();
+                if (t == q.b - 1) {  // nothing follows: the last W - 1 rows
+#pragma unroll 1
+                    for (int j = 0; j < W - 1; ++j) {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-#pragma unroll
-                    for (int i = 0; i < P; ++i) g[W - 1][i] = both(0.f);
-                    emit(t - (W - 1) + 1 + j, j);
-                    shift();
+                        for (int i = 0; i < P; ++i) g[W - 1][i] = both(0.f);
+                        emit(t - (W - 1) + 1 + j, j);
+                        shift();
+                    }
                 }
             }
         }
@@ -358,7 +413,7 @@ cudaError_t launch_w(const ConvArgs &a, int what, bool bf16, bool dy_bf16, cudaS
     auto tiles = [&](int v) { return (unsigned)((a.C + kThreads * v - 1) / (kThreads * v)); };
     const unsigned gx = (unsigned)(a.runs + (a.N + kTailRows - 1) / kTailRows);
     if (what == 0) {
-        if (bf16 && a.wide) kda_conv_fwd_kernel<true, 8, W><<<dim3(gx, tiles(8)), kThreads, 0, st>>>(a);
+        if (bf16 && a.wide) kda_conv_fwd_kernel<true, 4, W><<<dim3(gx, tiles(4)), kThreads, 0, st>>>(a);
         else if (bf16) kda_conv_fwd_kernel<true, 1, W><<<dim3(gx, tiles(1)), kThreads, 0, st>>>(a);
         else if (a.wide) kda_conv_fwd_kernel<false, 4, W><<<dim3(gx, tiles(4)), kThreads, 0, st>>>(a);
         else kda_conv_fwd_kernel<false, 1, W><<<dim3(gx, tiles(1)), kThreads, 0, st>>>(a);

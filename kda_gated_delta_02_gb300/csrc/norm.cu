@@ -24,22 +24,33 @@ namespace kda {
 namespace {
 using namespace layer;
 
-// the sum of x over the THREADS threads of a row; every one of them gets it.
-// Rows of more than a warp: one row per block at a time, buf holds a sum per warp.
-template <int THREADS>
-__device__ __forceinline__ float row_sum(float x, float *buf) {
+// the sums of x[..] over the THREADS threads of a row; every one of them gets
+// them.  Rows of more than a warp: one row per block at a time; buf holds a
+// sum per warp, in two places by turns, so that one barrier is enough.
+template <int THREADS, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], float (*buf)[N][THREADS > 32 ? THREADS / 32 : 4], int &turn) {
 #pragma unroll
-    for (int o = (THREADS < 32 ? THREADS : 32) / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int o = (THREADS < 32 ? THREADS : 32) / 2; o > 0; o >>= 1) x[k] += __shfl_xor_sync(0xffffffffu, x[k], o);
     if constexpr (THREADS > 32) {
-        const int warp = threadIdx.x >> 5;
-        __syncthreads();  // the previous sum has been read
-        if ((threadIdx.x & 31) == 0) buf[warp] = x;
-        __syncthreads();
-        x = 0.f;
+        if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-        for (int i = 0; i < THREADS / 32; ++i) x += buf[i];
+            for (int k = 0; k < N; ++k) buf[turn][k][threadIdx.x >> 5] = x[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float2 s = both(0.f);
+#pragma unroll
+            for (int i = 0; i < THREADS / 32; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(&buf[turn][k][i]);
+                s = __fadd2_rn(s, __fadd2_rn(make_float2(v.x, v.y), make_float2(v.z, v.w)));
+            }
+            x[k] = s.x + s.y;
+        }
+        turn ^= 1;
     }
-    return x;
 }
 
 // rows of a block at a time.  (A row of 32 threads or fewer shares a block
@@ -63,61 +74,109 @@ struct Row {
     }
 };
 
+// A thread's channels of a weight or bias: in registers where they are few,
+// read again for every row (from L1) where a row takes many.
+template <int V, int THREADS, int ITERS>
+struct Channels {
+    static constexpr bool HELD = V * ITERS <= 8;
+    const float *p;
+    float none;
+    int lane, d;
+    float held[HELD ? ITERS : 1][V];
+    __device__ __forceinline__ Channels(const float *p, float none, int lane, int d) : p(p), none(none), lane(lane), d(d) {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int i = 0; i < ITERS; ++i) fetch(i, held[i]);
+        }
+    }
+    __device__ __forceinline__ void fetch(int i, float (&x)[V]) const {
+        const int c = (i * THREADS + lane) * V;
+        if (!p || c >= d) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = none;
+        } else if constexpr (V >= 4) {
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                const float4 q = __ldg(reinterpret_cast<const float4 *>(p + c + j));
+                x[j] = q.x, x[j + 1] = q.y, x[j + 2] = q.z, x[j + 3] = q.w;
+            }
+        } else {
+            x[0] = __ldg(p + c);
+        }
+    }
+    __device__ __forceinline__ void get(int i, float (&x)[V]) const {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = held[i][j];
+        } else {
+            fetch(i, x);
+        }
+    }
+};
+
+// rows asked for ahead: one, where two fit into the registers
+template <int V, int ITERS>
+__host__ __device__ constexpr bool ahead() { return V * ITERS <= 16; }
+
 template <bool BF16, int V, int THREADS, int ITERS, bool LAYER>
 __global__ void __launch_bounds__(block_size<THREADS>())
 kda_norm_fwd_kernel(NormArgs a) {
     using E = Elem<BF16>;
     constexpr int ROWS = block_rows<THREADS>();
-    __shared__ float buf[THREADS > 32 ? THREADS / 32 : 1];
+    constexpr bool AHEAD = ahead<V, ITERS>();
+    __shared__ __align__(16) float buf[2][1][THREADS > 32 ? THREADS / 32 : 4];
+    int turn = 0;
     const int lane = threadIdx.x % THREADS, d = a.d;
     const float inv_d = 1.f / (float)d;
     const E *x = static_cast<const E *>(a.x);
     E *y = static_cast<E *>(a.y);
-    float w[ITERS][V], b[ITERS][V];
-#pragma unroll
-    for (int i = 0; i < ITERS; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (i * THREADS + lane) * V + j;
-            w[i][j] = a.weight && c < d ? a.weight[c] : 1.f;
-            b[i][j] = a.bias && c < d ? a.bias[c] : 0.f;
-        }
+    const Channels<V, THREADS, ITERS> weight(a.weight, 1.f, lane, d), bias(a.bias, 0.f, lane, d);
     // every thread of a warp makes the same number of turns: the sums are warp-wide
     const long long step = (long long)gridDim.x * ROWS;
-    for (long long base = (long long)blockIdx.x * ROWS; base < a.rows; base += step) {
+    long long base = (long long)blockIdx.x * ROWS;
+    auto row_of = [&](long long b) { return min(b + threadIdx.x / THREADS, a.rows - 1); };
+    Row<BF16, V, THREADS, ITERS> r, next;
+    if (AHEAD) next.load(x + row_of(base) * a.x_stride, lane, d);
+    for (; base < a.rows; base += step) {
         const long long row = base + threadIdx.x / THREADS;
-        const bool live = row < a.rows;
-        Row<BF16, V, THREADS, ITERS> r;
-        r.load(x + (live ? row : base) * a.x_stride, lane, d);
-        float m = 0.f;
+        if constexpr (AHEAD) {
+            r = next;
+            if (base + step < a.rows) next.load(x + row_of(base + step) * a.x_stride, lane, d);
+        } else {
+            r.load(x + row_of(base) * a.x_stride, lane, d);
+        }
+        float m = 0.f, s[1];
         if constexpr (LAYER) {
-            float s = 0.f;
+            s[0] = 0.f;
 #pragma unroll
             for (int i = 0; i < ITERS; ++i)
 #pragma unroll
-                for (int j = 0; j < V; ++j) s += r.raw[i].get(j);
-            m = row_sum<THREADS>(s, buf) * inv_d;
+                for (int j = 0; j < V; ++j) s[0] += r.raw[i].get(j);
+            row_sums<THREADS>(s, buf, turn);
+            m = s[0] * inv_d;
         }
-        float q = 0.f;
+        s[0] = 0.f;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             const bool in = (i * THREADS + lane) * V < d;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float c = in ? r.raw[i].get(j) - m : 0.f;
-                q = fmaf(c, c, q);
+                s[0] = fmaf(c, c, s[0]);
             }
         }
-        q = row_sum<THREADS>(q, buf) * inv_d;
-        const float rs = rsqrtf(q + a.eps);
-        if (!live) continue;
+        row_sums<THREADS>(s, buf, turn);
+        const float rs = rsqrtf(s[0] * inv_d + a.eps);
+        if (row >= a.rows) continue;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             const int c = (i * THREADS + lane) * V;
             if (c >= d) continue;
-            float o[V];
+            float o[V], w[V], b[V];
+            weight.get(i, w);
+            bias.get(i, b);
 #pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = fmaf((r.raw[i].get(j) - m) * rs, w[i][j], b[i][j]);
+            for (int j = 0; j < V; ++j) o[j] = fmaf((r.raw[i].get(j) - m) * rs, w[j], b[j]);
             Vec<BF16, V> out;
             out.set(o);
             out.store(y + row * a.y_stride + c);
@@ -132,14 +191,16 @@ __global__ void __launch_bounds__(block_size<THREADS>())
 kda_norm_bwd_kernel(NormArgs a) {
     using E = Elem<BF16>;
     constexpr int ROWS = block_rows<THREADS>(), BLOCK = block_size<THREADS>();
-    constexpr bool ACC = V * ITERS > 16;
+    constexpr bool ACC = V * ITERS > 16, AHEAD = ahead<V, ITERS>();
     extern __shared__ float acc[];  // ACC: [2][ITERS * V][THREADS]; else [ROWS][2][d] when ROWS > 1
-    __shared__ float buf[THREADS > 32 ? THREADS / 32 : 1];
+    __shared__ __align__(16) float buf1[2][1][THREADS > 32 ? THREADS / 32 : 4], buf3[2][3][THREADS > 32 ? THREADS / 32 : 4];
+    int turn1 = 0, turn3 = 0;
     const int lane = threadIdx.x % THREADS, d = a.d;
     const float inv_d = 1.f / (float)d;
     const E *x = static_cast<const E *>(a.x), *dy = static_cast<const E *>(a.dy);
     E *dx = static_cast<E *>(a.dx);
-    float w[ACC ? 1 : ITERS][V], dw[ACC ? 1 : ITERS][V], db[ACC ? 1 : ITERS][V];
+    const Channels<V, THREADS, ITERS> weight(a.weight, 1.f, lane, d);
+    float dw[ACC ? 1 : ITERS][V], db[ACC ? 1 : ITERS][V];
     if constexpr (ACC) {
         for (int i = threadIdx.x; i < 2 * ITERS * V * THREADS; i += BLOCK) acc[i] = 0.f;
         __syncthreads();
@@ -147,63 +208,62 @@ kda_norm_bwd_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < ITERS; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (i * THREADS + lane) * V + j;
-                w[i][j] = a.weight && c < d ? a.weight[c] : 1.f;
-                dw[i][j] = db[i][j] = 0.f;
-            }
+            for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = 0.f;
     }
-    auto weight = [&](int i, int j) -> float {
-        if constexpr (ACC) {
-            const int c = (i * THREADS + lane) * V + j;
-            return a.weight && c < d ? __ldg(a.weight + c) : 1.f;
-        } else {
-            return w[i][j];
-        }
-    };
     const long long step = (long long)gridDim.x * ROWS;
-    for (long long base = (long long)blockIdx.x * ROWS; base < a.rows; base += step) {
+    long long base = (long long)blockIdx.x * ROWS;
+    auto row_of = [&](long long b) { return min(b + threadIdx.x / THREADS, a.rows - 1); };
+    Row<BF16, V, THREADS, ITERS> r, g, next, gnext;
+    auto load = [&](Row<BF16, V, THREADS, ITERS> &r, Row<BF16, V, THREADS, ITERS> &g, long long b) {
+        r.load(x + row_of(b) * a.x_stride, lane, d);
+        g.load(dy + row_of(b) * a.dy_stride, lane, d);
+    };
+    if (AHEAD) load(next, gnext, base);
+    for (; base < a.rows; base += step) {
         const long long row = base + threadIdx.x / THREADS;
-        const bool live = row < a.rows;
-        Row<BF16, V, THREADS, ITERS> r, g;
-        r.load(x + (live ? row : base) * a.x_stride, lane, d);
-        g.load(dy + (live ? row : base) * a.dy_stride, lane, d);
+        if constexpr (AHEAD) {
+            r = next, g = gnext;
+            if (base + step < a.rows) load(next, gnext, base + step);
+        } else {
+            load(r, g, base);
+        }
         float m = 0.f;
         if constexpr (LAYER) {
-            float s = 0.f;
+            float s[1] = {0.f};
 #pragma unroll
             for (int i = 0; i < ITERS; ++i)
 #pragma unroll
-                for (int j = 0; j < V; ++j) s += r.raw[i].get(j);
-            m = row_sum<THREADS>(s, buf) * inv_d;
+                for (int j = 0; j < V; ++j) s[0] += r.raw[i].get(j);
+            row_sums<THREADS>(s, buf1, turn1);
+            m = s[0] * inv_d;
         }
-        // sums of (x - m)^2, u (x - m) and u
-        float q = 0.f, ux = 0.f, us = 0.f;
+        float s[3] = {0.f, 0.f, 0.f};  // of (x - m)^2, u (x - m) and u
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             const bool in = (i * THREADS + lane) * V < d;
+            float w[V];
+            weight.get(i, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float c = in ? r.raw[i].get(j) - m : 0.f, u = g.raw[i].get(j) * weight(i, j);
-                q = fmaf(c, c, q);
-                ux = fmaf(u, c, ux);
-                us += u;
+                const float c = in ? r.raw[i].get(j) - m : 0.f, u = g.raw[i].get(j) * w[j];
+                s[0] = fmaf(c, c, s[0]);
+                s[1] = fmaf(u, c, s[1]);
+                s[2] += u;
             }
         }
-        q = row_sum<THREADS>(q, buf) * inv_d;
-        ux = row_sum<THREADS>(ux, buf) * inv_d;
-        us = LAYER ? row_sum<THREADS>(us, buf) * inv_d : 0.f;
-        const float rs = rsqrtf(q + a.eps), k = ux * rs;
-        if (!live) continue;
+        row_sums<THREADS>(s, buf3, turn3);
+        const float rs = rsqrtf(s[0] * inv_d + a.eps), k = s[1] * inv_d * rs, us = LAYER ? s[2] * inv_d : 0.f;
+        if (row >= a.rows) continue;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             const int c = (i * THREADS + lane) * V;
             if (c >= d) continue;
-            float o[V];
+            float o[V], w[V];
+            weight.get(i, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float n = (r.raw[i].get(j) - m) * rs, e = g.raw[i].get(j);
-                o[j] = rs * (fmaf(e, weight(i, j), -us) - n * k);
+                o[j] = rs * (fmaf(e, w[j], -us) - n * k);
                 if constexpr (ACC) {
                     float *p = acc + (i * V + j) * THREADS + lane;
                     p[0] = fmaf(e, n, p[0]);
@@ -308,7 +368,7 @@ struct Shape {
     // leaves a partial row, so fewer of the wide ones
     static long long blocks(const NormArgs &a, int sms, bool bwd) {
         const long long need = (a.rows + kRows - 1) / kRows;
-        const long long most = (long long)sms * (bwd ? (kBlock > 256 ? 1 : 4) : 2048 / kBlock);
+        const long long most = (long long)sms * (bwd ? (kBlock > 256 ? 1 : 768 / kBlock) : (kBlock > 256 ? 1024 : 1536) / kBlock);
         return need < most ? need : most;
     }
     static cudaError_t fwd(const NormArgs &a, int sms, cudaStream_t st) {
