@@ -711,95 +711,100 @@ def cache4_attention(q, cache, block_table, seq_len, cu_seqlens, page_size, scal
 
 
 # ------------------------------------------------------------------ norm, short convolution, selective scan
+_here = contextlib.nullcontext()
+
+
 class _Device:
-    """The device of a call's tensors as the current one, and the stream it launches on as the one that the tensors it
-    makes belong to (see _on)."""
+    """The device of a call's tensors and the stream it launches on.  `with d.guard` makes them the current ones where
+    they are not, so that the tensors that the call makes belong to them (see _on)."""
+
+    __slots__ = ("index", "guard", "stream", "like")
 
     def __init__(self, t, stream):
-        if not t.is_cuda:
+        self.index, self.like = t.get_device(), t
+        if self.index < 0:
             raise KDAError("KDA calls take CUDA tensors")
-        self.device = t.device
-        self.guards = []
         if stream is not None:
             if stream.device != t.device:
                 raise KDAError(f"stream is on {stream.device}, the tensors on {t.device}")
-            self.guards.append(torch.cuda.stream(stream))
-        elif torch.cuda.current_device() != t.device.index:
-            self.guards.append(torch.cuda.device(t.device))
+            self.guard, self.stream = torch.cuda.stream(stream), stream.cuda_stream
+        else:
+            self.guard = _here if torch.cuda.current_device() == self.index else torch.cuda.device(self.index)
+            self.stream = (torch.cuda.current_stream(self.index).cuda_stream if _raw_stream is None
+                           else _raw_stream(self.index))
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+    def _fits(self, t, name, dtype, shape):
+        if t.dtype != dtype:
+            raise KDAError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise KDAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.get_device() != self.index:
+            raise KDAError(f"{name} must be on {self.like.device}, got {t.device}")
 
     def flat(self, t, name, dtype=torch.float32, shape=None):
         """Pointer of a contiguous tensor (None: null)."""
         if t is None:
             return None
-        if t.dtype != dtype:
-            raise KDAError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and t.shape != shape:
-            raise KDAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device != self.device:
-            raise KDAError(f"{name} must be on {self.device}, got {t.device}")
+        self._fits(t, name, dtype, shape)
         if not t.is_contiguous():
             raise KDAError(f"{name} must be contiguous")
         return t.data_ptr()
 
-    def rows(self, t, name, dtype, shape):
-        """(pointer, stride in elements) of rows: the last axes of `shape` past the first are one contiguous row, rows may
-        lie further apart."""
+    def rows(self, t, name, dtype, shape, width):
+        """(pointer, stride in elements) of rows: all axes of `shape` past the first are one contiguous row of `width`
+        elements, rows may lie further apart."""
         if t is None:
-            return None, _width(shape)
-        if t.dtype != dtype:
-            raise KDAError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise KDAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device != self.device:
-            raise KDAError(f"{name} must be on {self.device}, got {t.device}")
-        width, strides = 1, t.stride()
-        for n, s in zip(reversed(t.shape[1:]), reversed(strides[1:])):
-            if n != 1 and s != width:
+            return None, width
+        self._fits(t, name, dtype, shape)
+        if t.is_contiguous():
+            return t.data_ptr(), width
+        n, strides = 1, t.stride()
+        for size, step in zip(reversed(t.shape[1:]), reversed(strides[1:])):
+            if size != 1 and step != n:
                 raise KDAError(f"{name}'s rows must be contiguous")
-            width *= n
-        if t.shape[0] > 1 and strides[0] < width:
+            n *= size
+        if t.shape[0] < 2:
+            return t.data_ptr(), width
+        if strides[0] < width:
             raise KDAError(f"{name}'s rows must not overlap")
-        return t.data_ptr(), strides[0] if t.shape[0] > 1 else width
+        return t.data_ptr(), strides[0]
 
     def tails(self, t, name, dtype, shape):
         """rows() of tails [N, W - 1, C]: all their N (W - 1) rows the same way apart."""
-        if t is None:
-            return None, shape[2]
         N, m, C = shape
-        if t.shape != shape:
-            raise KDAError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t is None:
+            return None, C
+        self._fits(t, name, dtype, shape)
+        if t.is_contiguous():
+            return t.data_ptr(), C
         if m > 1 and N > 1 and t.stride(0) != m * t.stride(1):
             raise KDAError(f"{name}'s rows must all lie the same way apart")
         step = t.stride(1) if m > 1 else t.stride(0)
-        return self.rows(t.as_strided((N * m, C), (step, t.stride(2))) if N * m else t.view(0, C), name, dtype, (N * m, C))
+        return self.rows(t.as_strided((N * m, C), (step, t.stride(2))), name, dtype, (N * m, C), C)
 
     def workspace(self, t, need):
         """(pointer, bytes) of a workspace of `need` bytes: t where it is large enough, else a new one."""
         if need == 0:
             return None, 0
         if t is None or t.nbytes < need:
-            t = torch.empty(need, dtype=torch.uint8, device=self.device)
+            t = torch.empty(need, dtype=torch.uint8, device=self.like.device)
         return self.flat(t, "workspace", t.dtype), t.nbytes
 
+    def new(self, *shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device=self.like.device)
 
-def _width(shape):
-    n = 1
-    for k in shape[1:]:
-        n *= k
-    return n
+    def out(self, t, like):
+        """t, or a new contiguous tensor of like's shape and type."""
+        if t is not None:
+            return t
+        return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=like.device)
 
 
 def _norm_rows(d, t, name, like):
     """(pointer, stride) of rows [.., n]: contiguous, or two axes with rows apart."""
+    if t.is_contiguous():
+        d._fits(t, name, like.dtype, like.shape)
+        return t.data_ptr(), t.shape[-1]
     if t.dtype != like.dtype:
         raise KDAError(f"{name} must be {like.dtype}, got {t.dtype}")
     if t.shape != like.shape:
@@ -808,7 +813,7 @@ def _norm_rows(d, t, name, like):
         if not t.is_contiguous():
             raise KDAError(f"{name} must be contiguous, or rows of two axes")
         t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(0, t.shape[-1])
-    return d.rows(t, name, t.dtype, t.shape)
+    return d.rows(t, name, t.dtype, t.shape, t.shape[1])
 
 
 def norm_fwd(x, weight=None, bias=None, eps=1e-6, kind=NORM_RMS, out=None, stream=None):
@@ -818,13 +823,13 @@ def norm_fwd(x, weight=None, bias=None, eps=1e-6, kind=NORM_RMS, out=None, strea
     if x.dim() < 1 or x.shape[-1] < 1:
         raise KDAError("x must be [.., n]")
     dt, n = _in_dtype(x), x.shape[-1]
-    with _Device(x, stream) as d:
+    d = _Device(x, stream)
+    with d.guard:
         xp, xs = _norm_rows(d, x, "x", x)
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = d.out(out, x)
         op, os_ = _norm_rows(d, out, "out", x)
         rc = load_library().kda_norm_fwd(xp, d.flat(weight, "weight", shape=(n,)), d.flat(bias, "bias", shape=(n,)),
-                                         x.numel() // n, n, xs, os_, float(eps), int(kind), op, dt, _stream(stream))
+                                         x.numel() // n, n, xs, os_, float(eps), int(kind), op, dt, d.stream)
         _check(rc, "kda_norm_fwd")
         return out
 
@@ -836,18 +841,17 @@ def norm_bwd(x, dy, weight=None, eps=1e-6, kind=NORM_RMS, dx=None, want_dweight=
         raise KDAError("x must be [.., n]")
     dt, n = _in_dtype(x), x.shape[-1]
     rows = x.numel() // n
-    with _Device(x, stream) as d:
+    d = _Device(x, stream)
+    with d.guard:
         lib = load_library()
         xp, xs = _norm_rows(d, x, "x", x)
         gp, gs = _norm_rows(d, dy, "dy", x)
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = d.out(dx, x)
         op, os_ = _norm_rows(d, dx, "dx", x)
-        new = lambda want: torch.empty(n, dtype=torch.float32, device=x.device) if want else None
-        dw, db = new(want_dweight), new(want_dbias)
+        dw, db = d.new(n) if want_dweight else None, d.new(n) if want_dbias else None
         ws, nb = d.workspace(workspace, lib.kda_norm_bwd_workspace_size(rows, n, dt) if want_dweight or want_dbias else 0)
         rc = lib.kda_norm_bwd(xp, gp, d.flat(weight, "weight", shape=(n,)), rows, n, xs, gs, os_, float(eps), int(kind), op,
-                              d.flat(dw, "dweight"), d.flat(db, "dbias"), dt, ws, nb, _stream(stream))
+                              d.flat(dw, "dweight"), d.flat(db, "dbias"), dt, ws, nb, d.stream)
         _check(rc, "kda_norm_bwd")
         return dx, dw, db
 
@@ -868,18 +872,18 @@ def conv_fwd(x, conv_w, cu_seqlens, bias=None, tail=None, output_tail=True, conv
     that decode_verify_replay, conv_step and a following call continue from.  Rows of no sequence are not written."""
     T, C, W = _conv_shape(x, conv_w, cu_seqlens)
     N, dt = cu_seqlens.shape[0] - 1, _in_dtype(x)
-    with _Device(x, stream) as d:
-        if out is None:
-            out = torch.empty((T, C), dtype=x.dtype, device=x.device)
+    d = _Device(x, stream)
+    with d.guard:
+        out = d.out(out, x)
         if tail_out is None and output_tail:
-            tail_out = torch.empty((N, W - 1, C), dtype=x.dtype, device=x.device)
-        xp, xs = d.rows(x, "x", x.dtype, (T, C))
-        yp, ys = d.rows(out, "out", x.dtype, (T, C))
+            tail_out = d.new(N, W - 1, C, dtype=x.dtype)
+        xp, xs = d.rows(x, "x", x.dtype, (T, C), C)
+        yp, ys = d.rows(out, "out", x.dtype, (T, C), C)
         tp, ts = d.tails(tail, "tail", x.dtype, (N, W - 1, C))
         op, os_ = d.tails(tail_out, "tail_out", x.dtype, (N, W - 1, C))
         rc = load_library().kda_conv_fwd(xp, d.flat(cu_seqlens, "cu_seqlens", torch.int32), d.flat(conv_w, "conv_w", shape=(C, W)),
                                          d.flat(bias, "bias", shape=(C,)), tp, N, T, C, W, xs, ts, ys, os_, int(conv_act), yp, op,
-                                         dt, d.flat(status, "status", torch.int32), _stream(stream))
+                                         dt, d.flat(status, "status", torch.int32), d.stream)
         _check(rc, "kda_conv_fwd")
         return out, tail_out
 
@@ -892,23 +896,22 @@ def conv_bwd(x, conv_w, cu_seqlens, dy, bias=None, tail=None, dtail_out=None, co
     N, dt, f32 = cu_seqlens.shape[0] - 1, _in_dtype(x), torch.float32
     if dy.dtype != x.dtype and dy.dtype != f32:
         raise KDAError(f"dy must be {x.dtype} or {f32}, got {dy.dtype}")
-    with _Device(x, stream) as d:
+    d = _Device(x, stream)
+    with d.guard:
         lib = load_library()
-        if dx is None:
-            dx = torch.empty((T, C), dtype=x.dtype, device=x.device)
-        new = lambda *s: torch.empty(s, dtype=f32, device=x.device)
-        dw, db = new(C, W), new(C) if bias is not None else None
-        dtail = new(N, W - 1, C) if tail is not None else None
-        xp, xs = d.rows(x, "x", x.dtype, (T, C))
-        gp, gs = d.rows(dy, "dy", dy.dtype, (T, C))
-        op, os_ = d.rows(dx, "dx", x.dtype, (T, C))
+        dx = d.out(dx, x)
+        dw, db = d.new(C, W), d.new(C) if bias is not None else None
+        dtail = d.new(N, W - 1, C) if tail is not None else None
+        xp, xs = d.rows(x, "x", x.dtype, (T, C), C)
+        gp, gs = d.rows(dy, "dy", dy.dtype, (T, C), C)
+        op, os_ = d.rows(dx, "dx", x.dtype, (T, C), C)
         tp, ts = d.tails(tail, "tail", x.dtype, (N, W - 1, C))
         ws, nb = d.workspace(workspace, lib.kda_conv_bwd_workspace_size(T, C, W))
         rc = lib.kda_conv_bwd(xp, d.flat(cu_seqlens, "cu_seqlens", torch.int32), d.flat(conv_w, "conv_w", shape=(C, W)),
                               d.flat(bias, "bias", shape=(C,)), tp, gp, d.flat(dtail_out, "dtail_out", shape=(N, W - 1, C)), N, T,
                               C, W, xs, ts, gs, os_, int(conv_act), op, d.flat(dw, "dw"), d.flat(db, "dbias"),
                               d.flat(dtail, "dtail"), dt, _in_dtype(dy), ws, nb, d.flat(status, "status", torch.int32),
-                              _stream(stream))
+                              d.stream)
         _check(rc, "kda_conv_bwd")
         return dx, dw, db, dtail
 
@@ -917,14 +920,14 @@ def conv_step(x, conv_w, tail, bias=None, conv_act=CONV_SILU, out=None, stream=N
     """conv_fwd for one token of each request: x [R, C]; tail [R, W - 1, C] moves on in place.  Returns y [R, C]."""
     R, C, W = _conv_shape(x, conv_w, None)
     dt = _in_dtype(x)
-    with _Device(x, stream) as d:
-        if out is None:
-            out = torch.empty((R, C), dtype=x.dtype, device=x.device)
-        xp, xs = d.rows(x, "x", x.dtype, (R, C))
-        yp, ys = d.rows(out, "out", x.dtype, (R, C))
+    d = _Device(x, stream)
+    with d.guard:
+        out = d.out(out, x)
+        xp, xs = d.rows(x, "x", x.dtype, (R, C), C)
+        yp, ys = d.rows(out, "out", x.dtype, (R, C), C)
         tp, ts = d.tails(tail, "tail", x.dtype, (R, W - 1, C))
         rc = load_library().kda_conv_step(xp, d.flat(conv_w, "conv_w", shape=(C, W)), d.flat(bias, "bias", shape=(C,)), tp, R, C,
-                                          W, xs, ts, ys, int(conv_act), yp, dt, _stream(stream))
+                                          W, xs, ts, ys, int(conv_act), yp, dt, d.stream)
         _check(rc, "kda_conv_step")
         return out
 
@@ -935,11 +938,11 @@ def _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias):
         raise KDAError("x and dt must be [T, D], A [D, S], B and C [T, G, S]")
     T, n = x.shape
     G, S = B.shape[1:]
-    xp, xs = d.rows(x, "x", x.dtype, (T, n))
-    dtp, dts = d.rows(dt, "dt", x.dtype, (T, n))
-    zp, zs = d.rows(z, "z", x.dtype, (T, n))
-    bp, bs = d.rows(B, "B", x.dtype, (T, G, S))
-    cp, cs = d.rows(C, "C", x.dtype, (T, G, S))
+    xp, xs = d.rows(x, "x", x.dtype, (T, n), n)
+    dtp, dts = d.rows(dt, "dt", x.dtype, (T, n), n)
+    zp, zs = d.rows(z, "z", x.dtype, (T, n), n)
+    bp, bs = d.rows(B, "B", x.dtype, (T, G, S), G * S)
+    cp, cs = d.rows(C, "C", x.dtype, (T, G, S), G * S)
     ptrs = (xp, dtp, d.flat(A, "A", shape=(n, S)), bp, cp, d.flat(D, "D", shape=(n,)), zp, d.flat(dt_bias, "dt_bias", shape=(n,)))
     return ptrs, (T, n, G, S), (xs, dts, bs, cs, zs)
 
@@ -958,26 +961,26 @@ def scan_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, initial_s
     Returns (y [T, D], final_state f32 [N, D, S] or None), and with save the states that scan_bwd starts from (4 / 8 S
     bytes per token and channel).  Rows of no sequence are not written."""
     N, f32 = _scan_sequences(cu_seqlens), torch.float32
-    with _Device(x, stream) as d:
+    d = _Device(x, stream)
+    with d.guard:
         lib = load_library()
         ptrs, (T, n, G, S), strides = _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias)
-        if out is None:
-            out = torch.empty((T, n), dtype=x.dtype, device=x.device)
+        out = d.out(out, x)
         if final_state is None and output_final_state:
-            final_state = torch.empty((N, n, S), dtype=f32, device=x.device)
+            final_state = d.new(N, n, S)
         if save:
             need = lib.kda_scan_saved_size(N, T, n, S) // 4
             if saved is None:
-                saved = torch.empty(need, dtype=f32, device=x.device)
+                saved = d.new(need)
             elif saved.numel() < need:
                 raise KDAError(f"saved must hold {need} f32 values, got {saved.numel()}")
-        yp, ys = d.rows(out, "out", x.dtype, (T, n))
+        yp, ys = d.rows(out, "out", x.dtype, (T, n), n)
         ws, nb = d.workspace(workspace, lib.kda_scan_workspace_size(N, T, n, G, S))
         rc = lib.kda_scan_fwd(*ptrs, d.flat(cu_seqlens, "cu_seqlens", torch.int32), N, T, n, G, S, *strides, ys,
                               d.flat(initial_state, "initial_state", shape=(N, n, S)),
                               d.flat(final_state, "final_state", shape=(N, n, S)), int(bool(dt_softplus)), yp,
                               d.flat(saved, "saved") if save else None, _in_dtype(x), ws, nb,
-                              d.flat(status, "status", torch.int32), _stream(stream))
+                              d.flat(status, "status", torch.int32), d.stream)
         _check(rc, "kda_scan_fwd")
         return (out, final_state, saved) if save else (out, final_state)
 
@@ -988,7 +991,8 @@ def scan_bwd(x, dt, A, B, C, cu_seqlens, dy, saved, D=None, z=None, dt_bias=None
     [T, D], dA f32 [D, S], dB, dC [T, G, S], dD f32 [D], dz [T, D], ddt_bias f32 [D], dinitial_state f32 [N, D, S]), None
     for what the call has not got.  dx, ddt, dB, dC and dz are of x's dtype."""
     N, f32 = _scan_sequences(cu_seqlens), torch.float32
-    with _Device(x, stream) as d:
+    d = _Device(x, stream)
+    with d.guard:
         lib = load_library()
         ptrs, (T, n, G, S), strides = _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias)
         if initial_state is not None:
@@ -996,18 +1000,18 @@ def scan_bwd(x, dt, A, B, C, cu_seqlens, dy, saved, D=None, z=None, dt_bias=None
         need = lib.kda_scan_saved_size(N, T, n, S) // 4
         if saved.numel() < need:
             raise KDAError(f"saved must hold {need} f32 values, got {saved.numel()}")
-        gp, gs = d.rows(dy, "dy", x.dtype, (T, n))
-        new = lambda have, dtype, *s: torch.empty(s, dtype=dtype, device=x.device) if have is not None else None
-        dx, ddt, dz = new(x, x.dtype, T, n), new(x, x.dtype, T, n), new(z, x.dtype, T, n)
-        dB, dC, dA = new(x, x.dtype, T, G, S), new(x, x.dtype, T, G, S), new(x, f32, n, S)
-        dD, dbias, dh = new(D, f32, n), new(dt_bias, f32, n), new(initial_state, f32, N, n, S)
+        gp, gs = d.rows(dy, "dy", x.dtype, (T, n), n)
+        rows, of = lambda *s: d.new(*s, dtype=x.dtype), lambda have, *s: None if have is None else d.new(*s)
+        dx, ddt, dz = rows(T, n), rows(T, n), None if z is None else rows(T, n)
+        dB, dC, dA = rows(T, G, S), rows(T, G, S), d.new(n, S)
+        dD, dbias, dh = of(D, n), of(dt_bias, n), of(initial_state, N, n, S)
         ws, nb = d.workspace(workspace, lib.kda_scan_bwd_workspace_size(N, T, n, G, S))
         ptr = lambda t: None if t is None else t.data_ptr()
         rc = lib.kda_scan_bwd(*ptrs, d.flat(cu_seqlens, "cu_seqlens", torch.int32), gp,
                               d.flat(dfinal_state, "dfinal_state", shape=(N, n, S)), d.flat(saved, "saved"), N, T, n, G, S,
                               *strides, gs, int(bool(dt_softplus)), ptr(dx), ptr(ddt), ptr(dA), ptr(dB), ptr(dC), ptr(dD),
                               ptr(dz), ptr(dbias), ptr(dh), _in_dtype(x), ws, nb, d.flat(status, "status", torch.int32),
-                              _stream(stream))
+                              d.stream)
         _check(rc, "kda_scan_bwd")
         return dx, ddt, dA, dB, dC, dD, dz, dbias, dh
 
@@ -1015,12 +1019,12 @@ def scan_bwd(x, dt, A, B, C, cu_seqlens, dy, saved, D=None, z=None, dt_bias=None
 def scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus=True, out=None, stream=None):
     """scan_fwd for one token of each request: x, dt, z [R, D], B, C [R, G, S]; state f32 [R, D, S] moves on in place.
     Returns y [R, D]."""
-    with _Device(x, stream) as d:
+    d = _Device(x, stream)
+    with d.guard:
         ptrs, (R, n, G, S), strides = _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias)
-        if out is None:
-            out = torch.empty((R, n), dtype=x.dtype, device=x.device)
-        yp, ys = d.rows(out, "out", x.dtype, (R, n))
+        out = d.out(out, x)
+        yp, ys = d.rows(out, "out", x.dtype, (R, n), n)
         rc = load_library().kda_scan_step(*ptrs, d.flat(state, "state", shape=(R, n, S)), R, n, G, S, *strides, ys,
-                                          int(bool(dt_softplus)), yp, _in_dtype(x), _stream(stream))
+                                          int(bool(dt_softplus)), yp, _in_dtype(x), d.stream)
         _check(rc, "kda_scan_step")
         return out
