@@ -745,9 +745,10 @@ class _Device:
         """Pointer of a contiguous tensor (None: null)."""
         if t is None:
             return None
-        self._fits(t, name, dtype, shape)
-        if not t.is_contiguous():
-            raise KDAError(f"{name} must be contiguous")
+        if not (t.dtype is dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous()):
+            self._fits(t, name, dtype, shape)
+            if not t.is_contiguous():
+                raise KDAError(f"{name} must be contiguous")
         return t.data_ptr()
 
     def rows(self, t, name, dtype, shape, width):
@@ -755,9 +756,9 @@ class _Device:
         elements, rows may lie further apart."""
         if t is None:
             return None, width
-        self._fits(t, name, dtype, shape)
-        if t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
             return t.data_ptr(), width
+        self._fits(t, name, dtype, shape)
         n, strides = 1, t.stride()
         for size, step in zip(reversed(t.shape[1:]), reversed(strides[1:])):
             if size != 1 and step != n:
@@ -803,7 +804,8 @@ class _Device:
 def _norm_rows(d, t, name, like):
     """(pointer, stride) of rows [.., n]: contiguous, or two axes with rows apart."""
     if t.is_contiguous():
-        d._fits(t, name, like.dtype, like.shape)
+        if t is not like:
+            d._fits(t, name, like.dtype, like.shape)
         return t.data_ptr(), t.shape[-1]
     if t.dtype != like.dtype:
         raise KDAError(f"{name} must be {like.dtype}, got {t.dtype}")

@@ -44,10 +44,10 @@ struct Layout {
     static constexpr int M = 8, LN = S / M, PAIRS = 32 / LN, CH = 2 * PAIRS * WARPS;
     static constexpr int V4 = 2 * M / 4;           // float4s of a thread's states, and of its dB and dC
     static constexpr int hist = K / 2 * V4 * 32;   // float4s of a warp
-    static constexpr int red = V4 * 32;
+    static constexpr int red = 2 * V4 * 32;        // two tokens'
     static constexpr int vals = 5 * K * PAIRS;     // float2s of a warp
-    static constexpr int out = K * 2 * S;          // floats of a warp, and of B and C
-    static constexpr int bytes = WARPS * (16 * (hist + red) + 8 * vals + 4 * out) + 4 * out;
+    static constexpr int out = (K + 1) * 2 * S;    // floats of a warp (the last row takes what is of no token)
+    static constexpr int bytes = WARPS * (16 * (hist + red) + 8 * vals + 4 * out) + 4 * K * 2 * S;
 };
 
 // two neighbouring channels of a row, of which `one` and `two` say which are there
@@ -84,9 +84,9 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = lane / PAIRS, pl = lane % PAIRS;
     float4 *hist = reinterpret_cast<float4 *>(smem) + warp * L::hist;                              // [K / 2][V4][32]
-    float4 *red = reinterpret_cast<float4 *>(smem) + WARPS * L::hist + warp * L::red;              // [V4][32]
+    float4 *red = reinterpret_cast<float4 *>(smem) + WARPS * L::hist + warp * L::red;              // [2][V4][32]
     float2 *vals = reinterpret_cast<float2 *>(smem + 16 * WARPS * (L::hist + L::red)) + warp * L::vals;  // [5][K][PAIRS]
-    float *outs = reinterpret_cast<float *>(smem + WARPS * (16 * (L::hist + L::red) + 8 * L::vals));    // [WARPS][K][2 S]
+    float *outs = reinterpret_cast<float *>(smem + WARPS * (16 * (L::hist + L::red) + 8 * L::vals));    // [WARPS][K + 1][2 S]
     float *bc = outs + WARPS * L::out;                                                             // [K][2 S]
     const Segment g = segment_of(a.cu_seqlens, a.N, a.T, a.seg, blockIdx.x);
     if (tid == 0 && blockIdx.y == 0) check_sequence(a, blockIdx.x);
@@ -217,9 +217,48 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
         float2 dAt[2][M / 2], dDt = both(0.f), dbt = both(0.f);
 #pragma unroll
         for (int n = 0; n < M / 2; ++n) dAt[0][n] = dAt[1][n] = both(0.f);
-        // A token back: sums over the thread's states for (lB, lA, y) of both channels, and dB and dC.
+        // dB and dC of token k from `red`, place buf.  Row v there is four outputs of all lanes.  A lane adds up a row
+        // over the PART lanes of its part (rotated, so that eight neighbours read eight places), and parts of one ln are joined.
+        auto channels = [&](int k, int buf) {
+            constexpr int PARTS = 32 / V4, PART = 32 / PARTS, JOIN = PARTS / LN;
+            const int v = lane / PARTS, part = lane % PARTS;
+            const float4 *p = red + (buf * V4 + v) * 32 + part * PART;
+            float2 f0 = both(0.f), f1 = both(0.f);
+#pragma unroll
+            for (int j = 0; j < PART; ++j) {
+                const float4 w = p[(j + (part >> 1)) % PART];
+                f0 = __fadd2_rn(f0, make_float2(w.x, w.y)), f1 = __fadd2_rn(f1, make_float2(w.z, w.w));
+            }
+            // outputs of the lane's part: B for rows below M / 4, C above
+            const int which = v >= M / 4, n0 = (part / JOIN) * M + (v - which * (M / 4)) * 4;
+            float *out = outs + (warp * (K + 1) + k) * 2 * S + which * S + n0;
+            if constexpr (JOIN >= 2) {  // two lanes: each keeps two of the four
+                const bool up = part & 1;
+                const float2 send = up ? f0 : f1;
+                float2 mine = up ? f1 : f0;
+                mine.x += __shfl_xor_sync(0xffffffffu, send.x, 1), mine.y += __shfl_xor_sync(0xffffffffu, send.y, 1);
+                if constexpr (JOIN >= 4) {
+                    const bool up2 = part & 2;
+                    const float s2 = up2 ? mine.x : mine.y;
+                    float m2 = up2 ? mine.y : mine.x;
+                    m2 += __shfl_xor_sync(0xffffffffu, s2, 2);
+                    if constexpr (JOIN >= 8) m2 += __shfl_xor_sync(0xffffffffu, m2, 4);
+                    if (JOIN < 8 || (part & 4) == 0) out[(up ? 2 : 0) + (up2 ? 1 : 0)] = m2;
+                } else {
+                    out[up ? 2 : 0] = mine.x, out[up ? 3 : 1] = mine.y;
+                }
+            } else {
+                *reinterpret_cast<float4 *>(out) = make_float4(f0.x, f0.y, f1.x, f1.y);
+            }
+        };
+        // A token back: sums over the thread's states for (lB, lA, y) of both channels, and its share of dB and dC into
+        // `red`.  Those of the token before it in the walk are added up meanwhile: later tokens of a pair use place 1,
+        // earlier ones place 0.
+        int before = K;
         auto back = [&](auto later, int k, float2 (&sums)[3]) {
             constexpr bool LATER = decltype(later)::value;
+            channels(before, !LATER ? 1 : 0);  // (no wait for them: the operations below are others)
+            before = k;
             const float2 d = vals[k * PAIRS + pl], x = vals[(K + k) * PAIRS + pl], ev = vals[(2 * K + k) * PAIRS + pl];
             const float4 *b4 = reinterpret_cast<const float4 *>(bc + k * 2 * S + ln * M), *c4 = b4 + S / 4;
             const float2 dq[2] = {both(d.x), both(d.y)}, in[2] = {both(d.x * x.x), both(d.y * x.y)}, eq[2] = {both(ev.x), both(ev.y)};
@@ -251,48 +290,13 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
                         sC[e] = q ? __ffma2_rn(hk, eq[q], sC[e]) : __fmul2_rn(hk, eq[q]);
                     }
                 }
-                red[n * 32 + lane] = make_float4(sB[0].x, sB[0].y, sB[1].x, sB[1].y);
-                red[(M / 4 + n) * 32 + lane] = make_float4(sC[0].x, sC[0].y, sC[1].x, sC[1].y);
+                red[((LATER ? V4 : 0) + n) * 32 + lane] = make_float4(sB[0].x, sB[0].y, sB[1].x, sB[1].y);
+                red[((LATER ? V4 : 0) + M / 4 + n) * 32 + lane] = make_float4(sC[0].x, sC[0].y, sC[1].x, sC[1].y);
             }
             sums[0] = make_float2(lB[0].x + lB[0].y, lB[1].x + lB[1].y);
             sums[1] = make_float2(lA[0].x + lA[0].y, lA[1].x + lA[1].y);
             sums[2] = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
             __syncwarp();
-            // Row v of `red` is four outputs of all lanes.  A lane adds up a row over the PART lanes of its part
-            // (rotated, so that eight neighbours read eight places), and parts of one ln are joined.
-            {
-                constexpr int PARTS = 32 / V4, PART = 32 / PARTS, JOIN = PARTS / LN;
-                const int v = lane / PARTS, part = lane % PARTS;
-                const float4 *p = red + v * 32 + part * PART;
-                float2 f0 = both(0.f), f1 = both(0.f);
-#pragma unroll
-                for (int j = 0; j < PART; ++j) {
-                    const float4 w = p[(j + (part >> 1)) % PART];
-                    f0 = __fadd2_rn(f0, make_float2(w.x, w.y)), f1 = __fadd2_rn(f1, make_float2(w.z, w.w));
-                }
-                // outputs of the lane's part: B for rows below M / 4, C above
-                const int which = v >= M / 4, n0 = (part / JOIN) * M + (v - which * (M / 4)) * 4;
-                float *out = outs + (warp * K + k) * 2 * S + which * S + n0;
-                if constexpr (JOIN >= 2) {  // two lanes: each keeps two of the four
-                    const bool up = part & 1;
-                    const float2 send = up ? f0 : f1;
-                    float2 mine = up ? f1 : f0;
-                    mine.x += __shfl_xor_sync(0xffffffffu, send.x, 1), mine.y += __shfl_xor_sync(0xffffffffu, send.y, 1);
-                    if constexpr (JOIN >= 4) {
-                        const bool up2 = part & 2;
-                        const float s2 = up2 ? mine.x : mine.y;
-                        float m2 = up2 ? mine.y : mine.x;
-                        m2 += __shfl_xor_sync(0xffffffffu, s2, 2);
-                        if constexpr (JOIN >= 8) m2 += __shfl_xor_sync(0xffffffffu, m2, 4);
-                        if (JOIN < 8 || (part & 4) == 0) out[(up ? 2 : 0) + (up2 ? 1 : 0)] = m2;
-                    } else {
-                        out[up ? 2 : 0] = mine.x, out[up ? 3 : 1] = mine.y;
-                    }
-                } else {
-                    *reinterpret_cast<float4 *>(out) = make_float4(f0.x, f0.y, f1.x, f1.y);
-                }
-            }
-            __syncwarp();  // `red` has been read
         };
         // a token's own gradients, from its sums over all states
         auto finish = [&](int k, const float2 (&sums)[3]) {
@@ -335,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
                 if (ln % (LN / 2) == 0 && (pair || !up)) finish(k + up, late);
             }
         }
+        channels(before, 0);
 #pragma unroll
         for (int n = 0; n < M / 2; ++n) dA[0][n] = __fadd2_rn(dA[0][n], dAt[0][n]), dA[1][n] = __fadd2_rn(dA[1][n], dAt[1][n]);
         dD = __fadd2_rn(dD, dDt), dbias = __fadd2_rn(dbias, dbt);
