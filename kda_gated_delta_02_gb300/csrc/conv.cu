@@ -92,7 +92,7 @@ __device__ __forceinline__ void load_row(Vec<BF16, V> &r, const Elem<BF16> *p, b
 }
 
 template <bool BF16, int V, int W>
-__global__ void __launch_bounds__(kThreads) kda_conv_fwd_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) kda_conv_fwd_kernel(ConvArgs a) {
     using E = Elem<BF16>;
     const int c = (blockIdx.y * kThreads + threadIdx.x) * V;
     const bool live = c < a.C;

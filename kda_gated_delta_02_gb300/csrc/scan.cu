@@ -96,6 +96,10 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
     // row r of the walk: forward from the first token, or backward from the last
     auto token = [&](int r) { return (long long)(MODE == REVERSE ? g.t1 - 1 - r : g.t0 + r); };
 
+    // rows of tile i: copied to their place at once, or (rows off 16-byte boundaries) by way of registers, to be
+    // stored after the tile before has been worked on
+    constexpr int PART = VEC ? 1 : kTile * CH / kThreads;
+    E held[3][PART];
     auto stage = [&](int i) {
         E *dst = raw + (i & 1) * 3 * kTile * CH;
 #pragma unroll
@@ -112,13 +116,26 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
                     cp_async16(dst + (k * kTile + r) * CH + o, src + (ok ? token(at) * stride + o : 0), ok);
                 }
             } else {
-                for (int e = tid; e < kTile * CH; e += kThreads) {
-                    const int r = e / CH, o = e % CH, at = i * kTile + r;
-                    if (at < count && o < left) dst[(k * kTile + r) * CH + o] = src[token(at) * stride + o];
+#pragma unroll
+                for (int e = 0; e < PART; ++e) {
+                    const int r = (tid + e * kThreads) / CH, o = (tid + e * kThreads) % CH, at = i * kTile + r;
+                    held[k][e] = (E)0.f;
+                    if (at < count && o < left) held[k][e] = src[token(at) * stride + o];
                 }
             }
         }
-        cp_async_commit();
+        if constexpr (VEC) cp_async_commit();
+    };
+    auto put = [&](int i) {
+        if constexpr (!VEC) {
+            E *dst = raw + (i & 1) * 3 * kTile * CH;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if (k == 2 && !third) break;
+#pragma unroll
+                for (int e = 0; e < PART; ++e) dst[k * kTile * CH + tid + e * kThreads] = held[k][e];
+            }
+        }
     };
     // four neighbouring values of B and C at a time (REVERSE wants C alone)
     constexpr int BCN = (kTile * 2 * S + 4 * kThreads - 1) / (4 * kThreads);
@@ -149,10 +166,11 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
     if (steps > 0) {
         stage(0);
         bc_load(0);
+        put(0);
         bc_store(0);
     }
     for (int i = 0; i < steps; ++i) {
-        cp_async_wait_all();
+        if constexpr (VEC) cp_async_wait_all();
         __syncthreads();
         const bool more = i + 1 < steps;
         if (more) {
@@ -240,7 +258,10 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
                 }
             }
         }
-        if (more) bc_store(i + 1);
+        if (more) {
+            put(i + 1);
+            bc_store(i + 1);
+        }
     }
     if constexpr (MODE != WALK) {
 #pragma unroll
