@@ -1,10 +1,11 @@
 """A serving loop of a hybrid model's two kinds of layers: one KDA layer with its fixed-size state and one attention
 layer with a paged 4-bit key/value cache, for a ragged batch.
 
-Prompts are admitted (page_plan, chunk_fwd, cache4_append, cache4_attention), then a few decode steps follow (page_plan,
-decode_verify_replay with an empty draft window, cache4_append, cache4_attention).  Projections are random: the point is
+Prompts are admitted (page_plan, conv_fwd, chunk_fwd, norm_fwd, cache4_append, cache4_attention), then a few decode
+steps follow (page_plan, decode_verify_replay with an empty draft window, from the state and the convolution tail that
+the prompts left, cache4_append, cache4_attention).  Projections are random: the point is
 the order of the calls and what passes between them.  Every attention output is compared with plain attention in 32
-bits over the values that the cache holds.
+bits over the values that the cache holds, and the single tokens of the KDA layer with its prefill of the whole sequences.
 
     python examples/hybrid_serving.py
 """
@@ -34,6 +35,33 @@ class AttentionLayer:
         q, k, v = (t.view(t.shape[0], -1, D) for t in qkv.split([HQ * D, HKV * D, HKV * D], dim=1))
         kda.cache4_append(k, v, slots, self.cache, PAGE, status=status)
         return q, kda.cache4_attention(q, self.cache, table, seq_len, cu, PAGE, max_new=max_new, status=status)
+
+
+class RecurrentLayer:
+    """One KDA layer behind its projections: convolution, input norm and gates, recurrence, output norm."""
+
+    def __init__(self, gen):
+        self.conv_w = 0.5 * torch.randn(3 * H * D, 4, generator=gen, device="cuda")
+        self.norm_w = torch.ones(D, device="cuda")
+
+    def prefill(self, qkv, g, beta, cu, status):
+        """Outputs [T, H, D], the state in bf16 and the tail that single tokens continue from."""
+        x, tail = kda.conv_fwd(qkv, self.conv_w, cu, status=status)
+        q, k, v = (t.unflatten(1, (H, D)) for t in x.split(H * D, dim=1))
+        q, k = (torch.nn.functional.normalize(t.float(), dim=-1).bfloat16() for t in (q, k))
+        o, state = kda.chunk_fwd(q, k, v.contiguous(), -torch.nn.functional.softplus(g.float()).unflatten(1, (H, D)),
+                                 torch.sigmoid(beta.float()), cu, status=status)
+        return kda.norm_fwd(o, self.norm_w), state.bfloat16(), tail
+
+    def token(self, qkv, g, beta, state, tail, status):
+        R, (none, accepted) = qkv.shape[0], self.no_drafts(qkv.shape[0])
+        return kda.decode_verify_replay(state, tail, self.conv_w, none(3 * H * D), none(H * D), none(H), accepted,
+                                        qkv.view(R, 1, -1), g.view(R, 1, -1), beta.view(R, 1, -1), self.norm_w,
+                                        status=status)[:, 0]
+
+    @staticmethod
+    def no_drafts(R):
+        return lambda n: torch.zeros(R, 0, n, dtype=torch.bfloat16, device="cuda"), torch.zeros(R, dtype=torch.int32, device="cuda")
 
 
 def plain_attention(q, layer, plan, table):
@@ -72,32 +100,33 @@ def main(prompts=(70, 130, 5), steps=4, seed=0):
     # ---- prompts
     plan = kda.page_plan(length, torch.tensor(prompts, **i32), count, table, free, left, PAGE, T, status=status)
     length, count, left = plan[1], plan[4], plan[5]
-    unit = lambda t: torch.nn.functional.normalize(t, dim=-1).bfloat16()
-    _, state = kda.chunk_fwd(unit(randn(T, H, D)), unit(randn(T, H, D)), randn(T, H, D).bfloat16(),
-                             -torch.nn.functional.softplus(randn(T, H, D)), torch.sigmoid(randn(T, H)), plan[0], status=status)
+    total, kda_layer = T + R * steps, RecurrentLayer(gen)
+    rows = [randn(total, n).bfloat16() for n in (3 * H * D, H * D, H)]  # q, k and v, decay and beta of all tokens
+    starts = [sum(prompts[:i]) + i * steps for i in range(R)]
+    prompt = torch.cat([torch.arange(a, a + n) for a, n in zip(starts, prompts)]).cuda()
+    last = torch.tensor([a + n for a, n in zip(starts, prompts)], device="cuda")
+    _, state, tail = kda_layer.prefill(*(t[prompt] for t in rows), plan[0], status)
     x = randn(T, HIDDEN).bfloat16()
     q, o = layer(x, plan, table, max(prompts), status)
     worst = max(worst, check(q, o, plan))
 
     # ---- single tokens
-    C = 3 * H * D
-    state, tail = state.bfloat16(), torch.zeros(R, 3, C, dtype=torch.bfloat16, device="cuda")
-    conv_w, norm_w = 0.5 * randn(C, 4), torch.ones(D, device="cuda")
-    none = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
-    accepted, one = torch.zeros(R, **i32), torch.ones(R, **i32)
-    for _ in range(steps):
+    one, tokens = torch.ones(R, **i32), []
+    for i in range(steps):
         plan = kda.page_plan(length, one, count, table, free, left, PAGE, R, status=status)
         length, count, left = plan[1], plan[4], plan[5]
-        y = kda.decode_verify_replay(state, tail, conv_w, none(R, 0, C), none(R, 0, H * D), none(R, 0, H), accepted,
-                                     randn(R, 1, C).bfloat16(), randn(R, 1, H * D).bfloat16(), randn(R, 1, H).bfloat16(),
-                                     norm_w, status=status)
+        tokens.append(kda_layer.token(*(t[last + i] for t in rows), state, tail, status))
         q, o = layer(randn(R, HIDDEN).bfloat16(), plan, table, 1, status)
         worst = max(worst, check(q, o, plan))
-        assert torch.isfinite(y).all()
+    # ---- the same tokens by prefills of the whole sequences (which round the convolution's outputs to bf16)
+    whole, _, end = kda_layer.prefill(*rows, torch.tensor([*starts, total], **i32), status)
+    want = torch.stack([whole[last + i] for i in range(steps)]).float()
+    apart = float((torch.stack(tokens).float() - want).abs().max() / want.abs().max())
+    assert apart < 0.05 and torch.equal(tail, end), apart
     assert status.item() == 0, f"status {status.item():#x}"
     assert left.item() == PAGES - sum(-(-(p + steps) // PAGE) for p in prompts)
     print(f"{R} requests, {T} prompt tokens and {steps} decode steps; pages left {left.item()} of {PAGES}; "
-          f"attention within {worst:.1e} of plain attention")
+          f"attention within {worst:.1e} of plain attention, single tokens within {apart:.1e} of a prefill")
     return worst
 
 
