@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(256) kda_scan_chain_kernel(ScanArgs a, int S, 
 // channel's lanes (each of them forming all cost 110 instructions a state of four,
 // 82 us for 256 x 8192 channels of 16 states).
 template <bool BF16, int S>
-__global__ void __launch_bounds__(256) kda_scan_step_kernel(ScanArgs a, int rows) {
+__global__ void __launch_bounds__(256, 4) kda_scan_step_kernel(ScanArgs a, int rows) {
     using E = Elem<BF16>;
     constexpr int LANES = S / 4, U = 4, OWN = LANES < U ? U / LANES : 1, DEAL = U / OWN;  // lanes that share the work
     const int lane = threadIdx.x & 31, ln = threadIdx.x % LANES, mine = ln % DEAL * OWN, per = a.D / a.G;
