@@ -801,6 +801,11 @@ class _Device:
         return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=like.device)
 
 
+def _at(t):
+    """Pointer of a tensor that the call made (None: null)."""
+    return None if t is None else t.data_ptr()
+
+
 def _norm_rows(d, t, name, like):
     """(pointer, stride) of rows [.., n]: contiguous, or two axes with rows apart."""
     if t.is_contiguous():
@@ -850,10 +855,11 @@ def norm_bwd(x, dy, weight=None, eps=1e-6, kind=NORM_RMS, dx=None, want_dweight=
         gp, gs = _norm_rows(d, dy, "dy", x)
         dx = d.out(dx, x)
         op, os_ = _norm_rows(d, dx, "dx", x)
-        dw, db = d.new(n) if want_dweight else None, d.new(n) if want_dbias else None
+        dw = None if not want_dweight else d.new(n) if weight is None else torch.empty_like(weight)
+        db = d.new(n) if want_dbias else None
         ws, nb = d.workspace(workspace, lib.kda_norm_bwd_workspace_size(rows, n, dt) if want_dweight or want_dbias else 0)
         rc = lib.kda_norm_bwd(xp, gp, d.flat(weight, "weight", shape=(n,)), rows, n, xs, gs, os_, float(eps), int(kind), op,
-                              d.flat(dw, "dweight"), d.flat(db, "dbias"), dt, ws, nb, d.stream)
+                              _at(dw), _at(db), dt, ws, nb, d.stream)
         _check(rc, "kda_norm_bwd")
         return dx, dw, db
 
@@ -893,7 +899,8 @@ def conv_fwd(x, conv_w, cu_seqlens, bias=None, tail=None, output_tail=True, conv
 def conv_bwd(x, conv_w, cu_seqlens, dy, bias=None, tail=None, dtail_out=None, conv_act=CONV_SILU, dx=None, workspace=None,
              status=None, stream=None):
     """Gradients of conv_fwd for dy [T, C] (x's dtype or f32, as chunk_bwd's are) and dtail_out f32 [N, W - 1, C] (or
-    None): (dx in x's dtype, dw f32 [C, W], dbias f32 [C] or None without bias, dtail f32 [N, W - 1, C] or None without tail)."""
+    None): (dx in x's dtype, dw f32 [C, W], dbias f32 [C] or None without bias, dtail f32 [N, W - 1, C] or None without
+    tail).  Rows of no sequence are not written."""
     T, C, W = _conv_shape(x, conv_w, cu_seqlens)
     N, dt, f32 = cu_seqlens.shape[0] - 1, _in_dtype(x), torch.float32
     if dy.dtype != x.dtype and dy.dtype != f32:
@@ -902,7 +909,7 @@ def conv_bwd(x, conv_w, cu_seqlens, dy, bias=None, tail=None, dtail_out=None, co
     with d.guard:
         lib = load_library()
         dx = d.out(dx, x)
-        dw, db = d.new(C, W), d.new(C) if bias is not None else None
+        dw, db = torch.empty_like(conv_w), torch.empty_like(bias) if bias is not None else None
         dtail = d.new(N, W - 1, C) if tail is not None else None
         xp, xs = d.rows(x, "x", x.dtype, (T, C), C)
         gp, gs = d.rows(dy, "dy", dy.dtype, (T, C), C)
@@ -911,8 +918,7 @@ def conv_bwd(x, conv_w, cu_seqlens, dy, bias=None, tail=None, dtail_out=None, co
         ws, nb = d.workspace(workspace, lib.kda_conv_bwd_workspace_size(T, C, W))
         rc = lib.kda_conv_bwd(xp, d.flat(cu_seqlens, "cu_seqlens", torch.int32), d.flat(conv_w, "conv_w", shape=(C, W)),
                               d.flat(bias, "bias", shape=(C,)), tp, gp, d.flat(dtail_out, "dtail_out", shape=(N, W - 1, C)), N, T,
-                              C, W, xs, ts, gs, os_, int(conv_act), op, d.flat(dw, "dw"), d.flat(db, "dbias"),
-                              d.flat(dtail, "dtail"), dt, _in_dtype(dy), ws, nb, d.flat(status, "status", torch.int32),
+                              C, W, xs, ts, gs, os_, int(conv_act), op, _at(dw), _at(db), _at(dtail), dt, _in_dtype(dy), ws, nb, d.flat(status, "status", torch.int32),
                               d.stream)
         _check(rc, "kda_conv_bwd")
         return dx, dw, db, dtail
@@ -991,7 +997,7 @@ def scan_bwd(x, dt, A, B, C, cu_seqlens, dy, saved, D=None, z=None, dt_bias=None
              dt_softplus=True, workspace=None, status=None, stream=None):
     """Gradients of scan_fwd, from its inputs, what it saved, dy [T, D] and dfinal_state f32 [N, D, S] (or None): (dx, ddt
     [T, D], dA f32 [D, S], dB, dC [T, G, S], dD f32 [D], dz [T, D], ddt_bias f32 [D], dinitial_state f32 [N, D, S]), None
-    for what the call has not got.  dx, ddt, dB, dC and dz are of x's dtype."""
+    for what the call has not got.  dx, ddt, dB, dC and dz are of x's dtype; their rows of no sequence are not set."""
     N, f32 = _scan_sequences(cu_seqlens), torch.float32
     d = _Device(x, stream)
     with d.guard:
@@ -1003,16 +1009,13 @@ def scan_bwd(x, dt, A, B, C, cu_seqlens, dy, saved, D=None, z=None, dt_bias=None
         if saved.numel() < need:
             raise KDAError(f"saved must hold {need} f32 values, got {saved.numel()}")
         gp, gs = d.rows(dy, "dy", x.dtype, (T, n), n)
-        rows, of = lambda *s: d.new(*s, dtype=x.dtype), lambda have, *s: None if have is None else d.new(*s)
-        dx, ddt, dz = rows(T, n), rows(T, n), None if z is None else rows(T, n)
-        dB, dC, dA = rows(T, G, S), rows(T, G, S), d.new(n, S)
-        dD, dbias, dh = of(D, n), of(dt_bias, n), of(initial_state, N, n, S)
+        dx, ddt, dz, dB, dC = (None if t is None else d.out(None, t) for t in (x, dt, z, B, C))
+        dA, dD, dbias, dh = (None if t is None else torch.empty_like(t) for t in (A, D, dt_bias, initial_state))
         ws, nb = d.workspace(workspace, lib.kda_scan_bwd_workspace_size(N, T, n, G, S))
-        ptr = lambda t: None if t is None else t.data_ptr()
         rc = lib.kda_scan_bwd(*ptrs, d.flat(cu_seqlens, "cu_seqlens", torch.int32), gp,
                               d.flat(dfinal_state, "dfinal_state", shape=(N, n, S)), d.flat(saved, "saved"), N, T, n, G, S,
-                              *strides, gs, int(bool(dt_softplus)), ptr(dx), ptr(ddt), ptr(dA), ptr(dB), ptr(dC), ptr(dD),
-                              ptr(dz), ptr(dbias), ptr(dh), _in_dtype(x), ws, nb, d.flat(status, "status", torch.int32),
+                              *strides, gs, int(bool(dt_softplus)), _at(dx), _at(ddt), _at(dA), _at(dB), _at(dC), _at(dD),
+                              _at(dz), _at(dbias), _at(dh), _in_dtype(x), ws, nb, d.flat(status, "status", torch.int32),
                               d.stream)
         _check(rc, "kda_scan_bwd")
         return dx, ddt, dA, dB, dC, dD, dz, dbias, dh

@@ -3,16 +3,19 @@
 //
 //   h_t = e^{d_t A[c][n]} h_{t-1} + d_t x_t B_t[n],   y_t = (sum_n C_t[n] h_t + D[c] x_t) z_t sigmoid(z_t)
 //
-// What bounds it: instructions.  A token and channel costs 8 bytes (bf16 x,
-// dt, z, y) and, with 16 states, 16 exponentials and 32 pairs of packed fp32
-// operations: about 0.6 cycles of an SM, where 8 bytes take 0.34.
+// What bounds it: exponentials and the instructions around them.  A token and
+// channel costs 8 bytes (bf16 x, dt, z, y) and, with 16 states, 21 special functions (0.66
+// cycles of an SM) and 32 packed pairs of operations (0.5 and more), where 8
+// bytes take 0.34.  16384 tokens x 4096 channels: 306 us in the walk (1.3 cycles) where blocks
+// fill the SMs, 422 with 3.4 blocks an SM.
 //
-// A thread keeps 8 states of a channel, in pairs for the packed operations; S / 8
-// neighbouring lanes share a channel.  Of eight tokens each of these lanes
-// forms the steps, and at the end the outputs, of its own 8 / (S / 8): the steps go round by
-// shuffles, and the lanes' shares of the outputs are added on the way to
-// their token's lane.  (A channel to a thread took as many instructions but
-// half the warps at twice the registers, and 5 cycles an instruction.)  A
+// A thread keeps 8 or 16 states of a channel, in pairs for the packed
+// operations; the lanes that share a channel are neighbours.  Of eight tokens each of
+// them forms the steps, and at the end the outputs, of its own share: the steps
+// go round by shuffles, and the lanes' shares of the outputs are added on the
+// way to their token's lane.  Eight tokens at a time give the long chains of a
+// step (softplus: 20 operations) others to overlap with; with registers for four
+// blocks an SM rather than seven the walk of 16384 tokens took 422 us and not 601.  A
 // block of 128 threads walks its tokens 16 at a time: x, dt and z of the next
 // 16 come by cp.async while these are worked on, and B and C (the same for all
 // channels of a group) are widened to 32 bits once per block, so that a thread
@@ -23,7 +26,7 @@
 // cut into segments: a first kernel forms every segment's own end state from
 // zero and its sum of d (the segment's decay is e^{A sum d}, exactly), a second
 // chains these, and the walk then starts each segment from its true state.  The
-// first kernel costs about 0.8 of the walk, so the cut has to buy more.
+// first kernel costs 0.75 of the walk (233 us beside 306), so the cut has to buy more.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -83,8 +86,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
 #pragma unroll
         for (int i = 0; i < M / 4; ++i) {
             const float4 v = p[i];
-            A2[2 * i] = make_float2(v.x * kLog2e, v.y * kLog2e);
-            A2[2 * i + 1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+            A2[2 * i] = make_float2(v.x, v.y);
+            A2[2 * i + 1] = make_float2(v.z, v.w);
             const float4 w = h0 ? q[i] : make_float4(0.f, 0.f, 0.f, 0.f);
             h2[2 * i] = make_float2(w.x, w.y);
             h2[2 * i + 1] = make_float2(w.z, w.w);
@@ -169,6 +172,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
         put(0);
         bc_store(0);
     }
+#pragma unroll
+    for (int i = 0; i < M / 2; ++i) A2[i] = make_float2(rate(A2[i].x), rate(A2[i].y));
     for (int i = 0; i < steps; ++i) {
         if constexpr (VEC) cp_async_wait_all();
         __syncthreads();
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(256) kda_scan_chain_kernel(ScanArgs a, int S, 
     if (count < 2) return;
     const int c = (int)(e / S);
     const long long u0 = b0 / a.seg + s;
-    const float A = a.A[e] * kLog2e;
+    const float A = rate(a.A[e]);
     float *st = a.seg_state + u0 * size + e;
     const float *sum = a.seg_sum + u0 * a.D + c;
     const float *first = reverse ? a.dfinal : a.initial_state;
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(256, 4) kda_scan_step_kernel(ScanArgs a, int r
     const bool live = at < a.D;
     const int c = live ? at : a.D - 1, grp = c / per;
     float4 A4 = reinterpret_cast<const float4 *>(a.A + (size_t)c * S)[ln];
-    const float2 A[2] = {make_float2(A4.x * kLog2e, A4.y * kLog2e), make_float2(A4.z * kLog2e, A4.w * kLog2e)};
+    const float2 A[2] = {make_float2(rate(A4.x), rate(A4.y)), make_float2(rate(A4.z), rate(A4.w))};
     const float skip = a.Dskip ? a.Dskip[c] : 0.f, bias = a.dt_bias ? a.dt_bias[c] : 0.f;
     const E *x = static_cast<const E *>(a.x) + c, *dt = static_cast<const E *>(a.dt) + c, *z = static_cast<const E *>(a.z) + c;
     const E *B = static_cast<const E *>(a.B) + (size_t)grp * S + 4 * ln, *C = static_cast<const E *>(a.C) + (size_t)grp * S + 4 * ln;

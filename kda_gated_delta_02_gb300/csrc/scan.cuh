@@ -12,6 +12,13 @@ constexpr int kThreads = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSaveEvery = kScanSaveEvery;
 
+// A in powers of two.  A rate of -infinity is held finite, so that a step of 0
+// (past a sequence's end) leaves a state as it is.
+__device__ __forceinline__ float rate(float A) {
+    const float r = A * kLog2e;
+    return r < -3.0e38f ? -3.0e38f : r;
+}
+
 // Segment j of sequence s (tokens [a, b), cut every `seg` tokens; 0: not cut)
 // is unit floor(a / seg) + s + j: distinct, in order, below floor(T / seg) + N.
 struct Segment {

@@ -7,19 +7,24 @@
 //   dB_t = sum over channels of l_t d_t x_t,  dC_t = sum over channels of e_t h_t
 //   dA = sum_t d_t l_t a_t h_{t-1},  dD = sum_t e_t x_t,  dz_t = dy_t (sum_n C_t h_t + D x_t) sigma'(z_t)
 //
-// What bounds it: instructions, as the forward only more so: 15 packed
-// operations and four exponentials (two of them the recomputed states') per pair of
-// states, and the sums of dB and dC over channels.  A thread keeps 2 channels of 8 states; S / 8 lanes
+// What bounds it: instructions and shared memory.  A pair of states costs 15
+// packed operations and four exponentials (two of them the recomputed states'), and the sums
+// of dB and dC over channels go through shared memory: 8 sequences of 2048 tokens x
+// 4096 channels in 16 x 152 blocks 1.25 ms, 5.4 cycles of an SM for a token and channel, issue slots
+// 55 % and shared memory 68 % busy.  A thread keeps 2 channels of 8 states; S / 8 lanes
 // share a pair of channels, and the tokens' own work (steps, gates, outputs) is dealt
 // out to them.  The eight tokens from a saved state run forward with every
 // second state kept in shared memory, then backward: of the two tokens that
 // share a kept state H, the later one goes forward from it (a H, a H + b) and
 // the earlier one back (H - b, H), neither with an operation more.  The sums over channels
-// add two in a thread's registers, then go through shared memory, four floats
-// at a time: 4 stores, 4 loads and 20 additions and exchanges per token, where
+// add two in a thread's registers, then four floats at a time in shared
+// memory: 4 stores, 4 loads and 20 additions and exchanges per token, where
 // exchanges alone would take 62.  A block's four warps add theirs once per eight
 // tokens, and a second kernel adds the blocks' in order.  Sums along the tokens (dA, dD,
-// ddt_bias) are taken over eight tokens first.
+// ddt_bias) are taken over eight tokens first.  The rows of the eight tokens
+// before are in registers already, those of the eight before them on their way into L2
+// (1.60 ms without).  Saved states cost 8 bytes a token and channel at 16
+// states, written and read once; every sixteenth token would halve them for a sixth more operations.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -107,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
 #pragma unroll
         for (int i = 0; i < M / 4; ++i) {
             const float4 v = reinterpret_cast<const float4 *>(a.A + o)[i];
-            A2[q][2 * i] = make_float2(v.x * kLog2e, v.y * kLog2e), A2[q][2 * i + 1] = make_float2(v.z * kLog2e, v.w * kLog2e);
+            A2[q][2 * i] = make_float2(rate(v.x), rate(v.y)), A2[q][2 * i + 1] = make_float2(rate(v.z), rate(v.w));
             const float4 w = from && (q ? two : one) ? reinterpret_cast<const float4 *>(from + o)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
             carry[q][2 * i] = make_float2(w.x, w.y), carry[q][2 * i + 1] = make_float2(w.z, w.w);
             dA[q][2 * i] = dA[q][2 * i + 1] = both(0.f);

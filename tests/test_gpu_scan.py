@@ -210,6 +210,30 @@ def test_bad_sequences_are_reported_and_skipped():
         assert status.item() == kda.STATUS_BAD_SEQLENS, cu
 
 
+def test_no_tokens():
+    """Empty sequences alone: states pass through, gradients too; sums are zero."""
+    s = _inputs(0, 24, 1, 16, torch.bfloat16, 2)
+    cu = _cu([0, 0])
+    y, fin, saved = kda.scan_fwd(*_args(s), cu, initial_state=s["h0"], D=s["D"], dt_bias=s["dt_bias"], save=True)
+    assert y.shape == (0, 24) and torch.equal(fin, s["h0"])
+    grads = kda.scan_bwd(*_args(s), cu, s["dy"], saved, initial_state=s["h0"], dfinal_state=s["dfinal"], D=s["D"], dt_bias=s["dt_bias"])
+    assert torch.equal(grads[8], s["dfinal"]) and not any(grads[i].any() for i in (2, 5, 7))
+
+
+@pytest.mark.parametrize("n", [1, 8, 13, 700])
+def test_rates_of_infinity_forget(n):
+    """A = -inf: a state is what the last token put there, to the end of a tile that the sequence does not fill."""
+    s = _inputs(n, 16, 1, 16, torch.float32)
+    s["A"][3, 5] = float("-inf")
+    y, fin = kda.scan_fwd(*_args(s), _cu([n]), initial_state=s["h0"])
+    v = s["dt"][-1, 3].double()
+    want = torch.nn.functional.softplus(v) * s["x"][-1, 3].double() * s["B"][-1, 0, 5].double()
+    assert torch.isfinite(y).all() and torch.isfinite(fin).all() and abs(fin[0, 3, 5].double() - want) <= 16 * ref.U * abs(want)
+    state = s["h0"].clone()
+    kda.scan_step(s["x"][-1:], s["dt"][-1:], s["A"], s["B"][-1:], s["C"][-1:], state)
+    assert abs(state[0, 3, 5].double() - want) <= 16 * ref.U * abs(want)
+
+
 @pytest.mark.parametrize("lens,D", [([300, 3, 500, 77], 64), ([100] * 40, 1024)])
 def test_same_bits_again_and_captured(lens, D):
     s = _inputs(sum(lens), D, 1, 16, torch.bfloat16, len(lens))
