@@ -1487,7 +1487,7 @@ int kda_norm_bwd(const void *x, const void *dy, const float *weight, long long r
     if (sums && err == cudaSuccess) {
         kda::SumRowsArgs s = {a.parts, rows > 0 ? kda::norm_bwd_blocks(a, dtype == KDA_DTYPE_BF16, sm_count()) : 0, 2 * d,
                               {dweight, dbias, nullptr}, {0, d, 2 * d, 2 * d}, {1, 1, 1}};
-        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, st); });
+        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, sm_count(), st); });
     }
     return cuda_status(err);
 }
@@ -1573,7 +1573,7 @@ int kda_conv_bwd(const void *x, const int32_t *cu_seqlens, const float *w, const
     });
     if (sums && err == cudaSuccess) {
         kda::SumRowsArgs s = {a.parts, a.runs, (W + 1) * C, {dw, dbias, nullptr}, {0, W * C, (W + 1) * C, (W + 1) * C}, {W, 1, 1}};
-        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, st); });
+        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, sm_count(), st); });
     }
     return cuda_status(err);
 }
@@ -1790,7 +1790,7 @@ int kda_scan_bwd(const void *x, const void *dt, const float *A, const void *B, c
     if (err == cudaSuccess) {
         const int n = (int)DS;
         kda::SumRowsArgs s = {a.parts, L.units, (int)kda::scan_parts_width(D, S), {dA, dskip, ddt_bias}, {0, n, n + D, n + 2 * D}, {1, 1, 1}};
-        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, st); });
+        err = timed_launch(KDA_KERNEL_SUMS, st, [&] { return kda::launch_sum_rows(s, sm_count(), st); });
     }
     return cuda_status(err);
 }

@@ -7,18 +7,21 @@
 //   q_t = dy_t y'(p_t),  dx_e = sum_k w[c][W - 1 - k] q_{e + k} (same sequence) + what the new tail passes back
 //   dw[c][j] = sum_t q_t x_{t - (W - 1) + j},  dbias = sum_t q_t
 //
-// What bounds it: bytes (x in, y out; backward x and dy in, dx out), once the
-// instructions are few enough: about 10 per element forward, 19 backward, in packed pairs of
-// channels.  A thread owns four neighbouring channels and walks a run of tokens, with the
-// W - 1 rows behind it in registers and the next four rows asked for; only
-// W - 1 rows of a run of 8 to 128 are read twice, and the neighbouring run has
-// them in L2.  (Eight channels a thread had 118 registers and half the warps: 149 us
-// for 16384 tokens x 8192 channels.)  Runs do not stop at sequence ends, so short sequences
-// cost no threads: where one ends the window is filled from the next one's
-// tail, token by token; four tokens of one sequence go without such checks.
-// The backward walks W - 1 tokens past its run, for the gradients that
-// reach back into it.  Its sums for dw leave as one partial row per run and are
-// added up in a fixed order.
+// What bounds it: bytes (x in, y out; backward x and dy in, dx out), and nearly
+// as much the instructions, which go in packed pairs of channels.  A thread owns four
+// neighbouring channels and walks a run of tokens, with the W - 1 rows behind
+// it in registers and the next four rows asked for; only W - 1 rows of a run of
+// 8 to 128 are read twice, and the neighbouring run has them in L2.  Runs do
+// not stop at sequence ends, so short sequences cost no threads: where one ends
+// the window is filled from the next one's tail, token by token; four tokens of
+// one sequence go without such checks.  The backward walks W - 1 tokens past
+// its run, for the gradients that reach back into it.  Its sums for dw leave as
+// one partial row per run and are added up in a fixed order.
+// 16384 tokens x 8192 channels, bf16: forward 97 us (5.5 TB/s), backward 160 us
+// (5.0 TB/s) and 10 for the sums; 16384 ragged tokens x 36864 channels 436 us (6.1
+// TB/s).  Eight channels a thread with checks at every token took 149 us, 64
+// registers (eight blocks an SM) rather than 71 gained 5 %; two channels a thread in
+// the backward lost 16 %, its 126 registers forced to 102 spill and double it.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -42,6 +45,16 @@ struct Walk {
 // in order and in [0, T]; a caller skips tokens before its start.
 __device__ __forceinline__ Walk next_sequence(const int32_t *cu, int N, int T, int s, int t) {
     for (; s < N; ++s) {
+        if (cu[s + 1] <= t) {  // empty ones, and as many as there are: by bisection
+            int lo = s + 1, hi = N;
+            while (lo < hi) {
+                const int mid = lo + (hi - lo) / 2;
+                if (cu[mid + 1] > t) hi = mid;
+                else lo = mid + 1;
+            }
+            s = lo;
+            if (s >= N) break;
+        }
         const int a = cu[s], b = cu[s + 1];
         if (a >= 0 && a < b && b <= T && b > t) return {s, a, b};
     }
@@ -91,7 +104,7 @@ __device__ __forceinline__ void load_row(Vec<BF16, V> &r, const Elem<BF16> *p, b
     else r.zero();
 }
 
-template <bool BF16, int V, int W>
+template <bool BF16, int V, int W, bool ACT>
 __global__ void __launch_bounds__(kThreads, 8) kda_conv_fwd_kernel(ConvArgs a) {
     using E = Elem<BF16>;
     const int c = (blockIdx.y * kThreads + threadIdx.x) * V;
@@ -138,28 +151,30 @@ __global__ void __launch_bounds__(kThreads, 8) kda_conv_fwd_kernel(ConvArgs a) {
     };
     if (q.a <= ta) fill(ta);
     // the output of the row that win[W - 1] holds, and the window moved on
-    auto token = [&](int t) {
+    auto token = [&](E *to) {
         Vec<BF16, V> out;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             float2 p = bias[i];
 #pragma unroll
             for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j][i], p);
-            out.set_pair(i, a.act ? silu2(p) : p);
+            out.set_pair(i, ACT ? silu2(p) : p);
         }
-        out.store(y + (long long)t * a.y_stride);
+        out.store(to);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
             for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i];
     };
     Vec<BF16, V> next[U];
+    const E *ahead = x + (long long)ta * a.x_stride;  // of the rows asked for next
     auto ask = [&](int t0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t0 + u < tb) next[u].load(x + (long long)(t0 + u) * a.x_stride);
+        for (int u = 0; u < U; ++u, ahead += a.x_stride)
+            if (t0 + u < tb) next[u].load(ahead);
     };
     ask(ta);
+    E *yp = y + (long long)ta * a.y_stride;
 #pragma unroll 1
     for (int t0 = ta; t0 < tb; t0 += U) {
         Vec<BF16, V> now[U];
@@ -172,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 8) kda_conv_fwd_kernel(ConvArgs a) {
             for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) win[W - 1][i] = now[u].pair(i);
-                token(t0 + u);
+                token(yp);
+                yp += a.y_stride;
             }
         } else {
 #pragma unroll 1
@@ -184,15 +200,16 @@ __global__ void __launch_bounds__(kThreads, 8) kda_conv_fwd_kernel(ConvArgs a) {
                 if (t < q.a) continue;  // rows of no sequence
                 if (t == q.a && t > ta) fill(t);
                 load_pairs<BF16, V>(win[W - 1], x + (long long)t * a.x_stride, true);
-                token(t);
+                token(y + (long long)t * a.y_stride);
             }
+            yp += U * a.y_stride;
         }
     }
 }
 
 // dy of its own type (DYBF16): a following layer's gradients may be 32-bit
 // beside bf16 activations.
-template <bool BF16, bool DYBF16, int V, int W>
+template <bool BF16, bool DYBF16, int V, int W, bool ACT>
 __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
     using E = Elem<BF16>;
     using G = Elem<DYBF16>;
@@ -287,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             float2 d = g[W - 1][i];
-            if (a.act) {
+            if constexpr (ACT) {
                 float2 p = bias[i];
 #pragma unroll
                 for (int j = 0; j < W; ++j) p = __ffma2_rn(w[i][j], win[j][i], p);
@@ -304,15 +321,18 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
     const int end = min(tb + W - 1, a.T);  // the walk's own tokens end at tb
     Vec<BF16, V> next[U];
     Vec<DYBF16, V> dnext[U];
+    const E *ahead = x + (long long)ta * a.x_stride;
+    const G *dahead = dy + (long long)ta * a.dy_stride;
     auto ask = [&](int t0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u, ahead += a.x_stride, dahead += a.dy_stride)
             if (t0 + u < tb) {
-                next[u].load(x + (long long)(t0 + u) * a.x_stride);
-                dnext[u].load(dy + (long long)(t0 + u) * a.dy_stride);
+                next[u].load(ahead);
+                dnext[u].load(dahead);
             }
     };
     ask(ta);
+    E *to = dx + ((long long)ta - (W - 1)) * a.dx_stride;  // of the row that token t0 completes
 #pragma unroll 1
     for (int t0 = ta; t0 < end; t0 += U) {
         Vec<BF16, V> now[U];
@@ -334,10 +354,12 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
                     for (int k = 0; k < W; ++k) o = __ffma2_rn(w[i][W - 1 - k], g[k][i], o);
                     out.set_pair(i, o);
                 }
-                out.store(dx + (long long)(t0 + u - (W - 1)) * a.dx_stride);
+                out.store(to);
+                to += a.dx_stride;
                 shift();
             }
         } else {
+            to += U * a.dx_stride;
 #pragma unroll 1
             for (int t = t0; t < min(t0 + U, end); ++t) {
                 if (t >= q.b) {
@@ -408,31 +430,33 @@ __global__ void __launch_bounds__(kThreads) kda_conv_step_kernel(ConvArgs a) {
     }
 }
 
+unsigned tiles(const ConvArgs &a, int v) { return (unsigned)((a.C + kThreads * v - 1) / (kThreads * v)); }
+
+template <int W, bool ACT>
+cudaError_t launch_walk(const ConvArgs &a, bool backward, bool bf16, bool dy_bf16, cudaStream_t st) {
+    const int v = a.wide ? 4 : 1;
+    const dim3 grid((unsigned)(a.runs + (a.N + kTailRows - 1) / kTailRows), tiles(a, v));
+    auto go = [&](void (*kern)(ConvArgs)) {
+        kern<<<grid, kThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    };
+    if (!backward) {
+        if (bf16) return go(a.wide ? kda_conv_fwd_kernel<true, 4, W, ACT> : kda_conv_fwd_kernel<true, 1, W, ACT>);
+        return go(a.wide ? kda_conv_fwd_kernel<false, 4, W, ACT> : kda_conv_fwd_kernel<false, 1, W, ACT>);
+    }
+    if (bf16 && dy_bf16) return go(a.wide ? kda_conv_bwd_kernel<true, true, 4, W, ACT> : kda_conv_bwd_kernel<true, true, 1, W, ACT>);
+    if (bf16) return go(a.wide ? kda_conv_bwd_kernel<true, false, 4, W, ACT> : kda_conv_bwd_kernel<true, false, 1, W, ACT>);
+    return go(a.wide ? kda_conv_bwd_kernel<false, false, 4, W, ACT> : kda_conv_bwd_kernel<false, false, 1, W, ACT>);
+}
+
 template <int W>
 cudaError_t launch_w(const ConvArgs &a, int what, bool bf16, bool dy_bf16, cudaStream_t st) {
-    auto tiles = [&](int v) { return (unsigned)((a.C + kThreads * v - 1) / (kThreads * v)); };
-    const unsigned gx = (unsigned)(a.runs + (a.N + kTailRows - 1) / kTailRows);
-    if (what == 0) {
-        if (bf16 && a.wide) kda_conv_fwd_kernel<true, 4, W><<<dim3(gx, tiles(4)), kThreads, 0, st>>>(a);
-        else if (bf16) kda_conv_fwd_kernel<true, 1, W><<<dim3(gx, tiles(1)), kThreads, 0, st>>>(a);
-        else if (a.wide) kda_conv_fwd_kernel<false, 4, W><<<dim3(gx, tiles(4)), kThreads, 0, st>>>(a);
-        else kda_conv_fwd_kernel<false, 1, W><<<dim3(gx, tiles(1)), kThreads, 0, st>>>(a);
-    } else if (what == 1) {
-        // (four channels a thread: eight would hold 136 registers of windows and sums)
-        const dim3 g4(gx, tiles(4)), g1(gx, tiles(1));
-        if (bf16 && dy_bf16 && a.wide) kda_conv_bwd_kernel<true, true, 4, W><<<g4, kThreads, 0, st>>>(a);
-        else if (bf16 && dy_bf16) kda_conv_bwd_kernel<true, true, 1, W><<<g1, kThreads, 0, st>>>(a);
-        else if (bf16 && a.wide) kda_conv_bwd_kernel<true, false, 4, W><<<g4, kThreads, 0, st>>>(a);
-        else if (bf16) kda_conv_bwd_kernel<true, false, 1, W><<<g1, kThreads, 0, st>>>(a);
-        else if (a.wide) kda_conv_bwd_kernel<false, false, 4, W><<<g4, kThreads, 0, st>>>(a);
-        else kda_conv_bwd_kernel<false, false, 1, W><<<g1, kThreads, 0, st>>>(a);
-    } else {
-        const unsigned R = (unsigned)a.runs;
-        if (bf16 && a.wide) kda_conv_step_kernel<true, 8, W><<<R * tiles(8), kThreads, 0, st>>>(a);
-        else if (bf16) kda_conv_step_kernel<true, 1, W><<<R * tiles(1), kThreads, 0, st>>>(a);
-        else if (a.wide) kda_conv_step_kernel<false, 4, W><<<R * tiles(4), kThreads, 0, st>>>(a);
-        else kda_conv_step_kernel<false, 1, W><<<R * tiles(1), kThreads, 0, st>>>(a);
-    }
+    if (what < 2) return a.act ? launch_walk<W, true>(a, what == 1, bf16, dy_bf16, st) : launch_walk<W, false>(a, what == 1, bf16, dy_bf16, st);
+    const unsigned R = (unsigned)a.runs;
+    if (bf16 && a.wide) kda_conv_step_kernel<true, 8, W><<<R * tiles(a, 8), kThreads, 0, st>>>(a);
+    else if (bf16) kda_conv_step_kernel<true, 1, W><<<R * tiles(a, 1), kThreads, 0, st>>>(a);
+    else if (a.wide) kda_conv_step_kernel<false, 4, W><<<R * tiles(a, 4), kThreads, 0, st>>>(a);
+    else kda_conv_step_kernel<false, 1, W><<<R * tiles(a, 1), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -271,7 +271,7 @@ struct SumRowsArgs {
     float *out[kOuts];
     int begin[kOuts + 1], cols[kOuts];
 };
-cudaError_t launch_sum_rows(const SumRowsArgs &a, cudaStream_t st);
+cudaError_t launch_sum_rows(const SumRowsArgs &a, int sms, cudaStream_t st);
 
 // Short causal convolution (conv.cu).
 struct ConvArgs {

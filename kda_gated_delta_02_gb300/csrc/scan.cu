@@ -343,7 +343,10 @@ __global__ void __launch_bounds__(256, 4) kda_scan_step_kernel(ScanArgs a, int r
     const E *x = static_cast<const E *>(a.x) + c, *dt = static_cast<const E *>(a.dt) + c, *z = static_cast<const E *>(a.z) + c;
     const E *B = static_cast<const E *>(a.B) + (size_t)grp * S + 4 * ln, *C = static_cast<const E *>(a.C) + (size_t)grp * S + 4 * ln;
     const int r0 = chunk * rows, r1 = min(r0 + rows, a.N);
-    for (int r = r0; r < r1; r += U) {
+    const size_t DS = (size_t)a.D * S;
+    float *sp = a.state + r0 * DS + (size_t)c * S + 4 * ln;
+    B += r0 * a.b_stride, C += r0 * a.c_stride;
+    for (int r = r0; r < r1; r += U, sp += U * DS, B += U * a.b_stride, C += U * a.c_stride) {
         float4 h[U];
         Vec<BF16, 4> vb[U], vc[U];
         float xv[OWN], d[OWN], zv[OWN], in[OWN], y[U];
@@ -356,9 +359,14 @@ __global__ void __launch_bounds__(256, 4) kda_scan_step_kernel(ScanArgs a, int r
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long q = min(r + u, r1 - 1);
-            h[u] = reinterpret_cast<const float4 *>(a.state + ((size_t)q * a.D + c) * S)[ln];
-            const E *bp = B + q * a.b_stride, *cp = C + q * a.c_stride;
+            if (r + u >= r1) {
+                h[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                vb[u].zero();
+                vc[u].zero();
+                continue;
+            }
+            h[u] = *reinterpret_cast<const float4 *>(sp + u * DS);
+            const E *bp = B + u * a.b_stride, *cp = C + u * a.c_stride;
             if (a.wide_bc) {
                 vb[u].load(bp);
                 vc[u].load(cp);
@@ -387,7 +395,7 @@ __global__ void __launch_bounds__(256, 4) kda_scan_step_kernel(ScanArgs a, int r
             }
             y[u] = s.x + s.y;
             if (live && r + u < r1)
-                reinterpret_cast<float4 *>(a.state + ((size_t)(r + u) * a.D + c) * S)[ln] = make_float4(k[0].x, k[0].y, k[1].x, k[1].y);
+                *reinterpret_cast<float4 *>(sp + u * DS) = make_float4(k[0].x, k[0].y, k[1].x, k[1].y);
         }
         // a channel's lanes' shares added up, each request's in its lane
 #pragma unroll
