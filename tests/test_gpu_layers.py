@@ -162,6 +162,31 @@ def test_guard_bands(dtype):
             assert (f[:4096] == 7).all() and (f[-4096:] == 7).all(), (name, k)
 
 
+@pytest.mark.parametrize("width", [40, 41])
+def test_outputs_beside_inputs_in_one_buffer(width):
+    """Inputs and outputs as neighbouring columns of the same rows (width: on and off 16-byte boundaries)."""
+    lens, n = [50, 7], 57
+    cu, r = _cu(lens), _gen(11)
+    rows = r(n, 6 * width).to(BF)
+    col = lambda i: rows[:, i * width:(i + 1) * width]
+    x, w, nw = col(0).clone(), r(width, 4), r(width)
+    want_norm, want_conv = kda.norm_fwd(x, nw), kda.conv_fwd(x, w, cu)[0]
+    dt, B, C, A = r(n, width).to(BF), r(n, 1, 16).to(BF), r(n, 1, 16).to(BF), -torch.exp(r(width, 16))
+    want_scan = kda.scan_fwd(x, dt, A, B, C, cu, z=x)[0]
+    want_dx = kda.conv_bwd(x, w, cu, x)[0]
+    kda.norm_fwd(col(0), nw, out=col(1))
+    kda.conv_fwd(col(0), w, cu, out=col(2))
+    kda.scan_fwd(col(0), dt, A, B, C, cu, z=col(0), out=col(3))
+    kda.conv_bwd(col(0), w, cu, col(0), dx=col(4))
+    for i, want in enumerate((x, want_norm, want_conv, want_scan, want_dx)):
+        assert torch.equal(col(i), want), i
+    for bad in (lambda: kda.conv_fwd(col(0), w, cu, out=rows[:, width - 8:2 * width - 8]),
+                lambda: kda.scan_fwd(col(0), dt, A, B, C, cu, out=rows[:, 8:width + 8]),
+                lambda: kda.norm_fwd(col(0), nw, out=rows[:, 1:width + 1])):
+        with pytest.raises(kda.KDAError, match="invalid argument"):
+            bad()
+
+
 def test_streams_and_two_calls_at_once():
     """Calls on a stream of their own while the current one is busy; two of them side by side; the same bits."""
     calls = _calls(BF)

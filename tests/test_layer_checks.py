@@ -38,6 +38,8 @@ def no_cuda(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(kda, "_raw_stream", lambda device: 0)
 
+    real = torch.empty_like
+    monkeypatch.setattr(torch, "empty_like", lambda t: Fake(*t.shape, dtype=t.dtype) if isinstance(t, Fake) else real(t))
     monkeypatch.setattr(kda._Device, "new", lambda self, *s, dtype=F32: Fake(*s, dtype=dtype))
     monkeypatch.setattr(kda._Device, "out", lambda self, t, like: Fake(*like.shape, dtype=like.dtype) if t is None else t)
 
@@ -109,6 +111,22 @@ def test_norm_rejects():
         kda.norm_bwd(x, Fake(7, 12))
     with pytest.raises(kda.KDAError, match="dx must have shape"):
         kda.norm_bwd(x, x, dx=Fake(7, 11, dtype=BF))
+
+
+def test_another_device_becomes_the_current_one(monkeypatch):
+    """Tensors on a device that is not the current one: the call goes there, with that device's current stream."""
+    monkeypatch.setattr(torch.cuda, "device", lambda index: ("device", index))
+    monkeypatch.setattr(kda, "_raw_stream", lambda device: 0x100 + device)
+    there, here = kda._Device(Fake(3, device=1), None), kda._Device(Fake(3), None)
+    assert there.guard == ("device", 1) and there.stream == 0x101 and here.guard is kda._here and here.stream == 0x100
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0x77
+
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: ("stream", s))
+    assert kda._Device(Fake(3, device=1), Stream).guard == ("stream", Stream) and kda._Device(Fake(3, device=1), Stream).stream == 0x77
+    with pytest.raises(kda.KDAError, match="stream is on cuda:1"):
+        kda._Device(Fake(3), Stream)
 
 
 def _scan(**kw):
