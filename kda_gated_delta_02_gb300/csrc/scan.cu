@@ -30,6 +30,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kda_internal.h"
 #include "layer.cuh"
 #include "scan.cuh"
@@ -186,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
         const float *bt = bc + (i & 1) * kTile * 2 * S + ln * M + (MODE == REVERSE ? S : 0);
         const int rows = min(kTile, count - i * kTile);
         // eight tokens at a time.  Past the end the step is 0: decay 1 and nothing added.
-#pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += GROUP) {
+        auto group = [&](auto all, int r0) {
+            constexpr bool ALL = decltype(all)::value;  // no token past the end among the eight
             const int mine = r0 + ln * OWN;  // the lane's own tokens
             float d[OWN], in[OWN], y[GROUP];
 #pragma unroll
@@ -197,12 +199,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
                 float2 x = make_float2((float)xs[p], (float)xs[q]), sig;
                 float2 v = __fadd2_rn(make_float2((float)ds[p], (float)ds[q]), both(bias));
                 if (a.dt_softplus) v = softplus2(v, sig);
-                if (mine + j >= rows) v.x = 0.f;
-                if (mine + j + NEXT >= rows) v.y = 0.f;
+                if (!ALL && mine + j >= rows) v.x = 0.f;
+                if (!ALL && mine + j + NEXT >= rows) v.y = 0.f;
                 if (MODE == REVERSE && third) x = __fmul2_rn(x, silu2(make_float2((float)zs[p], (float)zs[q])));
                 if (MODE != REVERSE) x = __fmul2_rn(v, x);
                 d[j] = v.x, d[j + NEXT] = v.y;
-                in[j] = mine + j < rows ? x.x : 0.f, in[j + NEXT] = mine + j + NEXT < rows ? x.y : 0.f;
+                in[j] = ALL || mine + j < rows ? x.x : 0.f, in[j + NEXT] = ALL || mine + j + NEXT < rows ? x.y : 0.f;
                 if (MODE != WALK) sum += NEXT ? v.x + v.y : v.x;
             }
             if constexpr (MODE == WALK) {
@@ -258,10 +260,15 @@ __global__ void __launch_bounds__(kThreads, 4) kda_scan_kernel(ScanArgs a) {
                     const int p = (mine + j) * CH, q = (mine + j + NEXT) * CH;
                     float2 out = __ffma2_rn(both(skip), make_float2((float)xs[p], (float)xs[q]), make_float2(y[j], y[j + NEXT]));
                     if (third) out = __fmul2_rn(out, silu2(make_float2((float)zs[p], (float)zs[q])));
-                    if (live && mine + j < rows) yp[j * a.y_stride] = (E)out.x;
-                    if (NEXT && live && mine + j + NEXT < rows) yp[(j + NEXT) * a.y_stride] = (E)out.y;
+                    if (live && (ALL || mine + j < rows)) yp[j * a.y_stride] = (E)out.x;
+                    if (NEXT && live && (ALL || mine + j + NEXT < rows)) yp[(j + NEXT) * a.y_stride] = (E)out.y;
                 }
             }
+        };
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += GROUP) {
+            if (r0 + GROUP <= rows) group(std::true_type(), r0);
+            else group(std::false_type(), r0);
         }
         if (more) {
             put(i + 1);
