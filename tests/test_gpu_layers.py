@@ -187,6 +187,46 @@ def test_outputs_beside_inputs_in_one_buffer(width):
             bad()
 
 
+def test_offsets_past_32_bits():
+    """Rows, saved states and partial sums whose places pass 2^31 elements: the last rows equal those of calls on them alone."""
+    r = _gen(13)
+    # norm: 17M rows of 128
+    x = r(1 << 14, 128).to(BF).repeat(1040, 1)
+    assert x.numel() > 1 << 31
+    w = r(128)
+    y = kda.norm_fwd(x, w)
+    assert torch.equal(y[-(1 << 14):], y[:1 << 14]) and torch.equal(y[-5:], kda.norm_fwd(x[-5:].clone(), w))
+    dx = kda.norm_bwd(x, x, w)[0]
+    assert torch.equal(dx[-(1 << 14):], dx[:1 << 14])
+    del x, y, dx
+    # convolution: 70,000 tokens of 32,768 channels in two sequences, the second the last 100
+    T, C = 70000, 32768
+    x, w, cu = r(1000, C).to(BF).repeat(70, 1), 0.5 * r(C, 4), _cu([T - 100, 100])
+    assert x.numel() > 1 << 31
+    y, tail = kda.conv_fwd(x, w, cu)
+    few = kda.conv_fwd(x[-100:].clone(), w, _cu([100]))
+    assert torch.equal(y[-100:], few[0]) and torch.equal(tail[1:], few[1])
+    dx = kda.conv_bwd(x, w, cu, x)[0]
+    assert torch.equal(dx[-100:], kda.conv_bwd(x[-100:].clone(), w, _cu([100]), x[-100:].clone())[0])
+    del x, y, dx
+    # scan: states of 4,096 channels saved 33,000 times
+    T, D, S, last = 264000, 4096, 16, 100
+    x, dt = (r(1000, D).to(BF).repeat(264, 1) for _ in range(2))
+    B, C = (r(T, 1, S).to(BF) for _ in range(2))
+    A, bias, cu = -torch.exp(r(D, S)), -3 + r(D), _cu([T - last, last])
+    y, fin, saved = kda.scan_fwd(x, dt, A, B, C, cu, dt_bias=bias, save=True)
+    assert saved.numel() > 1 << 31
+    end = [t[-last:].clone() for t in (x, dt, B, C)]
+    want = kda.scan_fwd(end[0], end[1], A, end[2], end[3], _cu([last]), dt_bias=bias, save=True)
+    # (one is cut into segments, the other is not: the same states but for roundings)
+    near = lambda p, q: (p.double() - q.double()).norm() <= 2.0 ** -8 * q.double().norm()
+    assert near(y[-last:], want[0]) and near(fin[1], want[1][0])
+    got = kda.scan_bwd(x, dt, A, B, C, cu, x, saved, dt_bias=bias)
+    few = kda.scan_bwd(end[0], end[1], A, end[2], end[3], _cu([last]), end[0], want[2], dt_bias=bias)
+    for i in (0, 1, 3, 4):
+        assert near(got[i][-last:], few[i]), i
+
+
 def test_streams_and_two_calls_at_once():
     """Calls on a stream of their own while the current one is busy; two of them side by side; the same bits."""
     calls = _calls(BF)
