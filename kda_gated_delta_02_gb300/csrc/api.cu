@@ -1616,7 +1616,7 @@ static int scan_shape(int N, int T, int D, int G, int S, int dtype) {
 // sequences' blocks cover the SMs (twice forward, four times backward: half
 // the threads), only sequences of over four times the mean length are cut (of
 // over twice: 32 prompts of 0 to 4096 tokens took 1.11 ms and not 0.82); else all are, for
-// 16 blocks per SM (16384 tokens x 4096 channels: 540 us; with 4, 609).
+// 16 blocks per SM (16384 tokens x 4096 channels: 540 us, with 4 609).
 static int scan_segment(int N, int T, int D, int G, int S, bool backward) {
     if (T < 512 || N > kMaxGridY) return 0;
     const int ch = backward ? kda::scan_bwd_channels(S) : kda::scan_channels(S), sms = sm_count();

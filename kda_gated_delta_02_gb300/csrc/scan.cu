@@ -3,18 +3,18 @@
 //
 //   h_t = e^{d_t A[c][n]} h_{t-1} + d_t x_t B_t[n],   y_t = (sum_n C_t[n] h_t + D[c] x_t) z_t sigmoid(z_t)
 //
-// What bounds it: exponentials and the instructions around them.  A token and
-// channel costs 8 bytes (bf16 x, dt, z, y) and, with 16 states, 21 special functions (0.66
-// cycles of an SM) and 32 packed pairs of operations (0.5 and more), where 8
-// bytes take 0.34.  16384 tokens x 4096 channels: 306 us in the walk (1.3 cycles) where blocks
-// fill the SMs, 422 with 3.4 blocks an SM.
+// What bounds it: issue slots.  A token and channel costs 8 bytes (bf16 x, dt,
+// z, y) and, with 16 states, 20 special functions (0.6 cycles of an SM) and 32 packed
+// pairs of operations, which take two slots each (0.5), beside the exponentials', the
+// loads' and the token's own slots (0.55), where 8 bytes take 0.34.  16384 tokens x 4096 channels: 295 us in the
+// walk (1.27 cycles) where blocks fill the SMs, 400 with 3.4 blocks an SM.
 //
 // A thread keeps 8 or 16 states of a channel, in pairs for the packed
 // operations; the lanes that share a channel are neighbours.  Of eight tokens each of
 // them forms the steps, and at the end the outputs, of its own share: the steps
 // go round by shuffles, and the lanes' shares of the outputs are added on the
 // way to their token's lane.  Eight tokens at a time give the long chains of a
-// step (softplus: 20 operations) others to overlap with; with registers for four
+// step (softplus: 13 operations) others to overlap with; with registers for four
 // blocks an SM rather than seven the walk of 16384 tokens took 422 us and not 601.  A
 // block of 128 threads walks its tokens 16 at a time: x, dt and z of the next
 // 16 come by cp.async while these are worked on, and B and C (the same for all
@@ -26,7 +26,7 @@
 // cut into segments: a first kernel forms every segment's own end state from
 // zero and its sum of d (the segment's decay is e^{A sum d}, exactly), a second
 // chains these, and the walk then starts each segment from its true state.  The
-// first kernel costs 0.75 of the walk (233 us beside 306), so the cut has to buy more.
+// first kernel costs 0.75 of the walk (214 us beside 295), so the cut has to buy more.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -455,8 +455,8 @@ cudaError_t launch_scan_s(const ScanArgs &a, int what, int sms, cudaStream_t st)
         if (what == SCAN_FORWARD) return launch_scan_t<BF16, S, 8, FORWARD, true>(a, st);
         if (what == SCAN_REVERSE) return launch_scan_t<BF16, S, 8, REVERSE, true>(a, st);
         // 16 states a thread leave a fifth fewer instructions (no shuffles at 16 states a channel), but
-        // half the warps: 16384 tokens x 4096 channels in many segments 311 us against 367, 8 sequences
-        // of 2048, two blocks an SM, 500 and more against 422.  So where blocks fill the SMs.
+        // half the warps: 16384 tokens x 4096 channels in many segments 306 us against 367, 8 sequences
+        // of 2048, 1.7 blocks an SM, 566 against 404, 16 of them 733 against 688.  So where blocks fill the SMs.
         if constexpr (S >= 16) {
             using L = Layout<BF16, S, 16>;
             const int per = a.D / a.G, tiles = (per + L::CH - 1) / L::CH;
