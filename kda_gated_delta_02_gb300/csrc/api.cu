@@ -1616,9 +1616,12 @@ static int scan_shape(int N, int T, int D, int G, int S, int dtype) {
 // sequences' blocks cover the SMs (twice forward, four times backward: half
 // the threads), only sequences of over four times the mean length are cut (of
 // over twice: 32 prompts of 0 to 4096 tokens took 1.11 ms and not 0.82); else all are, for
-// 16 blocks per SM (16384 tokens x 4096 channels: 540 us, with 4 609).
+// 16 blocks per SM (16384 tokens x 4096 channels: 540 us, with 4 609).  A token
+// of a whole sequence takes 0.11 us forward and 0.59 back, the two launches more
+// 10: 400 tokens x 1024 channels 43 and 237 us whole, 12 and 26 beside 37 in
+// segments of 64 and 32.
 static int scan_segment(int N, int T, int D, int G, int S, bool backward) {
-    if (T < 512 || N > kMaxGridY) return 0;
+    if (T < (backward ? 96 : 256) || N > kMaxGridY) return 0;
     const int ch = backward ? kda::scan_bwd_channels(S) : kda::scan_channels(S), sms = sm_count();
     const long long tiles = (long long)G * ((D / G + ch - 1) / ch), enough = backward ? 4LL * sms : 2LL * sms;
     long long seg;
@@ -1628,7 +1631,7 @@ static int scan_segment(int N, int T, int D, int G, int S, bool backward) {
     } else {
         const long long parts = tiles < 16LL * sms ? 16LL * sms / tiles : 1;
         seg = (T + parts - 1) / parts;
-        if (seg < 128) seg = 128;
+        if (seg < (backward ? 32 : 64)) seg = backward ? 32 : 64;
     }
     seg = (seg + 15) / 16 * 16;
     return seg >= T ? 0 : (int)seg;

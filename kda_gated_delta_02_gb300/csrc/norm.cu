@@ -256,7 +256,8 @@ kda_norm_bwd_kernel(NormArgs a) {
             weight.get(i, w);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const float2 c = LAYER ? __fadd2_rn(r.raw[i].pair(j), mm) : r.raw[i].pair(j), u = __fmul2_rn(g.raw[i].pair(j), w[j]);
+                const float2 c = LAYER ? __fadd2_rn(r.raw[i].pair(j), mm) : r.raw[i].pair(j), e = g.raw[i].pair(j);
+                const float2 u = make_float2(__fmul_rn(e.x, w[j].x), __fmul_rn(e.y, w[j].y));
                 t[0] = __ffma2_rn(c, c, t[0]);
                 t[1] = __ffma2_rn(u, c, t[1]);
                 if (LAYER) t[2] = __fadd2_rn(t[2], u);
@@ -280,7 +281,11 @@ kda_norm_bwd_kernel(NormArgs a) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const float2 x = LAYER ? __fadd2_rn(r.raw[i].pair(j), mm) : r.raw[i].pair(j), n = __fmul2_rn(x, rs), e = g.raw[i].pair(j);
-                out.set_pair(j, __fmul2_rn(rs, __ffma2_rn(n, kk, LAYER ? __ffma2_rn(e, w[j], us) : __fmul2_rn(e, w[j]))));
+                // (u rounded as it was when it was added up, so that a single channel's mean takes all of it away;
+                // the packed product and sum would be contracted)
+                const float2 u = make_float2(__fmul_rn(e.x, w[j].x), __fmul_rn(e.y, w[j].y));
+                const float2 v = LAYER ? make_float2(__fadd_rn(u.x, us.x), __fadd_rn(u.y, us.y)) : u;
+                out.set_pair(j, __fmul2_rn(rs, __ffma2_rn(n, kk, v)));
                 if constexpr (ACC && V == 1) {
                     float *p = acc + i * THREADS + lane;
                     p[0] = fmaf(e.x, n.x, p[0]);

@@ -112,6 +112,15 @@ def test_values_that_are_not_finite_stay_in_their_row(d):
         assert torch.equal(kda.norm_fwd(zero, w, b, kind=kind), b.expand(3, d))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_one_channel(dtype):
+    """Layer norm of a single channel: the bias, whatever the row, and no gradient of it."""
+    x, dy, w, b = _inputs(700, 1, DTYPES[dtype])
+    assert torch.equal(kda.norm_fwd(x, w, b, kind=kda.NORM_LAYER), b.to(x.dtype).expand(700, 1))
+    dx, dw, _ = kda.norm_bwd(x, dy, w, kind=kda.NORM_LAYER)
+    assert not dx.any() and not dw.any()
+
+
 def test_large_mean_costs_no_digits():
     """The variance is taken of differences: a mean a thousand times the spread leaves n right to a thousand roundings."""
     gen = torch.Generator(device="cuda")

@@ -275,7 +275,7 @@ def test_scan_abi_refuses_before_any_launch(lib):
 
 def test_workspaces_and_sizes(lib):
     """Whole sequences need no workspace; few or uneven long ones do.  Nothing for shapes that are refused."""
-    assert lib.kda_scan_workspace_size(8, 511, 64, 1, 16) == 0
+    assert lib.kda_scan_workspace_size(8, 255, 64, 1, 16) == 0
     assert lib.kda_scan_workspace_size(1, 20000, 64, 1, 16) > 0
     assert lib.kda_scan_workspace_size(2, 1000, 64, 1, 12) == 0 and lib.kda_scan_bwd_workspace_size(2, 1000, 64, 3, 16) == 0
     assert lib.kda_conv_bwd_workspace_size(1000, 64, 5) == 0 and lib.kda_norm_bwd_workspace_size(10, 16385, 0) == 0
