@@ -267,7 +267,6 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
             const float2 d = vals[k * PAIRS + pl], x = vals[(K + k) * PAIRS + pl], ev = vals[(2 * K + k) * PAIRS + pl];
             const float4 *b4 = reinterpret_cast<const float4 *>(bc + k * 2 * S + ln * M), *c4 = b4 + S / 4;
             const float2 dq[2] = {both(d.x), both(d.y)}, in[2] = {both(d.x * x.x), both(d.y * x.y)}, eq[2] = {both(ev.x), both(ev.y)};
-            const float2 minus[2] = {both(-in[0].x), both(-in[1].x)};
             float2 lB[2] = {both(0.f), both(0.f)}, lA[2] = {both(0.f), both(0.f)}, y[2] = {both(0.f), both(0.f)};
 #pragma unroll
             for (int n = 0; n < M / 4; ++n) {
@@ -282,7 +281,10 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
                         const float2 B = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
                         const float2 C = e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y);
                         const float2 H = e ? make_float2(H4.z, H4.w) : make_float2(H4.x, H4.y);
-                        const float2 ah = LATER ? __fmul2_rn(dec, H) : __ffma2_rn(minus[q], B, H);
+                        // (H less the product as the forward rounded it: nothing where nothing was there before; packed,
+                        // product and difference would be contracted)
+                        const float2 ah = LATER ? __fmul2_rn(dec, H)
+                                                : make_float2(__fsub_rn(H.x, __fmul_rn(in[q].x, B.x)), __fsub_rn(H.y, __fmul_rn(in[q].y, B.y)));
                         const float2 hk = LATER ? __ffma2_rn(in[q], B, ah) : H;
                         const float2 l = __ffma2_rn(C, eq[q], carry[q][2 * n + e]);
                         const float2 u = __fmul2_rn(l, ah);

@@ -210,6 +210,16 @@ def test_bad_sequences_are_reported_and_skipped():
         assert status.item() == kda.STATUS_BAD_SEQLENS, cu
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_first_tokens_have_no_gradient_of_the_rates(dtype):
+    """Sequences of one token from zero states: no decay was applied, so dA is zero to the bit."""
+    s = _inputs(9, 40, 1, 16, DTYPES[dtype], 9)
+    cu = _cu([1] * 9)
+    saved = kda.scan_fwd(*_args(s), cu, z=s["z"], save=True)[2]
+    grads = kda.scan_bwd(*_args(s), cu, s["dy"], saved, z=s["z"], dfinal_state=s["dfinal"])
+    assert not grads[2].any() and grads[0].any() and grads[3].any()
+
+
 def test_no_tokens():
     """Empty sequences alone: states pass through, gradients too; sums are zero."""
     s = _inputs(0, 24, 1, 16, torch.bfloat16, 2)
