@@ -3,7 +3,7 @@
 // gated sum, e_t = dy_t z_t sigmoid(z_t), and l_t the gradient of h_t, last token first:
 //
 //   l_t = C_t e_t + a_{t+1} l_{t+1},  a_t = e^{d_t A}
-//   dx_t = d_t sum_n l_t B_t + D e_t,   dd_t = x_t sum_n l_t B_t + sum_n l_t A a_t h_{t-1},   ddt = dd (1 - e^{-d})
+//   dx_t = d_t sum_n l_t B_t + D e_t,   dd_t = x_t sum_n l_t B_t + sum_n l_t A a_t h_{t-1},   ddt = dd e^v / (1 + e^v)
 //   dB_t = sum over channels of l_t d_t x_t,  dC_t = sum over channels of e_t h_t
 //   dA = sum_t d_t l_t a_t h_{t-1},  dD = sum_t e_t x_t,  dz_t = dy_t (sum_n C_t h_t + D x_t) sigma'(z_t)
 //
@@ -16,7 +16,7 @@
 // out to them.  The eight tokens from a saved state run forward with every
 // second state kept in shared memory, then backward: of the two tokens that
 // share a kept state H, the later one goes forward from it (a H, a H + b) and
-// the earlier one back (H - b, H), neither with an operation more.  The sums over channels
+// the earlier one back (H - b, H).  The sums over channels
 // add two in a thread's registers, then four floats at a time in shared
 // memory: 4 stores, 4 loads and 20 additions and exchanges per token, where
 // exchanges alone would take 62.  A block's four warps add theirs once per eight
