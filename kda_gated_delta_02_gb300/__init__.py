@@ -784,12 +784,14 @@ class _Device:
         return self.rows(t.as_strided((N * m, C), (step, t.stride(2))), name, dtype, (N * m, C), C)
 
     def workspace(self, t, need):
-        """(pointer, bytes) of a workspace of `need` bytes: t where it is large enough, else a new one."""
+        """(tensor, pointer, bytes) of a workspace of `need` bytes: t where it is large enough, else a new one, which the
+        caller holds until the library call has returned: freed before, its memory may be given to another thread (the
+        call lets go of the interpreter's lock) or back to the driver ahead of the launches that use it."""
         if need == 0:
-            return None, 0
+            return None, None, 0
         if t is None or t.nbytes < need:
             t = torch.empty(need, dtype=torch.uint8, device=self.like.device)
-        return self.flat(t, "workspace", t.dtype), t.nbytes
+        return t, self.flat(t, "workspace", t.dtype), t.nbytes
 
     def new(self, *shape, dtype=torch.float32):
         return torch.empty(shape, dtype=dtype, device=self.like.device)
@@ -857,7 +859,7 @@ def norm_bwd(x, dy, weight=None, eps=1e-6, kind=NORM_RMS, dx=None, want_dweight=
         op, os_ = _norm_rows(d, dx, "dx", x)
         dw = None if not want_dweight else d.new(n) if weight is None else torch.empty_like(weight)
         db = d.new(n) if want_dbias else None
-        ws, nb = d.workspace(workspace, lib.kda_norm_bwd_workspace_size(rows, n, dt) if want_dweight or want_dbias else 0)
+        held, ws, nb = d.workspace(workspace, lib.kda_norm_bwd_workspace_size(rows, n, dt) if want_dweight or want_dbias else 0)
         rc = lib.kda_norm_bwd(xp, gp, d.flat(weight, "weight", shape=(n,)), rows, n, xs, gs, os_, float(eps), int(kind), op,
                               _at(dw), _at(db), dt, ws, nb, d.stream)
         _check(rc, "kda_norm_bwd")
@@ -915,7 +917,7 @@ def conv_bwd(x, conv_w, cu_seqlens, dy, bias=None, tail=None, dtail_out=None, co
         gp, gs = d.rows(dy, "dy", dy.dtype, (T, C), C)
         op, os_ = d.rows(dx, "dx", x.dtype, (T, C), C)
         tp, ts = d.tails(tail, "tail", x.dtype, (N, W - 1, C))
-        ws, nb = d.workspace(workspace, lib.kda_conv_bwd_workspace_size(T, C, W))
+        held, ws, nb = d.workspace(workspace, lib.kda_conv_bwd_workspace_size(T, C, W))
         rc = lib.kda_conv_bwd(xp, d.flat(cu_seqlens, "cu_seqlens", torch.int32), d.flat(conv_w, "conv_w", shape=(C, W)),
                               d.flat(bias, "bias", shape=(C,)), tp, gp, d.flat(dtail_out, "dtail_out", shape=(N, W - 1, C)), N, T,
                               C, W, xs, ts, gs, os_, int(conv_act), op, _at(dw), _at(db), _at(dtail), dt, _in_dtype(dy), ws, nb, d.flat(status, "status", torch.int32),
@@ -983,7 +985,7 @@ def scan_fwd(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, initial_s
             elif saved.numel() < need:
                 raise KDAError(f"saved must hold {need} f32 values, got {saved.numel()}")
         yp, ys = d.rows(out, "out", x.dtype, (T, n), n)
-        ws, nb = d.workspace(workspace, lib.kda_scan_workspace_size(N, T, n, G, S))
+        held, ws, nb = d.workspace(workspace, lib.kda_scan_workspace_size(N, T, n, G, S))
         rc = lib.kda_scan_fwd(*ptrs, d.flat(cu_seqlens, "cu_seqlens", torch.int32), N, T, n, G, S, *strides, ys,
                               d.flat(initial_state, "initial_state", shape=(N, n, S)),
                               d.flat(final_state, "final_state", shape=(N, n, S)), int(bool(dt_softplus)), yp,
@@ -1011,7 +1013,7 @@ def scan_bwd(x, dt, A, B, C, cu_seqlens, dy, saved, D=None, z=None, dt_bias=None
         gp, gs = d.rows(dy, "dy", x.dtype, (T, n), n)
         dx, ddt, dz, dB, dC = (None if t is None else d.out(None, t) for t in (x, dt, z, B, C))
         dA, dD, dbias, dh = (None if t is None else torch.empty_like(t) for t in (A, D, dt_bias, initial_state))
-        ws, nb = d.workspace(workspace, lib.kda_scan_bwd_workspace_size(N, T, n, G, S))
+        held, ws, nb = d.workspace(workspace, lib.kda_scan_bwd_workspace_size(N, T, n, G, S))
         rc = lib.kda_scan_bwd(*ptrs, d.flat(cu_seqlens, "cu_seqlens", torch.int32), gp,
                               d.flat(dfinal_state, "dfinal_state", shape=(N, n, S)), d.flat(saved, "saved"), N, T, n, G, S,
                               *strides, gs, int(bool(dt_softplus)), _at(dx), _at(ddt), _at(dA), _at(dB), _at(dC), _at(dD),

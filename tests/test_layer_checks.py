@@ -1,5 +1,6 @@
 """Refusals of the norm, convolution and scan calls (binding and C ABI, no GPU)."""
 import ctypes
+import weakref
 
 import pytest
 import torch
@@ -286,3 +287,40 @@ def test_workspaces_and_sizes(lib):
     N, T, D = 600, 511, 130
     up = lambda x: (x + 255) // 256 * 256
     assert lib.kda_scan_bwd_workspace_size(N, T, D, 1, 16) == up(N * ((D * 18 + 3) // 4 * 4) * 4) + up(2 * T * 32 * 4)
+
+
+# ------------------------------------------------------------------ memory that a call makes for itself
+def test_workspaces_live_until_the_library_call_has_returned(monkeypatch):
+    """A workspace that the binding makes is held until the launches that use it are enqueued."""
+    made, alive, size = [], {}, 1 << 14
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_size"):
+                return lambda *a: size
+
+            def called(*a):
+                alive[name] = [m() is not None for m in made]
+                return 0
+            return called
+
+    lib, real = Lib(), torch.empty
+
+    def empty(*shape, **kw):  # (the workspace is all that these calls make so: their outputs are the fixture's fakes)
+        if kw.get("dtype") is not torch.uint8:
+            return real(*shape, **kw)
+        t = Fake(t=real(*shape, dtype=torch.uint8))
+        made.append(weakref.ref(t))
+        return t
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(kda, "load_library", lambda: lib)
+    x, dy, saved = Fake(7, 12, dtype=BF), Fake(7, 12, dtype=BF), Fake(size // 4)
+    scan = _scan()
+    calls = {"kda_norm_bwd": lambda: kda.norm_bwd(x, dy), "kda_conv_bwd": lambda: kda.conv_bwd(**_conv(dy=dy)),
+             "kda_scan_fwd": lambda: kda.scan_fwd(**scan), "kda_scan_bwd": lambda: kda.scan_bwd(**scan, dy=scan["x"], saved=saved)}
+    for name, call in calls.items():
+        del made[:]
+        call()
+        assert alive[name] == [True], name
+        assert [r() for r in made] == [None], name  # and no longer than the call
