@@ -803,6 +803,12 @@ class _Device:
         return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=like.device)
 
 
+def _int32(sizes):
+    """Sizes that the C ABI takes as 32-bit integers, which ctypes would cut off.  `sizes`: several, or'ed together."""
+    if sizes >> 31:
+        raise KDAError("sizes must be below 2^31")
+
+
 def _at(t):
     """Pointer of a tensor that the call made (None: null)."""
     return None if t is None else t.data_ptr()
@@ -832,6 +838,7 @@ def norm_fwd(x, weight=None, bias=None, eps=1e-6, kind=NORM_RMS, out=None, strea
     if x.dim() < 1 or x.shape[-1] < 1:
         raise KDAError("x must be [.., n]")
     dt, n = _in_dtype(x), x.shape[-1]
+    _int32(n)
     d = _Device(x, stream)
     with d.guard:
         xp, xs = _norm_rows(d, x, "x", x)
@@ -849,6 +856,7 @@ def norm_bwd(x, dy, weight=None, eps=1e-6, kind=NORM_RMS, dx=None, want_dweight=
     if x.dim() < 1 or x.shape[-1] < 1:
         raise KDAError("x must be [.., n]")
     dt, n = _in_dtype(x), x.shape[-1]
+    _int32(n)
     rows = x.numel() // n
     d = _Device(x, stream)
     with d.guard:
@@ -871,7 +879,9 @@ def _conv_shape(x, conv_w, cu_seqlens):
         raise KDAError("x must be [T, C] and conv_w [C, W]")
     if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2):
         raise KDAError("cu_seqlens must be int32 [N + 1] with N >= 1")
-    return x.shape[0], x.shape[1], conv_w.shape[1]
+    (T, C), W = x.shape, conv_w.shape[1]
+    _int32(T | C | W | (0 if cu_seqlens is None else cu_seqlens.shape[0]))
+    return T, C, W
 
 
 def conv_fwd(x, conv_w, cu_seqlens, bias=None, tail=None, output_tail=True, conv_act=CONV_SILU, out=None, tail_out=None,
@@ -948,6 +958,7 @@ def _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias):
         raise KDAError("x and dt must be [T, D], A [D, S], B and C [T, G, S]")
     T, n = x.shape
     G, S = B.shape[1:]
+    _int32(T | n | G | S)
     xp, xs = d.rows(x, "x", x.dtype, (T, n), n)
     dtp, dts = d.rows(dt, "dt", x.dtype, (T, n), n)
     zp, zs = d.rows(z, "z", x.dtype, (T, n), n)
@@ -960,6 +971,7 @@ def _scan_inputs(d, x, dt, A, B, C, D, z, dt_bias):
 def _scan_sequences(cu_seqlens):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise KDAError("cu_seqlens must be int32 [N + 1] with N >= 1")
+    _int32(cu_seqlens.shape[0])
     return cu_seqlens.shape[0] - 1
 
 

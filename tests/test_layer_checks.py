@@ -324,3 +324,24 @@ def test_workspaces_live_until_the_library_call_has_returned(monkeypatch):
         call()
         assert alive[name] == [True], name
         assert [r() for r in made] == [None], name  # and no longer than the call
+
+
+def test_sizes_past_31_bits_are_refused():
+    """The C ABI's sizes are 32-bit integers: larger ones are refused, not cut off."""
+    far = lambda *s, dtype=F32: Fake(t=torch.empty(s, dtype=dtype, device="meta"))
+    n = 2 ** 32 + 8
+    cu, w = Fake(3, dtype=I32), Fake(1, 4)
+    calls = [lambda: kda.norm_fwd(far(1, n)), lambda: kda.norm_bwd(far(1, n), far(1, n)),
+             lambda: kda.conv_fwd(far(n, 1), w, cu), lambda: kda.conv_fwd(Fake(8, 1), w, far(n, dtype=I32)),
+             lambda: kda.conv_bwd(far(n, 1), w, cu, far(n, 1)), lambda: kda.conv_fwd(far(2, n), far(n, 1), cu),
+             lambda: kda.conv_fwd(Fake(2, 1), far(1, n), cu), lambda: kda.conv_step(far(n, 1), w, far(n, 3, 1))]
+    for rows, D, S, G in ((n, 1, 8, 1), (2, n, 8, 1), (2, 1, n, 1), (2, 1, 8, n)):
+        x, A, B = far(rows, D), far(D, S), far(rows, G, S)
+        calls += [lambda a=(x, x, A, B, B): kda.scan_fwd(*a, cu), lambda a=(x, x, A, B, B): kda.scan_bwd(*a, cu, a[0], Fake(9)),
+                  lambda a=(x, x, A, B, B), s=far(rows, D, S): kda.scan_step(*a, s)]
+    x, A, B = Fake(2, 1), Fake(1, 8), Fake(2, 1, 8)
+    calls += [lambda: kda.scan_fwd(x, x, A, B, B, far(n, dtype=I32))]
+    for i, call in enumerate(calls):
+        with pytest.raises(kda.KDAError, match="below 2\\^31"):
+            call()
+            pytest.fail(str(i))
