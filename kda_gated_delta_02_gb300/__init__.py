@@ -825,9 +825,7 @@ def _norm_rows(d, t, name, like):
     if t.shape != like.shape:
         raise KDAError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
     if t.dim() != 2:
-        if not t.is_contiguous():
-            raise KDAError(f"{name} must be contiguous, or rows of two axes")
-        t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(0, t.shape[-1])
+        raise KDAError(f"{name} must be contiguous, or rows of two axes")
     return d.rows(t, name, t.dtype, t.shape, t.shape[1])
 
 
