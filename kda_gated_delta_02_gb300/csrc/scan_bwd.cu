@@ -14,9 +14,11 @@
 // three quarters (packed operations take two) and shared memory 68 % busy.  A thread keeps 2 channels of 8 states; S / 8 lanes
 // share a pair of channels, and the tokens' own work (steps, gates, outputs) is dealt
 // out to them.  The eight tokens from a saved state run forward with every
-// second state kept in shared memory, then backward: of the two tokens that
-// share a kept state H, the later one goes forward from it (a H, a H + b) and
-// the earlier one back (H - b, H).  The sums over channels
+// second token's decayed state G = a h kept in shared memory, then backward: of the
+// two tokens that share it, the earlier one has what it needs (G, G + b), the
+// later one goes forward from it (a (G + b), and its own b more).  The state h = G + b kept in
+// its place, and G taken back as h - b, took as long, and cost a state that
+// forgets to e^-10 in a token all but three digits of dA.  The sums over channels
 // add two in a thread's registers, then four floats at a time in shared
 // memory: 4 stores, 4 loads and 20 additions and exchanges per token, where
 // exchanges alone would take 62.  A block's four warps add theirs once per eight
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
         }
         if (i > 1) ahead(t0 - 2 * K);
         __syncthreads();
-        // forward, the states after tokens 0, 2, 4 and 6 kept
+        // forward, the decayed states of tokens 0, 2, 4 and 6 kept
 #pragma unroll 1
         for (int k = 0; k < min(rows, K - 1); ++k) {
             const float2 d = vals[k * PAIRS + pl], x = vals[(K + k) * PAIRS + pl];
@@ -208,14 +210,14 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
                 const float4 B4 = b4[n];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
+                    float2 ah[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float2 arg = __ffma2_rn(A2[q][2 * n + e], dq[q], both(kExp2Low)), b = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
-                        h[q][2 * n + e] = __ffma2_rn(make_float2(exp2_fast(arg.x), exp2_fast(arg.y)), h[q][2 * n + e], __fmul2_rn(in[q], b));
+                        ah[e] = __fmul2_rn(make_float2(exp2_fast(arg.x), exp2_fast(arg.y)), h[q][2 * n + e]);
+                        h[q][2 * n + e] = __ffma2_rn(in[q], b, ah[e]);
                     }
-                    if ((k & 1) == 0)
-                        hist[((k >> 1) * V4 + q * (M / 4) + n) * 32 + lane] =
-                            make_float4(h[q][2 * n].x, h[q][2 * n].y, h[q][2 * n + 1].x, h[q][2 * n + 1].y);
+                    if ((k & 1) == 0) hist[((k >> 1) * V4 + q * (M / 4) + n) * 32 + lane] = make_float4(ah[0].x, ah[0].y, ah[1].x, ah[1].y);
                 }
             }
         }
@@ -267,10 +269,17 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
             const float2 d = vals[k * PAIRS + pl], x = vals[(K + k) * PAIRS + pl], ev = vals[(2 * K + k) * PAIRS + pl];
             const float4 *b4 = reinterpret_cast<const float4 *>(bc + k * 2 * S + ln * M), *c4 = b4 + S / 4;
             const float2 dq[2] = {both(d.x), both(d.y)}, in[2] = {both(d.x * x.x), both(d.y * x.y)}, eq[2] = {both(ev.x), both(ev.y)};
+            float2 in0[2];  // of the earlier token
+            if constexpr (LATER) {
+                const float2 d0 = vals[(k - 1) * PAIRS + pl], x0 = vals[(K + k - 1) * PAIRS + pl];
+                in0[0] = both(d0.x * x0.x), in0[1] = both(d0.y * x0.y);
+            }
             float2 lB[2] = {both(0.f), both(0.f)}, lA[2] = {both(0.f), both(0.f)}, y[2] = {both(0.f), both(0.f)};
 #pragma unroll
             for (int n = 0; n < M / 4; ++n) {
                 const float4 B4 = b4[n], C4 = c4[n];
+                float4 P4;  // B of the earlier token
+                if constexpr (LATER) P4 = (b4 - 2 * S / 4)[n];
                 float2 sB[2], sC[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -281,11 +290,9 @@ __global__ void __launch_bounds__(kThreads, 3) kda_scan_bwd_kernel(ScanArgs a) {
                         const float2 B = e ? make_float2(B4.z, B4.w) : make_float2(B4.x, B4.y);
                         const float2 C = e ? make_float2(C4.z, C4.w) : make_float2(C4.x, C4.y);
                         const float2 H = e ? make_float2(H4.z, H4.w) : make_float2(H4.x, H4.y);
-                        // (H less the product as the forward rounded it: nothing where nothing was there before; packed,
-                        // product and difference would be contracted)
-                        const float2 ah = LATER ? __fmul2_rn(dec, H)
-                                                : make_float2(__fsub_rn(H.x, __fmul_rn(in[q].x, B.x)), __fsub_rn(H.y, __fmul_rn(in[q].y, B.y)));
-                        const float2 hk = LATER ? __ffma2_rn(in[q], B, ah) : H;
+                        float2 ah = H;  // of the earlier token, kept
+                        if constexpr (LATER) ah = __fmul2_rn(dec, __ffma2_rn(in0[q], e ? make_float2(P4.z, P4.w) : make_float2(P4.x, P4.y), H));
+                        const float2 hk = __ffma2_rn(in[q], B, ah);
                         const float2 l = __ffma2_rn(C, eq[q], carry[q][2 * n + e]);
                         const float2 u = __fmul2_rn(l, ah);
                         carry[q][2 * n + e] = __fmul2_rn(dec, l);

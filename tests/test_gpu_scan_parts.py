@@ -124,6 +124,24 @@ def test_gradients_of_cut_sequences_against_differences():
         assert abs(diff - want) < (32 * e * e + 256 * 2.0 ** -24 / e) * want, (name, diff, want)
 
 
+@pytest.mark.parametrize("S", [8, 16, 32, 64])
+@pytest.mark.parametrize("lens", [[1], [2], [3, 8], [40, 1, 5], [300, 0, 200]])
+def test_rates_of_states_that_forget(lens, S):
+    """Decays down to e^-19 a token: what is left of a state beside what is added keeps its relative precision in dA, element
+    by element.  All terms are positive, so that every one is within its own roundings: 8.5 for each unit of an exponent up to
+    19.5, 60 each for the state and what comes back, 40 for products and sums, in all below 512."""
+    D, G = 34, 2
+    s, r = ref.inputs(lens, D, G, S, torch.float32), lambda *n: 0.5 + torch.rand(n, device="cuda")
+    torch.manual_seed(S)
+    s = {k: r(*v.shape) for k, v in s.items()}
+    s.update(D=None, z=None, dt_bias=None, dt=1.5 * s["dt"] - 1.75, A=-torch.linspace(0.5, 20, S, device="cuda").repeat(D, 1))
+    got, want = _both(s, lens), ref.scan(s, lens)
+    off = np.abs(got["dA"].double().cpu().numpy() - want["dA"]) / want["dA"]
+    assert off.max() <= 512 * 2.0 ** -24, off.max() * 2 ** 24
+    for name in ("dB", "dC", "dx", "ddt"):
+        ref.check(name, got[name], want[name], lens)
+
+
 # ------------------------------------------------------------------ the hardware's 2^x
 def _decays(tokens, back):
     """A state of 1 that only decays, by 2^-7 to 2^-3 powers of two a token or so: the mean over the states of what a token's
