@@ -632,8 +632,9 @@ size_t kda_cache4_attention_workspace_size(int R, int T, int Hq, int Hkv, int d,
  * group are a multiple of 16 bytes) wider accesses run.  Other tensors are contiguous and
  * start on 16-byte boundaries.  dtype is bf16 or f32.  Outputs overlap neither
  * inputs nor one another (kda_norm_*: y may be x, and dx may be x or dy, row for
- * row): KDA_ERR_INVALID_ARG.  Sums, statistics and states are fp32; an output
- * is rounded once.  The same inputs give the same bits.
+ * row): KDA_ERR_INVALID_ARG.  Sums, statistics and states are fp32 (rows whose squares
+ * add up to 2^128 or more come out 0, as 1 / infinity); an output is rounded
+ * once.  The same inputs give the same bits.
  * Sequences: cu_seqlens device int32 [N + 1], N >= 1, T <= 2^30.  A sequence
  * whose ends are not in order or not in [0, T] sets KDA_STATUS_BAD_SEQLENS, and
  * its outputs and those of the sequences behind it are unspecified.  Rows of no
@@ -695,7 +696,7 @@ int kda_conv_bwd(const void *x, const int32_t *cu_seqlens, const float *w, const
                  void *stream);
 size_t kda_conv_bwd_workspace_size(int T, int C, int W);
 
-/* One token for each of R requests: y from x and the tail (rows of C, [R][W - 1] of them), which
+/* One token for each of R >= 1 requests: y from x and the tail (rows of C, [R][W - 1] of them), which
  * moves on in place. */
 int kda_conv_step(const void *x, const float *w, const float *bias, void *tail, int R, int C, int W,
                   long long x_stride, long long tail_stride, long long y_stride, int conv_act, void *y,
@@ -744,7 +745,7 @@ int kda_scan_bwd(const void *x, const void *dt, const float *A, const void *B, c
                  size_t workspace_bytes, uint32_t *status, void *stream);
 size_t kda_scan_bwd_workspace_size(int N, int T, int D, int G, int S);
 
-/* One token for each of R requests (rows as above, R of them); state device f32 [R][D][S] moves on in
+/* One token for each of R >= 1 requests (rows as above, R of them); state device f32 [R][D][S] moves on in
  * place. */
 int kda_scan_step(const void *x, const void *dt, const float *A, const void *B, const void *C,
                   const float *skip, const void *z, const float *dt_bias, float *state, int R, int D,

@@ -1615,11 +1615,13 @@ static int scan_shape(int N, int T, int D, int G, int S, int dtype) {
 // Tokens of a segment (a multiple of 16), or 0 for whole sequences.  Where the
 // sequences' blocks cover the SMs (twice forward, four times backward: half
 // the threads), only sequences of over four times the mean length are cut (of
-// over twice: 32 prompts of 0 to 4096 tokens took 1.11 ms and not 0.82); else all are, for
-// 16 blocks per SM (16384 tokens x 4096 channels: 540 us, with 4 609).  A token
-// of a whole sequence takes 0.11 us forward and 0.59 back, the two launches more
-// 10: 400 tokens x 1024 channels 43 and 237 us whole, 12 and 26 beside 37 in
-// segments of 64 and 32.
+// over twice: 32 prompts of 0 to 4096 tokens take 1.10 ms and not 0.78).  The host does not
+// see the lengths: where none is that long the two launches for segments find
+// nothing to do, which costs 8 us of 389 (8 x 2048 tokens x 4096 channels), 11 of 666
+// (16 x 2048) and 27 of 184 (64 x 128; backward 31 of 683).  Else all are cut, for
+// 16 blocks per SM (16384 tokens x 4096 channels: 516 us, with 4 573; whole 1404).  A token
+// of a whole sequence takes 0.09 us forward and 0.6 back: 400 tokens x 1024 channels, as
+// launches of a graph, 36 and 243 us whole, 16 and 36 in segments of 64 and 32.
 static int scan_segment(int N, int T, int D, int G, int S, bool backward) {
     if (T < (backward ? 96 : 256) || N > kMaxGridY) return 0;
     const int ch = backward ? kda::scan_bwd_channels(S) : kda::scan_channels(S), sms = sm_count();

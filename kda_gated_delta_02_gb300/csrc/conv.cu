@@ -21,7 +21,11 @@
 // (5.0 TB/s) and 10 for the sums; 16384 ragged tokens x 36864 channels 436 us (6.1
 // TB/s).  Eight channels a thread with checks at every token took 149 us, 64
 // registers (eight blocks an SM) rather than 71 gained 5 %; two channels a thread in
-// the backward lost 16 %, its 126 registers forced to 102 spill and double it.
+// the backward lost 16 %, its 123 registers forced to 102 spill and double it.  That
+// backward is four blocks an SM that wait for rows asked for: latency.  All of this for
+// bf16.  32-bit rows: forward 217 us (4.9 TB/s; 104 bytes of spills under the 64 registers), backward
+// 277; 32-bit dy beside bf16 rows (144 registers, three blocks an SM) 218, where dy of bf16
+// takes 174 measured the same way, after a flush of L2.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -399,8 +403,10 @@ __global__ void __launch_bounds__(kThreads) kda_conv_bwd_kernel(ConvArgs a) {
 
 // One token per request; tail [R][W - 1][C] moves on in place.  A block takes
 // `run` requests, so that the taps (16 bytes a channel, as many as two bf16
-// tails) are read once for them.  Bytes bound it: 256 x 36864 channels, bf16, 24.7 us
-// (6.1 TB/s) with part of the tails in L2, 31 with other ones each time.
+// tails) are read once for them.  256 x 36864 channels, bf16: 31.4 us with other tails
+// each time (4.8 TB/s), 26 with part of them in L2; 32-bit 54 (5.6 TB/s).  The tail is written in
+// place, so a request's rows are asked for only after the one before has stored its
+// own: loads in flight bound it, not bytes (17 stalls on them per instruction issued).
 template <bool BF16, int V, int W>
 __global__ void __launch_bounds__(kThreads) kda_conv_step_kernel(ConvArgs a) {
     using E = Elem<BF16>;
@@ -473,7 +479,7 @@ int conv_run(int T, int C, int v, bool backward, int sms) {
 }
 
 // Requests of a block of single tokens: up to 16, while every SM has 4 blocks
-// (256 x 36864 channels: 26.0 us, with 2 blocks 27.7, with 16 30.9)
+// (256 x 36864 channels, part of the tails in L2: 26.0 us, with 2 blocks 27.7, with 16 30.9)
 int conv_step_run(int R, int C, int v, int sms) {
     const long long tiles = (C + kThreads * v - 1) / (kThreads * v);
     int run = 16;

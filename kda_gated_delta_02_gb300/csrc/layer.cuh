@@ -102,7 +102,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return y;
 }
 
-// 1 / (1 + e^-x): past e^-x = 2^126 it comes out 0, as it should
+// 1 / (1 + e^-x): past e^-x = 2^126 it comes out 0 (where x sigmoid(x) is below 1.1e-36)
 __device__ __forceinline__ float sigmoid(float x) { return rcp_fast(1.f + __expf(-x)); }
 // x sigmoid(x); -inf gives NaN, as the product does
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }

@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(256) kda_scan_chain_kernel(ScanArgs a, int S, 
 // a channel S / 4 lanes, and a block walks `rows` requests with the rates A in
 // registers.  The four requests' steps and outputs are dealt out to a
 // channel's lanes.  256 x 8192 channels of 16 states: 51 us (5.6 TB/s); 82 with every lane
-// forming all four, 58 with registers for two blocks an SM rather than four.
+// forming all four, 58 with registers for two blocks an SM rather than four.  (32-bit rows
+// spill under that cap: 66 us against 45 for their bytes, and 90 against 50 with 8 states.)
 template <bool BF16, int S>
 __global__ void __launch_bounds__(256, 4) kda_scan_step_kernel(ScanArgs a, int rows) {
     using E = Elem<BF16>;
@@ -446,7 +447,7 @@ template <bool BF16, int S>
 cudaError_t launch_scan_s(const ScanArgs &a, int what, int sms, cudaStream_t st) {
     if (what == SCAN_STEP) {
         const int blocks = (a.D + 1024 / S - 1) / (1024 / S);
-        // requests of a block: the rates are read once for them, while the grid covers the SMs twice
+        // requests of a block: the rates are read once for them, while every SM has 16 blocks (four times what runs at once)
         int rows = 16;
         while (rows > 1 && (long long)blocks * ((a.N + rows - 1) / rows) < 16LL * sms) rows /= 2;
         kda_scan_step_kernel<BF16, S><<<blocks * ((a.N + rows - 1) / rows), 256, 0, st>>>(a, rows);

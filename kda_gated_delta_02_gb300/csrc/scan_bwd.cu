@@ -10,8 +10,8 @@
 // What bounds it: instructions and shared memory.  A pair of states costs 15
 // packed operations and four exponentials (two of them the recomputed states'), and the sums
 // of dB and dC over channels go through shared memory: 8 sequences of 2048 tokens x
-// 4096 channels in 16 x 152 blocks 1.24 ms, 5.3 cycles of an SM for a token and channel, issue slots
-// three quarters (packed operations take two) and shared memory 68 % busy.  A thread keeps 2 channels of 8 states; S / 8 lanes
+// 4096 channels in 16 x 152 blocks 1.25 ms, 5.3 cycles of an SM for a token and channel, issue slots
+// three quarters (packed operations take two) and shared memory 69 % busy.  A thread keeps 2 channels of 8 states; S / 8 lanes
 // share a pair of channels, and the tokens' own work (steps, gates, outputs) is dealt
 // out to them.  The eight tokens from a saved state run forward with every
 // second token's decayed state G = a h kept in shared memory, then backward: of the
