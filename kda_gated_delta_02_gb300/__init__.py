@@ -786,7 +786,7 @@ class _Device:
     def workspace(self, t, need):
         """(tensor, pointer, bytes) of a workspace of `need` bytes: t where it is large enough, else a new one, which the
         caller holds until the library call has returned: freed before, its memory may be given to another thread (the
-        call lets go of the interpreter's lock) or back to the driver ahead of the launches that use it."""
+        call lets go of the interpreter's lock) or returned by the allocator ahead of the launches that use it."""
         if need == 0:
             return None, None, 0
         if t is None or t.nbytes < need:
